@@ -125,12 +125,13 @@ def work(case):
 
 def _quantise(c):
     """The latents' e4m3 codes (as bytes) and their scales' biased exponents. The scale of a
-    group is the least power of two that brings its largest magnitude to 448 or less."""
+    group is the least power of two, from 2^-110 to 2^119, that brings its largest magnitude to
+    448 or less; what 2^119 leaves above that becomes 448."""
     g = c.float().unflatten(-1, (-1, GROUP))
     m, e = torch.frexp(g.abs().amax(-1))                 # amax = m 2^e, m in [0.5, 1)
     e = torch.where(m > 0.875, e - 8, e - 9)
-    e = torch.where(m == 0, -110, e.clamp(-110, 120))
-    codes = torch.ldexp(g, -e[..., None]).to(torch.float8_e4m3fn).flatten(-2)
+    e = torch.where(m == 0, -110, e.clamp(-110, 119))
+    codes = torch.ldexp(g, -e[..., None]).clamp(-448, 448).to(torch.float8_e4m3fn).flatten(-2)
     return codes.view(torch.uint8), (e + 127).to(torch.uint8)
 
 
@@ -374,7 +375,7 @@ def _exact_append(s):
         pos = torch.arange(hi - lo, device="cuda") + int(s["past"][b])
         at = s["table"][b, pos // BLOCK].long() * BLOCK + pos % BLOCK
         g = c[lo:hi].reshape(-1, R // GROUP, GROUP)
-        e = torch.ceil(torch.log2(g.abs().amax(-1, keepdim=True) / 448)).clamp(-110, 120)
-        values[at] = (g * torch.exp2(-e)).reshape(-1, R)
+        e = torch.ceil(torch.log2(g.abs().amax(-1, keepdim=True) / 448)).clamp(-110, 119)
+        values[at] = (g * torch.exp2(-e)).clamp(-448, 448).reshape(-1, R)
         rope[at] = s["k"][lo:hi].double()
     return {"codes": values.view(s["codes"].shape), "scales": None, "rope": rope.view(s["rope"].shape)}
