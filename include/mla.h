@@ -20,6 +20,8 @@
  * support): MLA_KV_INT2_ROT_QR keeps the rope key unrotated as further INT2
  * groups; MLA_KV_INT2_JOINT rotates the latent and the rope key together by one
  * eigenbasis of the whole row and quantises the result.
+ * MLA_KV_MXFP8 keeps the latent unrotated as 8-bit e4m3 values with one power-of-two
+ * scale for every 32 of them (the microscaling layout), and the rope key in bf16.
  *
  * Definitions (per sequence b, query row i, head h, cached token t):
  *   s = scale * (q[b,i,h,:] . [c_t ; kR_t])          (rotated kind: q_lat . R)
@@ -73,10 +75,13 @@ typedef enum {
     MLA_KV_INT2_ROT_QR = 3,    /* rotated latent and the (unrotated) rope key, both
                                   as grouped INT2: [c . R ; k_R] in (r + d_R) /
                                   group_size groups; d_R a multiple of group_size */
-    MLA_KV_INT2_JOINT = 4      /* the whole row rotated by one eigenbasis R_j of
+    MLA_KV_INT2_JOINT = 4,     /* the whole row rotated by one eigenbasis R_j of
                                   [c ; k_R] ((r + d_R) x (r + d_R)) and stored as
                                   grouped INT2: [c ; k_R] . R_j in (r + d_R) /
                                   group_size groups; generic kernel only */
+    MLA_KV_MXFP8 = 5           /* latent as e4m3 codes with a power-of-two scale per
+                                  32 values + bf16 rope key; r a multiple of 32,
+                                  group_size 32, d_R at least 8 */
 } mla_kv_kind;
 
 typedef enum {
@@ -134,6 +139,11 @@ typedef enum {
  *               scale_zero [num_blocks, block_size, (r + d_R) / group_size, 2]
  *                          fp16, as above over the row [c . R ; k_R]; rope unused
  *   INT2_JOINT: codes and scale_zero as INT2_ROT_QR, over the row [c ; k_R] . R_j
+ *   MXFP8:      codes      [num_blocks, block_size, r]        uint8, e4m3 (sign, 4
+ *               exponent bits of bias 7, 3 fraction bits)
+ *               scale_zero [num_blocks, block_size, r / 32]   uint8, the biased
+ *               exponent e + 127 of the group's scale 2^e; value = code * 2^e
+ *               rope       [num_blocks, block_size, d_R]      bf16
  * Unused members are NULL. */
 typedef struct {
     void *latent;
@@ -168,6 +178,11 @@ size_t mla_workspace_bytes(const mla_shape *shape, int32_t B, int32_t q_len);
  * zero) / scale), 0, 3), 0 when scale == 0. INT2_ROT_QR: the rope groups encode
  * k_R as given (bf16 widened to fp32, not rotated) with their own thresholds.
  * INT2_JOINT: y = [c ; k_R] . R_j by the same fp32 chain over all r + d_R inputs.
+ * MXFP8 encoding per token and group of 32: e is the least exponent with max |c| /
+ * 2^e <= 448, within [-110, 119] (a group of zeros: -110); code = the nearest e4m3
+ * value to c / 2^e, ties to even (magnitudes above 448 * 2^119 become that).
+ * Every value read back is a bf16. A group with an infinity or a NaN in it gets the scale byte 255 and reads
+ * back as NaN. R and clip are not used.
  *   Source: OSCAR issue #10, maintainer reply (rotated + quantised latent in
  *   the cache, thresholds fit on the rotated latent). */
 mla_status mla_latent_append(const mla_shape *shape, const mla_cache *cache,
@@ -176,6 +191,26 @@ mla_status mla_latent_append(const mla_shape *shape, const mla_cache *cache,
                              int32_t num_new, const void *c_kv, const void *k_rope,
                              const float *R, const float *clip, int32_t *status,
                              void *stream);
+
+/* Read cached tokens back as dense rows: the reverse of mla_latent_append, with the
+ * same description of the tokens.
+ *   start_pos   [B] int32: position of the first token to read of each sequence.
+ *   cu_rows     [B + 1] int32: prefix sums of the tokens to read; row n of sequence b
+ *               (cu_rows[b] <= n < cu_rows[b+1]) is the token at position
+ *               start_pos[b] + n - cu_rows[b].
+ *   num_rows    host int: cu_rows[B], or an upper bound of it that `rows` has room
+ *               for (rows from cu_rows[B] on are left as they were).
+ *   rows        [num_rows, r + d_R]: the latent, then the rope key. bf16 for the BF16
+ *               and MXFP8 kinds (exact for both); fp32 for the others (FP32 as stored;
+ *               INT2: fmaf(code, scale, zero), in the cache's rotated basis, and the
+ *               bf16 rope key widened).
+ *   status      optional [1] int32 device word; flags are OR-ed into it.
+ * A token whose block id is out of range, or whose position is outside the block
+ * table, raises a flag and its row is written as NaN. */
+mla_status mla_latent_read(const mla_shape *shape, const mla_cache *cache, const int32_t *block_table,
+                           int32_t max_blocks_per_seq, int32_t B, const int32_t *start_pos,
+                           const int32_t *cu_rows, int32_t num_rows, void *rows, int32_t *status,
+                           void *stream);
 
 /* Decode attention, one query row per sequence (q_len = 1).
  *   seq_lens   [B] int32: tokens in the cache per sequence (>= 1).
@@ -231,6 +266,41 @@ mla_status mla_verify(const mla_shape *shape, const mla_cache *cache,
                       const int32_t *seq_lens, int32_t B, int32_t q_len, const void *q,
                       const void *W_UV, const float *R, float scale, void *out,
                       float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Prefill: attention of chunks of new tokens, of a length of their own for each
+ * sequence, over the paged cache that already holds them (appended before, as for
+ * mla_verify). Works in the decompressed form: per-head keys W_UK[h] . c and values
+ * W_UV[h]^T . c of every cached token are made once per call, so the query is NOT
+ * absorbed, and a (new token, cached token) pair costs d_n + d_R + d_v multiply-adds a
+ * head instead of the absorbed form's 2 r + d_R. For a chunk of fewer than about r / 3
+ * tokens over a long cache mla_verify does less work.
+ *   seq_lens   [B] int32: tokens in the cache per sequence, the new ones included.
+ *   cu_q       [B + 1] int32: prefix sums of the new tokens; those of sequence b are
+ *              rows cu_q[b] .. cu_q[b+1]-1 of q and its last cached positions. A
+ *              sequence may have none (its cache is then not read).
+ *   num_q      host int: cu_q[B], or an upper bound of it that q, out and lse have room
+ *              for (rows from cu_q[B] on are left as they were).
+ *   max_tokens host int: sum of seq_lens over the sequences with new tokens, or an upper
+ *              bound of it. Sizes the workspace; sequences that go past it are refused
+ *              on the device (flag, NaN rows).
+ *   nope_dim   d_n, a multiple of 8, at most 512.
+ *   q          [num_q, H, d_n + d_R] (nope part, then rope part), bf16 (FP32 kind: fp32).
+ *   W_UK       [H, d_n, r], W_UV [H, r, d_v], bf16 (FP32 kind: fp32).
+ *   out        [num_q, H, d_v] bf16 (FP32 kind: fp32).
+ *   lse        [num_q, H] fp32 natural-log softmax denominators, or NULL.
+ *   workspace  at least mla_prefill_workspace_bytes(shape, B, num_q, max_tokens, d_n).
+ * New token i of sequence b sees positions 0 .. seq_lens[b] - n_b + i. Keys and values
+ * are rounded to bf16 before the products (BF16 and MXFP8 kinds), as a layer that
+ * decompresses its cache stores them. Kinds: BF16, FP32, MXFP8; MLA_ERR_UNSUPPORTED
+ * for the INT2 kinds (use mla_verify) and for v_head_dim > 1024. A sequence with a bad
+ * length or block gets NaN rows; mla_get_status(workspace) reports the flags. */
+size_t mla_prefill_workspace_bytes(const mla_shape *shape, int32_t B, int32_t num_q, int32_t max_tokens,
+                                   int32_t nope_dim);
+mla_status mla_prefill(const mla_shape *shape, const mla_cache *cache, const int32_t *block_table,
+                       int32_t max_blocks_per_seq, const int32_t *seq_lens, const int32_t *cu_q, int32_t B,
+                       int32_t num_q, int32_t max_tokens, int32_t nope_dim, const void *q, const void *W_UK,
+                       const void *W_UV, float scale, void *out, float *lse, void *workspace,
+                       size_t workspace_bytes, void *stream);
 
 /* mla_decode for callers that cannot allocate device memory at call time, such
  * as an inference-engine plugin whose enqueue step must not allocate, or a

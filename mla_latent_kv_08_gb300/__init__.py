@@ -31,6 +31,7 @@ MLA_KV_FP32 = 1
 MLA_KV_INT2_ROT = 2
 MLA_KV_INT2_ROT_QR = 3
 MLA_KV_INT2_JOINT = 4
+MLA_KV_MXFP8 = 5
 
 MLA_IMPL_AUTO = 0
 MLA_IMPL_SIMT = 1
@@ -47,6 +48,7 @@ EXPORTED = (
     "mla_latent_append_index", "mla_fold_rotation", "mla_append_decode",
     "mla_calib_covariance", "mla_calib_projection_energy", "mla_calib_eigh", "mla_calib_eigh_weighted",
     "mla_calib_project_abs", "mla_calib_thresholds",
+    "mla_latent_read", "mla_prefill", "mla_prefill_workspace_bytes",
 )
 
 
@@ -121,6 +123,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     for name in ("mla_calib_covariance", "mla_calib_projection_energy", "mla_calib_eigh", "mla_calib_eigh_weighted",
                  "mla_calib_project_abs", "mla_calib_thresholds"):
         getattr(lib, name).restype = i32
+    lib.mla_latent_read.argtypes = [sp, cp, vp, i32, i32, vp, vp, i32, vp, vp, vp]
+    lib.mla_latent_read.restype = i32
+    lib.mla_prefill_workspace_bytes.argtypes = [sp, i32, i32, i32, i32]
+    lib.mla_prefill_workspace_bytes.restype = sz
+    lib.mla_prefill.argtypes = [sp, cp, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp, vp, ctypes.c_float, vp, vp, vp,
+                                sz, vp]
+    lib.mla_prefill.restype = i32
     lib.mla_profile_enable.argtypes = [i32]
     lib.mla_profile_enable.restype = i32
     lib.mla_profile_read.argtypes = [ctypes.POINTER(ctypes.c_double), i32p, i32p]
@@ -214,6 +223,10 @@ class Cache:
                        codes=alloc((nb, bs, (r + dR) // 4), dtype=torch.uint8, device=device),
                        scale_zero=alloc((nb, bs, (r + dR) // shape.group_size, 2), dtype=torch.float16,
                                         device=device))
+        if shape.kind == MLA_KV_MXFP8:
+            return cls(shape, codes=alloc((nb, bs, r), dtype=torch.uint8, device=device),
+                       scale_zero=alloc((nb, bs, r // 32), dtype=torch.uint8, device=device),
+                       rope=alloc((nb, bs, dR), dtype=torch.bfloat16, device=device))
         dt = torch.float32 if shape.kind == MLA_KV_FP32 else torch.bfloat16
         return cls(shape, latent=alloc((nb, bs, r + dR + shape.index_dim), dtype=dt, device=device))
 
@@ -224,6 +237,8 @@ class Cache:
         if s.kind in (MLA_KV_INT2_ROT_QR, MLA_KV_INT2_JOINT):
             qd = s.kv_lora_rank + s.rope_dim
             return qd // 4 + (qd // s.group_size) * 4
+        if s.kind == MLA_KV_MXFP8:
+            return s.kv_lora_rank + s.kv_lora_rank // 32 + 2 * s.rope_dim
         return (4 if s.kind == MLA_KV_FP32 else 2) * (s.kv_lora_rank + s.rope_dim + s.index_dim)
 
 
@@ -262,6 +277,43 @@ def mla_latent_append_index(cache: Cache, block_table, start_pos, cu_new, index_
                                        _ptr(cu_new), int(index_key.shape[0]), _ptr(index_key), _ptr(status),
                                        _stream(stream))
     _check(code, "mla_latent_append_index")
+
+
+def mla_latent_read(cache: Cache, block_table, start_pos, cu_rows, rows, status=None, stream=None) -> None:
+    """Cached tokens back as dense rows [len(rows), r + d_R] (see include/mla.h): bf16 for
+    the BF16 and MXFP8 kinds, fp32 for the others."""
+    lib = load_library()
+    code = lib.mla_latent_read(ctypes.byref(cache.shape.c()), ctypes.byref(cache.c()), _ptr(block_table),
+                               int(block_table.shape[1]), int(start_pos.shape[0]), _ptr(start_pos), _ptr(cu_rows),
+                               int(rows.shape[0]), _ptr(rows), _ptr(status), _stream(stream))
+    _check(code, "mla_latent_read")
+
+
+def mla_prefill_workspace_bytes(shape: Shape, B: int, num_q: int, max_tokens: int, nope_dim: int) -> int:
+    n = load_library().mla_prefill_workspace_bytes(ctypes.byref(shape.c()), int(B), int(num_q), int(max_tokens),
+                                                   int(nope_dim))
+    if n == 0:
+        raise MlaError(MLA_ERR_INVALID, "mla_prefill_workspace_bytes")
+    return int(n)
+
+
+def alloc_prefill_workspace(shape: Shape, B: int, num_q: int, max_tokens: int, nope_dim: int, device="cuda"):
+    import torch
+    return torch.empty(mla_prefill_workspace_bytes(shape, B, num_q, max_tokens, nope_dim), dtype=torch.uint8,
+                       device=device)
+
+
+def mla_prefill(cache: Cache, block_table, seq_lens, cu_q, q, W_UK, W_UV, scale: float, out, workspace,
+                max_tokens: int, lse=None, stream=None, shape: Optional[Shape] = None) -> None:
+    """Attention of chunks of new tokens, q [num_q, H, d_n + d_R] (not absorbed), over the
+    cache that holds them already -> out [num_q, H, d_v], lse [num_q, H] (see include/mla.h)."""
+    lib = load_library()
+    code = lib.mla_prefill(ctypes.byref((shape or cache.shape).c()), ctypes.byref(cache.c()), _ptr(block_table),
+                           int(block_table.shape[1]), _ptr(seq_lens), _ptr(cu_q), int(seq_lens.shape[0]),
+                           int(q.shape[0]), int(max_tokens), int(W_UK.shape[1]), _ptr(q), _ptr(W_UK), _ptr(W_UV),
+                           float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
+                           int(workspace.numel() * workspace.element_size()), _stream(stream))
+    _check(code, "mla_prefill")
 
 
 def mla_decode(cache: Cache, block_table, seq_lens, q, W_UV, scale: float, out, lse, workspace,

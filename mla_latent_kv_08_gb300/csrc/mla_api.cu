@@ -15,6 +15,11 @@ static int device_sm_count() {
 
 static bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
+// The three arrays of an 8-bit cache.
+static bool mx_cache_ok(const mla_cache *c) {
+    return c->codes && c->scale_zero && c->rope && aligned16(c->codes) && aligned16(c->scale_zero) && aligned16(c->rope);
+}
+
 // ---- benchmarking diagnostics (see mla_profile_enable) ----------------------
 struct Profile {
     bool on = false;
@@ -54,11 +59,13 @@ static mla_status check_shape(const mla_shape *s) {
     if (s->num_heads < 1 || s->kv_lora_rank < 8 || s->kv_lora_rank % 8 || s->rope_dim < 0 ||
         s->rope_dim % 8 || s->v_head_dim < 1 || s->block_size < 1 || s->num_blocks < 1)
         return MLA_ERR_INVALID;
-    if (s->kind != MLA_KV_BF16 && s->kind != MLA_KV_FP32 && !is_int2(s->kind)) return MLA_ERR_INVALID;
+    if (s->kind != MLA_KV_BF16 && s->kind != MLA_KV_FP32 && !is_int2(s->kind) && !is_mx(s->kind))
+        return MLA_ERR_INVALID;
     if (s->impl < MLA_IMPL_AUTO || s->impl > MLA_IMPL_TCGEN05 || s->num_splits_hint < 0)
         return MLA_ERR_INVALID;
     if (s->index_dim < 0 || s->index_dim % 8 || s->index_dim > 1024) return MLA_ERR_INVALID;
-    if (is_int2(s->kind) && s->index_dim != 0) return MLA_ERR_INVALID;
+    if ((is_int2(s->kind) || is_mx(s->kind)) && s->index_dim != 0) return MLA_ERR_INVALID;
+    if (is_mx(s->kind) && (s->group_size != 32 || s->kv_lora_rank % 32 || s->rope_dim < 8)) return MLA_ERR_INVALID;
     if (s->flags & ~(int32_t)(MLA_FLAG_WUV_FOLDED | MLA_FLAG_Q_ROTATED)) return MLA_ERR_INVALID;
     // the joint kind's folded up-projection would be [H, r + d_R, d_v]: not offered
     if ((s->flags & (MLA_FLAG_WUV_FOLDED | MLA_FLAG_Q_ROTATED)) && (!is_int2(s->kind) || s->kind == MLA_KV_INT2_JOINT))
@@ -85,7 +92,7 @@ static ShapeArgs shape_args(const mla_shape *s) {
     a.num_blocks = s->num_blocks;
     a.gs = s->group_size;
     a.kind = s->kind;
-    a.ix = is_int2(s->kind) ? 0 : s->index_dim;
+    a.ix = is_int2(s->kind) || is_mx(s->kind) ? 0 : s->index_dim;
     return a;
 }
 
@@ -158,7 +165,7 @@ static mla_status run_attention(const mla_shape *s, const mla_cache *cache, cons
     if (!cache || !block_table || !seq_lens || !q || !W_UV || !out || !lse || !workspace) return MLA_ERR_INVALID;
     if (B < 1 || q_len < 1 || max_blocks < 1) return MLA_ERR_INVALID;
     if (!(scale == scale)) return MLA_ERR_INVALID;
-    const bool int2 = is_int2(s->kind);
+    const bool int2 = is_int2(s->kind), mx = is_mx(s->kind);
     const bool rope_bf16 = s->kind == MLA_KV_INT2_ROT;      // INT2_ROT_QR holds the rope key as codes
     if (int2) {
         // R is read for the query (unless it comes rotated) and for the output (unless
@@ -168,6 +175,8 @@ static mla_status run_attention(const mla_shape *s, const mla_cache *cache, cons
             return MLA_ERR_INVALID;
         if (!aligned16(cache->codes) || !aligned16(cache->scale_zero) || (rope_bf16 && !aligned16(cache->rope)))
             return MLA_ERR_INVALID;
+    } else if (mx) {
+        if (!mx_cache_ok(cache)) return MLA_ERR_INVALID;
     } else {
         if (!cache->latent || !aligned16(cache->latent)) return MLA_ERR_INVALID;
     }
@@ -190,6 +199,7 @@ static mla_status run_attention(const mla_shape *s, const mla_cache *cache, cons
     p.latent = cache->latent;
     p.codes = (const uint8_t *)cache->codes;
     p.scale_zero = (const __half *)cache->scale_zero;
+    p.mx_scale = (const uint8_t *)cache->scale_zero;
     p.rope = (const __nv_bfloat16 *)cache->rope;
     p.q = q;
     p.q_rope = q;
@@ -323,6 +333,8 @@ static mla_status append_params(const mla_shape *shape, const mla_cache *cache, 
     if (int2) {
         if (!cache->codes || !cache->scale_zero || (shape->kind == MLA_KV_INT2_ROT && !cache->rope) || !R || !clip)
             return MLA_ERR_INVALID;
+    } else if (is_mx(shape->kind)) {
+        if (!mx_cache_ok(cache)) return MLA_ERR_INVALID;
     } else {
         if (!cache->latent || !aligned16(cache->latent)) return MLA_ERR_INVALID;
     }
@@ -341,8 +353,31 @@ static mla_status append_params(const mla_shape *shape, const mla_cache *cache, 
     p.latent = cache->latent;
     p.codes = (uint8_t *)cache->codes;
     p.scale_zero = (__half *)cache->scale_zero;
+    p.mx_scale = (uint8_t *)cache->scale_zero;
     p.rope = (__nv_bfloat16 *)cache->rope;
     p.status = status;
+    return MLA_OK;
+}
+
+// The cache's side of mla_latent_read and mla_prefill, after check_shape.
+static mla_status read_params(const mla_shape *shape, const mla_cache *cache, ReadParams &p) {
+    if (is_int2(shape->kind)) {
+        const bool rope = shape->kind == MLA_KV_INT2_ROT;
+        if (!cache->codes || !cache->scale_zero || (rope && !cache->rope) || !aligned16(cache->codes) ||
+            !aligned16(cache->scale_zero) || (rope && !aligned16(cache->rope)))
+            return MLA_ERR_INVALID;
+    } else if (is_mx(shape->kind)) {
+        if (!mx_cache_ok(cache)) return MLA_ERR_INVALID;
+    } else {
+        if (!cache->latent || !aligned16(cache->latent)) return MLA_ERR_INVALID;
+    }
+    memset(&p, 0, sizeof p);
+    p.s = shape_args(shape);
+    p.latent = cache->latent;
+    p.codes = (const uint8_t *)cache->codes;
+    p.scale_zero = (const __half *)cache->scale_zero;
+    p.mx_scale = (const uint8_t *)cache->scale_zero;
+    p.rope = (const __nv_bfloat16 *)cache->rope;
     return MLA_OK;
 }
 
@@ -384,13 +419,151 @@ mla_status mla_append_decode(const mla_shape *shape, const mla_cache *cache, con
                          workspace, workspace_bytes, stream, num_new > 0 ? &a : nullptr);
 }
 
+mla_status mla_latent_read(const mla_shape *shape, const mla_cache *cache, const int32_t *block_table,
+                           int32_t max_blocks_per_seq, int32_t B, const int32_t *start_pos,
+                           const int32_t *cu_rows, int32_t num_rows, void *rows, int32_t *status, void *stream) {
+    mla_status st = check_shape(shape);
+    if (st != MLA_OK) return st;
+    if (!cache || !block_table || !start_pos || !cu_rows || B < 1 || max_blocks_per_seq < 1 || num_rows < 0)
+        return MLA_ERR_INVALID;
+    if (num_rows == 0) return MLA_OK;
+    if (!rows || !aligned16(rows)) return MLA_ERR_INVALID;
+    ReadParams p;
+    st = read_params(shape, cache, p);
+    if (st != MLA_OK) return st;
+    p.B = B;
+    p.max_blocks = max_blocks_per_seq;
+    p.num_rows = num_rows;
+    p.block_table = block_table;
+    p.start_pos = start_pos;
+    p.cu_rows = cu_rows;
+    p.rows = rows;
+    p.status = status;
+    if (launch_read(p, (cudaStream_t)stream) != cudaSuccess) return MLA_ERR_CUDA;
+    prof_kernels(1);
+    return MLA_OK;
+}
+
+// ---- prefill ----------------------------------------------------------------
+struct PrefillWs {
+    size_t kv_off, tile_off, bad, rows, k, v, total;
+    int32_t cap_rows;            // every sequence's rows start at a multiple of 128
+    int32_t heads;               // heads per pass
+};
+
+// Keys and values of `heads` heads are held at a time: as many as fit into this.
+constexpr size_t kPrefillKvBytes = (size_t)1 << 30;
+
+static mla_status check_prefill(const mla_shape *s, int32_t B, int32_t num_q, int32_t max_tokens, int32_t dn) {
+    mla_status st = check_shape(s);
+    if (st != MLA_OK) return st;
+    if (B < 1 || num_q < 0 || max_tokens < 0 || dn < 8 || dn % 8) return MLA_ERR_INVALID;
+    if (is_int2(s->kind) || dn > 512 || s->v_head_dim > 1024) return MLA_ERR_UNSUPPORTED;
+    // dense rows and tiles are counted in 32 bits
+    if ((int64_t)max_tokens + 128ll * B > INT32_MAX - 256 || (int64_t)num_q + 256ll * B > INT32_MAX - 256)
+        return MLA_ERR_UNSUPPORTED;
+    if (s->impl == MLA_IMPL_TCGEN05) return MLA_ERR_UNSUPPORTED;
+    return MLA_OK;
+}
+
+static PrefillWs prefill_ws(const mla_shape *s, int32_t B, int32_t max_tokens, int32_t dn) {
+    PrefillWs w;
+    memset(&w, 0, sizeof w);
+    w.cap_rows = (int32_t)((((int64_t)max_tokens + 127) / 128 + B) * 128);
+    const size_t es = s->kind == MLA_KV_FP32 ? 4 : 2;
+    const size_t ekv = 4;
+    const size_t head = (size_t)w.cap_rows * (size_t)(dn + s->v_head_dim) * ekv;
+    size_t n = kPrefillKvBytes / head;
+    w.heads = (int32_t)(n < 1 ? 1 : n > (size_t)s->num_heads ? (size_t)s->num_heads : n);
+    size_t off = 256;            // the flags word
+    w.kv_off = off;    off = up256(off + sizeof(int32_t) * ((size_t)B + 1));
+    w.tile_off = off;  off = up256(off + sizeof(int32_t) * ((size_t)B + 1));
+    w.bad = off;       off = up256(off + sizeof(int32_t) * (size_t)B);
+    w.rows = off;      off = up256(off + (size_t)w.cap_rows * (s->kv_lora_rank + s->rope_dim) * es);
+    w.k = off;         off = up256(off + (size_t)w.heads * w.cap_rows * dn * ekv);
+    w.v = off;         off = up256(off + (size_t)w.heads * w.cap_rows * s->v_head_dim * ekv);
+    w.total = off;
+    return w;
+}
+
+size_t mla_prefill_workspace_bytes(const mla_shape *shape, int32_t B, int32_t num_q, int32_t max_tokens,
+                                   int32_t nope_dim) {
+    if (check_prefill(shape, B, num_q, max_tokens, nope_dim) != MLA_OK) return 0;
+    return prefill_ws(shape, B, max_tokens, nope_dim).total;
+}
+
+mla_status mla_prefill(const mla_shape *shape, const mla_cache *cache, const int32_t *block_table,
+                       int32_t max_blocks_per_seq, const int32_t *seq_lens, const int32_t *cu_q, int32_t B,
+                       int32_t num_q, int32_t max_tokens, int32_t nope_dim, const void *q, const void *W_UK,
+                       const void *W_UV, float scale, void *out, float *lse, void *workspace,
+                       size_t workspace_bytes, void *stream) {
+    mla_status st = check_prefill(shape, B, num_q, max_tokens, nope_dim);
+    if (st != MLA_OK) return st;
+    if (!cache || !block_table || !seq_lens || !cu_q || !W_UK || !W_UV || !workspace || max_blocks_per_seq < 1 ||
+        !(scale == scale) || (num_q > 0 && (!q || !out)))
+        return MLA_ERR_INVALID;
+    if (!aligned16(q) || !aligned16(W_UK) || !aligned16(W_UV) || !aligned16(out) || !aligned16(workspace))
+        return MLA_ERR_INVALID;
+    ReadParams r;
+    st = read_params(shape, cache, r);
+    if (st != MLA_OK) return st;
+    const PrefillWs w = prefill_ws(shape, B, max_tokens, nope_dim);
+    if (workspace_bytes < w.total) return MLA_ERR_WORKSPACE;
+    cudaStream_t stream_ = (cudaStream_t)stream;
+    char *ws = (char *)workspace;
+    PrefillParams p;
+    memset(&p, 0, sizeof p);
+    p.s = shape_args(shape);
+    p.B = B;
+    p.max_blocks = max_blocks_per_seq;
+    p.num_q = num_q;
+    p.dn = nope_dim;
+    p.tile_q = 16;
+    p.cap_rows = w.cap_rows;
+    p.seq_lens = seq_lens;
+    p.cu_q = cu_q;
+    p.kv_off = (int32_t *)(ws + w.kv_off);
+    p.tile_off = (int32_t *)(ws + w.tile_off);
+    p.bad = (int32_t *)(ws + w.bad);
+    p.status = (int32_t *)ws;
+    p.rows = ws + w.rows;
+    p.k = ws + w.k;
+    p.v = ws + w.v;
+    p.q = q;
+    p.W_UK = W_UK;
+    p.W_UV = W_UV;
+    p.scale = scale;
+    p.out = out;
+    p.lse = lse;
+    if (launch_prefill_plan(p, stream_) != cudaSuccess) return MLA_ERR_CUDA;
+    prof_kernels(1);
+    if (num_q == 0) return MLA_OK;
+    r.B = B;
+    r.max_blocks = max_blocks_per_seq;
+    r.num_rows = w.cap_rows;
+    r.block_table = block_table;
+    r.cu_rows = p.kv_off;
+    r.lens = seq_lens;
+    r.rows = ws + w.rows;
+    r.status = p.status;
+    r.bad = p.bad;
+    if (launch_read(r, stream_) != cudaSuccess) return MLA_ERR_CUDA;
+    prof_kernels(1);
+    for (p.h0 = 0; p.h0 < shape->num_heads; p.h0 += w.heads) {
+        p.nh = shape->num_heads - p.h0 < w.heads ? shape->num_heads - p.h0 : w.heads;
+        if (launch_prefill_simt(p, stream_) != cudaSuccess) return MLA_ERR_CUDA;
+        prof_kernels(3);
+    }
+    return MLA_OK;
+}
+
 mla_status mla_latent_append_index(const mla_shape *shape, const mla_cache *cache, const int32_t *block_table,
                                    int32_t max_blocks_per_seq, int32_t B, const int32_t *start_pos,
                                    const int32_t *cu_new, int32_t num_new, const void *index_key,
                                    int32_t *status, void *stream) {
     mla_status st = check_shape(shape);
     if (st != MLA_OK) return st;
-    if (is_int2(shape->kind) || shape->index_dim == 0) return MLA_ERR_INVALID;
+    if (is_int2(shape->kind) || is_mx(shape->kind) || shape->index_dim == 0) return MLA_ERR_INVALID;
     if (!cache || !block_table || !start_pos || !cu_new || B < 1 || max_blocks_per_seq < 1 || num_new < 0)
         return MLA_ERR_INVALID;
     if (num_new == 0) return MLA_OK;

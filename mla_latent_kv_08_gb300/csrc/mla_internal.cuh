@@ -71,6 +71,9 @@ __host__ __device__ constexpr bool is_int2(int32_t kind) {
     return kind == MLA_KV_INT2_ROT || kind == MLA_KV_INT2_ROT_QR || kind == MLA_KV_INT2_JOINT;
 }
 
+// 8-bit latent codes with power-of-two scales (MLA_KV_MXFP8)
+__host__ __device__ constexpr bool is_mx(int32_t kind) { return kind == MLA_KV_MXFP8; }
+
 // Everything a decode kernel reads.
 struct DecodeParams {
     ShapeArgs s;
@@ -78,9 +81,10 @@ struct DecodeParams {
     const int32_t *block_table;
     const int32_t *seq_lens;
     const void *latent;          // BF16 / FP32 kinds
-    const uint8_t *codes;        // INT2
+    const uint8_t *codes;        // INT2, MXFP8
     const __half *scale_zero;    // INT2
-    const __nv_bfloat16 *rope;   // INT2
+    const uint8_t *mx_scale;     // MXFP8: biased scale exponents
+    const __nv_bfloat16 *rope;   // INT2, MXFP8
     const void *q;               // caller's absorbed query
     const void *q_rope;          // the caller's bf16 query, whose rope dims the tensor-core
                                  // INT2_ROT decode reads as they are (the query itself)
@@ -128,8 +132,49 @@ struct AppendParams {
     void *latent;
     uint8_t *codes;
     __half *scale_zero;
+    uint8_t *mx_scale;
     __nv_bfloat16 *rope;
     int32_t *status;
+};
+
+// Cached tokens as dense rows (mla_latent_read, and the prefill's own first step).
+struct ReadParams {
+    ShapeArgs s;
+    int32_t B, max_blocks, num_rows;
+    const int32_t *block_table;
+    const int32_t *start_pos;    // nullptr: 0
+    const int32_t *cu_rows;      // [B + 1]
+    const int32_t *lens;         // prefill: rows from lens[b] on are zeros; else nullptr
+    const void *latent;
+    const uint8_t *codes;
+    const __half *scale_zero;
+    const uint8_t *mx_scale;
+    const __nv_bfloat16 *rope;
+    void *rows;
+    int32_t *status;
+    int32_t *bad;                // prefill: [B], set where a block is out of range; else nullptr
+};
+
+// mla_prefill. The new tokens of each sequence are cut into tiles of `tile_q`; the plan
+// kernel writes, per sequence, the first dense row of its tokens (a multiple of 128),
+// its first tile and whether its lengths are unusable.
+struct PrefillParams {
+    ShapeArgs s;
+    int32_t B, max_blocks, num_q, dn, tile_q;
+    int32_t cap_rows;            // dense rows the workspace holds
+    int32_t h0, nh;              // the heads of this pass
+    const int32_t *seq_lens, *cu_q;
+    int32_t *kv_off;             // [B + 1]
+    int32_t *tile_off;           // [B + 1]
+    int32_t *bad;                // [B]
+    int32_t *status;
+    const void *rows;            // [cap_rows, r + d_R]
+    void *k;                     // [nh, cap_rows, d_n]
+    void *v;                     // [nh, cap_rows, d_v]
+    const void *q, *W_UK, *W_UV;
+    float scale;
+    void *out;
+    float *lse;
 };
 
 // ---- launchers (defined in mla_simt.cu) ------------------------------------
@@ -169,6 +214,11 @@ cudaError_t launch_combine(const CombineParams &p, cudaStream_t st);
 cudaError_t launch_append(const AppendParams &p, cudaStream_t st);
 cudaError_t launch_append_index(const AppendParams &p, cudaStream_t st);
 cudaError_t launch_fold_rotation(const ShapeArgs &s, const float *R, const void *W_UV, void *W_folded, cudaStream_t st);
+// ---- reading the cache back (defined in mla_read.cu) ------------------------
+cudaError_t launch_read(const ReadParams &p, cudaStream_t st);
+// ---- prefill on the CUDA cores (defined in mla_prefill.cu) ------------------
+cudaError_t launch_prefill_plan(const PrefillParams &p, cudaStream_t st);
+cudaError_t launch_prefill_simt(const PrefillParams &p, cudaStream_t st);
 // ---- tensor-core decode (defined in mla_tc.cu) -----------------------------
 bool tc_shape_supported(const ShapeArgs &s);
 cudaError_t launch_decode_tc(const DecodeParams &p, int32_t max_work, cudaStream_t st);
@@ -201,6 +251,15 @@ __device__ __forceinline__ float warp_sum(float v) {
 __device__ __forceinline__ float4 bf16x4_to_float4(uint2 u) {
     return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
                        __uint_as_float(u.y & 0xffff0000u));
+}
+// Largest b with cu[b] <= n among sequences 0 .. B - 1.
+__device__ __forceinline__ int find_seq(const int32_t *cu, int B, int n) {
+    int lo = 0, hi = B - 1;
+    while (lo < hi) {
+        int mid = (lo + hi + 1) >> 1;
+        if (cu[mid] <= n) lo = mid; else hi = mid - 1;
+    }
+    return lo;
 }
 __device__ __forceinline__ void raise_flag(int32_t *status, int32_t f) {
     if (status) atomicOr(status, f);

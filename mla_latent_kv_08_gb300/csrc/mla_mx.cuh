@@ -1,0 +1,109 @@
+// The 8-bit latent cache (MLA_KV_MXFP8): its codes, their scales and a warp's
+// quantisation of one token.
+//
+// A group of 32 latent values shares a scale 2^e, held as the biased exponent e + 127
+// in one byte (255: not a number); a value is held as an e4m3 code (sign, 4 exponent
+// bits of bias 7, 3 fraction bits; largest 448) of c / 2^e. Both multiplications by 2^e
+// are exact in fp32 and in bf16, so the only rounding is that of the code.
+//
+// e is the least with amax / 2^e <= 448 = 1.75 * 2^8, so no value saturates: for
+// amax = 1.f * 2^E it is E - 8 where 1.f <= 1.75 and E - 7 above, read off the bf16 bits.
+// e is held within [-110, 119], where every value a code stands for is a normal bf16 or
+// zero, so that reading back in bf16 is exact: the smallest is 2^-9 * 2^-110, the largest
+// 448 * 2^119 = 1.75 * 2^127 (the few bf16 values above it become it).
+#pragma once
+
+#include "mla_internal.cuh"
+
+#include <cuda_fp8.h>
+
+namespace mla {
+
+constexpr int kMxGroup = 32;
+constexpr int kMxMinE = -110, kMxMaxE = 119;
+
+// Biased scale exponent of a group whose largest magnitude has the bf16 bits `amax`
+// (sign cleared; 0x7f80 and above: infinite or not a number).
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax) {
+    const int E = (int)(amax >> 7);
+    if (E == 255) return 255u;
+    if (E == 0) return (uint32_t)(kMxMinE + 127);          // zero or subnormal: far below the range
+    const int e = E - 127 - 8 + ((amax & 0x7fu) > 0x60u ? 1 : 0);
+    return (uint32_t)(max(kMxMinE, min(kMxMaxE, e)) + 127);
+}
+// 2^(b - 127) in fp32; 255: NaN.
+__device__ __forceinline__ float mx_scale_f32(uint32_t b) {
+    return __uint_as_float(b == 255u ? 0x7fc00000u : b == 0u ? 0x00400000u : b << 23);
+}
+// The same in both halves of a bf16 pair.
+__device__ __forceinline__ __nv_bfloat162 mx_scale_bf162(uint32_t b) {
+    const uint32_t h = b == 255u ? 0x7fc0u : b == 0u ? 0x0040u : b << 7;
+    const uint32_t u = h | (h << 16);
+    return *(const __nv_bfloat162 *)&u;
+}
+// Four codes (a word, memory order) times their group's scale, as two bf16 pairs. A code's
+// exponent and fraction bits placed 4 up in a bf16 (whose exponent field is then the
+// code's) stand for the code's value times 2^-120, subnormal codes included; one exact
+// multiplication by 2^120 gives the value, a second the scale.
+__device__ __forceinline__ void mx_expand4(uint32_t w, __nv_bfloat162 scale, uint32_t &o0, uint32_t &o1) {
+    const uint32_t k120u = 0x7b807b80u;                    // 2^120 twice
+    const __nv_bfloat162 k120 = *(const __nv_bfloat162 *)&k120u;
+    const uint32_t lo = __byte_perm(w, 0u, 0x1404), hi = __byte_perm(w, 0u, 0x3424);
+    const uint32_t a = ((lo >> 4) & 0x07f007f0u) | (lo & 0x80008000u);
+    const uint32_t b = ((hi >> 4) & 0x07f007f0u) | (hi & 0x80008000u);
+    const __nv_bfloat162 x = __hmul2(__hmul2(*(const __nv_bfloat162 *)&a, k120), scale);
+    const __nv_bfloat162 y = __hmul2(__hmul2(*(const __nv_bfloat162 *)&b, k120), scale);
+    o0 = *(const uint32_t *)&x;
+    o1 = *(const uint32_t *)&y;
+}
+// One code and its scale byte in fp32 (the CUDA-core kernels).
+__device__ __forceinline__ float mx_value(uint32_t code, uint32_t scale_byte) {
+    const uint32_t h = ((code & 0x7fu) << 4) | ((code & 0x80u) << 8);
+    return __uint_as_float(h << 16) * 0x1p120f * mx_scale_f32(scale_byte);
+}
+
+// New token n (bf16 latent of r values at c, bf16 rope key at k) into token row `row` of
+// the cache, by one warp: a lane takes 16 values, two lanes a group.
+__device__ __forceinline__ void mx_write_token(const AppendParams &p, const __nv_bfloat16 *c, const __nv_bfloat16 *k,
+                                               size_t row) {
+    const int lane = threadIdx.x & 31;
+    const int r = p.s.r, dR = p.s.dR, ng = r / kMxGroup;
+    uint8_t *codes = p.codes + row * r;
+    uint8_t *scales = p.mx_scale + row * ng;
+    for (int g0 = 0; g0 < ng; g0 += 16) {
+        const int g = g0 + (lane >> 1);
+        const bool act = g < ng;
+        uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        if (act) {
+            const uint4 *src = (const uint4 *)(c + g * kMxGroup + 16 * (lane & 1));
+            u[0] = src[0];
+            u[1] = src[1];
+        }
+        const uint32_t *w = (const uint32_t *)u;
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+        m = max(m & 0xffffu, m >> 16);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        const uint32_t sb = mx_scale_byte(m);
+        if (!act) continue;
+        // 2^-e: exponent field 127 - e = 254 - sb, normal for every e of the range
+        const float inv = __uint_as_float((254u - min(sb, 254u)) << 23);
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 x = make_float2(__uint_as_float(w[2 * i] << 16) * inv, __uint_as_float(w[2 * i] & 0xffff0000u) * inv);
+            const float2 y = make_float2(__uint_as_float(w[2 * i + 1] << 16) * inv,
+                                         __uint_as_float(w[2 * i + 1] & 0xffff0000u) * inv);
+            o[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3) |
+                   ((uint32_t)__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3) << 16);
+            if (sb == 255u) o[i] = 0x7f7f7f7fu;
+        }
+        *(uint4 *)(codes + g * kMxGroup + 16 * (lane & 1)) = make_uint4(o[0], o[1], o[2], o[3]);
+        if ((lane & 1) == 0) scales[g] = (uint8_t)sb;
+    }
+    uint4 *dst = (uint4 *)(p.rope + row * dR);
+    for (int v = lane; v < dR / 8; v += 32) dst[v] = ((const uint4 *)k)[v];
+}
+
+}  // namespace mla

@@ -7,6 +7,7 @@
 // and INT2 caches. Both write the same partial format, so the planner and the
 // combine here serve both.
 #include "mla_internal.cuh"
+#include "mla_mx.cuh"
 
 #include <math_constants.h>
 
@@ -398,6 +399,30 @@ __device__ __forceinline__ void gather_tile(const DecodeParams &p, int b, int tb
                 dst[0] = dst[1] = dst[2] = dst[3] = 0.f;
             }
         }
+    } else if (KIND == MLA_KV_MXFP8) {
+        // four codes per thread step, then the bf16 rope key
+        const int nw = r / 4, ng = r / kMxGroup;
+        for (int idx = threadIdx.x; idx < kTT * nw; idx += blockDim.x) {
+            int tt = idx / nw, k = idx % nw;
+            int blk1 = sValid[tt];
+            float *dst = sK + tt * Dp + 4 * k;
+            if (blk1) {
+                size_t row = (size_t)(blk1 - 1) * bs + (tb + tt) % bs;
+                const uint32_t w = *((const uint32_t *)(p.codes + row * r) + k);
+                const uint32_t sb = p.mx_scale[row * ng + k / (kMxGroup / 4)];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dst[e] = mx_value((w >> (8 * e)) & 0xffu, sb);
+            } else {
+                dst[0] = dst[1] = dst[2] = dst[3] = 0.f;
+            }
+        }
+        for (int idx = threadIdx.x; idx < kTT * dR; idx += blockDim.x) {
+            int tt = idx / dR, d = idx % dR;
+            int blk1 = sValid[tt];
+            float v = 0.f;
+            if (blk1) v = __bfloat162float(p.rope[((size_t)(blk1 - 1) * bs + (tb + tt) % bs) * dR + d]);
+            sK[tt * Dp + r + d] = v;
+        }
     } else {
         // INT2: one thread per code byte (4 dims), then the bf16 rope key (INT2_ROT_QR:
         // the rope key's codes follow the latent's in the row, so the bytes cover it).
@@ -593,6 +618,7 @@ cudaError_t launch_decode_simt(const DecodeParams &p, int32_t max_work, cudaStre
     switch (p.s.kind) {
         case MLA_KV_BF16: return launch_decode_kind<MLA_KV_BF16>(p, max_work, st);
         case MLA_KV_FP32: return launch_decode_kind<MLA_KV_FP32>(p, max_work, st);
+        case MLA_KV_MXFP8: return launch_decode_kind<MLA_KV_MXFP8>(p, max_work, st);
         default: return launch_decode_kind<MLA_KV_INT2_ROT>(p, max_work, st);
     }
 }
@@ -724,15 +750,6 @@ cudaError_t launch_combine(const CombineParams &p, cudaStream_t st) {
 // order, which fixes the integer codes), then per (token, group) clip, range,
 // fp16 scale/zero, codes and 2-bit packing.
 // ============================================================================
-__device__ __forceinline__ int find_seq(const int32_t *cu_new, int B, int n) {
-    int lo = 0, hi = B - 1;                   // largest b with cu_new[b] <= n
-    while (lo < hi) {
-        int mid = (lo + hi + 1) >> 1;
-        if (cu_new[mid] <= n) lo = mid; else hi = mid - 1;
-    }
-    return lo;
-}
-
 // Returns the token row index (blk * bs + slot) or -1 after raising a flag.
 __device__ __forceinline__ long long locate_slot(const AppendParams &p, int n) {
     const int b = find_seq(p.cu_new, p.B, n);
@@ -760,6 +777,20 @@ __device__ __forceinline__ void copy_token(const AppendParams &p, int n) {
     const uint4 *src_r = (const uint4 *)((const T *)p.k_rope + (size_t)n * dR);
     for (int v = lane; v < r / E; v += 32) dst[v] = src_c[v];
     for (int v = lane; v < dR / E; v += 32) dst[r / E + v] = src_r[v];
+}
+
+// The 8-bit kind: one warp quantises its token as it writes it.
+struct MxToken {};
+template <>
+__device__ __forceinline__ void copy_token<MxToken>(const AppendParams &p, int n) {
+    const int lane = threadIdx.x & 31;
+    if (n >= p.num_new) return;
+    long long row = 0;
+    if (lane == 0) row = locate_slot(p, n);
+    row = __shfl_sync(0xffffffffu, row, 0);
+    if (row < 0) return;
+    mx_write_token(p, (const __nv_bfloat16 *)p.c_kv + (size_t)n * p.s.r, (const __nv_bfloat16 *)p.k_rope + (size_t)n * p.s.dR,
+                   (size_t)row);
 }
 
 template <typename T>
@@ -1017,7 +1048,9 @@ cudaError_t launch_plan_prep(const DecodeParams &p, int32_t max_work, const Appe
         split_blocks = (r_n + nt * 8 - 1) / (nt * 8);
     }
     const dim3 grid(1 + pp.copy_blocks + split_blocks);
-    auto kern = (a && a->s.kind == MLA_KV_FP32) ? plan_prep_kernel<float> : plan_prep_kernel<__nv_bfloat16>;
+    auto kern = (a && a->s.kind == MLA_KV_FP32) ? plan_prep_kernel<float>
+                : (a && is_mx(a->s.kind))       ? plan_prep_kernel<MxToken>
+                                                : plan_prep_kernel<__nv_bfloat16>;
     return launch_pdl(kern, grid, dim3(nt), (size_t)nt * 28, st, p, max_work, pp);
 }
 
@@ -1027,6 +1060,8 @@ cudaError_t launch_append(const AppendParams &p, cudaStream_t st) {
         return launch_pdl(append_copy_kernel<__nv_bfloat16>, dim3((p.num_new + 7) / 8), dim3(256), 0, st, p);
     } else if (p.s.kind == MLA_KV_FP32) {
         return launch_pdl(append_copy_kernel<float>, dim3((p.num_new + 7) / 8), dim3(256), 0, st, p);
+    } else if (is_mx(p.s.kind)) {
+        return launch_pdl(append_copy_kernel<MxToken>, dim3((p.num_new + 7) / 8), dim3(256), 0, st, p);
     } else {
         // column blocks of whole groups, at most 128 columns (group_size <= 128): 128,
         // 96 or 64 where that splits the rotated row into whole blocks (compiled), else
