@@ -454,6 +454,10 @@ struct PrefillWs {
 // Keys and values of `heads` heads are held at a time: as many as fit into this.
 constexpr size_t kPrefillKvBytes = (size_t)1 << 30;
 
+static bool prefill_tc(const mla_shape *s, int32_t dn) {
+    return s->impl != MLA_IMPL_SIMT && prefill_tc_supported(shape_args(s), dn);
+}
+
 static mla_status check_prefill(const mla_shape *s, int32_t B, int32_t num_q, int32_t max_tokens, int32_t dn) {
     mla_status st = check_shape(s);
     if (st != MLA_OK) return st;
@@ -462,7 +466,7 @@ static mla_status check_prefill(const mla_shape *s, int32_t B, int32_t num_q, in
     // dense rows and tiles are counted in 32 bits
     if ((int64_t)max_tokens + 128ll * B > INT32_MAX - 256 || (int64_t)num_q + 256ll * B > INT32_MAX - 256)
         return MLA_ERR_UNSUPPORTED;
-    if (s->impl == MLA_IMPL_TCGEN05) return MLA_ERR_UNSUPPORTED;
+    if (s->impl == MLA_IMPL_TCGEN05 && !prefill_tc(s, dn)) return MLA_ERR_UNSUPPORTED;
     return MLA_OK;
 }
 
@@ -471,7 +475,7 @@ static PrefillWs prefill_ws(const mla_shape *s, int32_t B, int32_t max_tokens, i
     memset(&w, 0, sizeof w);
     w.cap_rows = (int32_t)((((int64_t)max_tokens + 127) / 128 + B) * 128);
     const size_t es = s->kind == MLA_KV_FP32 ? 4 : 2;
-    const size_t ekv = 4;
+    const size_t ekv = prefill_tc(s, dn) ? 2 : 4;        // the CUDA-core path keeps fp32 keys and values
     const size_t head = (size_t)w.cap_rows * (size_t)(dn + s->v_head_dim) * ekv;
     size_t n = kPrefillKvBytes / head;
     w.heads = (int32_t)(n < 1 ? 1 : n > (size_t)s->num_heads ? (size_t)s->num_heads : n);
@@ -518,7 +522,8 @@ mla_status mla_prefill(const mla_shape *shape, const mla_cache *cache, const int
     p.max_blocks = max_blocks_per_seq;
     p.num_q = num_q;
     p.dn = nope_dim;
-    p.tile_q = 16;
+    const bool tc = prefill_tc(shape, nope_dim);
+    p.tile_q = tc ? 256 : 16;
     p.cap_rows = w.cap_rows;
     p.seq_lens = seq_lens;
     p.cu_q = cu_q;
@@ -551,8 +556,8 @@ mla_status mla_prefill(const mla_shape *shape, const mla_cache *cache, const int
     prof_kernels(1);
     for (p.h0 = 0; p.h0 < shape->num_heads; p.h0 += w.heads) {
         p.nh = shape->num_heads - p.h0 < w.heads ? shape->num_heads - p.h0 : w.heads;
-        if (launch_prefill_simt(p, stream_) != cudaSuccess) return MLA_ERR_CUDA;
-        prof_kernels(3);
+        if ((tc ? launch_prefill_tc(p, stream_) : launch_prefill_simt(p, stream_)) != cudaSuccess) return MLA_ERR_CUDA;
+        prof_kernels(tc ? 2 : 3);
     }
     return MLA_OK;
 }

@@ -219,6 +219,9 @@ cudaError_t launch_read(const ReadParams &p, cudaStream_t st);
 // ---- prefill on the CUDA cores (defined in mla_prefill.cu) ------------------
 cudaError_t launch_prefill_plan(const PrefillParams &p, cudaStream_t st);
 cudaError_t launch_prefill_simt(const PrefillParams &p, cudaStream_t st);
+// ---- prefill on the tensor cores (defined in mla_prefill_tc.cu) -------------
+bool prefill_tc_supported(const ShapeArgs &s, int dn);
+cudaError_t launch_prefill_tc(const PrefillParams &p, cudaStream_t st);
 // ---- tensor-core decode (defined in mla_tc.cu) -----------------------------
 bool tc_shape_supported(const ShapeArgs &s);
 cudaError_t launch_decode_tc(const DecodeParams &p, int32_t max_work, cudaStream_t st);

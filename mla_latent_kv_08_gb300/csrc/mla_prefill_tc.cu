@@ -1,0 +1,585 @@
+// Prefill on the tensor cores (tcgen05 / TMEM / TMA) for the DeepSeek-V3 latent:
+// kv_lora_rank 512, rope 64, nope 128, v_head_dim 128, bf16 rows (BF16 and MXFP8 caches).
+//
+// expand_tc_kernel    K[h] = rows . W_UK[h]^T and V[h] = rows . W_UV[h] for the heads of
+//                     a pass, bf16 out
+// prefill_tc_kernel   causal attention of 256 new tokens of one head over K, V and the
+//                     rope keys in the dense rows
+//
+// Every wait is bounded (2 s): one that gives up records FLAG_TIMEOUT and the CTA winds
+// down without trapping.
+#include "mla_internal.cuh"
+#include "mla_ptx.cuh"
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <math_constants.h>
+#include <string.h>
+
+namespace mla {
+namespace pf {
+
+using namespace ptx;
+
+constexpr unsigned long long kTimeoutNs = 2000000000ull;       // 2 s bounded-wait safety net
+constexpr int kR = 512, kRope = 64, kDn = 128, kDv = 128;
+constexpr uint32_t kBlock = 128 * 128;                // [128 rows x 64 values] bf16: 16 KB
+
+// ============================================================================
+// Keys and values. A CTA makes 256 rows x (128 key + 128 value) columns of one head:
+// four M128 N128 accumulators, the whole 512 columns of tensor memory. W_UK[h] is K-major
+// as it lies ([d_n, r]), W_UV[h] MN-major ([r, d_v]).
+// ============================================================================
+namespace ex {
+constexpr int kThreads = 320;                          // warp 0 TMA, 1 MMA, 2..9 epilogue
+constexpr int kStages = 3;
+constexpr uint32_t kStage = 4 * kBlock;                // two row blocks, W_UK, W_UV: 64 KB
+constexpr int kChunks = kR / 64;
+constexpr uint32_t kOffBar = kStages * kStage;
+constexpr uint32_t kSmemBytes = kOffBar + 256 + 1024;  // + alignment slack
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+
+struct Bars {
+    uint64_t full[kStages], empty[kStages];
+    uint64_t done;
+    uint32_t tmem_base;
+    int32_t abort_flag;
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+expand_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constant__ CUtensorMap uk_map,
+                 const __grid_constant__ CUtensorMap uv_map, const __grid_constant__ CUtensorMap k_map,
+                 const __grid_constant__ CUtensorMap v_map, const PrefillParams p) {
+    const int m0 = blockIdx.x * 256, hl = blockIdx.y, h = p.h0 + hl;
+    const int rows_used = p.kv_off[p.B];
+    if (m0 >= rows_used) return;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    Bars *bars = (Bars *)(smem + kOffBar);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->empty[s], 1);
+        }
+        mbar_init(&bars->done, 1);
+        bars->abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_proxy_async();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&bars->tmem_base)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        return mbar_wait_bounded(bar, parity, &bars->abort_flag, p.status, FLAG_TIMEOUT, kTimeoutNs);
+    };
+    if (warp == 0) {
+        if (lane == 0) {
+            int c = 0;
+            for (; c < kChunks; ++c) {
+                const int s = c % kStages, use = c / kStages;
+                if (use > 0 && !wait(&bars->empty[s], (use - 1) & 1)) break;
+                uint8_t *st = smem + s * kStage;
+                mbar_expect_tx(&bars->full[s], kStage);
+                tma_load_2d(st, &rows_map, 64 * c, m0, &bars->full[s]);
+                tma_load_2d(st + kBlock, &rows_map, 64 * c, m0 + 128, &bars->full[s]);   // past the end: zeros
+                tma_load_2d(st + 2 * kBlock, &uk_map, 64 * c, h * kDn, &bars->full[s]);
+                tma_load_2d(st + 3 * kBlock, &uv_map, 0, h * kR + 64 * c, &bars->full[s]);
+                tma_load_2d(st + 3 * kBlock + kBlock / 2, &uv_map, 64, h * kR + 64 * c, &bars->full[s]);
+            }
+            // never leave a copy in flight into this CTA's shared memory
+            for (int u = c > kStages ? c - kStages : 0; u < c; ++u) mbar_drain(&bars->full[u % kStages], (u / kStages) & 1);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t kIdK = idesc_bf16(128, 128, false), kIdV = idesc_bf16(128, 128, true);
+            for (int c = 0; c < kChunks; ++c) {
+                const int s = c % kStages;
+                if (!wait(&bars->full[s], (c / kStages) & 1)) break;
+                tc_fence_after();
+                const uint32_t st = smem_u32(smem + s * kStage);
+                const uint64_t a0 = sdesc(st, 16, 1024), a1 = sdesc(st + kBlock, 16, 1024);
+                const uint64_t bk = sdesc(st + 2 * kBlock, 16, 1024);
+                // MN-major: 64-column atoms 8 KB apart, 8-row groups 1 KB apart
+                const uint64_t bv = sdesc(st + 3 * kBlock, kBlock / 2, 1024);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t acc = (c > 0 || k > 0) ? 1u : 0u;
+                    mma_ss(tmem, a0 + 2 * k, bk + 2 * k, kIdK, acc);
+                    mma_ss(tmem + 128, a0 + 2 * k, bv + 128 * k, kIdV, acc);
+                    mma_ss(tmem + 256, a1 + 2 * k, bk + 2 * k, kIdK, acc);
+                    mma_ss(tmem + 384, a1 + 2 * k, bv + 128 * k, kIdV, acc);
+                }
+                mma_commit(&bars->empty[s]);
+            }
+            mma_commit(&bars->done);
+            wait(&bars->done, 0);
+        }
+        __syncwarp();
+    } else {
+        // warp 2 + e: rows 32*(warp%4)..+31 (its tensor-memory lanes) of row block (warp-2)/4
+        const int q = warp & 3, mt = (warp - 2) >> 2;
+        const int row = m0 + 128 * mt + 32 * q;
+        const bool ok = __all_sync(0xffffffffu, wait(&bars->done, 0));
+        tc_fence_after();
+        // the stages are free: every copy has landed and every product has read it
+        uint8_t *box = smem + (warp - 2) * 4 * 4096;
+        if (ok && row < rows_used) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {              // 64 columns: key halves, value halves
+                uint32_t v[64];
+                const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + 256 * mt + 64 * c;
+                TMEM_LD32(at, v);
+                TMEM_LD32(at + 32, (v + 32));
+                tmem_wait_ld();
+                uint8_t *b = box + 4096 * c;
+#pragma unroll
+                for (int ch = 0; ch < 8; ++ch) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(v[8 * ch + 2 * e]),
+                                                                       __uint_as_float(v[8 * ch + 2 * e + 1]));
+                        w[e] = *(const uint32_t *)&x;
+                    }
+                    *(uint4 *)(b + sw128(lane, ch)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) {
+                    const CUtensorMap *map = c < 2 ? &k_map : &v_map;
+                    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                                     (uint64_t)map),
+                                 "r"(smem_u32(b)), "r"(64 * (c & 1)), "r"((int)((long long)hl * p.cap_rows) + row)
+                                 : "memory");
+                    bulk_commit();
+                }
+            }
+            if (lane == 0) bulk_wait_all();
+            __syncwarp();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+}  // namespace ex
+
+// ============================================================================
+// Attention. A CTA takes up to 256 new tokens of one sequence for one head, as two
+// sub-tiles of 128 rows that go through the same 128-token steps of the cache in turn:
+// while one warpgroup turns sub-tile 0's scores into weights, the tensor cores work on
+// sub-tile 1.
+//
+//   per step and sub-tile   S[128 x 128] = Q . K^T   12 x M128 N128 K16
+//                           P = 2^(S c - m)          a thread a row: no shuffles
+//                           O[128 x 128] += P . V    8 x M128 N128 K16, P from tensor memory
+//
+// P (bf16) is stored over the scores it came from. The products of one sub-tile are
+// issued in order by one thread, so that the next scores overwrite P only once P . V has
+// read it. m is raised lazily, only when it grows by more than 8 (P <= 2^8).
+//
+// Shared memory: Q 96 KB; a ring of eight 16 KB slots for the steps' three key blocks
+// ([128 tokens x 64 dims]) and two value blocks ([64 tokens x 128 dims], two 64-column
+// atoms), in the order of use, so that the copies run 1.6 steps ahead.
+// Tensor memory: S0, S1, O0, O1, 128 columns each.
+// ============================================================================
+constexpr int kThreads = 384;          // warp 0 TMA, 1 MMA, 4..7 and 8..11 softmax of sub-tiles 0 and 1
+constexpr int kTileQ = 256;
+constexpr int kSlots = 8;
+constexpr int kPerStep = 5;            // slots a step takes: 3 key blocks, 2 value blocks
+constexpr uint32_t kOffQ = 0;
+constexpr uint32_t kOffRing = 6 * kBlock;
+constexpr uint32_t kOffBar = kOffRing + kSlots * kBlock;
+constexpr uint32_t kSmemBytes = kOffBar + 256 + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+
+struct Bars {
+    uint64_t q_full[2];
+    uint64_t full[kSlots], empty[kSlots];
+    uint64_t s_full[2];        // scores of the sub-tile's step are there (and its earlier P . V)
+    uint64_t p_full[2];        // weights are stored
+    uint64_t o_full[2];
+    uint32_t tmem_base;
+    int32_t abort_flag;
+};
+static_assert(sizeof(Bars) <= 256, "barriers");
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(smem_u32(dst)), "l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                  const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap rope_map,
+                  const PrefillParams p) {
+    // the last tiles of a sequence see the most: they start first
+    const int tiles = p.tile_off[p.B];
+    if ((int)blockIdx.x >= tiles) return;
+    const int tile = tiles - 1 - (int)blockIdx.x;
+    const int b = find_seq(p.tile_off, p.B, tile);
+    const int hl = blockIdx.y, h = p.h0 + hl, H = p.s.H;
+    const int n = p.cu_q[b + 1] - p.cu_q[b], i0 = (tile - p.tile_off[b]) * kTileQ;
+    const size_t qrow0 = (size_t)p.cu_q[b] + i0;
+    const int rows_here = min(kTileQ, n - i0);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    __nv_bfloat16 *out = (__nv_bfloat16 *)p.out;
+    if (p.bad[b]) {
+        for (int e = tid; e < rows_here * kDv; e += kThreads)
+            out[((qrow0 + e / kDv) * H + h) * kDv + e % kDv] = __float2bfloat16_rn(CUDART_NAN_F);
+        if (p.lse)
+            for (int i = tid; i < rows_here; i += kThreads) p.lse[(qrow0 + i) * H + h] = CUDART_NAN_F;
+        return;
+    }
+    const int L = p.seq_lens[b];
+    // steps of each sub-tile (0: it has no rows); sub-tile 1 never has fewer than sub-tile 0
+    const int subs = rows_here > 128 ? 2 : 1;
+    const int steps0 = (L - n + i0 + min(128, rows_here) + 127) / 128;
+    const int steps1 = subs == 2 ? (L - n + i0 + rows_here + 127) / 128 : 0;
+    const int steps = max(steps0, steps1);
+
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    Bars *bars = (Bars *)(smem + kOffBar);
+    if (tid == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bars->q_full[s], 1);
+            mbar_init(&bars->s_full[s], 1);
+            mbar_init(&bars->p_full[s], 128);
+            mbar_init(&bars->o_full[s], 1);
+        }
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->empty[s], 1);
+        }
+        bars->abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_proxy_async();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&bars->tmem_base)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        return mbar_wait_bounded(bar, parity, &bars->abort_flag, p.status, FLAG_TIMEOUT, kTimeoutNs);
+    };
+    // slot, and phase of its use, of block i of the run of blocks
+    auto slot_of = [](int i) { return i & (kSlots - 1); };
+    auto phase_of = [](int i) { return (uint32_t)(i / kSlots) & 1u; };
+
+    if (warp == 0) {
+        // ================================================= copies
+        if (lane == 0) {
+            int issued = 0, q_issued = 0;
+            const int row0 = p.kv_off[b];
+            const int kv0 = hl * p.cap_rows + row0;           // fits: the pass's rows are counted in 32 bits
+            auto load_q = [&](int s) {
+                mbar_expect_tx(&bars->q_full[s], 3 * kBlock);
+                for (int c = 0; c < 3; ++c)
+                    tma_load_3d(smem + kOffQ + (3 * s + c) * kBlock, &q_map, 64 * c, h, (int)qrow0 + 128 * s, &bars->q_full[s]);
+                ++q_issued;
+            };
+            bool ok = true;
+            load_q(0);
+            for (int j = 0; j < steps && ok; ++j) {
+                for (int c = 0; c < kPerStep; ++c, ++issued) {
+                    const int s = slot_of(issued);
+                    if (issued >= kSlots && !wait(&bars->empty[s], phase_of(issued - kSlots))) { ok = false; break; }
+                    uint8_t *dst = smem + kOffRing + s * kBlock;
+                    mbar_expect_tx(&bars->full[s], kBlock);
+                    if (c < 2) {
+                        tma_load_2d(dst, &k_map, 64 * c, kv0 + 128 * j, &bars->full[s]);
+                    } else if (c == 2) {
+                        tma_load_2d(dst, &rope_map, kR, row0 + 128 * j, &bars->full[s]);
+                    } else {
+                        const int y = kv0 + 128 * j + 64 * (c - 3);
+                        tma_load_2d(dst, &v_map, 0, y, &bars->full[s]);
+                        tma_load_2d(dst + kBlock / 2, &v_map, 64, y, &bars->full[s]);
+                    }
+                    if (j == 0 && c == 2 && subs == 2) load_q(1);
+                }
+            }
+            // never leave a copy in flight into this CTA's shared memory
+            for (int s = 0; s < q_issued; ++s) mbar_drain(&bars->q_full[s], 0);
+            for (int i = max(0, issued - kSlots); i < issued; ++i) mbar_drain(&bars->full[slot_of(i)], phase_of(i));
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ================================================= products: lane 0 alone
+        if (lane == 0) {
+            constexpr uint32_t kIdS = idesc_bf16(128, 128, false), kIdO = idesc_bf16(128, 128, true);
+            const uint32_t ring = smem_u32(smem + kOffRing), qs = smem_u32(smem + kOffQ);
+            // the blocks [i, i + count) have landed
+            auto landed = [&](int i, int count) {
+                for (int c = 0; c < count; ++c)
+                    if (!wait(&bars->full[slot_of(i + c)], phase_of(i + c))) return false;
+                return true;
+            };
+            auto scores = [&](int s, int j) {
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 3; ++c) {
+                    const uint64_t a = sdesc(qs + (3 * s + c) * kBlock, 16, 1024);
+                    const uint64_t k = sdesc(ring + slot_of(kPerStep * j + c) * kBlock, 16, 1024);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mma_ss(tmem + 128 * s, a + 2 * e, k + 2 * e, kIdS, (c > 0 || e > 0) ? 1u : 0u);
+                }
+                mma_commit(&bars->s_full[s]);
+            };
+            auto values = [&](int s, int j) {
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    // MN-major: 64-column atoms 8 KB apart, 8-token groups 1 KB apart
+                    const uint64_t v = sdesc(ring + slot_of(kPerStep * j + 3 + c) * kBlock, kBlock / 2, 1024);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        mma_ts(tmem + 256 + 128 * s, tmem + 128 * s + 32 * c + 8 * e, v + 128 * e, kIdO,
+                               (j > 0 || c > 0 || e > 0) ? 1u : 0u);
+                }
+            };
+            auto release = [&](int i, int count) {
+                for (int c = 0; c < count; ++c) mma_commit(&bars->empty[slot_of(i + c)]);
+            };
+            bool ok = true;
+            const int last = subs - 1;
+            for (int s = 0; s < subs && ok; ++s) {
+                ok = wait(&bars->q_full[s], 0) && landed(0, 3);
+                if (!ok) break;
+                scores(s, 0);
+            }
+            if (ok) release(0, 3);
+            for (int j = 0; j < steps && ok; ++j) {
+                for (int s = 0; s < subs && ok; ++s) {
+                    const int mine = s == 0 ? steps0 : steps1;
+                    if (j >= mine) continue;
+                    ok = wait(&bars->p_full[s], j & 1) && landed(kPerStep * j + 3, 2);
+                    if (!ok) break;
+                    values(s, j);
+                    if (s == last) release(kPerStep * j + 3, 2);
+                    if (j + 1 == mine) mma_commit(&bars->o_full[s]);
+                    if (j + 1 < mine) {
+                        ok = landed(kPerStep * (j + 1), 3);
+                        if (!ok) break;
+                        scores(s, j + 1);
+                    }
+                    if (s == last && j + 1 < steps) release(kPerStep * (j + 1), 3);
+                }
+            }
+            if (ok) {
+                wait(&bars->o_full[last], 0);
+            } else {
+                // products in flight must end before the tensor memory is given back
+                mma_commit(&bars->o_full[last]);
+                mbar_drain(&bars->o_full[last], 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ================================================= softmax and output
+        const int s = (warp - 4) >> 2, wq = warp & 3;
+        const int row = 32 * wq + lane;                        // of the sub-tile
+        const int mine = s == 0 ? steps0 : steps1;
+        const int i = i0 + 128 * s + row;                      // of the sequence's new tokens
+        const uint32_t lane_addr = tmem + ((uint32_t)(32 * wq) << 16);
+        const uint32_t tS = lane_addr + 128 * s, tO = lane_addr + 256 + 128 * s;
+        const int seen = L - n + min(i, n - 1) + 1;            // tokens this row sees
+        // where the scale is positive the maximum commutes with it: one fma per exponent
+        const bool pos_scale = p.scale > 0.f;
+        const float c2 = p.scale * kLog2e, cs = pos_scale ? c2 : 1.f;
+        float m = -CUDART_INF_F, l = 0.f;
+        bool ok = true;
+        for (int j = 0; j < mine; ++j) {
+            ok = __all_sync(0xffffffffu, wait(&bars->s_full[s], j & 1));
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t sv[128];
+            TMEM_LD32(tS, sv);
+            TMEM_LD32(tS + 32, (sv + 32));
+            TMEM_LD32(tS + 64, (sv + 64));
+            TMEM_LD32(tS + 96, (sv + 96));
+            tmem_wait_ld();
+            const int vis = seen - 128 * j;
+            if (!pos_scale || __any_sync(0xffffffffu, vis < 128)) {
+#pragma unroll
+                for (int e = 0; e < 128; ++e) {
+                    const float v = pos_scale ? __uint_as_float(sv[e]) : __uint_as_float(sv[e]) * c2;
+                    sv[e] = __float_as_uint(e < vis ? v : -CUDART_INF_F);
+                }
+            }
+            float mx[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(sv[e]);
+#pragma unroll
+            for (int e = 4; e < 128; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(sv[e]));
+            const float m_new = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs);
+            float alpha = 1.f;
+            bool rescale = false;
+            if (m_new > m + 8.f) {
+                alpha = exp2f(m - m_new);                      // 0 at the first step
+                m = m_new;
+                rescale = j > 0;
+            }
+            const float nm = m == -CUDART_INF_F ? -CUDART_INF_F : -m;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < 64; ++e) {
+                const float x = ex2(fmaf(__uint_as_float(sv[2 * e]), cs, nm));
+                const float y = ex2(fmaf(__uint_as_float(sv[2 * e + 1]), cs, nm));
+                const __nv_bfloat162 w = __floats2bfloat162_rn(x, y);
+                sum[(2 * e) & 3] += x;             // unrounded: the denominator does not see P's rounding
+                sum[(2 * e + 1) & 3] += y;
+                sv[e] = *(const uint32_t *)&w;
+            }
+            l = l * alpha + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+            // the scores' barrier says that the sub-tile's earlier P . V is done as well
+            if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t ov[32];
+                    TMEM_LD32(tO + 32 * c, ov);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                    TMEM_ST32(tO + 32 * c, ov);
+                }
+            }
+            TMEM_ST32(tS, sv);
+            TMEM_ST32(tS + 32, (sv + 32));
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&bars->p_full[s]);
+        }
+        if (ok && mine > 0) ok = __all_sync(0xffffffffu, wait(&bars->o_full[s], 0));
+        ok = ok && __all_sync(0xffffffffu, *(volatile int32_t *)&bars->abort_flag == 0);
+        if (mine > 0) {
+            tc_fence_after();
+            // O / l through this warp's part of its sub-tile's Q blocks (read for the last time
+            // by the last scores), then rows of 256 bytes
+            uint8_t *stage = smem + kOffQ + 3 * s * kBlock + wq * 32 * 256;
+            const float inv = ok ? 1.f / l : CUDART_NAN_F;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t ov[32];
+                TMEM_LD32(tO + 32 * c, ov);
+                tmem_wait_ld();
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(ov[8 * ch + 2 * e]) * inv,
+                                                                       __uint_as_float(ov[8 * ch + 2 * e + 1]) * inv);
+                        w[e] = *(const uint32_t *)&x;
+                    }
+                    // 16-byte chunks rotated by the row: no two lanes of a store on one bank
+                    *(uint4 *)(stage + lane * 256 + (((4 * c + ch) ^ (lane & 15)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            __syncwarp();
+            const int first = 128 * s + 32 * wq;               // of the tile
+            for (int rr = lane >> 4; rr < 32; rr += 2)
+                if (first + rr < rows_here)
+                    *(uint4 *)(out + ((qrow0 + first + rr) * H + h) * kDv + 8 * (lane & 15)) =
+                        *(const uint4 *)(stage + rr * 256 + (((lane & 15) ^ (rr & 15)) << 4));
+            if (p.lse && first + lane < rows_here)
+                p.lse[(qrow0 + first + lane) * H + h] = ok ? (m + log2f(l)) * kLn2 : CUDART_NAN_F;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------- host side
+static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    if (!fn) {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = (PFN_cuTensorMapEncodeTiled_v12000)ptr;
+    }
+    return fn;
+}
+
+// bf16 map over a row-major [rows, cols] matrix, 128-byte swizzled boxes of [box_rows, 64].
+// Loads past the last row read zeros.
+static bool map2d(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
+    cuuint32_t box[2] = {64, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The query [num_q, H, 192], boxes of 128 tokens x 64 dims of one head.
+static bool map_q(CUtensorMap *map, const void *base, int num_q, int H) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t d = kDn + kRope;
+    cuuint64_t dims[3] = {d, (cuuint64_t)H, (cuuint64_t)num_q};
+    cuuint64_t strides[2] = {d * 2, d * 2 * (cuuint64_t)H};
+    cuuint32_t box[3] = {64, 1, 128};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace pf
+
+bool prefill_tc_supported(const ShapeArgs &s, int dn) {
+    return (s.kind == MLA_KV_BF16 || is_mx(s.kind)) && s.r == pf::kR && s.dR == pf::kRope && s.dv == pf::kDv && dn == pf::kDn;
+}
+
+cudaError_t launch_prefill_tc(const PrefillParams &p, cudaStream_t st) {
+    using namespace pf;
+    const uint64_t kv_rows = (uint64_t)p.nh * p.cap_rows;
+    CUtensorMap rows, uk, uv, k_st, v_st, q, k_ld, v_ld;
+    if (!map2d(&rows, p.rows, p.cap_rows, kR + kRope, 128) || !map2d(&uk, p.W_UK, (uint64_t)p.s.H * kDn, kR, 128) ||
+        !map2d(&uv, p.W_UV, (uint64_t)p.s.H * kR, kDv, 64) || !map2d(&k_st, p.k, kv_rows, kDn, 32) ||
+        !map2d(&v_st, p.v, kv_rows, kDv, 32) || !map2d(&k_ld, p.k, kv_rows, kDn, 128) ||
+        !map2d(&v_ld, p.v, kv_rows, kDv, 64) || !map_q(&q, p.q, p.num_q, p.s.H))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(ex::expand_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ex::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(prefill_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    if (e != cudaSuccess) return e;
+    ex::expand_tc_kernel<<<dim3((p.cap_rows + 255) / 256, p.nh), ex::kThreads, ex::kSmemBytes, st>>>(rows, uk, uv, k_st, v_st, p);
+    prefill_tc_kernel<<<dim3(p.num_q / kTileQ + p.B, p.nh), kThreads, kSmemBytes, st>>>(q, k_ld, v_ld, rows, p);
+    return cudaGetLastError();
+}
+
+}  // namespace mla
