@@ -209,7 +209,7 @@ static mla_status run_attention(const mla_shape *s, const mla_cache *cache, cons
     p.num_work = (const int32_t *)(ws + w.status + sizeof(int32_t));
     // the bf16 decode that scores two blocks per MMA plans in 128-token steps, so that
     // only a sequence's last work item can end with an unpaired block
-    const bool wide = impl == MLA_IMPL_TCGEN05 && s->kind == MLA_KV_BF16;
+    const bool wide = impl == MLA_IMPL_TCGEN05 && (s->kind == MLA_KV_BF16 || mx);
     p.item_cost = impl == MLA_IMPL_TCGEN05 ? (wide ? kItemCostWide : kItemCostTc) : 0;
     p.plan_tile = wide ? 128 : 64;
     p.work = (const WorkItem *)(ws + w.work);

@@ -976,12 +976,12 @@ static bool make_out_map(CUtensorMap *map, void *base, int r, int rows_seq, int 
 
 bool tc_shape_supported(const ShapeArgs &s) {
     if (s.r != 512 || s.dR != 64 || s.bs != tc::kTile) return false;
-    return s.kind == MLA_KV_BF16 || ((s.kind == MLA_KV_INT2_ROT || s.kind == MLA_KV_INT2_ROT_QR) && s.gs == 32);
+    return s.kind == MLA_KV_BF16 || is_mx(s.kind) || ((s.kind == MLA_KV_INT2_ROT || s.kind == MLA_KV_INT2_ROT_QR) && s.gs == 32);
 }
 
 cudaError_t launch_decode_tc(const DecodeParams &p, int32_t max_work, cudaStream_t st) {
-    // the bf16 cache: two cache blocks per score MMA (mla_wide.cu)
-    if (p.s.kind == MLA_KV_BF16) return launch_decode_wide(p, max_work, st);
+    // the bf16 and 8-bit caches: two cache blocks per score MMA (mla_wide.cu)
+    if (p.s.kind == MLA_KV_BF16 || is_mx(p.s.kind)) return launch_decode_wide(p, max_work, st);
     tc::TcParams tp;
     tp.p = p;
     tp.row_tiles = (p.q_len * p.s.H + tc::kRows - 1) / tc::kRows;
