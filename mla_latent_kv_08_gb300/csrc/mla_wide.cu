@@ -42,7 +42,7 @@
 // bounded (2 s); a wait that gives up records FLAG_TIMEOUT and the CTA winds down
 // without trapping.
 //
-// The 8-bit cache (MX = true) runs the same kernel with four more warps (12..15), which
+// The 8-bit cache (MX = true) runs the same kernel with eight more warps (2, 3, 12..17), which
 // take the place of the TMA for the latent blocks: they read codes and scales into
 // registers, a batch ahead of the one they work on, and expand them into the same
 // swizzled bf16 blocks (exactly: a code times a power of two is a bf16), with zeros for
@@ -63,8 +63,8 @@ namespace wide {
 
 using namespace ptx;
 
-constexpr int kThreads = 384, kThreadsMx = 512;
-constexpr int kExpandThreads = 128;                    // warps 12..15 (MX)
+constexpr int kThreads = 384, kThreadsMx = 576;
+constexpr int kExpandThreads = 256;                    // warps 2, 3, 12..17 (MX)
 constexpr int kSoftmaxThreads = 256;                  // warps 4..11
 constexpr int kTile = 64;                             // tokens per cache block
 constexpr int kStep = 2 * kTile;                      // tokens per step (MMA N of the scores)
@@ -681,18 +681,18 @@ decode_wide_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_cons
             if (ok && have_next) ok = __all_sync(0xffffffffu, issue_q(i + 1, 1));
         }
         if (lane == 0) bulk_wait_all();   // this warp's output stores have landed
-    } else if (MX && warp >= 12) {
+    } else if (MX && (warp < 4 || warp >= 12)) {
         // ================================================= expansion of the 8-bit codes
-        // Warp e takes the rows 8 (e + 4 i) .. + 7 of the step, i < 4: a lane one row's 16
-        // codes of a 64-dim column block, four lanes a row (64 bytes of the cache row; the
-        // two 16-byte stores of a quarter warp fall on eight different swizzled chunks).
-        // Batch k of a step holds two column blocks: k = 0, 1 the other half's latent dims
-        // (score-only), k = 2, 3 the own ones. While a batch is expanded the next one's
-        // loads are in flight.
-        const int e = warp - 12, r8 = lane >> 2, piece = lane & 3;
+        // Warp e takes rows 8 e .. 8 e + 7 of both tiles: a lane one row's 16 codes of a
+        // 64-dim column block, four lanes a row (64 bytes of the cache row; the two 16-byte
+        // stores of a quarter warp fall on eight different swizzled chunks). Batch k of a
+        // step holds two column blocks: k = 0, 1 the other half's latent dims (score-only),
+        // k = 2, 3 the own ones. Two to three batches are in flight ahead of the one that is
+        // expanded, which covers the latency of L2.
+        const int e = warp < 4 ? warp - 2 : warp - 10, r8 = lane >> 2, piece = lane & 3;
         struct Batch {
-            uint4 c[4][2];
-            uint32_t s[4];
+            uint4 c[2][2];
+            uint32_t s[2];
         };
         struct Step {
             int row0[2], valid[2];         // token row of each tile's first slot; its tokens
@@ -711,39 +711,37 @@ decode_wide_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_cons
         };
         auto first_block = [&](int k) { return (k < 2 ? 4 * (1 - half) : 4 * half) + 2 * (k & 1); };
         auto load = [&](Batch &b, const Step &st, int k) {
-            const int cb = first_block(k);
+            const int cb = first_block(k), row = 8 * e + r8;                 // of either tile
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = 8 * (e + 4 * (i & 1)) + r8, u = i >> 1;      // of tile u
-                b.s[i] = 0;
-                b.c[i][0] = b.c[i][1] = make_uint4(0, 0, 0, 0);              // a zero for slots past the end
+            for (int u = 0; u < 2; ++u) {
+                b.s[u] = 0;
+                b.c[u][0] = b.c[u][1] = make_uint4(0, 0, 0, 0);              // a zero for slots past the end
                 if (row < st.valid[u]) {
                     const size_t tok = (size_t)(st.row0[u] + row);
                     const uint8_t *src = p.codes + tok * 512 + 64 * cb + 16 * piece;
 #pragma unroll
                     for (int w = 0; w < 2; ++w)
                         asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(b.c[i][w].x), "=r"(b.c[i][w].y), "=r"(b.c[i][w].z), "=r"(b.c[i][w].w)
+                                     : "=r"(b.c[u][w].x), "=r"(b.c[u][w].y), "=r"(b.c[u][w].z), "=r"(b.c[u][w].w)
                                      : "l"(src + 64 * w));
                     // the four scales of the two column blocks
-                    asm volatile("ld.global.u32 %0, [%1];" : "=r"(b.s[i]) : "l"(p.mx_scale + tok * 16 + 2 * cb));
+                    asm volatile("ld.global.u32 %0, [%1];" : "=r"(b.s[u]) : "l"(p.mx_scale + tok * 16 + 2 * cb));
                 }
             }
         };
         auto expand = [&](const Batch &b, int k) {
             const int cb = first_block(k);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int grp = (i >> 1) * 8 + e + 4 * (i & 1);              // 8-row group of the step
+            for (int u = 0; u < 2; ++u) {
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
-                    const __nv_bfloat162 sc = mx_scale_bf162((b.s[i] >> (16 * w + 8 * (piece >> 1))) & 0xffu);
+                    const __nv_bfloat162 sc = mx_scale_bf162((b.s[u] >> (16 * w + 8 * (piece >> 1))) & 0xffu);
                     uint4 o0, o1;
-                    mx_expand4(b.c[i][w].x, sc, o0.x, o0.y);
-                    mx_expand4(b.c[i][w].y, sc, o0.z, o0.w);
-                    mx_expand4(b.c[i][w].z, sc, o1.x, o1.y);
-                    mx_expand4(b.c[i][w].w, sc, o1.z, o1.w);
-                    uint8_t *dst = smem + kOffBuf + (cb + w) * kCol + grp * 1024 + r8 * 128;
+                    mx_expand4(b.c[u][w].x, sc, o0.x, o0.y);
+                    mx_expand4(b.c[u][w].y, sc, o0.z, o0.w);
+                    mx_expand4(b.c[u][w].z, sc, o1.x, o1.y);
+                    mx_expand4(b.c[u][w].w, sc, o1.z, o1.w);
+                    uint8_t *dst = smem + kOffBuf + (cb + w) * kCol + (8 * u + e) * 1024 + r8 * 128;
                     *(uint4 *)(dst + (((2 * piece) ^ r8) << 4)) = o0;
                     *(uint4 *)(dst + (((2 * piece + 1) ^ r8) << 4)) = o1;
                 }
@@ -753,9 +751,11 @@ decode_wide_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_cons
         WorkItem it = p.work[i];
         int L = p.seq_lens[it.b];
         Step cur = step_at(it, L, 0);
-        Batch x, y;
+        Batch x, y, z;
         load(x, cur, 0);
+        load(y, cur, 1);
         for (bool more = true; more; ++K) {
+            load(z, cur, 2);
             // the step after this one
             Step nxt = cur;
             if (++j == steps_of(it.t0, it.t1)) {
@@ -767,18 +767,17 @@ decode_wide_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_cons
                 }
             }
             if (more) nxt = step_at(it, L, j);
-            load(y, cur, 1);
             if (K > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->empty_a, (K - 1) & 1, bars, p.status))) break;
-            expand(x, 0);
-            load(x, cur, 2);
             expand(y, 1);
+            load(y, cur, 3);
+            expand(x, 0);
             fence_proxy_async();
             mbar_arrive(&bars->full_a);
-            load(y, cur, 3);
-            if (K > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->empty_v, (K - 1) & 1, bars, p.status))) break;
-            expand(x, 2);
             if (more) load(x, nxt, 0);
+            if (K > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->empty_v, (K - 1) & 1, bars, p.status))) break;
+            expand(z, 2);
             expand(y, 3);
+            if (more) load(y, nxt, 1);
             fence_proxy_async();
             mbar_arrive(&bars->full_v);
             cur = nxt;
