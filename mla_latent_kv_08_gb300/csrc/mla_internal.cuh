@@ -227,6 +227,8 @@ bool tc_shape_supported(const ShapeArgs &s);
 cudaError_t launch_decode_tc(const DecodeParams &p, int32_t max_work, cudaStream_t st);
 // ---- bf16 tensor-core decode, two cache blocks per score MMA (mla_wide.cu) ----
 cudaError_t launch_decode_wide(const DecodeParams &p, int32_t max_work, cudaStream_t st);
+// ---- the same over the 8-bit cache (mla_wide_mx.cu) ---------------------------
+cudaError_t launch_decode_mx(const DecodeParams &p, int32_t max_work, cudaStream_t st);
 // ---- tensor-core combine + W_UV (defined in mla_combine_tc.cu) --------------
 bool combine_tc_supported(const ShapeArgs &s);
 cudaError_t launch_combine_tc(const CombineParams &c, cudaStream_t st);

@@ -36,25 +36,55 @@ __device__ __forceinline__ float mx_scale_f32(uint32_t b) {
     return __uint_as_float(b == 255u ? 0x7fc00000u : b == 0u ? 0x00400000u : b << 23);
 }
 // The same in both halves of a bf16 pair.
-__device__ __forceinline__ __nv_bfloat162 mx_scale_bf162(uint32_t b) {
+__device__ __forceinline__ uint32_t mx_scale_bf162(uint32_t b) {
     const uint32_t h = b == 255u ? 0x7fc0u : b == 0u ? 0x0040u : b << 7;
-    const uint32_t u = h | (h << 16);
-    return *(const __nv_bfloat162 *)&u;
+    return h | (h << 16);
 }
-// Four codes (a word, memory order) times their group's scale, as two bf16 pairs. A code's
-// exponent and fraction bits placed 4 up in a bf16 (whose exponent field is then the
-// code's) stand for the code's value times 2^-120, subnormal codes included; one exact
-// multiplication by 2^120 gives the value, a second the scale.
-__device__ __forceinline__ void mx_expand4(uint32_t w, __nv_bfloat162 scale, uint32_t &o0, uint32_t &o1) {
-    const uint32_t k120u = 0x7b807b80u;                    // 2^120 twice
-    const __nv_bfloat162 k120 = *(const __nv_bfloat162 *)&k120u;
-    const uint32_t lo = __byte_perm(w, 0u, 0x1404), hi = __byte_perm(w, 0u, 0x3424);
-    const uint32_t a = ((lo >> 4) & 0x07f007f0u) | (lo & 0x80008000u);
-    const uint32_t b = ((hi >> 4) & 0x07f007f0u) | (hi & 0x80008000u);
-    const __nv_bfloat162 x = __hmul2(__hmul2(*(const __nv_bfloat162 *)&a, k120), scale);
-    const __nv_bfloat162 y = __hmul2(__hmul2(*(const __nv_bfloat162 *)&b, k120), scale);
-    o0 = *(const uint32_t *)&x;
-    o1 = *(const uint32_t *)&y;
+constexpr uint32_t kMx2p120 = 0x7b807b80u;                  // 2^120 twice, as a bf16 pair
+__device__ __forceinline__ uint32_t mul_bf162(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 x = __hmul2(*(const __nv_bfloat162 *)&a, *(const __nv_bfloat162 *)&b);
+    return *(const uint32_t *)&x;
+}
+// Four codes (a word, memory order) as two bf16 pairs of their values times 2^-120: a
+// code's exponent and fraction bits placed 4 up in a bf16, whose exponent field is then
+// the code's; subnormal codes become subnormal and stay right. The byte permute extends the
+// code's sign over the high byte of its half, so that a shift by 4 brings the sign to bit 15
+// and one mask clears what the shift put between.
+__device__ __forceinline__ void mx_place4(uint32_t w, uint32_t &o0, uint32_t &o1) {
+    uint32_t lo, hi;                                       // (the intrinsic has no sign mode)
+    asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(lo) : "r"(w));
+    asm("prmt.b32 %0, %1, 0, 0xb3a2;" : "=r"(hi) : "r"(w));
+    o0 = (lo << 4) & 0x87f087f0u;
+    o1 = (hi << 4) & 0x87f087f0u;
+}
+// Sixteen codes (memory order) as bf16: `first` times their placed values, where no scale
+// is above 1 the scale and 2^120 in one (mx_scale120), else 2^120 and then `second`. Every
+// product is exact.
+__device__ __forceinline__ void mx_expand16(const uint4 &c, uint32_t first, uint4 &o0, uint4 &o1) {
+    mx_place4(c.x, o0.x, o0.y);
+    mx_place4(c.y, o0.z, o0.w);
+    mx_place4(c.z, o1.x, o1.y);
+    mx_place4(c.w, o1.z, o1.w);
+    uint32_t *a = (uint32_t *)&o0, *b = (uint32_t *)&o1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        a[i] = mul_bf162(a[i], first);
+        b[i] = mul_bf162(b[i], first);
+    }
+}
+__device__ __forceinline__ void mx_expand16(const uint4 &c, uint32_t first, uint32_t second, uint4 &o0, uint4 &o1) {
+    mx_expand16(c, first, o0, o1);
+    uint32_t *a = (uint32_t *)&o0, *b = (uint32_t *)&o1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        a[i] = mul_bf162(a[i], second);
+        b[i] = mul_bf162(b[i], second);
+    }
+}
+// 2^(b - 127 + 120) in both halves, of byte `sel` of four scale bytes that are all at most
+// 127 (scales up to 1).
+__device__ __forceinline__ uint32_t mx_scale120(uint32_t bytes, uint32_t sel) {
+    return __byte_perm(bytes, 0u, 0x4040u | sel | (sel << 8)) * 128u + 0x3c003c00u;
 }
 // One code and its scale byte in fp32 (the CUDA-core kernels).
 __device__ __forceinline__ float mx_value(uint32_t code, uint32_t scale_byte) {

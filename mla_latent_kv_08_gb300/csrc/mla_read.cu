@@ -24,12 +24,8 @@ __device__ __forceinline__ void write_row(const ReadParams &p, long long tok, si
         const uint8_t *scales = p.mx_scale + (size_t)tok * (r / kMxGroup);
         for (int v = lane; v < r / 16; v += 32) {
             const uint4 c = codes[v];
-            const __nv_bfloat162 s = mx_scale_bf162(scales[v >> 1]);
             uint4 o0, o1;
-            mx_expand4(c.x, s, o0.x, o0.y);
-            mx_expand4(c.y, s, o0.z, o0.w);
-            mx_expand4(c.z, s, o1.x, o1.y);
-            mx_expand4(c.w, s, o1.z, o1.w);
+            mx_expand16(c, kMx2p120, mx_scale_bf162(scales[v >> 1]), o0, o1);
             dst[2 * v] = o0;
             dst[2 * v + 1] = o1;
         }

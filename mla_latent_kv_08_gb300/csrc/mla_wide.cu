@@ -41,16 +41,7 @@
 // loads, softmax and epilogue (warp w reads TMEM lanes 32*(w%4)..+31). Every wait is
 // bounded (2 s); a wait that gives up records FLAG_TIMEOUT and the CTA winds down
 // without trapping.
-//
-// The 8-bit cache (MX = true) runs the same kernel with eight more warps (2, 3, 12..17), which
-// take the place of the TMA for the latent blocks: they read codes and scales into
-// registers, a batch ahead of the one they work on, and expand them into the same
-// swizzled bf16 blocks (exactly: a code times a power of two is a bf16), with zeros for
-// tokens past the end. The rope key still comes by TMA. The score-only blocks are expanded
-// while the softmax and P . V of the step before run, the own blocks while the score MMAs
-// over the score-only blocks do, so that the expansion stays off the critical path.
 #include "mla_internal.cuh"
-#include "mla_mx.cuh"
 #include "mla_ptx.cuh"
 
 #include <cuda.h>
@@ -63,8 +54,7 @@ namespace wide {
 
 using namespace ptx;
 
-constexpr int kThreads = 384, kThreadsMx = 576;
-constexpr int kExpandThreads = 256;                    // warps 2, 3, 12..17 (MX)
+constexpr int kThreads = 384;
 constexpr int kSoftmaxThreads = 256;                  // warps 4..11
 constexpr int kTile = 64;                             // tokens per cache block
 constexpr int kStep = 2 * kTile;                      // tokens per step (MMA N of the scores)
@@ -165,8 +155,7 @@ __device__ __forceinline__ int block_of(const DecodeParams &p, int b, int lb) {
 
 __host__ __device__ constexpr int steps_of(int t0, int t1) { return (t1 - t0 + kStep - 1) / kStep; }
 
-template <bool MX>
-__global__ void __launch_bounds__(MX ? kThreadsMx : kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 decode_wide_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap q_map,
                    const __grid_constant__ CUtensorMap o_map, const WideParams wp) {
     const DecodeParams &p = wp.p;
@@ -186,8 +175,8 @@ decode_wide_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_cons
 #endif
 
     if (tid == 0) {
-        mbar_init(&bars->full_a, MX ? 1 + kExpandThreads : 1);
-        mbar_init(&bars->full_v, MX ? kExpandThreads : 1);
+        mbar_init(&bars->full_a, 1);
+        mbar_init(&bars->full_v, 1);
         mbar_init(&bars->empty_a, 1);
         mbar_init(&bars->empty_v, 1);
         mbar_init(&bars->tail_done, 1);
@@ -256,13 +245,7 @@ decode_wide_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_cons
                 const int nt = (it.t1 - it.t0 + kTile - 1) / kTile;
                 if (pt >= nt) { ++pi; pt = 0; continue; }
                 const int blk = block_of(p, it.b, it.t0 / kTile + pt);
-                if (MX) {
-                    if (blk >= 0) {
-                        prefetch_l2(p.codes + (size_t)blk * (kTile * 512), kTile * 512);
-                        prefetch_l2(p.mx_scale + (size_t)blk * (kTile * 16), kTile * 16);
-                        prefetch_l2(p.rope + (size_t)blk * (kTile * 64), kTile * 128);
-                    }
-                } else if (blk >= 0)       // the block's rows (index keys included: one contiguous range)
+                if (blk >= 0)       // the block's rows (index keys included: one contiguous range)
                     prefetch_l2((const __nv_bfloat16 *)p.latent + (size_t)blk * kTile * p.s.E(),
                                 (uint32_t)kTile * p.s.E() * 2);
                 ++pt;
@@ -295,16 +278,8 @@ decode_wide_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_cons
                     ok = false;
                     break;
                 }
-                if (lane == 0) mbar_expect_tx(&bars->full_a, (MX ? 2 : 10) * kBox);
+                if (lane == 0) mbar_expect_tx(&bars->full_a, 10 * kBox);
                 __syncwarp();
-                if (MX) {                                  // the rope key only
-                    if (lane < 2) tma_load_2d(smem + kOffBuf + 8 * kCol + lane * kBox, &kv_map, 0, row0[lane], &bars->full_a);
-                    if (lane == 0 && prefetcher) {
-                        ahead = max(0, ahead - 2);
-                        advance_prefetch();
-                    }
-                    continue;
-                }
                 if (lane < 10) {
                     const int u = lane / 5, c = score_only_block(half, lane % 5);
                     tma_load_2d(smem + kOffBuf + c * kCol + u * kBox, &kv_map, 64 * c, row0[u], &bars->full_a);
@@ -354,10 +329,9 @@ decode_wide_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_cons
             }
         }
         // drain: never leave a copy in flight into this CTA's shared memory
-        // (MX: the full barriers also count the expanding warps, which arrive or abort)
         if (K > 0) {
             mbar_drain(&bars->full_a, (K - 1) & 1);
-            if (!MX) mbar_drain(&bars->full_v, (K - 1) & 1);
+            mbar_drain(&bars->full_v, (K - 1) & 1);
         }
         (void)tail_issued;
         __syncwarp();
@@ -424,7 +398,7 @@ decode_wide_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_cons
                     WTRACE(6, K);
                     const int v0 = min(kTile, L - (it.t0 + 2 * j * kTile));
                     const int v1 = 2 * j + 1 < nt ? min(kTile, L - (it.t0 + (2 * j + 1) * kTile)) : 0;
-                    if (!MX && ((v0 > 0 && v0 < kTile) || (v1 > 0 && v1 < kTile))) {
+                    if ((v0 > 0 && v0 < kTile) || (v1 > 0 && v1 < kTile)) {
                         if (!mbar_wait(&bars->tail_done, tail_par & 1u, bars, p.status)) { ok = false; break; }
                         tail_par ^= 1u;
                     }
@@ -584,12 +558,13 @@ decode_wide_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_cons
                 }
                 const float nmb = m_used == -CUDART_INF_F ? -CUDART_INF_F : -m_used;
                 float sum0 = 0.f, sum1 = 0.f;
+                uint32_t pk[32];
 #pragma unroll
                 for (int jj = 0; jj < 32; ++jj) {
                     const float a = ex2(fmaf(__uint_as_float(sv[2 * jj]), cs, nmb));
                     const float c = ex2(fmaf(__uint_as_float(sv[2 * jj + 1]), cs, nmb));
                     const __nv_bfloat162 hh = __floats2bfloat162_rn(a, c);
-                    sv[jj] = *(const uint32_t *)&hh;        // in place: scores 2 jj, 2 jj + 1 are done with
+                    pk[jj] = *(const uint32_t *)&hh;
                     sum0 += a;             // fp32 row sum: the LSE does not see the rounding of P
                     sum1 += c;
                 }
@@ -607,7 +582,7 @@ decode_wide_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_cons
                         TMEM_ST32(lane_addr + kColO + 32 * c, ov);
                     }
                 }
-                TMEM_ST32(lane_addr + kColS + 32 * hs, sv);
+                TMEM_ST32(lane_addr + kColS + 32 * hs, pk);
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&bars->p_full);
@@ -681,108 +656,6 @@ decode_wide_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_cons
             if (ok && have_next) ok = __all_sync(0xffffffffu, issue_q(i + 1, 1));
         }
         if (lane == 0) bulk_wait_all();   // this warp's output stores have landed
-    } else if (MX && (warp < 4 || warp >= 12)) {
-        // ================================================= expansion of the 8-bit codes
-        // Warp e takes rows 8 e .. 8 e + 7 of both tiles: a lane one row's 16 codes of a
-        // 64-dim column block, four lanes a row (64 bytes of the cache row; the two 16-byte
-        // stores of a quarter warp fall on eight different swizzled chunks). Batch k of a
-        // step holds two column blocks: k = 0, 1 the other half's latent dims (score-only),
-        // k = 2, 3 the own ones. Two to three batches are in flight ahead of the one that is
-        // expanded, which covers the latency of L2.
-        const int e = warp < 4 ? warp - 2 : warp - 10, r8 = lane >> 2, piece = lane & 3;
-        struct Batch {
-            uint4 c[2][2];
-            uint32_t s[2];
-        };
-        struct Step {
-            int row0[2], valid[2];         // token row of each tile's first slot; its tokens
-        };
-        auto step_at = [&](const WorkItem &it, int L, int j) {
-            Step st;
-            const int nt = (it.t1 - it.t0 + kTile - 1) / kTile;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int t = 2 * j + u;
-                const int blk = t < nt ? block_of(p, it.b, it.t0 / kTile + t) : -1;
-                st.row0[u] = blk * kTile;
-                st.valid[u] = blk >= 0 ? min(kTile, L - (it.t0 + t * kTile)) : 0;
-            }
-            return st;
-        };
-        auto first_block = [&](int k) { return (k < 2 ? 4 * (1 - half) : 4 * half) + 2 * (k & 1); };
-        auto load = [&](Batch &b, const Step &st, int k) {
-            const int cb = first_block(k), row = 8 * e + r8;                 // of either tile
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                b.s[u] = 0;
-                b.c[u][0] = b.c[u][1] = make_uint4(0, 0, 0, 0);              // a zero for slots past the end
-                if (row < st.valid[u]) {
-                    const size_t tok = (size_t)(st.row0[u] + row);
-                    const uint8_t *src = p.codes + tok * 512 + 64 * cb + 16 * piece;
-#pragma unroll
-                    for (int w = 0; w < 2; ++w)
-                        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(b.c[u][w].x), "=r"(b.c[u][w].y), "=r"(b.c[u][w].z), "=r"(b.c[u][w].w)
-                                     : "l"(src + 64 * w));
-                    // the four scales of the two column blocks
-                    asm volatile("ld.global.u32 %0, [%1];" : "=r"(b.s[u]) : "l"(p.mx_scale + tok * 16 + 2 * cb));
-                }
-            }
-        };
-        auto expand = [&](const Batch &b, int k) {
-            const int cb = first_block(k);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const __nv_bfloat162 sc = mx_scale_bf162((b.s[u] >> (16 * w + 8 * (piece >> 1))) & 0xffu);
-                    uint4 o0, o1;
-                    mx_expand4(b.c[u][w].x, sc, o0.x, o0.y);
-                    mx_expand4(b.c[u][w].y, sc, o0.z, o0.w);
-                    mx_expand4(b.c[u][w].z, sc, o1.x, o1.y);
-                    mx_expand4(b.c[u][w].w, sc, o1.z, o1.w);
-                    uint8_t *dst = smem + kOffBuf + (cb + w) * kCol + (8 * u + e) * 1024 + r8 * 128;
-                    *(uint4 *)(dst + (((2 * piece) ^ r8) << 4)) = o0;
-                    *(uint4 *)(dst + (((2 * piece + 1) ^ r8) << 4)) = o1;
-                }
-            }
-        };
-        int i = i0, j = 0, K = 0;
-        WorkItem it = p.work[i];
-        int L = p.seq_lens[it.b];
-        Step cur = step_at(it, L, 0);
-        Batch x, y, z;
-        load(x, cur, 0);
-        load(y, cur, 1);
-        for (bool more = true; more; ++K) {
-            load(z, cur, 2);
-            // the step after this one
-            Step nxt = cur;
-            if (++j == steps_of(it.t0, it.t1)) {
-                j = 0;
-                more = ++i < i1;
-                if (more) {
-                    it = p.work[i];
-                    L = p.seq_lens[it.b];
-                }
-            }
-            if (more) nxt = step_at(it, L, j);
-            if (K > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->empty_a, (K - 1) & 1, bars, p.status))) break;
-            expand(y, 1);
-            load(y, cur, 3);
-            expand(x, 0);
-            fence_proxy_async();
-            mbar_arrive(&bars->full_a);
-            if (more) load(x, nxt, 0);
-            if (K > 0 && !__all_sync(0xffffffffu, mbar_wait(&bars->empty_v, (K - 1) & 1, bars, p.status))) break;
-            expand(z, 2);
-            expand(y, 3);
-            if (more) load(y, nxt, 1);
-            fence_proxy_async();
-            mbar_arrive(&bars->full_v);
-            cur = nxt;
-        }
-        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
@@ -809,13 +682,12 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// 2-D bf16 map over the first `cols` (576) columns of a row-major [rows, row_elems] matrix,
+// 2-D bf16 map over the first 576 columns of a row-major [rows, row_elems] matrix,
 // 128-byte swizzled boxes of [box_rows, 64]. Rows past the end read as zero.
-static bool make_map(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows, uint64_t row_elems,
-                     uint64_t cols = kD) {
+static bool make_map(CUtensorMap *map, const void *base, uint64_t rows, uint32_t box_rows, uint64_t row_elems) {
     auto fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)row_elems * 2};
     cuuint32_t box[2] = {64, box_rows};
     cuuint32_t estr[2] = {1, 1};
@@ -847,18 +719,16 @@ cudaError_t launch_decode_wide(const DecodeParams &p, int32_t max_work, cudaStre
     wp.p = p;
     wp.row_tiles = (p.q_len * p.s.H + wide::kRows - 1) / wide::kRows;
     CUtensorMap kv_map, q_map, o_map;
-    const bool mx = is_mx(p.s.kind);           // kv_map: the rope keys alone
-    if (!(mx ? wide::make_map(&kv_map, p.rope, (uint64_t)p.s.num_blocks * p.s.bs, wide::kTile, (uint64_t)p.s.dR, (uint64_t)p.s.dR)
-             : wide::make_map(&kv_map, p.latent, (uint64_t)p.s.num_blocks * p.s.bs, wide::kTile, (uint64_t)p.s.E())))
+    if (!wide::make_map(&kv_map, p.latent, (uint64_t)p.s.num_blocks * p.s.bs, wide::kTile, (uint64_t)p.s.E()))
         return cudaErrorInvalidValue;
     const int rows_seq = p.q_len * p.s.H;
     if (!wide::make_map(&q_map, p.q, (uint64_t)p.B * rows_seq, wide::kRows, wide::kD)) return cudaErrorInvalidValue;
     if (!wide::make_out_map(&o_map, p.part_o, p.s.r, rows_seq, max_work)) return cudaErrorInvalidValue;
-    auto kern = mx ? wide::decode_wide_kernel<true> : wide::decode_wide_kernel<false>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)wide::kSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(wide::decode_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)wide::kSmemBytes);
     if (e != cudaSuccess) return e;
     dim3 grid(2, wp.row_tiles, p.streams);
-    return launch_pdl(kern, grid, dim3(mx ? wide::kThreadsMx : wide::kThreads), wide::kSmemBytes, st, kv_map, q_map, o_map,
+    return launch_pdl(wide::decode_wide_kernel, grid, dim3(wide::kThreads), wide::kSmemBytes, st, kv_map, q_map, o_map,
                       wp);
 }
 
