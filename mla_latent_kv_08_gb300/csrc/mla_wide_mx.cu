@@ -8,24 +8,22 @@
 // rope key) released before the four own ones; P over the scores in tensor memory.
 //
 // A code times a power of two is a bf16, so expanding the codes into the bf16 blocks is
-// exact and everything after it is as over a bf16 cache of the same values. What differs:
-//   expansion  eight warps read codes and scales into registers, 36 registers a step half
-//              and thread, issued while the half before is worked on (so that the latency
-//              of L2, about a thousand cycles, is never waited for), and write the swizzled
-//              blocks, zeros for tokens past the end. The score-only blocks are expanded
-//              while softmax and P . V of the step before run, the own ones while the score
-//              MMAs over the score-only blocks do.
-//   softmax    four warps, a thread a row of 128 scores, in two passes over tensor memory
-//              (maximum; then weights, 32 columns at a time): no exchange between warps,
-//              and few enough registers that 14 warps get 128 each. With 18 warps (eight of
-//              softmax) a thread has 96, and the spilled ones, more than fit the L1 that is
-//              left beside 227 KB of shared memory, came from L2 at every step.
-// The rope key comes by TMA.
+// exact and everything after it is as over a bf16 cache of the same values. The rope key
+// comes by TMA; the latent blocks are written by four warps, which read codes and scales
+// into registers, a part of a step (score-only or own dims) ahead of the one they expand.
+// The score-only blocks are expanded while the softmax and P . V of the step before run,
+// the own ones while the score MMAs over the score-only blocks do.
 //
-// Tensor memory: O [0,256), S / P [256,384), Q's own latent dims [384,512).
+// Two things bound the expansion. Registers: with more than 16 warps a thread has 96, and
+// the spilled ones, more than fit the L1 that 227 KB of shared memory leave, came from L2
+// at every step. Instructions: with the roles' code laid out straight, the warps waited for
+// instruction fetches more than for anything else (3.9 warps an issue slot), so the
+// expansion is one loop body for all parts.
+//
+// Tensor memory: O [0,256), S / P [256,384), Q's other half of the latent dims [384,512).
 // Roles: warp 0 = rope keys (+ L2 prefetch of the codes); warp 1 = TMEM owner, lane 0
-// issues every MMA; warps 4..7 = Q loads, softmax, epilogue (TMEM lanes 32*(w%4)..+31);
-// warps 2, 3, 8..13 = expansion. Every wait is bounded (2 s); a wait that gives up records
+// issues every MMA; warps 4..11 = Q loads, softmax, epilogue (TMEM lanes 32*(w%4)..+31);
+// warps 12..15 = expansion. Every wait is bounded (2 s); a wait that gives up records
 // FLAG_TIMEOUT and the CTA winds down without trapping.
 #include "mla_internal.cuh"
 #include "mla_mx.cuh"
@@ -41,9 +39,15 @@ namespace wmx {
 
 using namespace ptx;
 
-constexpr int kThreads = 448;
-constexpr int kSoftmaxThreads = 128;                  // warps 4..7
-constexpr int kExpandThreads = 256;                   // warps 2, 3, 8..13
+constexpr int kThreads = 640;
+constexpr int kSoftmaxThreads = 256;                  // warps 4..11
+constexpr int kExpandThreads = 256;                   // warps 12..19
+// Registers a thread of the warpgroups (0: copies and MMA; 1, 2: softmax; 3, 4: expansion)
+// once they are split again: what the launch had, 5 x 96.
+constexpr int kRegsLaunch = 96, kRegsIssue = 64, kRegsSoftmax = 128, kRegsExpand = 80;
+static_assert(kRegsIssue + 2 * kRegsSoftmax + 2 * kRegsExpand <= 5 * kRegsLaunch, "register split");
+template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 constexpr int kTile = 64;                             // tokens per cache block
 constexpr int kStep = 2 * kTile;                      // tokens per step (MMA N of the scores)
 constexpr int kRows = 128;                            // query rows per CTA (MMA M)
@@ -52,26 +56,23 @@ constexpr int kBlocks = 9;                            // 64-dim column blocks pe
 constexpr uint32_t kBox = kTile * 128;                // [64 tokens x 64 dims] bf16: 8 KB
 constexpr uint32_t kCol = kStep * 128;                // one column block of a step: 16 KB
 constexpr uint32_t kQBlock = kRows * 128;             // [128 rows x 64 dims] bf16: 16 KB
-constexpr int kQTmemBlocks = 4;                       // Q's own latent dims
-constexpr int kQSmemBlocks = 5;                       // Q's score-only dims
+constexpr int kQTmemBlocks = 4;                       // Q's other half of the latent dims
+constexpr int kQSmemBlocks = 5;                       // Q's own latent dims, rope dims
 constexpr uint32_t kOffBuf = 0;
 constexpr uint32_t kOffQ = kOffBuf + kBlocks * kCol;          // 144 KB
 constexpr uint32_t kOffBar = kOffQ + kQSmemBlocks * kQBlock;   // 224 KB
-constexpr uint32_t kSmemBytes = kOffBar + 512 + 1024;          // + alignment slack
+constexpr uint32_t kOffXchg = kOffBar + 512;                   // [2][128] fp32 row values
+constexpr uint32_t kSmemBytes = kOffXchg + 1024 + 1024;        // + alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 384;
 constexpr uint32_t kEpiBoxBytes = 32 * 128;           // epilogue box: [32 rows x 64 dims] bf16
-static_assert(4 * 4 * kEpiBoxBytes <= kQSmemBlocks * kQBlock, "four boxes a warp");
+constexpr int kEpiBoxes = (int)((kQSmemBlocks * kQBlock) / (8 * kEpiBoxBytes));   // per warp at a time
+static_assert(kEpiBoxes >= 1 && 2 % kEpiBoxes == 0, "epilogue boxes");
 constexpr unsigned long long kTimeoutNs = 2000000000ull;       // 2 s bounded-wait safety net
 #ifndef MLA_MX_PREFETCH_AHEAD
 #define MLA_MX_PREFETCH_AHEAD 4
 #endif
 constexpr int kPrefetchAhead = MLA_MX_PREFETCH_AHEAD;       // blocks prefetched into L2 ahead
-
-// Column block of the step buffer that holds dims [64c, 64c + 64): own blocks are the
-// latent blocks 4*half .. 4*half + 3; the five score-only blocks are the other half's
-// latent blocks and the rope block (index 8).
-__device__ __forceinline__ int score_only_block(int half, int k) { return k < 4 ? 4 * (1 - half) + k : 8; }
 
 // Pipeline timestamps for performance analysis, compiled only with -DMLA_TRACE: clock64
 // at each hand-off of one CTA (stream MLA_TRACE_STREAM, half MLA_TRACE_HALF, row tile 0)
@@ -97,7 +98,7 @@ __device__ long long g_mxtrace[16][kTraceSteps];
 #endif
 #define WTRACE_E(ev)                          \
     do {                                      \
-        if (warp == 2 && lane == 0) WTRACE(ev, K); \
+        if (warp == 12 && lane == 0) WTRACE(ev, K); \
     } while (0)
 // events: 0 score-only boxes issued, 1 own boxes issued (producer), 2 score-only blocks
 // landed, 3 part 1 issued, 4 own blocks landed, 5 QK committed, 6 P seen, 7 PV issued
@@ -108,7 +109,7 @@ struct Bars {
     uint64_t full_a;          // the step's score-only blocks are there
     uint64_t full_v;          // the step's own blocks are there
     uint64_t empty_a;         // the score MMAs over the score-only blocks completed
-    uint64_t empty_v;         // PV of the step completed
+    uint64_t empty_v[2];      // PV over the step's first and second 64 tokens completed
     uint64_t s_full;
     uint64_t p_full;
     uint64_t pv_done;
@@ -117,6 +118,8 @@ struct Bars {
     uint64_t q_tmem;          // the tensor-memory part of Q is stored
     uint64_t qreg_free;       // every softmax thread is done with the Q region
     uint64_t mma_fin;
+    uint64_t xchg_full[4];    // lane quarter q: both halves of its rows wrote their value
+    uint64_t xchg_read[4];    // lane quarter q: both halves read the other's value
     uint32_t tmem_base;
     int32_t abort_flag;
 };
@@ -153,7 +156,8 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
         mbar_init(&bars->full_a, 1 + kExpandThreads);
         mbar_init(&bars->full_v, kExpandThreads);
         mbar_init(&bars->empty_a, 1);
-        mbar_init(&bars->empty_v, 1);
+        mbar_init(&bars->empty_v[0], 1);
+        mbar_init(&bars->empty_v[1], 1);
         mbar_init(&bars->s_full, 1);
         mbar_init(&bars->p_full, kSoftmaxThreads);
         mbar_init(&bars->pv_done, 1);
@@ -162,6 +166,10 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
         mbar_init(&bars->q_tmem, kSoftmaxThreads);
         mbar_init(&bars->qreg_free, kSoftmaxThreads);
         mbar_init(&bars->mma_fin, 1);
+        for (int q = 0; q < 4; ++q) {
+            mbar_init(&bars->xchg_full[q], 64);
+            mbar_init(&bars->xchg_read[q], 64);
+        }
         bars->abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
@@ -203,6 +211,7 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
 
     if (warp == 0) {
         // ================================================= rope keys (+ L2 prefetch)
+        reg_dec<kRegsIssue>();
         // The warp runs converged; one lane per box.
         const bool prefetcher = kPrefetchAhead > 0 && half == 0 && g == 0;
         int pi = i0, pt = 0, ahead = 0;
@@ -257,6 +266,7 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
         __syncwarp();
     } else if (warp == 1) {
         // ================================================= MMA issuer: lane 0 alone
+        reg_dec<kRegsIssue>();
         if (lane == 0) {
             constexpr uint32_t kIdQk = idesc_bf16(128, 128, false);
             constexpr uint32_t kIdPv = idesc_bf16(128, 256, true);
@@ -282,31 +292,33 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
                     // the item's first step: Q's shared-memory part may still be landing
                     if (j == 0 && !mbar_wait(&bars->q_smem, item_no & 1, bars, p.status)) { ok = false; break; }
                     tc_fence_after();
-                    // part 1: score-only blocks, Q from shared memory. K-step (k, s): Q slot k /
-                    // column block score_only_block(k), 32-byte step s inside the swizzle atom
-                    // (descriptor start addresses advance in 16-byte units)
+                    // part 1: score-only blocks; the latent ones with Q from tensor memory (8
+                    // columns per K-step), so that the products take half of the shared memory's
+                    // bandwidth while the own blocks are written (descriptor start addresses
+                    // advance in 16-byte units)
 #pragma unroll
-                    for (int k = 0; k < kQSmemBlocks; ++k) {
-                        const uint32_t cb = (uint32_t)score_only_block(half, k) * kCol;
+                    for (int k = 0; k < kQTmemBlocks; ++k) {
 #pragma unroll
                         for (int s = 0; s < 4; ++s) {
-                            const uint64_t a = qd + (uint64_t)((k * kQBlock + 32 * s) >> 4);
-                            const uint64_t b = bd + (uint64_t)((cb + 32 * s) >> 4);
-                            if (k == 0 && s == 0) mma_ss_k<kIdQk, 0>(d_s, a, b);
-                            else mma_ss_k<kIdQk, 1>(d_s, a, b);
+                            const uint64_t b = bd + (uint64_t)(((4 * (1 - half) + k) * kCol + 32 * s) >> 4);
+                            if (k == 0 && s == 0) mma_ts_k<kIdQk, 0>(d_s, qt, b);
+                            else mma_ts_k<kIdQk, 1>(d_s, qt + 32 * k + 8 * s, b);
                         }
                     }
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        mma_ss_k<kIdQk, 1>(d_s, qd + (uint64_t)((4 * kQBlock + 32 * s) >> 4), bd + (uint64_t)((8 * kCol + 32 * s) >> 4));
                     mma_commit(&bars->empty_a);
                     WTRACE(3, K);
                     if (!mbar_wait(&bars->full_v, K & 1, bars, p.status)) { ok = false; break; }
                     WTRACE(4, K);
                     tc_fence_after();
-                    // part 2: own blocks, Q from tensor memory (8 columns per K-step)
+                    // part 2: own blocks, Q from shared memory
 #pragma unroll
-                    for (int k = 0; k < kQTmemBlocks; ++k) {
+                    for (int k = 0; k < 4; ++k) {
 #pragma unroll
                         for (int s = 0; s < 4; ++s)
-                            mma_ts_k<kIdQk, 1>(d_s, qt + 32 * k + 8 * s,
+                            mma_ss_k<kIdQk, 1>(d_s, qd + (uint64_t)((k * kQBlock + 32 * s) >> 4),
                                                bd + (uint64_t)(((4 * half + k) * kCol + 32 * s) >> 4));
                     }
                     mma_commit(&bars->s_full);
@@ -321,9 +333,11 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
                     for (int kk = 0; kk < kStep / 16; ++kk) {
                         if (kk == 0 && j == 0) mma_ts_k<kIdPv, 0>(d_o, d_s, vd);
                         else mma_ts_k<kIdPv, 1>(d_o, d_s + 8 * kk, vd + (uint64_t)(128 * kk));
+                        // the first tile's rows are written again while the second's are read
+                        if (kk == kTile / 16 - 1) mma_commit(&bars->empty_v[0]);
                     }
                     mma_commit(&bars->pv_done);
-                    mma_commit(&bars->empty_v);
+                    mma_commit(&bars->empty_v[1]);
                     WTRACE(7, K);
                 }
             }
@@ -331,10 +345,12 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
             mbar_wait(&bars->mma_fin, 0, bars, p.status);
         }
         __syncwarp();
-    } else if (warp >= 4 && warp < 8) {
+    } else if (warp >= 4 && warp < 12) {
         // ================================================= Q loads, softmax, epilogue
-        // Thread (warp w, lane) owns query row 32*(w%4) + lane. Every branch around tcgen05.ld
-        // / tcgen05.st is warp-uniform.
+        reg_inc<kRegsSoftmax>();
+        // Warp w owns rows 32*(w%4)..+31 (its TMEM lane quarter) and half hs = (w-4)/4 of
+        // the step: score columns 64*hs..+63 (tile hs), P columns 32*hs..+31, output
+        // columns 128*hs..+127. Every branch around tcgen05.ld / tcgen05.st is warp-uniform.
         //
         // The Q region serves three uses in turn: staging the tensor-memory part of an
         // item's Q (TMA in, tcgen05.st out), the epilogue's output boxes, and Q's
@@ -342,17 +358,33 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
         // softmax thread is done with a staging or epilogue use; the TMA issuer (warp 4
         // lane 0) waits for it before loading into the region.
         const int wq = warp & 3;
+        const int hs = (warp - 4) >> 2;
         const int row = 32 * wq + lane;
         const int row_seq = g * kRows + row;
         const bool row_valid = row_seq < rows_seq;
         const bool issuer = warp == 4 && lane == 0;
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * wq) << 16);
-        const uint32_t tS = lane_addr + kColS;
+        float *xchg = (float *)(smem + kOffXchg);
         bool ok = true;
-        int K = 0, uses = 0, nstage = 0;
+        int K = 0, nx = 0, uses = 0, nstage = 0;
+        // Swap one value per row with the other half of the row (bounded waits). The
+        // tensor-memory fences order each side's tcgen05 accesses before the swap against
+        // the other side's after it.
+        auto exchange = [&](float v, float &other) -> bool {
+            if (nx > 0 && !mbar_wait(&bars->xchg_read[wq], (nx - 1) & 1, bars, p.status)) return false;
+            xchg[hs * 128 + row] = v;
+            tc_fence_before();
+            mbar_arrive(&bars->xchg_full[wq]);
+            if (!mbar_wait(&bars->xchg_full[wq], nx & 1, bars, p.status)) return false;
+            tc_fence_after();
+            other = xchg[(hs ^ 1) * 128 + row];
+            mbar_arrive(&bars->xchg_read[wq]);
+            ++nx;
+            return true;
+        };
         // TMA of Q part `round` of work item `item` into the Q region (issuer only): round
-        // 0 stages the tensor-memory part (the own latent blocks), round 1 loads the
-        // shared-memory part (the score-only dims, in score_only_block order).
+        // 0 stages the tensor-memory part (the other half's latent blocks), round 1 loads the
+        // shared-memory part (the own latent blocks, then the rope block).
         auto issue_q = [&](int item, int round) -> bool {
             if (!issuer) return true;
             if (uses > 0 && !mbar_wait(&bars->qreg_free, (uses - 1) & 1, bars, p.status)) return false;
@@ -360,20 +392,20 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
             if (round == 0) {
                 mbar_expect_tx(&bars->q_stage, kQTmemBlocks * kQBlock);
                 for (int k = 0; k < kQTmemBlocks; ++k)
-                    tma_load_2d(smem + kOffQ + k * kQBlock, &q_map, 64 * (4 * half + k), qrow, &bars->q_stage);
+                    tma_load_2d(smem + kOffQ + k * kQBlock, &q_map, 64 * (4 * (1 - half) + k), qrow, &bars->q_stage);
             } else {
                 mbar_expect_tx(&bars->q_smem, kQSmemBlocks * kQBlock);
                 for (int k = 0; k < kQSmemBlocks; ++k)
-                    tma_load_2d(smem + kOffQ + k * kQBlock, &q_map, 64 * score_only_block(half, k), qrow, &bars->q_smem);
+                    tma_load_2d(smem + kOffQ + k * kQBlock, &q_map, 64 * (k < 4 ? 4 * half + k : 8), qrow, &bars->q_smem);
             }
             return true;
         };
-        // Staged Q -> tensor memory, a thread its row.
+        // Staged Q -> tensor memory: thread (row, hs) moves blocks hs and hs + 2.
         auto load_q_tmem = [&]() -> bool {
             if (!__all_sync(0xffffffffu, mbar_wait(&bars->q_stage, nstage & 1, bars, p.status))) return false;
             ++nstage;
 #pragma unroll 1
-            for (int k = 0; k < kQTmemBlocks; ++k) {
+            for (int k = hs; k < kQTmemBlocks; k += 2) {
                 uint32_t v[32];
                 const uint8_t *blk = smem + kOffQ + k * kQBlock;
 #pragma unroll
@@ -396,10 +428,6 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
         ok = __all_sync(0xffffffffu, issue_q(i0, 0));
         ok = ok && load_q_tmem();
         ok = ok && __all_sync(0xffffffffu, issue_q(i0, 1));
-        // Scores stay unscaled where the scale is positive: the row max then commutes with
-        // the scaling and each exponent argument is one fma.
-        const bool pos_scale = p.scale_log2 > 0.f;
-        const float cs = pos_scale ? p.scale_log2 : 1.f;
         for (int i = i0; i < i1 && ok; ++i) {
             const WorkItem it = p.work[i];
             const int L = p.seq_lens[it.b];
@@ -407,7 +435,7 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
             const int nt = (t1 - t0 + kTile - 1) / kTile;
             const int ns = steps_of(t0, t1);
             const int last_vis = L - p.q_len + (row_valid ? row_seq / p.s.H : 0);
-            float m_used = -CUDART_INF_F, l = 0.f;
+            float m_used = -CUDART_INF_F, l = 0.f;       // l: this half's share of the row sum
             bool bad_item = false;
             for (int t = 0; t < nt; ++t) bad_item |= block_of(p, it.b, t0 / kTile + t) < 0;
             for (int j = 0; j < ns && ok; ++j, ++K) {
@@ -417,83 +445,69 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
                 }
                 tc_fence_after();
                 if (tid == 128) WTRACE(8, K);
-                const int n_vis = row_valid ? max(0, min(t1, last_vis + 1) - (t0 + j * kStep)) : 0;
-                const bool plain = pos_scale && __all_sync(0xffffffffu, n_vis >= kStep);
-                // hidden slots -> -inf
-                auto mask = [&](uint32_t (&sv)[32], int c) {
+                uint32_t sv[64];
+                TMEM_LD32(lane_addr + kColS + 64 * hs, sv);
+                TMEM_LD32(lane_addr + kColS + 64 * hs + 32, (sv + 32));
+                tmem_wait_ld();
+                const int tile_start = t0 + j * kStep + kTile * hs;
+                const int n_vis = row_valid ? max(0, min(t1, last_vis + 1) - tile_start) : 0;
+                // Scores stay unscaled where the scale is positive: the row max then commutes
+                // with the scaling and each exponent argument is one fma. Hidden slots -> -inf.
+                const bool pos_scale = p.scale_log2 > 0.f;
+                const float cs = pos_scale ? p.scale_log2 : 1.f;
+                if (!pos_scale || __any_sync(0xffffffffu, n_vis < kTile)) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const float v = pos_scale ? __uint_as_float(sv[e]) : __uint_as_float(sv[e]) * p.scale_log2;
-                        sv[e] = __float_as_uint(32 * c + e < n_vis ? v : -CUDART_INF_F);
+                    for (int jj = 0; jj < 64; ++jj) {
+                        const float v = pos_scale ? __uint_as_float(sv[jj]) : __uint_as_float(sv[jj]) * p.scale_log2;
+                        sv[jj] = __float_as_uint(jj < n_vis ? v : -CUDART_INF_F);
                     }
-                };
-                float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
-                auto max_of = [&](uint32_t (&sv)[32], int c) {
-                    if (!plain) mask(sv, c);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(sv[e]));
-                };
-                // (loops of two chunks, not unrolled: with every role's code laid out straight the
-                // warps waited for instructions more than for anything else)
-                uint32_t s0[32], s1[32];
-                TMEM_LD32(tS, s0);
-#pragma unroll 1
-                for (int c = 0; c < 4; c += 2) {
-                    tmem_wait_ld(s0);
-                    TMEM_LD32(tS + 32 * c + 32, s1);
-                    max_of(s0, c);
-                    tmem_wait_ld(s1);
-                    TMEM_LD32(tS + ((32 * c + 64) & 127), s0);     // at the end chunk 0 again
-                    max_of(s1, c + 1);
                 }
-                const float m_new = fmaxf(m_used, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs);
+                float mx = -CUDART_INF_F;
+#pragma unroll
+                for (int jj = 0; jj < 64; ++jj) mx = fmaxf(mx, __uint_as_float(sv[jj]));
+                mx *= cs;
+                // the row's max over both halves; after it, both halves have read their S
+                // columns, so P may be stored over them
+                {
+                    float other = -CUDART_INF_F;
+                    if (!__all_sync(0xffffffffu, exchange(mx, other))) { ok = false; break; }
+                    mx = fmaxf(mx, other);
+                }
                 if (tid == 128) WTRACE(9, K);
                 float alpha = 1.f;
                 bool rescale = false;
+                const float m_new = fmaxf(m_used, mx);
                 if (m_new > m_used + 8.f) {
                     alpha = exp2f(m_used - m_new);        // 0 when nothing was accumulated yet
                     m_used = m_new;
                     rescale = j > 0;
                 }
                 const float nmb = m_used == -CUDART_INF_F ? -CUDART_INF_F : -m_used;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                // weights of columns 32 c .. 32 c + 31, in place (16 registers), over the first
-                // columns of chunk c / 2, which have been read
-                auto weights = [&](uint32_t (&sv)[32], int c) {
-                    if (!plain) mask(sv, c);
+                float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float a = ex2(fmaf(__uint_as_float(sv[2 * e]), cs, nmb));
-                        const float b = ex2(fmaf(__uint_as_float(sv[2 * e + 1]), cs, nmb));
-                        const __nv_bfloat162 hh = __floats2bfloat162_rn(a, b);
-                        sv[e] = *(const uint32_t *)&hh;
-                        sum[(2 * e) & 3] += a;     // fp32 row sum: the LSE does not see the rounding of P
-                        sum[(2 * e + 1) & 3] += b;
-                    }
-                    TMEM_ST16(tS + 16 * c, sv);
-                };
-#pragma unroll 1
-                for (int c = 0; c < 4; c += 2) {
-                    tmem_wait_ld(s0);
-                    TMEM_LD32(tS + 32 * c + 32, s1);
-                    weights(s0, c);
-                    tmem_wait_ld(s1);
-                    if (c == 0) TMEM_LD32(tS + 64, s0);
-                    weights(s1, c + 1);
+                for (int jj = 0; jj < 32; ++jj) {
+                    const float a = ex2(fmaf(__uint_as_float(sv[2 * jj]), cs, nmb));
+                    const float c = ex2(fmaf(__uint_as_float(sv[2 * jj + 1]), cs, nmb));
+                    const __nv_bfloat162 hh = __floats2bfloat162_rn(a, c);
+                    sv[jj] = *(const uint32_t *)&hh;        // in place: scores 2 jj, 2 jj + 1 are done with
+                    sum0 += a;             // fp32 row sum: the LSE does not see the rounding of P
+                    sum1 += c;
                 }
-                l = l * alpha + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+                l = l * alpha + (sum0 + sum1);
                 // O *= alpha: the previous step's PV completed before these scores were
                 // computed (the MMA thread issues a step's score MMAs after it)
                 if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll 1
-                    for (int c = 0; c < 8; ++c) {
-                        TMEM_LD32(lane_addr + kColO + 32 * c, s0);
-                        tmem_wait_ld(s0);
+                    for (int c = 4 * hs; c < 4 * hs + 4; ++c) {
+                        uint32_t ov[32];
+                        TMEM_LD32(lane_addr + kColO + 32 * c, ov);
+                        tmem_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) s0[k] = __float_as_uint(__uint_as_float(s0[k]) * alpha);
-                        TMEM_ST32(lane_addr + kColO + 32 * c, s0);
+                        for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * alpha);
+                        TMEM_ST32(lane_addr + kColO + 32 * c, ov);
                     }
                 }
+                TMEM_ST32(lane_addr + kColS + 32 * hs, sv);
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&bars->p_full);
@@ -506,6 +520,9 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
             const bool have_next = i + 1 < i1;
             if (ok && have_next) ok = __all_sync(0xffffffffu, issue_q(i + 1, 0));
             if (ok && ns > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars->pv_done, (K - 1) & 1, bars, p.status));
+            float l_other = 0.f;
+            if (ok) ok = __all_sync(0xffffffffu, exchange(l, l_other));
+            const float l_row = l + l_other;
             tc_fence_after();
             if (ok && have_next) ok = load_q_tmem();
             if (ok && have_next)
@@ -515,19 +532,24 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
             // (128B-swizzled) through the region, one TMA store each; rows past the
             // sequence's rows are clipped by the tensor map.
             if (ok) {
-                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const float inv = l_row > 0.f ? 1.f / l_row : 0.f;
                 const uint64_t keep = l2_policy_evict_last();
-                uint8_t *boxes = smem + kOffQ + 4 * wq * kEpiBoxBytes;
+                uint8_t *boxes = smem + kOffQ + (warp - 4) * kEpiBoxes * kEpiBoxBytes;
                 const int y = g * kRows + 32 * wq;
                 const bool store = y < rows_seq;
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint8_t *box = boxes + c * kEpiBoxBytes;
+                for (int c = 0; c < 2; ++c) {
+                    const int bi = c % kEpiBoxes;
+                    if (bi == 0 && c > 0) {
+                        if (lane == 0) bulk_wait_read();
+                        __syncwarp();
+                    }
+                    uint8_t *box = boxes + bi * kEpiBoxBytes;
 #pragma unroll 1
                     for (int hh = 0; hh < 2; ++hh) {
                         uint32_t ov[32];
-                        TMEM_LD32(lane_addr + kColO + 64 * c + 32 * hh, ov);
-                        tmem_wait_ld(ov);
+                        TMEM_LD32(lane_addr + kColO + 128 * hs + 64 * c + 32 * hh, ov);
+                        tmem_wait_ld();
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             uint32_t pk4[4];
@@ -543,7 +565,7 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
                     fence_proxy_async();
                     __syncwarp();
                     if (lane == 0 && store) {
-                        tma_store_3d_hint(&o_map, box, 256 * half + 64 * c, y, i, keep);
+                        tma_store_3d_hint(&o_map, box, 256 * half + 128 * hs + 64 * c, y, i, keep);
                         bulk_commit();
                     }
                 }
@@ -552,35 +574,82 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
             }
             mbar_arrive(&bars->qreg_free);
             ++uses;
-            if (row_valid && half == 0)
+            if (row_valid && half == 0 && hs == 0)
                 p.part_lse[(size_t)i * rows_seq + row_seq] =
-                    bad ? CUDART_NAN_F : (l > 0.f ? m_used + log2f(l) : -CUDART_INF_F);
+                    bad ? CUDART_NAN_F : (l_row > 0.f ? m_used + log2f(l_row) : -CUDART_INF_F);
             tc_fence_before();     // O reads complete before the next item's first PV
             if (ok && have_next) ok = __all_sync(0xffffffffu, issue_q(i + 1, 1));
         }
         if (lane == 0) bulk_wait_all();   // this warp's output stores have landed
-    } else {
+    } else if (warp >= 12) {
         // ================================================= expansion of the codes
-        // Warp e takes rows 8 e .. 8 e + 7 of both tiles, four rows and a 128-byte line of
-        // each (two 64-dim column blocks) at a time. Eight lanes take 16 codes each: four of
-        // one row's first block and four of the neighbouring row's second, so that their
-        // 16-byte stores fall on eight different swizzled chunks.
-        const int e = warp < 4 ? warp - 2 : warp - 6, p8 = lane & 7;
+        reg_dec<kRegsExpand>();
+        // Warp e takes rows 8 e .. 8 e + 7 of a tile, four rows and a 128-byte line of each
+        // (two 64-dim column blocks) at a time. Eight lanes take 16 codes each: four of one
+        // row's first block and four of the neighbouring row's second, so that their 16-byte
+        // stores fall on eight different swizzled chunks.
+        const int e = warp - 12, p8 = lane & 7;
         const bool second = p8 >= 4;
         const int r4 = (lane >> 3) ^ (second ? 1 : 0);
-        // a lane's first chunk and the shared address of its row of the first 8-row atom
+        // a lane's first chunk and the shared address of its row of the warp's 8-row atom
         const uint32_t chunk = (uint32_t)((2 * (p8 & 3)) ^ r4) << 4;
         const uint32_t to0 = smem_u32(smem + kOffBuf) + (second ? kCol : 0u) + 1024u * e + 128u * r4;
-        struct Half {                      // of a step: the score-only or the own dims
-            uint4 c[2][2][2];              // [tile][row group][column block pair]
-            uint2 s[2][2];                 // the row's eight scales of these dims
+        struct Rows {                      // a lane's codes of one tile, the score-only or the own dims
+            uint4 c[2][2];                 // [row 4 q + r4][column block pair]
+            uint2 s[2];                    // the row's eight scales of these dims
         };
         struct Step {
             int row0[2], valid[2];         // token row of each tile's first slot; its tokens
         };
-        auto step_at = [&](const WorkItem &it, int L, int j) {
-            Step st;
-            const int nt = (it.t1 - it.t0 + kTile - 1) / kTile;
+        auto load = [&](Rows &x, int row0, int valid, int cb) {          // column blocks cb .. cb + 3
+            const int row = 8 * e + r4;
+            const size_t tok = (size_t)(row0 + row);
+            const uint8_t *src = p.codes + tok * 512 + 64 * cb + 16 * p8;
+            const uint8_t *scl = p.mx_scale + tok * 16 + 2 * cb;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                x.s[q] = make_uint2(0, 0);
+                x.c[q][0] = x.c[q][1] = make_uint4(0, 0, 0, 0);          // zeros for slots past the end
+                if (row + 4 * q < valid) {
+#pragma unroll
+                    for (int w = 0; w < 2; ++w)
+                        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(x.c[q][w].x), "=r"(x.c[q][w].y), "=r"(x.c[q][w].z), "=r"(x.c[q][w].w)
+                                     : "l"(src + 2048 * q + 128 * w));
+                    asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(x.s[q].x), "=r"(x.s[q].y) : "l"(scl + 64 * q));
+                }
+            }
+        };
+        auto expand = [&](const Rows &x, uint32_t to) {
+            // scales up to 1 take one multiplication
+            const uint32_t any = x.s[0].x | x.s[0].y | x.s[1].x | x.s[1].y;
+            const bool small = !__any_sync(0xffffffffu, any & 0x80808080u);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const uint32_t sw = w ? x.s[q].y : x.s[q].x;
+                    uint4 o0, o1;
+                    if (small) mx_expand16(x.c[q][w], mx_scale120(sw, p8 >> 1), o0, o1);
+                    else mx_expand16(x.c[q][w], kMx2p120, mx_scale_bf162((sw >> (8 * (p8 >> 1))) & 0xffu), o0, o1);
+                    // row 4 q + r4 of the warp's atom flips bit 2 of the chunk with q
+                    const uint32_t at = to + 512u * q + 2u * w * kCol;
+                    st_shared16(at + (chunk ^ (64u * q)), o0);
+                    st_shared16(at + (chunk ^ (64u * q) ^ 16u), o1);
+                }
+        };
+        // The steps in turn; false at the end.
+        int i = i0, j = -1;
+        WorkItem it = p.work[i];
+        int L = p.seq_lens[it.b], nt = (it.t1 - it.t0 + kTile - 1) / kTile;
+        auto next = [&](Step &st) {
+            if (2 * ++j >= nt) {
+                j = 0;
+                if (++i >= i1) return false;
+                it = p.work[i];
+                L = p.seq_lens[it.b];
+                nt = (it.t1 - it.t0 + kTile - 1) / kTile;
+            }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int t = 2 * j + u;
@@ -588,106 +657,48 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
                 st.row0[u] = blk * kTile;
                 st.valid[u] = blk >= 0 ? min(kTile, L - (it.t0 + t * kTile)) : 0;
             }
-            return st;
-        };
-        auto load = [&](Half &x, const Step &st, int cb) {     // column blocks cb .. cb + 3
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int row = 8 * e + 4 * q + r4;
-                    x.s[u][q] = make_uint2(0, 0);
-                    x.c[u][q][0] = x.c[u][q][1] = make_uint4(0, 0, 0, 0);    // zeros for slots past the end
-                    if (row < st.valid[u]) {
-                        const size_t tok = (size_t)(st.row0[u] + row);
-                        const uint8_t *src = p.codes + tok * 512 + 64 * cb + 16 * p8;
-#pragma unroll
-                        for (int w = 0; w < 2; ++w)
-                            asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(x.c[u][q][w].x), "=r"(x.c[u][q][w].y), "=r"(x.c[u][q][w].z), "=r"(x.c[u][q][w].w)
-                                         : "l"(src + 128 * w));
-                        asm volatile("ld.global.v2.u32 {%0, %1}, [%2];"
-                                     : "=r"(x.s[u][q].x), "=r"(x.s[u][q].y)
-                                     : "l"(p.mx_scale + tok * 16 + 2 * cb));
-                    }
-                }
-        };
-        auto expand = [&](const Half &x, int cb) {
-            // scales up to 1 take one multiplication
-            const uint32_t any = x.s[0][0].x | x.s[0][0].y | x.s[0][1].x | x.s[0][1].y | x.s[1][0].x | x.s[1][0].y |
-                                 x.s[1][1].x | x.s[1][1].y;
-            const bool small = !__any_sync(0xffffffffu, any & 0x80808080u);
-            const uint32_t to = to0 + (uint32_t)cb * kCol;
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-#pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        const uint32_t sw = w ? x.s[u][q].y : x.s[u][q].x;
-                        uint4 o0, o1;
-                        if (small) mx_expand16(x.c[u][q][w], mx_scale120(sw, p8 >> 1), o0, o1);
-                        else mx_expand16(x.c[u][q][w], kMx2p120, mx_scale_bf162((sw >> (8 * (p8 >> 1))) & 0xffu), o0, o1);
-                        // row 4 q + r4 of the atom flips bit 2 of the chunk with q
-                        const uint32_t at = to + (chunk ^ (64u * q)) + 512u * q + 8192u * u + 2u * w * kCol;
-                        const uint32_t at1 = to + (chunk ^ (64u * q) ^ 16u) + 512u * q + 8192u * u + 2u * w * kCol;
-                        st_shared16(at, o0);
-                        st_shared16(at1, o1);
-                    }
-        };
-        const int cb_a = 4 * (1 - half), cb_v = 4 * half;
-        // The steps in turn; false at the end.
-        int i = i0, j = -1;
-        WorkItem it = p.work[i];
-        int L = p.seq_lens[it.b], ns = steps_of(it.t0, it.t1);
-        auto next = [&](Step &st) {
-            if (++j == ns) {
-                j = 0;
-                if (++i >= i1) return false;
-                it = p.work[i];
-                L = p.seq_lens[it.b];
-                ns = steps_of(it.t0, it.t1);
-            }
-            st = step_at(it, L, j);
             return true;
         };
-        // Turn K: step K's own dims, then step K + 1's score-only ones, then the loads for the next
-        // turn, all at once: they have the time until the next P . V is done to arrive (a
-        // load issued shortly before a batch is used holds that up, too: loads share the few
-        // counters that a use waits for).
-        Step s0, s1, s2;                   // of K, K + 1, K + 2
-        Half x, a;                         // own dims of K, score-only ones of K + 1
-        bool more = next(s0);
-        load(x, s0, cb_a);
-        // turn -1 is step 0's score-only part; one copy of the expansion for both parts
-        for (int K = -1;; ++K) {
-            bool ok = true;
+        // Parts in turn: step K's score-only dims, its own dims, step K + 1's score-only dims
+        // and so on. The loads of a part start when the part before it is expanded: the own
+        // dims' have the time until the step's P . V is done to arrive, the score-only ones'
+        // that until the own ones are needed again. The step after the next is looked up when
+        // the next one's loads have been issued.
+        Step s0, s1;                       // of K, K + 1
+        Rows x, y;                         // of tile 0 and tile 1
+        next(s0);
+        load(x, s0.row0[0], s0.valid[0], 4 * (1 - half));
+        load(y, s0.row0[1], s0.valid[1], 4 * (1 - half));
+        bool more = next(s1), ok = true;
+        for (int K = 0, own = 0; ok; own ^= 1) {
+            const uint32_t to = to0 + 4u * (half ^ 1 ^ own) * kCol;
+            // one copy of the code for both tiles
 #pragma unroll 1
-            for (int part = K < 0 ? 1 : 0; part < 2 && ok; ++part) {
-                uint64_t *free_bar = part ? &bars->empty_a : &bars->empty_v;
-                const int use = part ? K : K - 1;              // the step that used the blocks before
-                if (use >= 0 && !__all_sync(0xffffffffu, mbar_wait(free_bar, use & 1, bars, p.status))) {
-                    ok = false;
-                    break;
-                }
-                WTRACE_E(part ? 12 : 14);
-                expand(x, part ? cb_a : cb_v);
-                fence_proxy_async();
-                mbar_arrive(part ? &bars->full_a : &bars->full_v);
-                WTRACE_E(part ? 13 : 15);
-                if (part == 0) {
-                    if (!more) ok = false;                     // no step K + 1
-                    else x = a;
-                }
+            for (int u = 0; u < 2; ++u) {
+                // the tile's blocks are free: the score MMAs over them, or its half of P . V, are done
+                uint64_t *bar = own ? &bars->empty_v[u] : &bars->empty_a;
+                ok = K == 0 || (!own && u) || __all_sync(0xffffffffu, mbar_wait(bar, (K - 1) & 1, bars, p.status));
+                if (!ok) break;
+                WTRACE_E(own ? 14 : 12);
+                expand(x, to + 8192u * u);
+                if (u == 0) x = y;
             }
             if (!ok) break;
-            if (K < 0) s1 = s0;
-            load(x, s1, cb_v);
-            more = next(s2);
-            if (more) load(a, s2, cb_a);
-            s1 = s2;
+            fence_proxy_async();
+            mbar_arrive(own ? &bars->full_v : &bars->full_a);
+            WTRACE_E(own ? 15 : 13);
+            if (own) {
+                if (!more) break;
+                s0 = s1;
+                ++K;
+            }
+            load(x, s0.row0[0], s0.valid[0], 4 * (half ^ own));
+            load(y, s0.row0[1], s0.valid[1], 4 * (half ^ own));
+            if (own) more = next(s1);
         }
         __syncwarp();
+    } else {
+        reg_dec<kRegsIssue>();
     }
     tc_fence_before();
     __syncthreads();
@@ -753,6 +764,11 @@ cudaError_t launch_decode_mx(const DecodeParams &p, int32_t max_work, cudaStream
     cudaError_t e = cudaFuncSetAttribute(wmx::decode_mx_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)wmx::kSmemBytes);
     if (e != cudaSuccess) return e;
+    // the register split draws on what the launch has: refuse a build that has less
+    cudaFuncAttributes at;
+    e = cudaFuncGetAttributes(&at, wmx::decode_mx_kernel);
+    if (e != cudaSuccess) return e;
+    if (at.numRegs < wmx::kRegsLaunch) return cudaErrorInvalidConfiguration;
     dim3 grid(2, (rows_seq + wmx::kRows - 1) / wmx::kRows, p.streams);
     return launch_pdl(wmx::decode_mx_kernel, grid, dim3(wmx::kThreads), wmx::kSmemBytes, st, rope_map, q_map, o_map, p);
 }
