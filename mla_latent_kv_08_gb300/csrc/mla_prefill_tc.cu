@@ -184,7 +184,7 @@ expand_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_cons
 // sub-tile 1.
 //
 //   per step and sub-tile   S[128 x 128] = Q . K^T   12 x M128 N128 K16
-//                           P = 2^(S c - m)          a thread a row: no shuffles
+//                           P = 2^(S c - m)          two threads a row, 64 columns each
 //                           O[128 x 128] += P . V    8 x M128 N128 K16, P from tensor memory
 //
 // P (bf16) is stored over the scores it came from. The products of one sub-tile are
@@ -196,26 +196,54 @@ expand_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_cons
 // atoms), in the order of use, so that the copies run 1.6 steps ahead.
 // Tensor memory: S0, S1, O0, O1, 128 columns each.
 // ============================================================================
-constexpr int kThreads = 384;          // warp 0 TMA, 1 MMA, 4..7 and 8..11 softmax of sub-tiles 0 and 1
+constexpr int kThreads = 640;          // warp 0 TMA, 1 MMA, 4..11 and 12..19 softmax of sub-tiles 0 and 1
+constexpr int kSubThreads = 256;
+// Registers a thread of the first warpgroup (copies and MMA) and of the other four (softmax)
+// once they are split again: what the launch had, 5 x 96.
+constexpr int kRegsLaunch = 96, kRegsIssue = 64, kRegsSoftmax = 104;
+static_assert(kRegsIssue + 4 * kRegsSoftmax <= 5 * kRegsLaunch, "register split");
+template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 constexpr int kTileQ = 256;
 constexpr int kSlots = 8;
 constexpr int kPerStep = 5;            // slots a step takes: 3 key blocks, 2 value blocks
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffRing = 6 * kBlock;
 constexpr uint32_t kOffBar = kOffRing + kSlots * kBlock;
-constexpr uint32_t kSmemBytes = kOffBar + 256 + 1024;
+constexpr uint32_t kOffXchg = kOffBar + 512;             // [2 sub-tiles][2 halves][128 rows] bf16
+constexpr uint32_t kSmemBytes = kOffXchg + 1024 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 struct Bars {
     uint64_t q_full[2];
-    uint64_t full[kSlots], empty[kSlots];
+    uint64_t k_full[2], v_full[2];     // the key / value blocks of an even, odd step landed
+    uint64_t k_empty[2], v_empty[2];   // the sub-tiles' products over them are done
     uint64_t s_full[2];        // scores of the sub-tile's step are there (and its earlier P . V)
     uint64_t p_full[2];        // weights are stored
     uint64_t o_full[2];
+    uint64_t xchg_full[2][4];  // sub-tile, 32 rows: both halves of the rows wrote their maximum
+    uint64_t xchg_read[2][4];  // ... and read the other's
     uint32_t tmem_base;
     int32_t abort_flag;
 };
-static_assert(sizeof(Bars) <= 256, "barriers");
+static_assert(sizeof(Bars) <= 512, "barriers");
+
+// Pipeline timestamps for performance analysis, compiled only with -DMLA_TRACE: clock64 at
+// each hand-off of CTA (0, 0) for its first kTraceSteps steps. Product builds contain none
+// of it. Events, 8 s + : 0 weights seen, 1 values landed, 2 P . V issued, 3 keys landed, 4
+// scores issued (MMA), 5 scores seen, 6 maximum agreed, 7 weights stored (softmax)
+#ifdef MLA_TRACE
+constexpr int kTraceSteps = 64;
+__device__ long long g_pftrace[16][kTraceSteps];
+#define PTRACE(ev, step)                                                                  \
+    do {                                                                                  \
+        if (blockIdx.x == 0 && blockIdx.y == 0 && (step) < kTraceSteps) g_pftrace[ev][step] = clock64(); \
+    } while (0)
+#else
+#define PTRACE(ev, step) \
+    do {                 \
+    } while (0)
+#endif
 
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
     asm volatile(
@@ -260,12 +288,18 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bars->q_full[s], 1);
             mbar_init(&bars->s_full[s], 1);
-            mbar_init(&bars->p_full[s], 128);
+            mbar_init(&bars->p_full[s], kSubThreads);
             mbar_init(&bars->o_full[s], 1);
+            for (int q = 0; q < 4; ++q) {
+                mbar_init(&bars->xchg_full[s][q], 64);
+                mbar_init(&bars->xchg_read[s][q], 64);
+            }
         }
-        for (int s = 0; s < kSlots; ++s) {
-            mbar_init(&bars->full[s], 1);
-            mbar_init(&bars->empty[s], 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bars->k_full[s], 1);
+            mbar_init(&bars->v_full[s], 1);
+            mbar_init(&bars->k_empty[s], 1);
+            mbar_init(&bars->v_empty[s], 1);
         }
         bars->abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -285,146 +319,149 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         return mbar_wait_bounded(bar, parity, &bars->abort_flag, p.status, FLAG_TIMEOUT, kTimeoutNs);
     };
-    // slot, and phase of its use, of block i of the run of blocks
-    auto slot_of = [](int i) { return i & (kSlots - 1); };
-    auto phase_of = [](int i) { return (uint32_t)(i / kSlots) & 1u; };
+    // offset in the ring of block c of step j; phase of step j's barriers
+    auto slot_at = [](int j, int c) { return (uint32_t)((kPerStep * j + c) & (kSlots - 1)) * kBlock; };
+    auto phase_of = [](int j) { return (uint32_t)(j >> 1) & 1u; };
 
     if (warp == 0) {
         // ================================================= copies
+        reg_dec<kRegsIssue>();
         if (lane == 0) {
-            int issued = 0, q_issued = 0;
             const int row0 = p.kv_off[b];
             const int kv0 = hl * p.cap_rows + row0;           // fits: the pass's rows are counted in 32 bits
+            int q_issued = 0, k_issued = 0, v_issued = 0;
             auto load_q = [&](int s) {
                 mbar_expect_tx(&bars->q_full[s], 3 * kBlock);
                 for (int c = 0; c < 3; ++c)
                     tma_load_3d(smem + kOffQ + (3 * s + c) * kBlock, &q_map, 64 * c, h, (int)qrow0 + 128 * s, &bars->q_full[s]);
                 ++q_issued;
             };
-            bool ok = true;
             load_q(0);
-            for (int j = 0; j < steps && ok; ++j) {
-                for (int c = 0; c < kPerStep; ++c, ++issued) {
-                    const int s = slot_of(issued);
-                    if (issued >= kSlots && !wait(&bars->empty[s], phase_of(issued - kSlots))) { ok = false; break; }
-                    uint8_t *dst = smem + kOffRing + s * kBlock;
-                    mbar_expect_tx(&bars->full[s], kBlock);
-                    if (c < 2) {
-                        tma_load_2d(dst, &k_map, 64 * c, kv0 + 128 * j, &bars->full[s]);
-                    } else if (c == 2) {
-                        tma_load_2d(dst, &rope_map, kR, row0 + 128 * j, &bars->full[s]);
-                    } else {
-                        const int y = kv0 + 128 * j + 64 * (c - 3);
-                        tma_load_2d(dst, &v_map, 0, y, &bars->full[s]);
-                        tma_load_2d(dst + kBlock / 2, &v_map, 64, y, &bars->full[s]);
-                    }
-                    if (j == 0 && c == 2 && subs == 2) load_q(1);
+            for (int j = 0; j < steps; ++j) {
+                // Step j's key blocks take the slots of step j - 2's last key block (released
+                // before its barrier was waited for below) and its value blocks; the value
+                // blocks those of step j - 1's first two key blocks.
+                uint64_t *bar = &bars->k_full[j & 1];
+                if (j > 1 && !wait(&bars->v_empty[j & 1], phase_of(j - 2))) break;
+                mbar_expect_tx(bar, 3 * kBlock);
+                tma_load_2d(smem + kOffRing + slot_at(j, 0), &k_map, 0, kv0 + 128 * j, bar);
+                tma_load_2d(smem + kOffRing + slot_at(j, 1), &k_map, 64, kv0 + 128 * j, bar);
+                tma_load_2d(smem + kOffRing + slot_at(j, 2), &rope_map, kR, row0 + 128 * j, bar);
+                ++k_issued;
+                if (j == 0 && subs == 2) load_q(1);
+                if (j > 0 && !wait(&bars->k_empty[(j - 1) & 1], phase_of(j - 1))) break;
+                bar = &bars->v_full[j & 1];
+                mbar_expect_tx(bar, 2 * kBlock);
+                for (int c = 0; c < 2; ++c) {
+                    uint8_t *dst = smem + kOffRing + slot_at(j, 3 + c);
+                    const int y = kv0 + 128 * j + 64 * c;
+                    tma_load_2d(dst, &v_map, 0, y, bar);
+                    tma_load_2d(dst + kBlock / 2, &v_map, 64, y, bar);
                 }
+                ++v_issued;
             }
             // never leave a copy in flight into this CTA's shared memory
             for (int s = 0; s < q_issued; ++s) mbar_drain(&bars->q_full[s], 0);
-            for (int i = max(0, issued - kSlots); i < issued; ++i) mbar_drain(&bars->full[slot_of(i)], phase_of(i));
+            for (int j = max(0, k_issued - 2); j < k_issued; ++j) mbar_drain(&bars->k_full[j & 1], phase_of(j));
+            for (int j = max(0, v_issued - 2); j < v_issued; ++j) mbar_drain(&bars->v_full[j & 1], phase_of(j));
         }
         __syncwarp();
     } else if (warp == 1) {
         // ================================================= products: lane 0 alone
+        // One thread for both sub-tiles, in turn: with a thread each, their products ran side
+        // by side, both sub-tiles' scores came at the same time, and the tensor cores waited
+        // while both softmaxes ran.
+        reg_dec<kRegsIssue>();
         if (lane == 0) {
             constexpr uint32_t kIdS = idesc_bf16(128, 128, false), kIdO = idesc_bf16(128, 128, true);
-            const uint32_t ring = smem_u32(smem + kOffRing), qs = smem_u32(smem + kOffQ);
-            // the blocks [i, i + count) have landed
-            auto landed = [&](int i, int count) {
-                for (int c = 0; c < count; ++c)
-                    if (!wait(&bars->full[slot_of(i + c)], phase_of(i + c))) return false;
-                return true;
-            };
+            const uint32_t ring = smem_u32(smem + kOffRing);
+            const uint64_t qd = sdesc(smem_u32(smem + kOffQ), 16, 1024);
+            const int last = subs - 1;
             auto scores = [&](int s, int j) {
-                tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < 3; ++c) {
-                    const uint64_t a = sdesc(qs + (3 * s + c) * kBlock, 16, 1024);
-                    const uint64_t k = sdesc(ring + slot_of(kPerStep * j + c) * kBlock, 16, 1024);
+                    const uint64_t a = qd + (uint64_t)((3 * s + c) * (kBlock >> 4));
+                    const uint64_t k = sdesc(ring + slot_at(j, c), 16, 1024);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) mma_ss(tmem + 128 * s, a + 2 * e, k + 2 * e, kIdS, (c > 0 || e > 0) ? 1u : 0u);
+                    for (int e = 0; e < 4; ++e) {
+                        if (c == 0 && e == 0) mma_ss_k<kIdS, 0>(tmem + 128 * s, a, k);
+                        else mma_ss_k<kIdS, 1>(tmem + 128 * s, a + 2 * e, k + 2 * e);
+                    }
                 }
                 mma_commit(&bars->s_full[s]);
+                if (s == last) mma_commit(&bars->k_empty[j & 1]);
             };
-            auto values = [&](int s, int j) {
-                tc_fence_after();
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    // MN-major: 64-column atoms 8 KB apart, 8-token groups 1 KB apart
-                    const uint64_t v = sdesc(ring + slot_of(kPerStep * j + 3 + c) * kBlock, kBlock / 2, 1024);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        mma_ts(tmem + 256 + 128 * s, tmem + 128 * s + 32 * c + 8 * e, v + 128 * e, kIdO,
-                               (j > 0 || c > 0 || e > 0) ? 1u : 0u);
-                }
-            };
-            auto release = [&](int i, int count) {
-                for (int c = 0; c < count; ++c) mma_commit(&bars->empty[slot_of(i + c)]);
-            };
-            bool ok = true;
-            const int last = subs - 1;
+            bool ok = wait(&bars->k_full[0], 0);
             for (int s = 0; s < subs && ok; ++s) {
-                ok = wait(&bars->q_full[s], 0) && landed(0, 3);
-                if (!ok) break;
-                scores(s, 0);
+                ok = wait(&bars->q_full[s], 0);
+                tc_fence_after();
+                if (ok) scores(s, 0);
             }
-            if (ok) release(0, 3);
             for (int j = 0; j < steps && ok; ++j) {
+                // the blocks first (they are usually there), so that after the weights' barrier
+                // nothing stands before the products
+                ok = wait(&bars->v_full[j & 1], phase_of(j)) &&
+                     (j + 1 == steps || wait(&bars->k_full[(j + 1) & 1], phase_of(j + 1)));
+#pragma unroll 1
                 for (int s = 0; s < subs && ok; ++s) {
                     const int mine = s == 0 ? steps0 : steps1;
                     if (j >= mine) continue;
-                    ok = wait(&bars->p_full[s], j & 1) && landed(kPerStep * j + 3, 2);
+                    PTRACE(8 * s + 1, j);
+                    ok = wait(&bars->p_full[s], j & 1);
                     if (!ok) break;
-                    values(s, j);
-                    if (s == last) release(kPerStep * j + 3, 2);
-                    if (j + 1 == mine) mma_commit(&bars->o_full[s]);
-                    if (j + 1 < mine) {
-                        ok = landed(kPerStep * (j + 1), 3);
-                        if (!ok) break;
-                        scores(s, j + 1);
+                    PTRACE(8 * s, j);
+                    tc_fence_after();
+                    const uint32_t tS = tmem + 128 * s, tO = tmem + 256 + 128 * s;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        // MN-major: 64-column atoms 8 KB apart, 8-token groups 1 KB apart
+                        const uint64_t v = sdesc(ring + slot_at(j, 3 + c), kBlock / 2, 1024);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            mma_ts(tO, tS + 32 * c + 8 * e, v + 128 * e, kIdO, (j > 0 || c > 0 || e > 0) ? 1u : 0u);
                     }
-                    if (s == last && j + 1 < steps) release(kPerStep * (j + 1), 3);
+                    if (s == last) mma_commit(&bars->v_empty[j & 1]);
+                    PTRACE(8 * s + 2, j);
+                    if (j + 1 < mine) scores(s, j + 1);
+                    else mma_commit(&bars->o_full[s]);
+                    PTRACE(8 * s + 4, j);
                 }
             }
-            if (ok) {
-                wait(&bars->o_full[last], 0);
-            } else {
-                // products in flight must end before the tensor memory is given back
-                mma_commit(&bars->o_full[last]);
-                mbar_drain(&bars->o_full[last], 0);
-            }
+            // products in flight must end before the tensor memory is given back
+            if (!ok) mma_commit(&bars->o_full[last]);
+            mbar_drain(&bars->o_full[last], 0);
         }
         __syncwarp();
     } else if (warp >= 4) {
         // ================================================= softmax and output
-        const int s = (warp - 4) >> 2, wq = warp & 3;
+        reg_inc<kRegsSoftmax>();
+        // warp w: sub-tile s, rows 32*wq..+31 (its tensor-memory lanes), half hs of the step's
+        // tokens: score columns 64*hs..+63, weight columns 32*hs..+31
+        const int s = (warp - 4) >> 3, hs = ((warp - 4) >> 2) & 1, wq = warp & 3;
         const int row = 32 * wq + lane;                        // of the sub-tile
         const int mine = s == 0 ? steps0 : steps1;
-        const int i = i0 + 128 * s + row;                      // of the sequence's new tokens
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * wq) << 16);
         const uint32_t tS = lane_addr + 128 * s, tO = lane_addr + 256 + 128 * s;
-        const int seen = L - n + min(i, n - 1) + 1;            // tokens this row sees
+        // tokens of this half of the steps that the row sees, from the first step on
+        int vis = L - n + min(i0 + 128 * s + row, n - 1) + 1 - 64 * hs;
         // where the scale is positive the maximum commutes with it: one fma per exponent
         const bool pos_scale = p.scale > 0.f;
         const float c2 = p.scale * kLog2e, cs = pos_scale ? c2 : 1.f;
+        __nv_bfloat16 *xchg = (__nv_bfloat16 *)(smem + kOffXchg) + 256 * s;
         float m = -CUDART_INF_F, l = 0.f;
         bool ok = true;
-        for (int j = 0; j < mine; ++j) {
+        for (int j = 0; j < mine; ++j, vis -= 128) {
             ok = __all_sync(0xffffffffu, wait(&bars->s_full[s], j & 1));
             if (!ok) break;
             tc_fence_after();
-            uint32_t sv[128];
-            TMEM_LD32(tS, sv);
-            TMEM_LD32(tS + 32, (sv + 32));
-            TMEM_LD32(tS + 64, (sv + 64));
-            TMEM_LD32(tS + 96, (sv + 96));
+            if (hs == 0 && wq == 0 && lane == 0) PTRACE(8 * s + 5, j);
+            uint32_t sv[64];
+            TMEM_LD32(tS + 64 * hs, sv);
+            TMEM_LD32(tS + 64 * hs + 32, (sv + 32));
             tmem_wait_ld();
-            const int vis = seen - 128 * j;
-            if (!pos_scale || __any_sync(0xffffffffu, vis < 128)) {
+            if (!pos_scale || __any_sync(0xffffffffu, vis < 64)) {
 #pragma unroll
-                for (int e = 0; e < 128; ++e) {
+                for (int e = 0; e < 64; ++e) {
                     const float v = pos_scale ? __uint_as_float(sv[e]) : __uint_as_float(sv[e]) * c2;
                     sv[e] = __float_as_uint(e < vis ? v : -CUDART_INF_F);
                 }
@@ -433,8 +470,25 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
 #pragma unroll
             for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(sv[e]);
 #pragma unroll
-            for (int e = 4; e < 128; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(sv[e]));
-            const float m_new = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs);
+            for (int e = 4; e < 64; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(sv[e]));
+            // The row's maximum over both halves, each rounded to bf16: any m near the maximum
+            // will do as long as both halves take the same. After the exchange both have read
+            // their scores, so weights may be stored over them.
+            const __nv_bfloat16 mine16 = __float2bfloat16_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs);
+            if (j > 0) {
+                ok = __all_sync(0xffffffffu, wait(&bars->xchg_read[s][wq], (j - 1) & 1));
+                if (!ok) break;
+            }
+            xchg[128 * hs + row] = mine16;
+            tc_fence_before();
+            mbar_arrive(&bars->xchg_full[s][wq]);
+            ok = __all_sync(0xffffffffu, wait(&bars->xchg_full[s][wq], j & 1));
+            if (!ok) break;
+            tc_fence_after();
+            const float other = __bfloat162float(xchg[128 * (hs ^ 1) + row]);
+            mbar_arrive(&bars->xchg_read[s][wq]);
+            const float m_new = fmaxf(m, fmaxf(__bfloat162float(mine16), other));
+            if (hs == 0 && wq == 0 && lane == 0) PTRACE(8 * s + 6, j);
             float alpha = 1.f;
             bool rescale = false;
             if (m_new > m + 8.f) {
@@ -443,21 +497,21 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                 rescale = j > 0;
             }
             const float nm = m == -CUDART_INF_F ? -CUDART_INF_F : -m;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
-            for (int e = 0; e < 64; ++e) {
+            for (int e = 0; e < 32; ++e) {
                 const float x = ex2(fmaf(__uint_as_float(sv[2 * e]), cs, nm));
                 const float y = ex2(fmaf(__uint_as_float(sv[2 * e + 1]), cs, nm));
                 const __nv_bfloat162 w = __floats2bfloat162_rn(x, y);
-                sum[(2 * e) & 3] += x;             // unrounded: the denominator does not see P's rounding
-                sum[(2 * e + 1) & 3] += y;
+                sum0 += x;                         // unrounded: the denominator does not see P's rounding
+                sum1 += y;
                 sv[e] = *(const uint32_t *)&w;
             }
-            l = l * alpha + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+            l = l * alpha + (sum0 + sum1);
             // the scores' barrier says that the sub-tile's earlier P . V is done as well
             if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 2 * hs; c < 2 * hs + 2; ++c) {
                     uint32_t ov[32];
                     TMEM_LD32(tO + 32 * c, ov);
                     tmem_wait_ld();
@@ -466,24 +520,31 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                     TMEM_ST32(tO + 32 * c, ov);
                 }
             }
-            TMEM_ST32(tS, sv);
-            TMEM_ST32(tS + 32, (sv + 32));
+            TMEM_ST32(tS + 32 * hs, sv);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&bars->p_full[s]);
+            if (hs == 0 && wq == 0 && lane == 0) PTRACE(8 * s + 7, j);
         }
         if (ok && mine > 0) ok = __all_sync(0xffffffffu, wait(&bars->o_full[s], 0));
         ok = ok && __all_sync(0xffffffffu, *(volatile int32_t *)&bars->abort_flag == 0);
         if (mine > 0) {
             tc_fence_after();
-            // O / l through this warp's part of its sub-tile's Q blocks (read for the last time
-            // by the last scores), then rows of 256 bytes
-            uint8_t *stage = smem + kOffQ + 3 * s * kBlock + wq * 32 * 256;
+            // The rows' sums over both halves, through the sub-tile's Q blocks (read for the last
+            // time by the last scores); then O / l, 64 value columns a half, through the
+            // warp's part of them, and rows of 128 bytes.
+            uint8_t *area = smem + kOffQ + 3 * s * kBlock;
+            float *sums = (float *)(area + 8 * 4096);
+            sums[128 * hs + row] = l;
+            mbar_arrive(&bars->xchg_full[s][wq]);
+            ok = __all_sync(0xffffffffu, wait(&bars->xchg_full[s][wq], mine & 1)) && ok;
+            l += sums[128 * (hs ^ 1) + row];
+            uint8_t *stage = area + (4 * hs + wq) * 4096;
             const float inv = ok ? 1.f / l : CUDART_NAN_F;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 2; ++c) {
                 uint32_t ov[32];
-                TMEM_LD32(tO + 32 * c, ov);
+                TMEM_LD32(tO + 64 * hs + 32 * c, ov);
                 tmem_wait_ld();
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch) {
@@ -495,18 +556,20 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                         w[e] = *(const uint32_t *)&x;
                     }
                     // 16-byte chunks rotated by the row: no two lanes of a store on one bank
-                    *(uint4 *)(stage + lane * 256 + (((4 * c + ch) ^ (lane & 15)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *(uint4 *)(stage + lane * 128 + (((4 * c + ch) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
             __syncwarp();
             const int first = 128 * s + 32 * wq;               // of the tile
-            for (int rr = lane >> 4; rr < 32; rr += 2)
+            for (int rr = lane >> 3; rr < 32; rr += 4)
                 if (first + rr < rows_here)
-                    *(uint4 *)(out + ((qrow0 + first + rr) * H + h) * kDv + 8 * (lane & 15)) =
-                        *(const uint4 *)(stage + rr * 256 + (((lane & 15) ^ (rr & 15)) << 4));
-            if (p.lse && first + lane < rows_here)
+                    *(uint4 *)(out + ((qrow0 + first + rr) * H + h) * kDv + 64 * hs + 8 * (lane & 7)) =
+                        *(const uint4 *)(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+            if (p.lse && hs == 0 && first + lane < rows_here)
                 p.lse[(qrow0 + first + lane) * H + h] = ok ? (m + log2f(l)) * kLn2 : CUDART_NAN_F;
         }
+    } else {
+        reg_dec<kRegsIssue>();
     }
     tc_fence_before();
     __syncthreads();
@@ -577,9 +640,20 @@ cudaError_t launch_prefill_tc(const PrefillParams &p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(prefill_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (e != cudaSuccess) return e;
+    // the register split draws on what the launch has: refuse a build that has less
+    cudaFuncAttributes at;
+    e = cudaFuncGetAttributes(&at, prefill_tc_kernel);
+    if (e != cudaSuccess) return e;
+    if (at.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
     ex::expand_tc_kernel<<<dim3((p.cap_rows + 255) / 256, p.nh), ex::kThreads, ex::kSmemBytes, st>>>(rows, uk, uv, k_st, v_st, p);
     prefill_tc_kernel<<<dim3(p.num_q / kTileQ + p.B, p.nh), kThreads, kSmemBytes, st>>>(q, k_ld, v_ld, rows, p);
     return cudaGetLastError();
 }
 
 }  // namespace mla
+
+#ifdef MLA_TRACE
+extern "C" int mla_prefill_trace_read(long long *events) {
+    return (int)cudaMemcpyFromSymbol(events, mla::pf::g_pftrace, sizeof(mla::pf::g_pftrace));
+}
+#endif
