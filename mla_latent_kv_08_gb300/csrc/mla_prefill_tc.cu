@@ -196,12 +196,12 @@ expand_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_cons
 // atoms), in the order of use, so that the copies run 1.6 steps ahead.
 // Tensor memory: S0, S1, O0, O1, 128 columns each.
 // ============================================================================
-constexpr int kThreads = 640;          // warp 0 TMA, 1 MMA, 4..11 and 12..19 softmax of sub-tiles 0 and 1
-constexpr int kSubThreads = 256;
+constexpr int kThreads = 384;          // warp 0 TMA, 1 MMA, 4..11 and 12..19 softmax of sub-tiles 0 and 1
+constexpr int kSubThreads = 128;
 // Registers a thread of the first warpgroup (copies and MMA) and of the other four (softmax)
 // once they are split again: what the launch had, 5 x 96.
-constexpr int kRegsLaunch = 96, kRegsIssue = 64, kRegsSoftmax = 104;
-static_assert(kRegsIssue + 4 * kRegsSoftmax <= 5 * kRegsLaunch, "register split");
+constexpr int kRegsLaunch = 168, kRegsIssue = 72, kRegsSoftmax = 216;
+static_assert(kRegsIssue + 2 * kRegsSoftmax <= 3 * kRegsLaunch, "register split");
 template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 constexpr int kTileQ = 256;
@@ -435,33 +435,33 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     } else if (warp >= 4) {
         // ================================================= softmax and output
         reg_inc<kRegsSoftmax>();
-        // warp w: sub-tile s, rows 32*wq..+31 (its tensor-memory lanes), half hs of the step's
-        // tokens: score columns 64*hs..+63, weight columns 32*hs..+31
-        const int s = (warp - 4) >> 3, hs = ((warp - 4) >> 2) & 1, wq = warp & 3;
+        const int s = (warp - 4) >> 2, wq = warp & 3;
         const int row = 32 * wq + lane;                        // of the sub-tile
         const int mine = s == 0 ? steps0 : steps1;
+        const int i = i0 + 128 * s + row;                      // of the sequence's new tokens
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * wq) << 16);
         const uint32_t tS = lane_addr + 128 * s, tO = lane_addr + 256 + 128 * s;
-        // tokens of this half of the steps that the row sees, from the first step on
-        int vis = L - n + min(i0 + 128 * s + row, n - 1) + 1 - 64 * hs;
+        const int seen = L - n + min(i, n - 1) + 1;            // tokens this row sees
         // where the scale is positive the maximum commutes with it: one fma per exponent
         const bool pos_scale = p.scale > 0.f;
         const float c2 = p.scale * kLog2e, cs = pos_scale ? c2 : 1.f;
-        __nv_bfloat16 *xchg = (__nv_bfloat16 *)(smem + kOffXchg) + 256 * s;
         float m = -CUDART_INF_F, l = 0.f;
         bool ok = true;
-        for (int j = 0; j < mine; ++j, vis -= 128) {
+        for (int j = 0; j < mine; ++j) {
             ok = __all_sync(0xffffffffu, wait(&bars->s_full[s], j & 1));
             if (!ok) break;
             tc_fence_after();
-            if (hs == 0 && wq == 0 && lane == 0) PTRACE(8 * s + 5, j);
-            uint32_t sv[64];
-            TMEM_LD32(tS + 64 * hs, sv);
-            TMEM_LD32(tS + 64 * hs + 32, (sv + 32));
+            if (wq == 0 && lane == 0) PTRACE(8 * s + 5, j);
+            uint32_t sv[128];
+            TMEM_LD32(tS, sv);
+            TMEM_LD32(tS + 32, (sv + 32));
+            TMEM_LD32(tS + 64, (sv + 64));
+            TMEM_LD32(tS + 96, (sv + 96));
             tmem_wait_ld();
-            if (!pos_scale || __any_sync(0xffffffffu, vis < 64)) {
+            const int vis = seen - 128 * j;
+            if (!pos_scale || __any_sync(0xffffffffu, vis < 128)) {
 #pragma unroll
-                for (int e = 0; e < 64; ++e) {
+                for (int e = 0; e < 128; ++e) {
                     const float v = pos_scale ? __uint_as_float(sv[e]) : __uint_as_float(sv[e]) * c2;
                     sv[e] = __float_as_uint(e < vis ? v : -CUDART_INF_F);
                 }
@@ -470,25 +470,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
 #pragma unroll
             for (int e = 0; e < 4; ++e) mx[e] = __uint_as_float(sv[e]);
 #pragma unroll
-            for (int e = 4; e < 64; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(sv[e]));
-            // The row's maximum over both halves, each rounded to bf16: any m near the maximum
-            // will do as long as both halves take the same. After the exchange both have read
-            // their scores, so weights may be stored over them.
-            const __nv_bfloat16 mine16 = __float2bfloat16_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs);
-            if (j > 0) {
-                ok = __all_sync(0xffffffffu, wait(&bars->xchg_read[s][wq], (j - 1) & 1));
-                if (!ok) break;
-            }
-            xchg[128 * hs + row] = mine16;
-            tc_fence_before();
-            mbar_arrive(&bars->xchg_full[s][wq]);
-            ok = __all_sync(0xffffffffu, wait(&bars->xchg_full[s][wq], j & 1));
-            if (!ok) break;
-            tc_fence_after();
-            const float other = __bfloat162float(xchg[128 * (hs ^ 1) + row]);
-            mbar_arrive(&bars->xchg_read[s][wq]);
-            const float m_new = fmaxf(m, fmaxf(__bfloat162float(mine16), other));
-            if (hs == 0 && wq == 0 && lane == 0) PTRACE(8 * s + 6, j);
+            for (int e = 4; e < 128; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(sv[e]));
+            const float m_new = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs);
+            if (wq == 0 && lane == 0) PTRACE(8 * s + 6, j);
             float alpha = 1.f;
             bool rescale = false;
             if (m_new > m + 8.f) {
@@ -497,21 +481,21 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                 rescale = j > 0;
             }
             const float nm = m == -CUDART_INF_F ? -CUDART_INF_F : -m;
-            float sum0 = 0.f, sum1 = 0.f;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
+            for (int e = 0; e < 64; ++e) {
                 const float x = ex2(fmaf(__uint_as_float(sv[2 * e]), cs, nm));
                 const float y = ex2(fmaf(__uint_as_float(sv[2 * e + 1]), cs, nm));
                 const __nv_bfloat162 w = __floats2bfloat162_rn(x, y);
-                sum0 += x;                         // unrounded: the denominator does not see P's rounding
-                sum1 += y;
+                sum[(2 * e) & 3] += x;             // unrounded: the denominator does not see P's rounding
+                sum[(2 * e + 1) & 3] += y;
                 sv[e] = *(const uint32_t *)&w;
             }
-            l = l * alpha + (sum0 + sum1);
+            l = l * alpha + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
             // the scores' barrier says that the sub-tile's earlier P . V is done as well
             if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll 1
-                for (int c = 2 * hs; c < 2 * hs + 2; ++c) {
+                for (int c = 0; c < 4; ++c) {
                     uint32_t ov[32];
                     TMEM_LD32(tO + 32 * c, ov);
                     tmem_wait_ld();
@@ -520,31 +504,25 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                     TMEM_ST32(tO + 32 * c, ov);
                 }
             }
-            TMEM_ST32(tS + 32 * hs, sv);
+            TMEM_ST32(tS, sv);
+            TMEM_ST32(tS + 32, (sv + 32));
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&bars->p_full[s]);
-            if (hs == 0 && wq == 0 && lane == 0) PTRACE(8 * s + 7, j);
+            if (wq == 0 && lane == 0) PTRACE(8 * s + 7, j);
         }
         if (ok && mine > 0) ok = __all_sync(0xffffffffu, wait(&bars->o_full[s], 0));
         ok = ok && __all_sync(0xffffffffu, *(volatile int32_t *)&bars->abort_flag == 0);
         if (mine > 0) {
             tc_fence_after();
-            // The rows' sums over both halves, through the sub-tile's Q blocks (read for the last
-            // time by the last scores); then O / l, 64 value columns a half, through the
-            // warp's part of them, and rows of 128 bytes.
-            uint8_t *area = smem + kOffQ + 3 * s * kBlock;
-            float *sums = (float *)(area + 8 * 4096);
-            sums[128 * hs + row] = l;
-            mbar_arrive(&bars->xchg_full[s][wq]);
-            ok = __all_sync(0xffffffffu, wait(&bars->xchg_full[s][wq], mine & 1)) && ok;
-            l += sums[128 * (hs ^ 1) + row];
-            uint8_t *stage = area + (4 * hs + wq) * 4096;
+            // O / l through this warp's part of its sub-tile's Q blocks (read for the last time
+            // by the last scores), then rows of 256 bytes
+            uint8_t *stage = smem + kOffQ + 3 * s * kBlock + wq * 32 * 256;
             const float inv = ok ? 1.f / l : CUDART_NAN_F;
 #pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < 4; ++c) {
                 uint32_t ov[32];
-                TMEM_LD32(tO + 64 * hs + 32 * c, ov);
+                TMEM_LD32(tO + 32 * c, ov);
                 tmem_wait_ld();
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch) {
@@ -556,16 +534,16 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                         w[e] = *(const uint32_t *)&x;
                     }
                     // 16-byte chunks rotated by the row: no two lanes of a store on one bank
-                    *(uint4 *)(stage + lane * 128 + (((4 * c + ch) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *(uint4 *)(stage + lane * 256 + (((4 * c + ch) ^ (lane & 15)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
             __syncwarp();
             const int first = 128 * s + 32 * wq;               // of the tile
-            for (int rr = lane >> 3; rr < 32; rr += 4)
+            for (int rr = lane >> 4; rr < 32; rr += 2)
                 if (first + rr < rows_here)
-                    *(uint4 *)(out + ((qrow0 + first + rr) * H + h) * kDv + 64 * hs + 8 * (lane & 7)) =
-                        *(const uint4 *)(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
-            if (p.lse && hs == 0 && first + lane < rows_here)
+                    *(uint4 *)(out + ((qrow0 + first + rr) * H + h) * kDv + 8 * (lane & 15)) =
+                        *(const uint4 *)(stage + rr * 256 + (((lane & 15) ^ (rr & 15)) << 4));
+            if (p.lse && first + lane < rows_here)
                 p.lse[(qrow0 + first + lane) * H + h] = ok ? (m + log2f(l)) * kLn2 : CUDART_NAN_F;
         }
     } else {
