@@ -178,55 +178,99 @@ expand_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_cons
 }  // namespace ex
 
 // ============================================================================
-// Attention. A CTA takes up to 256 new tokens of one sequence for one head, as two
-// sub-tiles of 128 rows that go through the same 128-token steps of the cache in turn:
-// while one warpgroup turns sub-tile 0's scores into weights, the tensor cores work on
-// sub-tile 1.
+// Attention. A pair of CTAs (a cluster of two) takes up to 512 new tokens of one sequence
+// for one head, as two sub-tiles of 256 rows, CTA r of the pair holding 128 rows of each.
+// Both sub-tiles go through the same 128-token steps of the cache in turn: while one's
+// warpgroups turn scores into weights, the tensor cores work on the other.
 //
-//   per step and sub-tile   S[128 x 128] = Q . K^T   12 x M128 N128 K16
-//                           P = 2^(S c - m)          two threads a row, 64 columns each
-//                           O[128 x 128] += P . V    8 x M128 N128 K16, P from tensor memory
+//   per step and sub-tile   S[256 x 128] = Q . K^T   12 x M256 N128 K16 over both SMs
+//                           P = 2^(S c - m)          a thread a row: no shuffles
+//                           O[256 x 128] += P . V    8 x M256 N128 K16, P from tensor memory
 //
-// P (bf16) is stored over the scores it came from. The products of one sub-tile are
-// issued in order by one thread, so that the next scores overwrite P only once P . V has
+// The pair shares the second operand: CTA r copies the keys of tokens 64 r .. 64 r + 63 of a
+// step and value columns 64 r .. 64 r + 63, 40 KB a step instead of the 80 KB that a CTA on
+// its own needs. That leaves room for three steps in flight (a CTA on its own had 1.6, and
+// its tensor cores waited a quarter of the time for keys), halves the reads of L2, and takes
+// the scores' operands (6 KB an MMA and SM, not 8) below the bandwidth of shared memory.
+//
+// P (bf16) is stored over the scores it came from. The products of one sub-tile are issued
+// in order by one thread of CTA 0, so that the next scores overwrite P only once P . V has
 // read it. m is raised lazily, only when it grows by more than 8 (P <= 2^8).
 //
-// Shared memory: Q 96 KB; a ring of eight 16 KB slots for the steps' three key blocks
-// ([128 tokens x 64 dims]) and two value blocks ([64 tokens x 128 dims], two 64-column
-// atoms), in the order of use, so that the copies run 1.6 steps ahead.
-// Tensor memory: S0, S1, O0, O1, 128 columns each.
+// Shared memory: Q 96 KB, three stages of key blocks ([64 tokens x 64 dims] each) and a value
+// block ([128 tokens x 64 columns]). Tensor memory: S0, S1, O0, O1, 128 columns each.
 // ============================================================================
-constexpr int kThreads = 384;          // warp 0 TMA, 1 MMA, 4..11 and 12..19 softmax of sub-tiles 0 and 1
-constexpr int kSubThreads = 128;
-// Registers a thread of the first warpgroup (copies and MMA) and of the other four (softmax)
-// once they are split again: what the launch had, 5 x 96.
+constexpr int kThreads = 384;          // warp 0 copies, 1 products (CTA 0), 4..7 and 8..11 softmax of sub-tiles 0 and 1
+// Registers a thread of the first warpgroup (copies and products) and of the other two
+// (softmax) once they are split again: what the launch had, 3 x 168.
 constexpr int kRegsLaunch = 168, kRegsIssue = 72, kRegsSoftmax = 216;
 static_assert(kRegsIssue + 2 * kRegsSoftmax <= 3 * kRegsLaunch, "register split");
 template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-constexpr int kTileQ = 256;
-constexpr int kSlots = 8;
-constexpr int kPerStep = 5;            // slots a step takes: 3 key blocks, 2 value blocks
+constexpr int kTileQ = 512;
+constexpr int kStages = 3;
+constexpr uint32_t kKBlock = 64 * 128;                  // 8 KB
+constexpr uint32_t kOffV = 3 * kKBlock;                 // of a stage
+constexpr uint32_t kStage = kOffV + kBlock;             // 40 KB
 constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffRing = 6 * kBlock;
-constexpr uint32_t kOffBar = kOffRing + kSlots * kBlock;
-constexpr uint32_t kOffXchg = kOffBar + 512;             // [2 sub-tiles][2 halves][128 rows] bf16
-constexpr uint32_t kSmemBytes = kOffXchg + 1024 + 1024;
+constexpr uint32_t kOffBar = kOffRing + kStages * kStage;
+constexpr uint32_t kSmemBytes = kOffBar + 512 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 struct Bars {
+    // of CTA 0: both CTAs' copies landed; both CTAs' weights are stored (a warp an arrival)
     uint64_t q_full[2];
-    uint64_t k_full[2], v_full[2];     // the key / value blocks of an even, odd step landed
-    uint64_t k_empty[2], v_empty[2];   // the sub-tiles' products over them are done
+    uint64_t k_full[kStages], v_full[kStages];
+    uint64_t p_full[2];
+    // of each CTA, from CTA 0's products
+    uint64_t k_empty[kStages], v_empty[kStages];
     uint64_t s_full[2];        // scores of the sub-tile's step are there (and its earlier P . V)
-    uint64_t p_full[2];        // weights are stored
     uint64_t o_full[2];
-    uint64_t xchg_full[2][4];  // sub-tile, 32 rows: both halves of the rows wrote their maximum
-    uint64_t xchg_read[2][4];  // ... and read the other's
     uint32_t tmem_base;
     int32_t abort_flag;
 };
 static_assert(sizeof(Bars) <= 512, "barriers");
+
+// ---- the pair: copies that report to CTA 0, products over both SMs ----------
+__device__ __forceinline__ void tma_pair_2d(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_u32(dst)), "l"((uint64_t)map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_pair_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(smem_u32(dst)), "l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+template <uint32_t IDESC, int ACC>
+__device__ __forceinline__ void mma2_ss(uint32_t d_tmem, uint64_t a, uint64_t b) {
+    asm volatile("tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, %4;" ::"r"(d_tmem), "l"(a), "l"(b), "n"(IDESC), "n"(ACC)
+                 : "memory");
+}
+__device__ __forceinline__ void mma2_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// Arrives, once the products issued so far are done, on this barrier of both CTAs.
+__device__ __forceinline__ void commit2(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     smem_u32(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+// An arrival on a barrier of either CTA of the pair. What it reports is in tensor memory,
+// complete (tcgen05.wait::st) and ordered by the tcgen05 fences on both sides; no other
+// memory hangs on it, so it needs no cluster-wide release (which took a thousand cycles and
+// more: it waits for every access of the thread).
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 
 // Pipeline timestamps for performance analysis, compiled only with -DMLA_TRACE: clock64 at
 // each hand-off of CTA (0, 0) for its first kTraceSteps steps. Product builds contain none
@@ -245,21 +289,14 @@ __device__ long long g_pftrace[16][kTraceSteps];
     } while (0)
 #endif
 
-__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-        ::"r"(smem_u32(dst)), "l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-        : "memory");
-}
-
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap rope_map,
                   const PrefillParams p) {
     // the last tiles of a sequence see the most: they start first
     const int tiles = p.tile_off[p.B];
-    if ((int)blockIdx.x >= tiles) return;
-    const int tile = tiles - 1 - (int)blockIdx.x;
+    if ((int)(blockIdx.x >> 1) >= tiles) return;         // both CTAs of a pair
+    const int tile = tiles - 1 - (int)(blockIdx.x >> 1), r = (int)cluster_ctarank();
     const int b = find_seq(p.tile_off, p.B, tile);
     const int hl = blockIdx.y, h = p.h0 + hl, H = p.s.H;
     const int n = p.cu_q[b + 1] - p.cu_q[b], i0 = (tile - p.tile_off[b]) * kTileQ;
@@ -268,16 +305,16 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     __nv_bfloat16 *out = (__nv_bfloat16 *)p.out;
     if (p.bad[b]) {
-        for (int e = tid; e < rows_here * kDv; e += kThreads)
+        for (int e = r * kThreads + tid; e < rows_here * kDv; e += 2 * kThreads)
             out[((qrow0 + e / kDv) * H + h) * kDv + e % kDv] = __float2bfloat16_rn(CUDART_NAN_F);
         if (p.lse)
-            for (int i = tid; i < rows_here; i += kThreads) p.lse[(qrow0 + i) * H + h] = CUDART_NAN_F;
+            for (int i = r * kThreads + tid; i < rows_here; i += 2 * kThreads) p.lse[(qrow0 + i) * H + h] = CUDART_NAN_F;
         return;
     }
     const int L = p.seq_lens[b];
     // steps of each sub-tile (0: it has no rows); sub-tile 1 never has fewer than sub-tile 0
-    const int subs = rows_here > 128 ? 2 : 1;
-    const int steps0 = (L - n + i0 + min(128, rows_here) + 127) / 128;
+    const int subs = rows_here > 256 ? 2 : 1;
+    const int steps0 = (L - n + i0 + min(256, rows_here) + 127) / 128;
     const int steps1 = subs == 2 ? (L - n + i0 + rows_here + 127) / 128 : 0;
     const int steps = max(steps0, steps1);
 
@@ -288,14 +325,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bars->q_full[s], 1);
             mbar_init(&bars->s_full[s], 1);
-            mbar_init(&bars->p_full[s], kSubThreads);
+            mbar_init(&bars->p_full[s], 8);
             mbar_init(&bars->o_full[s], 1);
-            for (int q = 0; q < 4; ++q) {
-                mbar_init(&bars->xchg_full[s][q], 64);
-                mbar_init(&bars->xchg_read[s][q], 64);
-            }
         }
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < kStages; ++s) {
             mbar_init(&bars->k_full[s], 1);
             mbar_init(&bars->v_full[s], 1);
             mbar_init(&bars->k_empty[s], 1);
@@ -306,22 +339,22 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         fence_proxy_async();
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&bars->tmem_base)),
                      "r"(512)
                      : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();                        // the other CTA's barriers and tensor memory are there
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         return mbar_wait_bounded(bar, parity, &bars->abort_flag, p.status, FLAG_TIMEOUT, kTimeoutNs);
     };
-    // offset in the ring of block c of step j; phase of step j's barriers
-    auto slot_at = [](int j, int c) { return (uint32_t)((kPerStep * j + c) & (kSlots - 1)) * kBlock; };
-    auto phase_of = [](int j) { return (uint32_t)(j >> 1) & 1u; };
+    // stage of step j, phase of its use
+    auto phase_of = [](int j) { return (uint32_t)(j / kStages) & 1u; };
 
     if (warp == 0) {
         // ================================================= copies
@@ -329,67 +362,65 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         if (lane == 0) {
             const int row0 = p.kv_off[b];
             const int kv0 = hl * p.cap_rows + row0;           // fits: the pass's rows are counted in 32 bits
-            int q_issued = 0, k_issued = 0, v_issued = 0;
+            auto leader = [&](uint64_t *bar) { return mapa(smem_u32(bar), 0); };
             auto load_q = [&](int s) {
-                mbar_expect_tx(&bars->q_full[s], 3 * kBlock);
+                if (r == 0) mbar_expect_tx(&bars->q_full[s], 6 * kBlock);
                 for (int c = 0; c < 3; ++c)
-                    tma_load_3d(smem + kOffQ + (3 * s + c) * kBlock, &q_map, 64 * c, h, (int)qrow0 + 128 * s, &bars->q_full[s]);
-                ++q_issued;
+                    tma_pair_3d(smem + kOffQ + (3 * s + c) * kBlock, &q_map, 64 * c, h, (int)qrow0 + 256 * s + 128 * r,
+                                leader(&bars->q_full[s]));
             };
+            int k_issued = 0, v_issued = 0;
             load_q(0);
             for (int j = 0; j < steps; ++j) {
-                // Step j's key blocks take the slots of step j - 2's last key block (released
-                // before its barrier was waited for below) and its value blocks; the value
-                // blocks those of step j - 1's first two key blocks.
-                uint64_t *bar = &bars->k_full[j & 1];
-                if (j > 1 && !wait(&bars->v_empty[j & 1], phase_of(j - 2))) break;
-                mbar_expect_tx(bar, 3 * kBlock);
-                tma_load_2d(smem + kOffRing + slot_at(j, 0), &k_map, 0, kv0 + 128 * j, bar);
-                tma_load_2d(smem + kOffRing + slot_at(j, 1), &k_map, 64, kv0 + 128 * j, bar);
-                tma_load_2d(smem + kOffRing + slot_at(j, 2), &rope_map, kR, row0 + 128 * j, bar);
+                const int st = j % kStages;
+                uint8_t *dst = smem + kOffRing + st * kStage;
+                if (j >= kStages && !wait(&bars->k_empty[st], phase_of(j - kStages))) break;
+                if (r == 0) mbar_expect_tx(&bars->k_full[st], 6 * kKBlock);
+                uint32_t bar = leader(&bars->k_full[st]);
+                tma_pair_2d(dst, &k_map, 0, kv0 + 128 * j + 64 * r, bar);
+                tma_pair_2d(dst + kKBlock, &k_map, 64, kv0 + 128 * j + 64 * r, bar);
+                tma_pair_2d(dst + 2 * kKBlock, &rope_map, kR, row0 + 128 * j + 64 * r, bar);
                 ++k_issued;
                 if (j == 0 && subs == 2) load_q(1);
-                if (j > 0 && !wait(&bars->k_empty[(j - 1) & 1], phase_of(j - 1))) break;
-                bar = &bars->v_full[j & 1];
-                mbar_expect_tx(bar, 2 * kBlock);
-                for (int c = 0; c < 2; ++c) {
-                    uint8_t *dst = smem + kOffRing + slot_at(j, 3 + c);
-                    const int y = kv0 + 128 * j + 64 * c;
-                    tma_load_2d(dst, &v_map, 0, y, bar);
-                    tma_load_2d(dst + kBlock / 2, &v_map, 64, y, bar);
-                }
+                if (j >= kStages && !wait(&bars->v_empty[st], phase_of(j - kStages))) break;
+                if (r == 0) mbar_expect_tx(&bars->v_full[st], 2 * kBlock);
+                tma_pair_2d(dst + kOffV, &v_map, 64 * r, kv0 + 128 * j, leader(&bars->v_full[st]));
                 ++v_issued;
             }
-            // never leave a copy in flight into this CTA's shared memory
-            for (int s = 0; s < q_issued; ++s) mbar_drain(&bars->q_full[s], 0);
-            for (int j = max(0, k_issued - 2); j < k_issued; ++j) mbar_drain(&bars->k_full[j & 1], phase_of(j));
-            for (int j = max(0, v_issued - 2); j < v_issued; ++j) mbar_drain(&bars->v_full[j & 1], phase_of(j));
+            // Never leave a copy in flight into the pair's shared memory: CTA 0 waits here for
+            // both CTAs' copies, CTA 1 for CTA 0 at the end.
+            if (r == 0) {
+                for (int s = 0; s < subs; ++s) mbar_drain(&bars->q_full[s], 0);
+                for (int j = max(0, k_issued - kStages); j < k_issued; ++j) mbar_drain(&bars->k_full[j % kStages], phase_of(j));
+                for (int j = max(0, v_issued - kStages); j < v_issued; ++j) mbar_drain(&bars->v_full[j % kStages], phase_of(j));
+            }
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ================================================= products: lane 0 alone
+        // ================================================= products: lane 0 of CTA 0 alone
         // One thread for both sub-tiles, in turn: with a thread each, their products ran side
         // by side, both sub-tiles' scores came at the same time, and the tensor cores waited
         // while both softmaxes ran.
         reg_dec<kRegsIssue>();
-        if (lane == 0) {
-            constexpr uint32_t kIdS = idesc_bf16(128, 128, false), kIdO = idesc_bf16(128, 128, true);
-            const uint32_t ring = smem_u32(smem + kOffRing);
+        if (lane == 0 && r == 0) {
+            constexpr uint32_t kIdS = idesc_bf16(256, 128, false), kIdO = idesc_bf16(256, 128, true);
+            const uint64_t ring = sdesc(smem_u32(smem + kOffRing), 16, 1024);
+            const uint64_t vring = sdesc(smem_u32(smem + kOffRing + kOffV), kBlock, 1024);    // MN-major
             const uint64_t qd = sdesc(smem_u32(smem + kOffQ), 16, 1024);
             const int last = subs - 1;
-            auto scores = [&](int s, int j) {
+            auto scores = [&](int s, int st) {
+                const uint64_t a = qd + (uint64_t)(3 * s * (kBlock >> 4));
+                const uint64_t k = ring + (uint64_t)(st * (kStage >> 4));
 #pragma unroll
-                for (int c = 0; c < 3; ++c) {
-                    const uint64_t a = qd + (uint64_t)((3 * s + c) * (kBlock >> 4));
-                    const uint64_t k = sdesc(ring + slot_at(j, c), 16, 1024);
+                for (int c = 0; c < 3; ++c)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        if (c == 0 && e == 0) mma_ss_k<kIdS, 0>(tmem + 128 * s, a, k);
-                        else mma_ss_k<kIdS, 1>(tmem + 128 * s, a + 2 * e, k + 2 * e);
+                        const uint64_t ao = a + c * (kBlock >> 4) + 2 * e, ko = k + c * (kKBlock >> 4) + 2 * e;
+                        if (c == 0 && e == 0) mma2_ss<kIdS, 0>(tmem + 128 * s, ao, ko);
+                        else mma2_ss<kIdS, 1>(tmem + 128 * s, ao, ko);
                     }
-                }
-                mma_commit(&bars->s_full[s]);
-                if (s == last) mma_commit(&bars->k_empty[j & 1]);
+                commit2(&bars->s_full[s]);
+                if (s == last) commit2(&bars->k_empty[st]);
             };
             bool ok = wait(&bars->k_full[0], 0);
             for (int s = 0; s < subs && ok; ++s) {
@@ -397,11 +428,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                 tc_fence_after();
                 if (ok) scores(s, 0);
             }
+            int st = 0, next = 1 % kStages;                    // stages of steps j, j + 1
             for (int j = 0; j < steps && ok; ++j) {
                 // the blocks first (they are usually there), so that after the weights' barrier
                 // nothing stands before the products
-                ok = wait(&bars->v_full[j & 1], phase_of(j)) &&
-                     (j + 1 == steps || wait(&bars->k_full[(j + 1) & 1], phase_of(j + 1)));
+                ok = wait(&bars->v_full[st], phase_of(j)) && (j + 1 == steps || wait(&bars->k_full[next], phase_of(j + 1)));
 #pragma unroll 1
                 for (int s = 0; s < subs && ok; ++s) {
                     const int mine = s == 0 ? steps0 : steps1;
@@ -412,23 +443,20 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                     PTRACE(8 * s, j);
                     tc_fence_after();
                     const uint32_t tS = tmem + 128 * s, tO = tmem + 256 + 128 * s;
+                    const uint64_t v = vring + (uint64_t)(st * (kStage >> 4));
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        // MN-major: 64-column atoms 8 KB apart, 8-token groups 1 KB apart
-                        const uint64_t v = sdesc(ring + slot_at(j, 3 + c), kBlock / 2, 1024);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            mma_ts(tO, tS + 32 * c + 8 * e, v + 128 * e, kIdO, (j > 0 || c > 0 || e > 0) ? 1u : 0u);
-                    }
-                    if (s == last) mma_commit(&bars->v_empty[j & 1]);
+                    for (int e = 0; e < 8; ++e) mma2_ts(tO, tS + 8 * e, v + 128 * e, kIdO, (j > 0 || e > 0) ? 1u : 0u);
+                    if (s == last) commit2(&bars->v_empty[st]);
                     PTRACE(8 * s + 2, j);
-                    if (j + 1 < mine) scores(s, j + 1);
-                    else mma_commit(&bars->o_full[s]);
+                    if (j + 1 < mine) scores(s, next);
+                    else commit2(&bars->o_full[s]);
                     PTRACE(8 * s + 4, j);
                 }
+                st = next;
+                next = next + 1 == kStages ? 0 : next + 1;
             }
             // products in flight must end before the tensor memory is given back
-            if (!ok) mma_commit(&bars->o_full[last]);
+            if (!ok) commit2(&bars->o_full[last]);
             mbar_drain(&bars->o_full[last], 0);
         }
         __syncwarp();
@@ -438,13 +466,14 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         const int s = (warp - 4) >> 2, wq = warp & 3;
         const int row = 32 * wq + lane;                        // of the sub-tile
         const int mine = s == 0 ? steps0 : steps1;
-        const int i = i0 + 128 * s + row;                      // of the sequence's new tokens
+        const int i = i0 + 256 * s + 128 * r + row;            // of the sequence's new tokens
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * wq) << 16);
         const uint32_t tS = lane_addr + 128 * s, tO = lane_addr + 256 + 128 * s;
         const int seen = L - n + min(i, n - 1) + 1;            // tokens this row sees
         // where the scale is positive the maximum commutes with it: one fma per exponent
         const bool pos_scale = p.scale > 0.f;
         const float c2 = p.scale * kLog2e, cs = pos_scale ? c2 : 1.f;
+        const uint32_t p_bar = mapa(smem_u32(&bars->p_full[s]), 0);
         float m = -CUDART_INF_F, l = 0.f;
         bool ok = true;
         for (int j = 0; j < mine; ++j) {
@@ -508,7 +537,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
             TMEM_ST32(tS + 32, (sv + 32));
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&bars->p_full[s]);
+            __syncwarp();
+            if (lane == 0) arrive_cluster(p_bar);
             if (wq == 0 && lane == 0) PTRACE(8 * s + 7, j);
         }
         if (ok && mine > 0) ok = __all_sync(0xffffffffu, wait(&bars->o_full[s], 0));
@@ -538,7 +568,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                 }
             }
             __syncwarp();
-            const int first = 128 * s + 32 * wq;               // of the tile
+            const int first = 256 * s + 128 * r + 32 * wq;     // of the tile
             for (int rr = lane >> 4; rr < 32; rr += 2)
                 if (first + rr < rows_here)
                     *(uint4 *)(out + ((qrow0 + first + rr) * H + h) * kDv + 8 * (lane & 15)) =
@@ -549,11 +579,14 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     } else {
         reg_dec<kRegsIssue>();
     }
+    // neither CTA leaves while the other may reach its barriers, its shared memory or its
+    // tensor memory
     tc_fence_before();
     __syncthreads();
+    cluster_sync();
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     }
 }
 
@@ -608,11 +641,11 @@ bool prefill_tc_supported(const ShapeArgs &s, int dn) {
 cudaError_t launch_prefill_tc(const PrefillParams &p, cudaStream_t st) {
     using namespace pf;
     const uint64_t kv_rows = (uint64_t)p.nh * p.cap_rows;
-    CUtensorMap rows, uk, uv, k_st, v_st, q, k_ld, v_ld;
+    CUtensorMap rows, uk, uv, k_st, v_st, q, k_ld, v_ld, rope;
     if (!map2d(&rows, p.rows, p.cap_rows, kR + kRope, 128) || !map2d(&uk, p.W_UK, (uint64_t)p.s.H * kDn, kR, 128) ||
         !map2d(&uv, p.W_UV, (uint64_t)p.s.H * kR, kDv, 64) || !map2d(&k_st, p.k, kv_rows, kDn, 32) ||
-        !map2d(&v_st, p.v, kv_rows, kDv, 32) || !map2d(&k_ld, p.k, kv_rows, kDn, 128) ||
-        !map2d(&v_ld, p.v, kv_rows, kDv, 64) || !map_q(&q, p.q, p.num_q, p.s.H))
+        !map2d(&v_st, p.v, kv_rows, kDv, 32) || !map2d(&k_ld, p.k, kv_rows, kDn, 64) ||
+        !map2d(&v_ld, p.v, kv_rows, kDv, 128) || !map2d(&rope, p.rows, p.cap_rows, kR + kRope, 64) || !map_q(&q, p.q, p.num_q, p.s.H))
         return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(ex::expand_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ex::kSmemBytes);
     if (e != cudaSuccess) return e;
@@ -624,7 +657,7 @@ cudaError_t launch_prefill_tc(const PrefillParams &p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (at.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
     ex::expand_tc_kernel<<<dim3((p.cap_rows + 255) / 256, p.nh), ex::kThreads, ex::kSmemBytes, st>>>(rows, uk, uv, k_st, v_st, p);
-    prefill_tc_kernel<<<dim3(p.num_q / kTileQ + p.B, p.nh), kThreads, kSmemBytes, st>>>(q, k_ld, v_ld, rows, p);
+    prefill_tc_kernel<<<dim3(2 * (p.num_q / kTileQ + p.B), p.nh), kThreads, kSmemBytes, st>>>(q, k_ld, v_ld, rope, p);
     return cudaGetLastError();
 }
 
