@@ -203,7 +203,7 @@ expand_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_cons
 constexpr int kThreads = 384;          // warp 0 copies, 1 products (CTA 0), 4..7 and 8..11 softmax of sub-tiles 0 and 1
 // Registers a thread of the first warpgroup (copies and products) and of the other two
 // (softmax) once they are split again: what the launch had, 3 x 168.
-constexpr int kRegsLaunch = 168, kRegsIssue = 72, kRegsSoftmax = 216;
+constexpr int kRegsLaunch = 168, kRegsIssue = 104, kRegsSoftmax = 200;
 static_assert(kRegsIssue + 2 * kRegsSoftmax <= 3 * kRegsLaunch, "register split");
 template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -221,10 +221,10 @@ static_assert(kSmemBytes <= 232448, "shared memory budget");
 struct Bars {
     // of CTA 0: both CTAs' copies landed; both CTAs' weights are stored (a warp an arrival)
     uint64_t q_full[2];
-    uint64_t k_full[kStages], v_full[kStages];
+    uint64_t full[kStages];
     uint64_t p_full[2];
     // of each CTA, from CTA 0's products
-    uint64_t k_empty[kStages], v_empty[kStages];
+    uint64_t empty[kStages];
     uint64_t s_full[2];        // scores of the sub-tile's step are there (and its earlier P . V)
     uint64_t o_full[2];
     uint32_t tmem_base;
@@ -263,6 +263,21 @@ __device__ __forceinline__ void commit2(uint64_t *bar) {
                      smem_u32(bar)),
                  "h"((uint16_t)3)
                  : "memory");
+}
+__device__ __forceinline__ bool mbar_test32(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// The bounded wait for a barrier that mbar_test32 found open, out of line.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, int32_t *abort_flag, int32_t *status) {
+    return mbar_wait_bounded((uint64_t *)__cvta_shared_to_generic(bar), parity, abort_flag, status, FLAG_TIMEOUT, kTimeoutNs);
 }
 // An arrival on a barrier of either CTA of the pair. What it reports is in tensor memory,
 // complete (tcgen05.wait::st) and ordered by the tcgen05 fences on both sides; no other
@@ -329,10 +344,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
             mbar_init(&bars->o_full[s], 1);
         }
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&bars->k_full[s], 1);
-            mbar_init(&bars->v_full[s], 1);
-            mbar_init(&bars->k_empty[s], 1);
-            mbar_init(&bars->v_empty[s], 1);
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->empty[s], 1);
         }
         bars->abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -353,8 +366,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         return mbar_wait_bounded(bar, parity, &bars->abort_flag, p.status, FLAG_TIMEOUT, kTimeoutNs);
     };
-    // stage of step j, phase of its use
-    auto phase_of = [](int j) { return (uint32_t)(j / kStages) & 1u; };
+    // The copies go in turns: turn t brings step t's keys and step t - 1's values, which the
+    // products take together (turn 0: keys only; turn `steps`: values only).
+    auto phase_of = [](int t) { return (uint32_t)(t / kStages) & 1u; };
 
     if (warp == 0) {
         // ================================================= copies
@@ -369,30 +383,27 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                     tma_pair_3d(smem + kOffQ + (3 * s + c) * kBlock, &q_map, 64 * c, h, (int)qrow0 + 256 * s + 128 * r,
                                 leader(&bars->q_full[s]));
             };
-            int k_issued = 0, v_issued = 0;
+            int issued = 0;
             load_q(0);
-            for (int j = 0; j < steps; ++j) {
-                const int st = j % kStages;
+            for (int u = 0; u <= steps; ++u, ++issued) {
+                const int st = u % kStages;
                 uint8_t *dst = smem + kOffRing + st * kStage;
-                if (j >= kStages && !wait(&bars->k_empty[st], phase_of(j - kStages))) break;
-                if (r == 0) mbar_expect_tx(&bars->k_full[st], 6 * kKBlock);
-                uint32_t bar = leader(&bars->k_full[st]);
-                tma_pair_2d(dst, &k_map, 0, kv0 + 128 * j + 64 * r, bar);
-                tma_pair_2d(dst + kKBlock, &k_map, 64, kv0 + 128 * j + 64 * r, bar);
-                tma_pair_2d(dst + 2 * kKBlock, &rope_map, kR, row0 + 128 * j + 64 * r, bar);
-                ++k_issued;
-                if (j == 0 && subs == 2) load_q(1);
-                if (j >= kStages && !wait(&bars->v_empty[st], phase_of(j - kStages))) break;
-                if (r == 0) mbar_expect_tx(&bars->v_full[st], 2 * kBlock);
-                tma_pair_2d(dst + kOffV, &v_map, 64 * r, kv0 + 128 * j, leader(&bars->v_full[st]));
-                ++v_issued;
+                if (u >= kStages && !wait(&bars->empty[st], phase_of(u - kStages))) break;
+                if (r == 0) mbar_expect_tx(&bars->full[st], (u < steps ? 6 * kKBlock : 0u) + (u > 0 ? 2 * kBlock : 0u));
+                const uint32_t bar = leader(&bars->full[st]);
+                if (u > 0) tma_pair_2d(dst + kOffV, &v_map, 64 * r, kv0 + 128 * (u - 1), bar);
+                if (u < steps) {
+                    tma_pair_2d(dst, &k_map, 0, kv0 + 128 * u + 64 * r, bar);
+                    tma_pair_2d(dst + kKBlock, &k_map, 64, kv0 + 128 * u + 64 * r, bar);
+                    tma_pair_2d(dst + 2 * kKBlock, &rope_map, kR, row0 + 128 * u + 64 * r, bar);
+                }
+                if (u == 0 && subs == 2) load_q(1);
             }
             // Never leave a copy in flight into the pair's shared memory: CTA 0 waits here for
             // both CTAs' copies, CTA 1 for CTA 0 at the end.
             if (r == 0) {
                 for (int s = 0; s < subs; ++s) mbar_drain(&bars->q_full[s], 0);
-                for (int j = max(0, k_issued - kStages); j < k_issued; ++j) mbar_drain(&bars->k_full[j % kStages], phase_of(j));
-                for (int j = max(0, v_issued - kStages); j < v_issued; ++j) mbar_drain(&bars->v_full[j % kStages], phase_of(j));
+                for (int u = max(0, issued - kStages); u < issued; ++u) mbar_drain(&bars->full[u % kStages], phase_of(u));
             }
         }
         __syncwarp();
@@ -408,9 +419,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
             const uint64_t vring = sdesc(smem_u32(smem + kOffRing + kOffV), kBlock, 1024);    // MN-major
             const uint64_t qd = sdesc(smem_u32(smem + kOffQ), 16, 1024);
             const int last = subs - 1;
-            auto scores = [&](int s, int st) {
+            auto scores = [&](int s, uint64_t k) {
                 const uint64_t a = qd + (uint64_t)(3 * s * (kBlock >> 4));
-                const uint64_t k = ring + (uint64_t)(st * (kStage >> 4));
 #pragma unroll
                 for (int c = 0; c < 3; ++c)
 #pragma unroll
@@ -420,40 +430,49 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                         else mma2_ss<kIdS, 1>(tmem + 128 * s, ao, ko);
                     }
                 commit2(&bars->s_full[s]);
-                if (s == last) commit2(&bars->k_empty[st]);
             };
-            bool ok = wait(&bars->k_full[0], 0);
+            bool ok = wait(&bars->full[0], 0);
             for (int s = 0; s < subs && ok; ++s) {
                 ok = wait(&bars->q_full[s], 0);
                 tc_fence_after();
-                if (ok) scores(s, 0);
+                if (ok) scores(s, ring);
             }
-            int st = 0, next = 1 % kStages;                    // stages of steps j, j + 1
+            if (ok) commit2(&bars->empty[0]);
+            // Between one product and the next stand as few instructions as can be: the thread's
+            // own pace bounded the kernel (a third of the time, with a barrier for each block
+            // and the general wait inlined everywhere).
+            const uint32_t full0 = smem_u32(&bars->full[0]), p0 = smem_u32(&bars->p_full[0]);
+            auto there = [&](uint32_t bar, uint32_t parity) {
+                return mbar_test32(bar, parity) || wait_slow(bar, parity, &bars->abort_flag, p.status);
+            };
+            int st = 1 % kStages;                              // stage and phase of turn j + 1
+            uint32_t ph = 0;
             for (int j = 0; j < steps && ok; ++j) {
-                // the blocks first (they are usually there), so that after the weights' barrier
-                // nothing stands before the products
-                ok = wait(&bars->v_full[st], phase_of(j)) && (j + 1 == steps || wait(&bars->k_full[next], phase_of(j + 1)));
+                ok = there(full0 + 8 * st, ph);
+                PTRACE(3, j);
+                const uint64_t k = ring + (uint64_t)(st * (kStage >> 4)), v = vring + (uint64_t)(st * (kStage >> 4));
 #pragma unroll 1
                 for (int s = 0; s < subs && ok; ++s) {
-                    const int mine = s == 0 ? steps0 : steps1;
-                    if (j >= mine) continue;
+                    const int left = (s == 0 ? steps0 : steps1) - j;     // of the sub-tile's steps
+                    if (left <= 0) continue;
                     PTRACE(8 * s + 1, j);
-                    ok = wait(&bars->p_full[s], j & 1);
+                    ok = there(p0 + 8 * s, j & 1);
                     if (!ok) break;
                     PTRACE(8 * s, j);
                     tc_fence_after();
                     const uint32_t tS = tmem + 128 * s, tO = tmem + 256 + 128 * s;
-                    const uint64_t v = vring + (uint64_t)(st * (kStage >> 4));
 #pragma unroll
                     for (int e = 0; e < 8; ++e) mma2_ts(tO, tS + 8 * e, v + 128 * e, kIdO, (j > 0 || e > 0) ? 1u : 0u);
-                    if (s == last) commit2(&bars->v_empty[st]);
                     PTRACE(8 * s + 2, j);
-                    if (j + 1 < mine) scores(s, next);
+                    if (left > 1) scores(s, k);
                     else commit2(&bars->o_full[s]);
                     PTRACE(8 * s + 4, j);
                 }
-                st = next;
-                next = next + 1 == kStages ? 0 : next + 1;
+                commit2(&bars->empty[st]);
+                if (++st == kStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
             }
             // products in flight must end before the tensor memory is given back
             if (!ok) commit2(&bars->o_full[last]);
