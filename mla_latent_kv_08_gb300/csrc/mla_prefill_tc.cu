@@ -25,213 +25,6 @@ constexpr unsigned long long kTimeoutNs = 2000000000ull;       // 2 s bounded-wa
 constexpr int kR = 512, kRope = 64, kDn = 128, kDv = 128;
 constexpr uint32_t kBlock = 128 * 128;                // [128 rows x 64 values] bf16: 16 KB
 
-// ============================================================================
-// Keys and values. A CTA makes 256 rows x (128 key + 128 value) columns of one head:
-// four M128 N128 accumulators, the whole 512 columns of tensor memory. W_UK[h] is K-major
-// as it lies ([d_n, r]), W_UV[h] MN-major ([r, d_v]).
-// ============================================================================
-namespace ex {
-constexpr int kThreads = 320;                          // warp 0 TMA, 1 MMA, 2..9 epilogue
-constexpr int kStages = 3;
-constexpr uint32_t kStage = 4 * kBlock;                // two row blocks, W_UK, W_UV: 64 KB
-constexpr int kChunks = kR / 64;
-constexpr uint32_t kOffBar = kStages * kStage;
-constexpr uint32_t kSmemBytes = kOffBar + 256 + 1024;  // + alignment slack
-static_assert(kSmemBytes <= 232448, "shared memory budget");
-
-struct Bars {
-    uint64_t full[kStages], empty[kStages];
-    uint64_t done;
-    uint32_t tmem_base;
-    int32_t abort_flag;
-};
-
-__global__ void __launch_bounds__(kThreads, 1)
-expand_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constant__ CUtensorMap uk_map,
-                 const __grid_constant__ CUtensorMap uv_map, const __grid_constant__ CUtensorMap k_map,
-                 const __grid_constant__ CUtensorMap v_map, const PrefillParams p) {
-    const int m0 = blockIdx.x * 256, hl = blockIdx.y, h = p.h0 + hl;
-    const int rows_used = p.kv_off[p.B];
-    if (m0 >= rows_used) return;
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    Bars *bars = (Bars *)(smem + kOffBar);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (tid == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&bars->full[s], 1);
-            mbar_init(&bars->empty[s], 1);
-        }
-        mbar_init(&bars->done, 1);
-        bars->abort_flag = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        fence_proxy_async();
-    }
-    if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_u32(&bars->tmem_base)),
-                     "r"(512)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = bars->tmem_base;
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-        return mbar_wait_bounded(bar, parity, &bars->abort_flag, p.status, FLAG_TIMEOUT, kTimeoutNs);
-    };
-    if (warp == 0) {
-        if (lane == 0) {
-            int c = 0;
-            for (; c < kChunks; ++c) {
-                const int s = c % kStages, use = c / kStages;
-                if (use > 0 && !wait(&bars->empty[s], (use - 1) & 1)) break;
-                uint8_t *st = smem + s * kStage;
-                mbar_expect_tx(&bars->full[s], kStage);
-                tma_load_2d(st, &rows_map, 64 * c, m0, &bars->full[s]);
-                tma_load_2d(st + kBlock, &rows_map, 64 * c, m0 + 128, &bars->full[s]);   // past the end: zeros
-                tma_load_2d(st + 2 * kBlock, &uk_map, 64 * c, h * kDn, &bars->full[s]);
-                tma_load_2d(st + 3 * kBlock, &uv_map, 0, h * kR + 64 * c, &bars->full[s]);
-                tma_load_2d(st + 3 * kBlock + kBlock / 2, &uv_map, 64, h * kR + 64 * c, &bars->full[s]);
-            }
-            // never leave a copy in flight into this CTA's shared memory
-            for (int u = c > kStages ? c - kStages : 0; u < c; ++u) mbar_drain(&bars->full[u % kStages], (u / kStages) & 1);
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t kIdK = idesc_bf16(128, 128, false), kIdV = idesc_bf16(128, 128, true);
-            for (int c = 0; c < kChunks; ++c) {
-                const int s = c % kStages;
-                if (!wait(&bars->full[s], (c / kStages) & 1)) break;
-                tc_fence_after();
-                const uint32_t st = smem_u32(smem + s * kStage);
-                const uint64_t a0 = sdesc(st, 16, 1024), a1 = sdesc(st + kBlock, 16, 1024);
-                const uint64_t bk = sdesc(st + 2 * kBlock, 16, 1024);
-                // MN-major: 64-column atoms 8 KB apart, 8-row groups 1 KB apart
-                const uint64_t bv = sdesc(st + 3 * kBlock, kBlock / 2, 1024);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t acc = (c > 0 || k > 0) ? 1u : 0u;
-                    mma_ss(tmem, a0 + 2 * k, bk + 2 * k, kIdK, acc);
-                    mma_ss(tmem + 128, a0 + 2 * k, bv + 128 * k, kIdV, acc);
-                    mma_ss(tmem + 256, a1 + 2 * k, bk + 2 * k, kIdK, acc);
-                    mma_ss(tmem + 384, a1 + 2 * k, bv + 128 * k, kIdV, acc);
-                }
-                mma_commit(&bars->empty[s]);
-            }
-            mma_commit(&bars->done);
-            wait(&bars->done, 0);
-        }
-        __syncwarp();
-    } else {
-        // warp 2 + e: rows 32*(warp%4)..+31 (its tensor-memory lanes) of row block (warp-2)/4
-        const int q = warp & 3, mt = (warp - 2) >> 2;
-        const int row = m0 + 128 * mt + 32 * q;
-        const bool ok = __all_sync(0xffffffffu, wait(&bars->done, 0));
-        tc_fence_after();
-        // the stages are free: every copy has landed and every product has read it
-        uint8_t *box = smem + (warp - 2) * 4 * 4096;
-        if (ok && row < rows_used) {
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {              // 64 columns: key halves, value halves
-                uint32_t v[64];
-                const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + 256 * mt + 64 * c;
-                TMEM_LD32(at, v);
-                TMEM_LD32(at + 32, (v + 32));
-                tmem_wait_ld();
-                uint8_t *b = box + 4096 * c;
-#pragma unroll
-                for (int ch = 0; ch < 8; ++ch) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(v[8 * ch + 2 * e]),
-                                                                       __uint_as_float(v[8 * ch + 2 * e + 1]));
-                        w[e] = *(const uint32_t *)&x;
-                    }
-                    *(uint4 *)(b + sw128(lane, ch)) = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) {
-                    const CUtensorMap *map = c < 2 ? &k_map : &v_map;
-                    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                                     (uint64_t)map),
-                                 "r"(smem_u32(b)), "r"(64 * (c & 1)), "r"((int)((long long)hl * p.cap_rows) + row)
-                                 : "memory");
-                    bulk_commit();
-                }
-            }
-            if (lane == 0) bulk_wait_all();
-            __syncwarp();
-        }
-    }
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 1) {
-        tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
-    }
-}
-}  // namespace ex
-
-// ============================================================================
-// Attention. A pair of CTAs (a cluster of two) takes up to 512 new tokens of one sequence
-// for one head, as two sub-tiles of 256 rows, CTA r of the pair holding 128 rows of each.
-// Both sub-tiles go through the same 128-token steps of the cache in turn: while one's
-// warpgroups turn scores into weights, the tensor cores work on the other.
-//
-//   per step and sub-tile   S[256 x 128] = Q . K^T   12 x M256 N128 K16 over both SMs
-//                           P = 2^(S c - m)          a thread a row: no shuffles
-//                           O[256 x 128] += P . V    8 x M256 N128 K16, P from tensor memory
-//
-// The pair shares the second operand: CTA r copies the keys of tokens 64 r .. 64 r + 63 of a
-// step and value columns 64 r .. 64 r + 63, 40 KB a step instead of the 80 KB that a CTA on
-// its own needs. That leaves room for three steps in flight (a CTA on its own had 1.6, and
-// its tensor cores waited a quarter of the time for keys), halves the reads of L2, and takes
-// the scores' operands (6 KB an MMA and SM, not 8) below the bandwidth of shared memory.
-//
-// P (bf16) is stored over the scores it came from. The products of one sub-tile are issued
-// in order by one thread of CTA 0, so that the next scores overwrite P only once P . V has
-// read it. m is raised lazily, only when it grows by more than 8 (P <= 2^8).
-//
-// Shared memory: Q 96 KB, three stages of key blocks ([64 tokens x 64 dims] each) and a value
-// block ([128 tokens x 64 columns]). Tensor memory: S0, S1, O0, O1, 128 columns each.
-// ============================================================================
-constexpr int kThreads = 384;          // warp 0 copies, 1 products (CTA 0), 4..7 and 8..11 softmax of sub-tiles 0 and 1
-// Registers a thread of the first warpgroup (copies and products) and of the other two
-// (softmax) once they are split again: what the launch had, 3 x 168.
-constexpr int kRegsLaunch = 168, kRegsIssue = 104, kRegsSoftmax = 200;
-static_assert(kRegsIssue + 2 * kRegsSoftmax <= 3 * kRegsLaunch, "register split");
-template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-constexpr int kTileQ = 512;
-constexpr int kStages = 3;
-constexpr uint32_t kKBlock = 64 * 128;                  // 8 KB
-constexpr uint32_t kOffV = 3 * kKBlock;                 // of a stage
-constexpr uint32_t kStage = kOffV + kBlock;             // 40 KB
-constexpr uint32_t kOffQ = 0;
-constexpr uint32_t kOffRing = 6 * kBlock;
-constexpr uint32_t kOffBar = kOffRing + kStages * kStage;
-constexpr uint32_t kSmemBytes = kOffBar + 512 + 1024;
-static_assert(kSmemBytes <= 232448, "shared memory budget");
-
-struct Bars {
-    // of CTA 0: both CTAs' copies landed; both CTAs' weights are stored (a warp an arrival)
-    uint64_t q_full[2];
-    uint64_t full[kStages];
-    uint64_t p_full[2];
-    // of each CTA, from CTA 0's products
-    uint64_t empty[kStages];
-    uint64_t s_full[2];        // scores of the sub-tile's step are there (and its earlier P . V)
-    uint64_t o_full[2];
-    uint32_t tmem_base;
-    int32_t abort_flag;
-};
-static_assert(sizeof(Bars) <= 512, "barriers");
-
 // ---- the pair: copies that report to CTA 0, products over both SMs ----------
 __device__ __forceinline__ void tma_pair_2d(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
     asm volatile(
@@ -243,6 +36,13 @@ __device__ __forceinline__ void tma_pair_3d(void *dst, const CUtensorMap *map, i
     asm volatile(
         "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
         ::"r"(smem_u32(dst)), "l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void mma2_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
 template <uint32_t IDESC, int ACC>
@@ -286,6 +86,265 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, int32_t *a
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// ============================================================================
+// Keys and values. A pair of CTAs makes 256 rows of two heads' keys, then of their values, then
+// the next two heads: the rows' 512 latent dims stay in shared memory (CTA r holds rows 128 r
+// .. 128 r + 127, 128 KB), only weights stream through it, CTA r holding head r's of the two.
+// So a CTA reads 128 KB of L2 per head for 67 MFLOP, 32 bytes a cycle at full rate; a tile of
+// its own of 256 x 256 reads twice that. Each product is M256 N256 K16 (the two heads'
+// columns). Keys and values have accumulators of their own, the whole of tensor memory, so
+// that one is rounded and stored while the other is made. W_UK[h] is K-major as it lies
+// ([d_n, r]), W_UV[h] MN-major ([r, d_v]).
+// ============================================================================
+namespace ex {
+constexpr int kThreads = 384;                          // warp 0 copies, 1 products (CTA 0), 4..11 output
+constexpr int kStages = 4;
+constexpr uint32_t kStage = kBlock;                    // 64 dims of a head's 128 columns: 16 KB
+constexpr int kChunks = kR / 64;
+constexpr uint32_t kOffW = kChunks * kBlock;           // after the rows
+constexpr uint32_t kOffOut = kOffW + kStages * kStage; // a 4 KB box a warp
+constexpr uint32_t kOffBar = kOffOut + 8 * 4096;
+constexpr uint32_t kSmemBytes = kOffBar + 256 + 1024;  // + alignment slack
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+
+struct Bars {
+    // of CTA 0: both CTAs' rows and weights landed; both CTAs' outputs of an accumulator are read
+    uint64_t rows_full, full[kStages], acc_free[2];
+    // of each CTA, from CTA 0's products
+    uint64_t empty[kStages], acc_full[2];
+    uint32_t tmem_base;
+    int32_t abort_flag;
+};
+static_assert(sizeof(Bars) <= 256, "barriers");
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+expand_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constant__ CUtensorMap uk_map,
+                 const __grid_constant__ CUtensorMap uv_map, const __grid_constant__ CUtensorMap k_map,
+                 const __grid_constant__ CUtensorMap v_map, const PrefillParams p, int heads) {
+    const int r = (int)cluster_ctarank(), m0 = (blockIdx.x >> 1) * 256;
+    const int rows_used = p.kv_off[p.B];
+    if (m0 >= rows_used) return;                       // both CTAs of a pair
+    const int hl0 = blockIdx.y * heads, nh = min(heads, p.nh - hl0);     // heads of this pass (`heads` is even)
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    Bars *bars = (Bars *)(smem + kOffBar);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        mbar_init(&bars->rows_full, 1);
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bars->acc_full[s], 1);
+            mbar_init(&bars->acc_free[s], 16);         // a warp of either CTA an arrival
+        }
+        bars->abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_proxy_async();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&bars->tmem_base)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                        // the other CTA's barriers and tensor memory are there
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        return mbar_wait_bounded(bar, parity, &bars->abort_flag, p.status, FLAG_TIMEOUT, kTimeoutNs);
+    };
+    const int parts = 2 * ((nh + 1) / 2), turns = parts * kChunks;       // a part: two heads' keys or values
+    if (warp == 0) {
+        if (lane == 0) {
+            auto leader = [&](uint64_t *bar) { return mapa(smem_u32(bar), 0); };
+            if (r == 0) mbar_expect_tx(&bars->rows_full, 2 * kChunks * kBlock);
+            for (int c = 0; c < kChunks; ++c)          // rows past the end read zeros
+                tma_pair_2d(smem + c * kBlock, &rows_map, 64 * c, m0 + 128 * r, leader(&bars->rows_full));
+            int u = 0;
+            for (; u < turns; ++u) {
+                const int s = u % kStages, use = u / kStages, c = u % kChunks, part = u / kChunks;
+                // this CTA's head; behind the pass's last one its products are not stored (and
+                // behind the layer's last one it reads zeros)
+                const int h = p.h0 + hl0 + 2 * (part >> 1) + r;
+                if (use > 0 && !wait(&bars->empty[s], (use - 1) & 1)) break;
+                if (r == 0) mbar_expect_tx(&bars->full[s], 2 * kStage);
+                uint8_t *st = smem + kOffW + s * kStage;
+                const uint32_t bar = leader(&bars->full[s]);
+                if ((part & 1) == 0) {
+                    tma_pair_2d(st, &uk_map, 64 * c, h * kDn, bar);
+                } else {
+                    tma_pair_2d(st, &uv_map, 0, h * kR + 64 * c, bar);
+                    tma_pair_2d(st + kBlock / 2, &uv_map, 64, h * kR + 64 * c, bar);
+                }
+            }
+            // Never leave a copy in flight into the pair's shared memory: CTA 0 waits here for
+            // both CTAs' copies, CTA 1 for CTA 0 at the end.
+            if (r == 0) {
+                mbar_drain(&bars->rows_full, 0);
+                for (int v = max(0, u - kStages); v < u; ++v) mbar_drain(&bars->full[v % kStages], (v / kStages) & 1);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && r == 0) {
+            constexpr uint32_t kIdK = idesc_bf16(256, 256, false), kIdV = idesc_bf16(256, 256, true);
+            const uint64_t rows = sdesc(smem_u32(smem), 16, 1024);
+            const uint64_t wk = sdesc(smem_u32(smem + kOffW), 16, 1024);
+            const uint64_t wv = sdesc(smem_u32(smem + kOffW), kBlock / 2, 1024);         // MN-major
+            const uint32_t full0 = smem_u32(&bars->full[0]), free0 = smem_u32(&bars->acc_free[0]);
+            auto there = [&](uint32_t bar, uint32_t parity) {
+                return mbar_test32(bar, parity) || wait_slow(bar, parity, &bars->abort_flag, p.status);
+            };
+            bool ok = wait(&bars->rows_full, 0);
+            int s = 0;
+            uint32_t ph = 0;                           // stage, phase of its use
+            for (int i = 0; i < parts && ok; ++i) {
+                const int v = i & 1;                   // keys, values
+                const uint32_t d = tmem + 256 * v, idesc = v ? kIdV : kIdK, step = v ? 128 : 2;
+                ok = i < 2 || there(free0 + 8 * v, ((i >> 1) - 1) & 1);
+                uint64_t a = rows;
+#pragma unroll 1
+                for (int c = 0; c < kChunks && ok; ++c) {
+                    ok = there(full0 + 8 * s, ph);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t w = (v ? wv : wk) + (uint64_t)(s * (kStage >> 4));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mma2_ss(d, a + 2 * e, w + step * e, idesc, (c > 0 || e > 0) ? 1u : 0u);
+                    commit2(&bars->empty[s]);
+                    a += kBlock >> 4;
+                    if (++s == kStages) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                }
+                commit2(&bars->acc_full[v]);
+            }
+            // products in flight must end before the tensor memory is given back
+            mbar_drain(&bars->acc_full[1], ((parts >> 1) - 1) & 1);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // warp w: rows 32*(w%4)..+31 (its tensor-memory lanes) of the first (w < 8) or second head
+        const int q = warp & 3, hv = (warp - 4) >> 2;
+        const int row = m0 + 128 * r + 32 * q;
+        uint8_t *box = smem + kOffOut + (warp - 4) * 4096;
+        for (int i = 0; i < parts; ++i) {
+            const int v = i & 1, hl = hl0 + (i & ~1) + hv;
+            if (!__all_sync(0xffffffffu, wait(&bars->acc_full[v], (i >> 1) & 1))) break;
+            tc_fence_after();
+            const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + 256 * v + 128 * hv;
+            const bool store = row < rows_used && hl < hl0 + nh;
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {              // 64 columns
+                uint32_t x[64];
+                TMEM_LD32(at + 64 * c, x);
+                TMEM_LD32(at + 64 * c + 32, (x + 32));
+                tmem_wait_ld();
+                if (lane == 0) bulk_wait_read();       // the box's last store has read it
+                __syncwarp();
+#pragma unroll
+                for (int ch = 0; ch < 8; ++ch) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const __nv_bfloat162 y = __floats2bfloat162_rn(__uint_as_float(x[8 * ch + 2 * e]),
+                                                                       __uint_as_float(x[8 * ch + 2 * e + 1]));
+                        w[e] = *(const uint32_t *)&y;
+                    }
+                    *(uint4 *)(box + sw128(lane, ch)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                if (c == 1) {                          // the accumulator is read
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_cluster(mapa(smem_u32(&bars->acc_free[v]), 0));
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0 && store) {
+                    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                                     (uint64_t)(v ? &v_map : &k_map)),
+                                 "r"(smem_u32(box)), "r"(64 * c), "r"((int)((long long)hl * p.cap_rows) + row)
+                                 : "memory");
+                    bulk_commit();
+                }
+            }
+        }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
+    }
+    // neither CTA leaves while the other may reach its barriers, its shared memory or its
+    // tensor memory
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+}  // namespace ex
+
+// ============================================================================
+// Attention. A pair of CTAs (a cluster of two) takes up to 512 new tokens of one sequence
+// for one head, as two sub-tiles of 256 rows, CTA r of the pair holding 128 rows of each.
+// Both sub-tiles go through the same 128-token steps of the cache in turn: while one's
+// warpgroups turn scores into weights, the tensor cores work on the other.
+//
+//   per step and sub-tile   S[256 x 128] = Q . K^T   12 x M256 N128 K16 over both SMs
+//                           P = 2^(S c - m)          a thread a row: no shuffles
+//                           O[256 x 128] += P . V    8 x M256 N128 K16, P from tensor memory
+//
+// The pair shares the second operand: CTA r copies the keys of tokens 64 r .. 64 r + 63 of a
+// step and value columns 64 r .. 64 r + 63, 40 KB a step instead of the 80 KB that a CTA on
+// its own needs. That leaves room for three steps in flight (a CTA on its own had 1.6, and
+// its tensor cores waited a quarter of the time for keys), halves the reads of L2, and takes
+// the scores' operands (6 KB an MMA and SM, not 8) below the bandwidth of shared memory.
+//
+// P (bf16) is stored over the scores it came from. The products of one sub-tile are issued
+// in order by one thread of CTA 0, so that the next scores overwrite P only once P . V has
+// read it. m is raised lazily, only when it grows by more than 8 (P <= 2^8).
+//
+// Shared memory: Q 96 KB, three stages of key blocks ([64 tokens x 64 dims] each) and a value
+// block ([128 tokens x 64 columns]). Tensor memory: S0, S1, O0, O1, 128 columns each.
+// ============================================================================
+constexpr int kThreads = 384;          // warp 0 copies, 1 products (CTA 0), 4..7 and 8..11 softmax of sub-tiles 0 and 1
+// Registers a thread of the first warpgroup (copies and products) and of the other two
+// (softmax) once they are split again: what the launch had, 3 x 168.
+constexpr int kRegsLaunch = 168, kRegsIssue = 104, kRegsSoftmax = 200;
+static_assert(kRegsIssue + 2 * kRegsSoftmax <= 3 * kRegsLaunch, "register split");
+constexpr int kTileQ = 512;
+constexpr int kStages = 3;
+constexpr uint32_t kKBlock = 64 * 128;                  // 8 KB
+constexpr uint32_t kOffV = 3 * kKBlock;                 // of a stage
+constexpr uint32_t kStage = kOffV + kBlock;             // 40 KB
+constexpr uint32_t kOffQ = 0;
+constexpr uint32_t kOffRing = 6 * kBlock;
+constexpr uint32_t kOffBar = kOffRing + kStages * kStage;
+constexpr uint32_t kSmemBytes = kOffBar + 512 + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+
+struct Bars {
+    // of CTA 0: both CTAs' copies landed; both CTAs' weights are stored (a warp an arrival)
+    uint64_t q_full[2];
+    uint64_t full[kStages];
+    uint64_t p_full[2];
+    // of each CTA, from CTA 0's products
+    uint64_t empty[kStages];
+    uint64_t s_full[2];        // scores of the sub-tile's step are there (and its earlier P . V)
+    uint64_t o_full[2];
+    uint32_t tmem_base;
+    int32_t abort_flag;
+};
+static_assert(sizeof(Bars) <= 512, "barriers");
 
 // Pipeline timestamps for performance analysis, compiled only with -DMLA_TRACE: clock64 at
 // each hand-off of CTA (0, 0) for its first kTraceSteps steps. Product builds contain none
@@ -675,7 +734,18 @@ cudaError_t launch_prefill_tc(const PrefillParams &p, cudaStream_t st) {
     e = cudaFuncGetAttributes(&at, prefill_tc_kernel);
     if (e != cudaSuccess) return e;
     if (at.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
-    ex::expand_tc_kernel<<<dim3((p.cap_rows + 255) / 256, p.nh), ex::kThreads, ex::kSmemBytes, st>>>(rows, uk, uv, k_st, v_st, p);
+    // Heads a pair makes in a row: as many as leave about four pairs' turns for each pair of
+    // SMs (the rows are then loaded seldom, and the last turn costs little).
+    int dev = 0, sms = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess ||
+        (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+        return e;
+    const long long tiles = (p.cap_rows + 255) / 256;
+    long long heads = p.nh * tiles / (2ll * sms);
+    heads = heads < 2 ? 2 : heads > p.nh ? p.nh : heads;
+    heads += heads & 1;
+    ex::expand_tc_kernel<<<dim3((unsigned)(2 * tiles), (unsigned)((p.nh + heads - 1) / heads)), ex::kThreads, ex::kSmemBytes, st>>>(
+        rows, uk, uv, k_st, v_st, p, (int)heads);
     prefill_tc_kernel<<<dim3(2 * (p.num_q / kTileQ + p.B), p.nh), kThreads, kSmemBytes, st>>>(q, k_ld, v_ld, rope, p);
     return cudaGetLastError();
 }
