@@ -101,12 +101,12 @@ template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setma
 // ============================================================================
 namespace ex {
 constexpr int kThreads = 384;                          // warp 0 copies, 1 products (CTA 0), 4..11 output
-constexpr int kStages = 4;
+constexpr int kStages = 5;
 constexpr uint32_t kStage = kBlock;                    // 64 dims of a head's 128 columns: 16 KB
 constexpr int kChunks = kR / 64;
 constexpr uint32_t kOffW = kChunks * kBlock;           // after the rows
-constexpr uint32_t kOffOut = kOffW + kStages * kStage; // a 4 KB box a warp
-constexpr uint32_t kOffBar = kOffOut + 8 * 4096;
+constexpr uint32_t kOffOut = kOffW + kStages * kStage; // a 2 KB box a warp: 32 rows x 32 columns
+constexpr uint32_t kOffBar = kOffOut + 8 * 2048;
 constexpr uint32_t kSmemBytes = kOffBar + 256 + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
@@ -122,8 +122,7 @@ static_assert(sizeof(Bars) <= 256, "barriers");
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 expand_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constant__ CUtensorMap uk_map,
-                 const __grid_constant__ CUtensorMap uv_map, const __grid_constant__ CUtensorMap k_map,
-                 const __grid_constant__ CUtensorMap v_map, const PrefillParams p, int heads) {
+                 const __grid_constant__ CUtensorMap uv_map, const PrefillParams p, int heads) {
     const int r = (int)cluster_ctarank(), m0 = (blockIdx.x >> 1) * 256;
     const int rows_used = p.kv_off[p.B];
     if (m0 >= rows_used) return;                       // both CTAs of a pair
@@ -236,23 +235,28 @@ expand_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_cons
         // warp w: rows 32*(w%4)..+31 (its tensor-memory lanes) of the first (w < 8) or second head
         const int q = warp & 3, hv = (warp - 4) >> 2;
         const int row = m0 + 128 * r + 32 * q;
-        uint8_t *box = smem + kOffOut + (warp - 4) * 4096;
+        uint8_t *box = smem + kOffOut + (warp - 4) * 2048;
         for (int i = 0; i < parts; ++i) {
             const int v = i & 1, hl = hl0 + (i & ~1) + hv;
             if (!__all_sync(0xffffffffu, wait(&bars->acc_full[v], (i >> 1) & 1))) break;
             tc_fence_after();
             const uint32_t at = tmem + ((uint32_t)(32 * q) << 16) + 256 * v + 128 * hv;
             const bool store = row < rows_used && hl < hl0 + nh;
+            // a lane's place of the stores: row lane / 4 of eight, 16 bytes lane % 4
+            __nv_bfloat16 *dst = (__nv_bfloat16 *)(v ? p.v : p.k) + ((size_t)hl * p.cap_rows + row + (lane >> 2)) * 128 + 8 * (lane & 3);
 #pragma unroll 1
-            for (int c = 0; c < 2; ++c) {              // 64 columns
-                uint32_t x[64];
-                TMEM_LD32(at + 64 * c, x);
-                TMEM_LD32(at + 64 * c + 32, (x + 32));
+            for (int c = 0; c < 4; ++c) {              // 32 columns
+                uint32_t x[32];
+                TMEM_LD32(at + 32 * c, x);
                 tmem_wait_ld();
-                if (lane == 0) bulk_wait_read();       // the box's last store has read it
-                __syncwarp();
+                if (c == 3) {                          // the accumulator is read
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_cluster(mapa(smem_u32(&bars->acc_free[v]), 0));
+                }
+                // rows of 64 bytes, 16-byte chunks rotated by the row pair
 #pragma unroll
-                for (int ch = 0; ch < 8; ++ch) {
+                for (int ch = 0; ch < 4; ++ch) {
                     uint32_t w[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -260,26 +264,20 @@ expand_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_cons
                                                                        __uint_as_float(x[8 * ch + 2 * e + 1]));
                         w[e] = *(const uint32_t *)&y;
                     }
-                    *(uint4 *)(box + sw128(lane, ch)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *(uint4 *)(box + lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                if (c == 1) {                          // the accumulator is read
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_cluster(mapa(smem_u32(&bars->acc_free[v]), 0));
-                }
-                fence_proxy_async();
                 __syncwarp();
-                if (lane == 0 && store) {
-                    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                                     (uint64_t)(v ? &v_map : &k_map)),
-                                 "r"(smem_u32(box)), "r"(64 * c), "r"((int)((long long)hl * p.cap_rows) + row)
-                                 : "memory");
-                    bulk_commit();
+                if (store) {
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {      // rows 8 g + lane / 4
+                        const int rr = 8 * g + (lane >> 2);
+                        *(uint4 *)(dst + (size_t)(8 * g) * 128 + 32 * c) =
+                            *(const uint4 *)(box + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
+                    }
                 }
+                __syncwarp();
             }
         }
-        if (lane == 0) bulk_wait_all();
-        __syncwarp();
     }
     // neither CTA leaves while the other may reach its barriers, its shared memory or its
     // tensor memory
@@ -719,10 +717,10 @@ bool prefill_tc_supported(const ShapeArgs &s, int dn) {
 cudaError_t launch_prefill_tc(const PrefillParams &p, cudaStream_t st) {
     using namespace pf;
     const uint64_t kv_rows = (uint64_t)p.nh * p.cap_rows;
-    CUtensorMap rows, uk, uv, k_st, v_st, q, k_ld, v_ld, rope;
+    CUtensorMap rows, uk, uv, q, k_ld, v_ld, rope;
     if (!map2d(&rows, p.rows, p.cap_rows, kR + kRope, 128) || !map2d(&uk, p.W_UK, (uint64_t)p.s.H * kDn, kR, 128) ||
-        !map2d(&uv, p.W_UV, (uint64_t)p.s.H * kR, kDv, 64) || !map2d(&k_st, p.k, kv_rows, kDn, 32) ||
-        !map2d(&v_st, p.v, kv_rows, kDv, 32) || !map2d(&k_ld, p.k, kv_rows, kDn, 64) ||
+        !map2d(&uv, p.W_UV, (uint64_t)p.s.H * kR, kDv, 64) || 
+        !map2d(&k_ld, p.k, kv_rows, kDn, 64) ||
         !map2d(&v_ld, p.v, kv_rows, kDv, 128) || !map2d(&rope, p.rows, p.cap_rows, kR + kRope, 64) || !map_q(&q, p.q, p.num_q, p.s.H))
         return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(ex::expand_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ex::kSmemBytes);
@@ -745,7 +743,7 @@ cudaError_t launch_prefill_tc(const PrefillParams &p, cudaStream_t st) {
     heads = heads < 2 ? 2 : heads > p.nh ? p.nh : heads;
     heads += heads & 1;
     ex::expand_tc_kernel<<<dim3((unsigned)(2 * tiles), (unsigned)((p.nh + heads - 1) / heads)), ex::kThreads, ex::kSmemBytes, st>>>(
-        rows, uk, uv, k_st, v_st, p, (int)heads);
+        rows, uk, uv, p, (int)heads);
     prefill_tc_kernel<<<dim3(2 * (p.num_q / kTileQ + p.B), p.nh), kThreads, kSmemBytes, st>>>(q, k_ld, v_ld, rope, p);
     return cudaGetLastError();
 }
