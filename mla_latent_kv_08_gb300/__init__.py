@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 from typing import Optional
 
@@ -149,6 +150,12 @@ def _check(code: int, where: str) -> None:
 
 # ---------------------------------------------------------------- shapes
 
+@functools.lru_cache(maxsize=256)
+def _shape_struct(*fields) -> mla_shape:
+    """The C struct of these fields (the library only reads it)."""
+    return mla_shape(*fields)
+
+
 @dataclasses.dataclass
 class Shape:
     """Problem shape (mirrors ``mla_shape``)."""
@@ -167,7 +174,7 @@ class Shape:
     flags: int = 0
 
     def c(self) -> mla_shape:
-        return mla_shape(self.num_heads, self.kv_lora_rank, self.rope_dim, self.v_head_dim,
+        return _shape_struct(self.num_heads, self.kv_lora_rank, self.rope_dim, self.v_head_dim,
                          self.block_size, self.num_blocks, self.group_size, self.kind, self.impl,
                          self.num_splits_hint, self.index_dim, self.flags)
 
@@ -189,8 +196,8 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:          # the current stream's handle, without an object for it (2.7 us of a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 

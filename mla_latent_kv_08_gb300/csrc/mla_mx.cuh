@@ -57,6 +57,27 @@ __device__ __forceinline__ void mx_place4(uint32_t w, uint32_t &o0, uint32_t &o1
     o0 = (lo << 4) & 0x87f087f0u;
     o1 = (hi << 4) & 0x87f087f0u;
 }
+// Eight codes (memory order) as bf16: `first` times their placed values, where no scale is
+// above 1 the scale and 2^120 in one (mx_scale120), else 2^120 and then `second`. Every
+// product is exact.
+__device__ __forceinline__ uint4 mx_expand8(uint2 c, uint32_t first) {
+    uint4 o;
+    mx_place4(c.x, o.x, o.y);
+    mx_place4(c.y, o.z, o.w);
+    o.x = mul_bf162(o.x, first);
+    o.y = mul_bf162(o.y, first);
+    o.z = mul_bf162(o.z, first);
+    o.w = mul_bf162(o.w, first);
+    return o;
+}
+__device__ __forceinline__ uint4 mx_expand8(uint2 c, uint32_t first, uint32_t second) {
+    uint4 o = mx_expand8(c, first);
+    o.x = mul_bf162(o.x, second);
+    o.y = mul_bf162(o.y, second);
+    o.z = mul_bf162(o.z, second);
+    o.w = mul_bf162(o.w, second);
+    return o;
+}
 // Sixteen codes (memory order) as bf16: `first` times their placed values, where no scale
 // is above 1 the scale and 2^120 in one (mx_scale120), else 2^120 and then `second`. Every
 // product is exact.
@@ -92,14 +113,17 @@ __device__ __forceinline__ float mx_value(uint32_t code, uint32_t scale_byte) {
     return __uint_as_float(h << 16) * 0x1p120f * mx_scale_f32(scale_byte);
 }
 
-// New token n (bf16 latent of r values at c, bf16 rope key at k) into token row `row` of
-// the cache, by one warp: a lane takes 16 values, two lanes a group.
-__device__ __forceinline__ void mx_write_token(const AppendParams &p, const __nv_bfloat16 *c, const __nv_bfloat16 *k,
-                                               size_t row) {
+// A new token's codes, by one warp: a lane takes 16 values (two lanes a group), 512 a pass.
+// `row()` gives the token row of the cache, or below 0 for none; it is asked for once the
+// loads are on their way, which do not depend on it (with the look-up first, its chain of
+// four loads stood before them).
+template <typename Row>
+__device__ __forceinline__ void mx_write_token(const AppendParams &p, const __nv_bfloat16 *c, const __nv_bfloat16 *k, Row row) {
     const int lane = threadIdx.x & 31;
     const int r = p.s.r, dR = p.s.dR, ng = r / kMxGroup;
-    uint8_t *codes = p.codes + row * r;
-    uint8_t *scales = p.mx_scale + row * ng;
+    uint4 rope = make_uint4(0, 0, 0, 0);
+    if (lane < dR / 8) rope = ((const uint4 *)k)[lane];            // d_R <= 128: 16 lanes
+    long long at = 0;
     for (int g0 = 0; g0 < ng; g0 += 16) {
         const int g = g0 + (lane >> 1);
         const bool act = g < ng;
@@ -108,6 +132,10 @@ __device__ __forceinline__ void mx_write_token(const AppendParams &p, const __nv
             const uint4 *src = (const uint4 *)(c + g * kMxGroup + 16 * (lane & 1));
             u[0] = src[0];
             u[1] = src[1];
+        }
+        if (g0 == 0) {
+            at = row();
+            if (at < 0) return;
         }
         const uint32_t *w = (const uint32_t *)u;
         uint32_t m = 0;
@@ -129,11 +157,10 @@ __device__ __forceinline__ void mx_write_token(const AppendParams &p, const __nv
                    ((uint32_t)__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3) << 16);
             if (sb == 255u) o[i] = 0x7f7f7f7fu;
         }
-        *(uint4 *)(codes + g * kMxGroup + 16 * (lane & 1)) = make_uint4(o[0], o[1], o[2], o[3]);
-        if ((lane & 1) == 0) scales[g] = (uint8_t)sb;
+        *(uint4 *)(p.codes + (size_t)at * r + g * kMxGroup + 16 * (lane & 1)) = make_uint4(o[0], o[1], o[2], o[3]);
+        if ((lane & 1) == 0) p.mx_scale[(size_t)at * ng + g] = (uint8_t)sb;
     }
-    uint4 *dst = (uint4 *)(p.rope + row * dR);
-    for (int v = lane; v < dR / 8; v += 32) dst[v] = ((const uint4 *)k)[v];
+    if (lane < dR / 8) ((uint4 *)(p.rope + (size_t)at * dR))[lane] = rope;
 }
 
 }  // namespace mla
