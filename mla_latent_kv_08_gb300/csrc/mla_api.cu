@@ -122,7 +122,8 @@ static WsLayout ws_layout(const mla_shape *s, int32_t B, int32_t q_len, int32_t 
     if (impl == MLA_IMPL_TCGEN05) {
         // one wave of persistent CTAs: 2 per stream per 128-row tile
         const int row_tiles = (q_len * s->num_heads + 127) / 128;
-        target = sms / (2 * row_tiles);
+        // (few rows of the 8-bit kind: one CTA a stream)
+        target = decode_narrow_supported(shape_args(s), q_len) ? sms : sms / (2 * row_tiles);
         if (target < 1) target = 1;
         if (s->num_splits_hint > 0 && s->num_splits_hint < target) target = s->num_splits_hint;
     } else {

@@ -229,6 +229,9 @@ cudaError_t launch_decode_tc(const DecodeParams &p, int32_t max_work, cudaStream
 cudaError_t launch_decode_wide(const DecodeParams &p, int32_t max_work, cudaStream_t st);
 // ---- the same over the 8-bit cache (mla_wide_mx.cu) ---------------------------
 cudaError_t launch_decode_mx(const DecodeParams &p, int32_t max_work, cudaStream_t st);
+// ---- and for at most 64 query rows a sequence (mla_narrow_mx.cu) ---------------
+bool decode_narrow_supported(const ShapeArgs &s, int32_t q_len);
+cudaError_t launch_decode_narrow(const DecodeParams &p, cudaStream_t st);
 // ---- tensor-core combine + W_UV (defined in mla_combine_tc.cu) --------------
 bool combine_tc_supported(const ShapeArgs &s);
 cudaError_t launch_combine_tc(const CombineParams &c, cudaStream_t st);

@@ -210,7 +210,9 @@ def _impl(mla, name):
 
 @pytest.mark.parametrize("impl", IMPLS)
 @pytest.mark.parametrize("H,q_len,lens", [(128, 1, [1, 63, 64, 65, 127, 128, 129, 700]), (16, 1, [300, 2]), (20, 3, [3, 130, 64]),
-                                          (1, 1, [77]), (128, 2, [513, 2]), (96, 8, [8, 9, 200])])
+                                          (1, 1, [77]), (128, 2, [513, 2]), (96, 8, [8, 9, 200]),
+                                          (32, 1, [1, 64, 128, 400, 2000]), (64, 1, [63, 65, 129, 1500]), (8, 8, [8, 70, 300]),
+                                          (4, 8, [130, 9]), (65, 1, [200])])
 def test_decode_and_verify(gpu_lib, impl, H, q_len, lens):
     import mla_latent_kv_08_gb300 as mla
     w = _workload(20 + H + q_len, lens, H=H, q_len=q_len)
@@ -232,11 +234,12 @@ def test_decode_other_shapes(gpu_lib, r, d_rope, d_v, H, bs):
     _check(w, out, lse, _stored(w))
 
 
+@pytest.mark.parametrize("H", [32, 128])
 @pytest.mark.parametrize("impl", IMPLS)
 @pytest.mark.parametrize("splits", [1, 7, 200])
-def test_split_count_does_not_matter(gpu_lib, impl, splits):
+def test_split_count_does_not_matter(gpu_lib, impl, splits, H):
     import mla_latent_kv_08_gb300 as mla
-    w = _workload(50, [2100, 64, 900], H=32)
+    w = _workload(50, [2100, 64, 900], H=H)
     shape = _shape(mla, w, impl=_impl(mla, impl), num_splits_hint=splits)
     cache, _ = gu.fill_cache(w, shape)
     out, lse, ws = gu.attend(w, shape, cache, w.q)
@@ -244,12 +247,13 @@ def test_split_count_does_not_matter(gpu_lib, impl, splits):
     _check(w, out, lse, _stored(w), [0, 2])
 
 
+@pytest.mark.parametrize("H", [16, 64, 128])
 @pytest.mark.parametrize("impl", IMPLS)
-def test_stale_slots_are_not_read(gpu_lib, impl):
+def test_stale_slots_are_not_read(gpu_lib, impl, H):
     """NaN codes, scales and rope keys behind a sequence's end (in its last block, and in
     blocks it does not use) leave no trace."""
     import mla_latent_kv_08_gb300 as mla
-    w = _workload(51, [1, 63, 65, 190], H=128)
+    w = _workload(51, [1, 63, 65, 190], H=H)
     shape = _shape(mla, w, impl=_impl(mla, impl))
     cache = mla.Cache.allocate(shape)
     cache.codes.fill_(0x7F), cache.scale_zero.fill_(0xFF), cache.rope.fill_(float("nan"))
@@ -259,10 +263,11 @@ def test_stale_slots_are_not_read(gpu_lib, impl):
     _check(w, out, lse, _stored(w))
 
 
+@pytest.mark.parametrize("H", [16, 128])
 @pytest.mark.parametrize("impl", IMPLS)
-def test_bad_lengths_and_blocks_give_nan_rows(gpu_lib, impl):
+def test_bad_lengths_and_blocks_give_nan_rows(gpu_lib, impl, H):
     import mla_latent_kv_08_gb300 as mla
-    w = _workload(52, [200, 300, 100, 70], H=128)
+    w = _workload(52, [200, 300, 100, 70], H=H)
     shape = _shape(mla, w, impl=_impl(mla, impl))
     cache, _ = gu.fill_cache(w, shape)
     lat = _stored(w)
@@ -275,11 +280,12 @@ def test_bad_lengths_and_blocks_give_nan_rows(gpu_lib, impl):
     _check(w, out, lse, lat, [0])
 
 
+@pytest.mark.parametrize("H", [16, 128])
 @pytest.mark.parametrize("k", [1, 3, 700])
-def test_append_decode_is_append_then_decode(gpu_lib, k):
+def test_append_decode_is_append_then_decode(gpu_lib, k, H):
     import mla_latent_kv_08_gb300 as mla
     import torch
-    w = _workload(53, [900, 800, 1000, 750, 801, 720], H=128)
+    w = _workload(53, [900, 800, 1000, 750, 801, 720], H=H)
     shape = _shape(mla, w)
     pos = (w.seq_lens - k).astype(np.int32)
     one, _ = gu.fill_cache(w, shape)
@@ -346,3 +352,57 @@ def test_decode_captured_and_replayed_on_a_side_stream(gpu_lib):
     lat = [c[:L] for c, L in zip(_stored(w), w.seq_lens)]
     w.rope = [c[:L] for c, L in zip(w.rope, w.seq_lens)]
     _check(w, out.float().cpu().numpy(), lse.cpu().numpy(), lat)
+
+
+@pytest.mark.parametrize("H", [32, 64, 128])
+def test_maxima_that_keep_rising(gpu_lib, H):
+    """Scores that grow along the cache: every step raises the running maximum past its bound."""
+    import mla_latent_kv_08_gb300 as mla
+    w = _workload(56, [1000, 130], H=H)
+    for b, L in enumerate(w.seq_lens):
+        ramp = np.linspace(0, 60, L, dtype=np.float32)[:, None]
+        w.rope[b] = workloads.bf16_round(np.abs(w.rope[b]) * np.float32(0.1) + ramp / 8)
+    w.q[..., 512:] = workloads.bf16_round(np.abs(w.q[..., 512:]))
+    w.q[:, :, ::3, 512:] *= -1                                   # and rows whose scores fall
+    shape = _shape(mla, w)
+    cache, _ = gu.fill_cache(w, shape)
+    out, lse, ws = gu.attend(w, shape, cache, w.q)
+    assert mla.mla_get_status(ws) == (mla.MLA_OK, 0)
+    lat = _stored(w)
+    for b in range(2):
+        ro, rl = attention.absorbed(w.q[b], lat[b], w.rope[b], w.W_UV, w.scale)
+        assert gu.rel_err(out[b], ro) <= gu.BF16_REL_TOL
+        assert np.max(np.abs(lse[b] - rl)) <= gu.BF16_LSE_TOL
+
+
+@pytest.mark.parametrize("H", [16, 128])
+@pytest.mark.parametrize("scale", [0.0, -0.05])
+def test_scales_of_either_sign(gpu_lib, H, scale):
+    import mla_latent_kv_08_gb300 as mla
+    w = _workload(57, [200, 65], H=H)
+    w.scale = scale
+    shape = _shape(mla, w)
+    cache, _ = gu.fill_cache(w, shape)
+    out, lse, ws = gu.attend(w, shape, cache, w.q)
+    assert mla.mla_get_status(ws) == (mla.MLA_OK, 0)
+    _check(w, out, lse, _stored(w))
+
+
+def test_scales_above_one(gpu_lib):
+    """Latents whose groups' scales are above 1 and below it take both ways through the expansion."""
+    import mla_latent_kv_08_gb300 as mla
+    for H in (16, 128):
+        w = _workload(58, [300, 70], H=H)
+        for c in w.latent:
+            c[::7] = workloads.bf16_round(c[::7] * np.float32(2000))
+        w.scale = 1e-4
+        shape = _shape(mla, w)
+        cache, _ = gu.fill_cache(w, shape)
+        out, lse, ws = gu.attend(w, shape, cache, w.q)
+        assert mla.mla_get_status(ws) == (mla.MLA_OK, 0)
+        assert int(cache.scale_zero.max()) > 127
+        lat = _stored(w)
+        for b in range(2):
+            ro, rl = attention.absorbed(w.q[b], lat[b], w.rope[b], w.W_UV, w.scale)
+            assert gu.rel_err(out[b], ro) <= gu.BF16_REL_TOL
+            assert np.max(np.abs(lse[b] - rl)) <= gu.BF16_LSE_TOL
