@@ -122,7 +122,7 @@ static WsLayout ws_layout(const mla_shape *s, int32_t B, int32_t q_len, int32_t 
     if (impl == MLA_IMPL_TCGEN05) {
         // one wave of persistent CTAs: 2 per stream per 128-row tile
         const int row_tiles = (q_len * s->num_heads + 127) / 128;
-        // (few rows of the 8-bit kind: one CTA a stream)
+        // (few rows of the 8-bit kind may get one CTA a stream: see run_attention)
         target = decode_narrow_supported(shape_args(s), q_len) ? sms : sms / (2 * row_tiles);
         if (target < 1) target = 1;
         if (s->num_splits_hint > 0 && s->num_splits_hint < target) target = s->num_splits_hint;
@@ -217,6 +217,11 @@ static mla_status run_attention(const mla_shape *s, const mla_cache *cache, cons
     p.split_start = (const int32_t *)(ws + w.split_start);
     p.stream_start = (const int32_t *)(ws + w.stream_start);
     p.streams = w.target;
+    if (impl == MLA_IMPL_TCGEN05 && decode_narrow_supported(p.s, q_len)) {
+        const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
+        p.narrow = decode_narrow_wins(p.s, q_len, (int64_t)B * max_blocks * s->block_size, sms);
+        if (!p.narrow && p.streams > sms / 2) p.streams = sms / 2;      // pairs of CTAs
+    }
     p.part_o = (float *)(ws + w.part_o);
     p.part_lse = (float *)(ws + w.part_lse);
 

@@ -98,6 +98,7 @@ struct DecodeParams {
     int32_t streams;
     int32_t item_cost;           // planner: units charged per sequence start (its Q load, epilogue)
     int32_t plan_tile;           // planner: tokens per cost unit; work items start at multiples of it
+    int32_t narrow;              // MXFP8 on the tensor cores: the kernel for few query rows, a CTA a stream
     float *part_o;
     float *part_lse;
 };
@@ -231,6 +232,8 @@ cudaError_t launch_decode_wide(const DecodeParams &p, int32_t max_work, cudaStre
 cudaError_t launch_decode_mx(const DecodeParams &p, int32_t max_work, cudaStream_t st);
 // ---- and for at most 64 query rows a sequence (mla_narrow_mx.cu) ---------------
 bool decode_narrow_supported(const ShapeArgs &s, int32_t q_len);
+// Whether it is the faster one for sequences of up to `tokens` cached tokens together.
+bool decode_narrow_wins(const ShapeArgs &s, int32_t q_len, int64_t tokens, int32_t sms);
 cudaError_t launch_decode_narrow(const DecodeParams &p, cudaStream_t st);
 // ---- tensor-core combine + W_UV (defined in mla_combine_tc.cu) --------------
 bool combine_tc_supported(const ShapeArgs &s);

@@ -13,10 +13,11 @@
 //                                        blocks read as an MN-major first operand, P^T an
 //                                        MN-major second one
 //
-// The row maxima run across threads here. They are raised lazily (P <= 2^8), and a step in
-// which no thread sees a score past its row's bound, nearly every one after a sequence's
-// first, needs no reduction: one vote of the four softmax warps. Row sums stay a thread's
-// own until the end of a work item.
+// The row maxima run across threads here, and any m will do that keeps the weights in the
+// range of their types. So m starts at 0, and a step whose exponents all stay below 2^20
+// (and, at an item's first, above 2^-20) takes one vote of the four softmax warps and no
+// reduction; one that does not finds the rows' maxima and moves m there. Row sums stay a
+// thread's own until the end of a work item.
 //
 // Shared memory: nine 16 KB column blocks of a step (the rope block, done with after the
 // scores, then holds P^T), Q, statistics. The blocks of dim tile c are written again for the
@@ -68,6 +69,7 @@ template <int N> struct Lay {
 constexpr uint32_t kColS = 0, kColO = 64;
 constexpr unsigned long long kTimeoutNs = 2000000000ull;       // 2 s bounded-wait safety net
 constexpr int kPrefetchAhead = 4;                     // blocks prefetched into L2 ahead
+constexpr float kBound = 20.f;                        // of the exponents, log2
 
 struct Bars {
     uint64_t full[4];         // dim tile c's two blocks are expanded
@@ -89,6 +91,22 @@ __host__ __device__ constexpr uint32_t idesc_mn(int M, int N) { return idesc_bf1
 // Shared-memory matrix descriptor: 64-byte swizzle (16-byte chunk index XOR row / 2 % 4).
 __device__ __forceinline__ uint64_t sdesc64(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
     return (sdesc(saddr, lbo, sbo) & ~((uint64_t)7 << 61)) | ((uint64_t)4 << 61);
+}
+
+__device__ __forceinline__ bool mbar_test32(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// The bounded wait for a barrier that mbar_test32 found open, out of line.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, int32_t *abort_flag, int32_t *status) {
+    return mbar_wait_bounded((uint64_t *)__cvta_shared_to_generic(bar), parity, abort_flag, status, FLAG_TIMEOUT, kTimeoutNs);
 }
 
 // OR over the four softmax warps.
@@ -118,6 +136,19 @@ __device__ __forceinline__ float reduce_rows(uint32_t (&v)[32]) {
     }
     return __uint_as_float(v[0]);
 }
+
+// Pipeline timestamps for performance analysis, compiled only with -DMLA_TRACE: clock64 at
+// each hand-off of CTA 0 for its first kTraceSteps steps. Product builds contain none of it.
+// Events: 0..3 dim tile expanded, 4 scores issued, 5 P seen, 6 P . V issued (MMA), 7 scores
+// seen, 8 voted, 9 P stored (softmax), 10 tile 0 free, 11 tile 0 expanded, 12 tile 3 free,
+// 13 tile 3 expanded (warp 8)
+#ifdef MLA_TRACE
+constexpr int kTraceSteps = 64;
+__device__ long long g_nmtrace[14][kTraceSteps];
+#define NTRACE(ev, step)                                                                  do {                                                                                      if (blockIdx.x == 0 && (step) < kTraceSteps) g_nmtrace[ev][step] = clock64();     } while (0)
+#else
+#define NTRACE(ev, step)     do {                     } while (0)
+#endif
 
 // Physical block of logical block `lb` of sequence b, or -1.
 __device__ __forceinline__ int block_of(const DecodeParams &p, int b, int lb) {
@@ -248,6 +279,12 @@ decode_narrow_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_
             const uint64_t pd = N > 32 ? sdesc(smem_u32(smem + kOffP), kCol, 1024) : sdesc64(smem_u32(smem + kOffP), kCol, 512);
             constexpr uint32_t kPStep = N > 32 ? 128 : 64;     // 16 tokens, in 16-byte units
             const uint32_t d_s = tmem + kColS;
+            // The thread's own pace counts here (68 products of few columns a step): the first
+            // probe of a barrier is inline, the bounded wait out of line.
+            const uint32_t full0 = smem_u32(&bars->full[0]), full_r = smem_u32(&bars->full_r), p_full = smem_u32(&bars->p_full);
+            auto there = [&](uint32_t bar, uint32_t parity) {
+                return mbar_test32(bar, parity) || wait_slow(bar, parity, &bars->abort_flag, p.status);
+            };
             bool ok = true;
             int K = 0, items = 0;
             for (int i = i0; i < i1 && ok; ++i, ++items) {
@@ -257,39 +294,48 @@ decode_narrow_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_
                 for (int j = 0; j < ns && ok; ++j, ++K) {
                     // scores, a dim tile's two blocks as they are expanded (descriptor start
                     // addresses advance in 16-byte units)
+                    uint64_t a = kd, b = qd;
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
-                        ok = wait(&bars->full[c], K & 1);
+                        ok = there(full0 + 8 * c, K & 1);
                         if (!ok) break;
+                        NTRACE(c, K);
                         tc_fence_after();
+                        mma_ss(d_s, a, b, kIdS, c > 0 ? 1u : 0u);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const uint64_t a = kd + (uint64_t)(((2 * c + (e >> 2)) * kCol + 32 * (e & 3)) >> 4);
-                            const uint64_t b = qd + (uint64_t)(((2 * c + (e >> 2)) * LY::kQBlock + 32 * (e & 3)) >> 4);
-                            mma_ss(d_s, a, b, kIdS, (c > 0 || e > 0) ? 1u : 0u);
-                        }
+                        for (int e = 1; e < 8; ++e)
+                            mma_ss_k<kIdS, 1>(d_s, a + (uint64_t)(((e >> 2) * kCol + 32 * (e & 3)) >> 4),
+                                              b + (uint64_t)(((e >> 2) * LY::kQBlock + 32 * (e & 3)) >> 4));
+                        a += (2 * kCol) >> 4;
+                        b += (2 * LY::kQBlock) >> 4;
                     }
-                    ok = ok && wait(&bars->full_r, K & 1);
+                    ok = ok && there(full_r, K & 1);
                     if (!ok) break;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        mma_ss_k<kIdS, 1>(d_s, kd + (uint64_t)((8 * kCol + 32 * e) >> 4), qd + (uint64_t)((8 * LY::kQBlock + 32 * e) >> 4));
+                    for (int e = 0; e < 4; ++e) mma_ss_k<kIdS, 1>(d_s, a + 2 * e, b + 2 * e);
                     mma_commit(&bars->s_full);
+                    NTRACE(4, K);
                     if (j + 1 == ns) mma_commit(&bars->q_free);
                     // P . V, a dim tile at a time: its blocks are free as soon as it is done
                     if (j == 0 && items > 0) ok = wait(&bars->o_free, (items - 1) & 1);
-                    ok = ok && wait(&bars->p_full, K & 1);
+                    ok = ok && there(p_full, K & 1);
                     if (!ok) break;
+                    NTRACE(5, K);
                     tc_fence_after();
+                    uint64_t v = vd;
+                    uint32_t d_o = tmem + kColO;
+                    uint64_t *bar = &bars->empty[0];
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
+                        mma_ss(d_o, v, pd, kIdO, j > 0 ? 1u : 0u);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            mma_ss(tmem + kColO + 64 * c, vd + (uint64_t)((2 * c * kCol) >> 4) + 128 * e, pd + kPStep * e, kIdO,
-                                   (j > 0 || e > 0) ? 1u : 0u);
-                        mma_commit(&bars->empty[c]);
+                        for (int e = 1; e < 8; ++e) mma_ss_k<kIdO, 1>(d_o, v + 128 * e, pd + kPStep * e);
+                        mma_commit(bar++);
+                        v += (2 * kCol) >> 4;
+                        d_o += 64;
                     }
                     mma_commit(&bars->pv_done);
+                    NTRACE(6, K);
                 }
             }
             // products in flight must end before the tensor memory is given back
@@ -322,6 +368,7 @@ decode_narrow_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_
             for (int j = 0; j < ns; ++j, ++K) {
                 const bool mine_ok = __all_sync(0xffffffffu, wait(&bars->s_full, K & 1));
                 tc_fence_after();
+                if (tok_row == 0) NTRACE(7, K);
                 const int tok = it.t0 + j * kStep + tok_row;
                 // rows before n_min do not see this token (drafts; or the slot is past the end)
                 const int n_min = tok >= it.t1 ? N : max(0, (tok - (L - p.q_len)) * p.s.H);
@@ -344,19 +391,24 @@ decode_narrow_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_
                             if (32 * h + n < n_min) sv[n] = __float_as_uint(-CUDART_INF_F);
                     }
                 };
-                float top = -CUDART_INF_F;                     // the largest exponent
+                float top = -CUDART_INF_F, low = CUDART_INF_F; // the largest and the least visible exponent
 #pragma unroll 1
                 for (int h = 0; h < N / 32; ++h) {
                     exponents(h);
 #pragma unroll
                     for (int n = 0; n < 32; ++n) top = fmaxf(top, __uint_as_float(sv[n]));
+                    if (j == 0)
+#pragma unroll
+                        for (int n = 0; n < 32; ++n)
+                            low = fminf(low, __uint_as_float(sv[n]) == -CUDART_INF_F ? 0.f : __uint_as_float(sv[n]));
                 }
-                const bool slow = soft_any(j == 0 || top > 8.f || !mine_ok);
+                const bool slow = soft_any(top > kBound || (j == 0 && low < -kBound) || !mine_ok);
+                if (tok_row == 0) NTRACE(8, K);
                 if (slow) {
                     ok = !soft_any(!mine_ok);
                     if (!ok) break;
-                    // The maxima of every row over the step's tokens; m rises where they are past
-                    // the bound (at the item's first step to the maximum itself).
+                    // The maxima of every row over the step's tokens; m becomes them at the item's
+                    // first step, and rises to them later where they are past the bound.
 #pragma unroll 1
                     for (int h = 0; h < N / 32; ++h) {
                         exponents(h);
@@ -366,7 +418,7 @@ decode_narrow_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_
                     if (tok_row < N) {
                         const float d = fmaxf(fmaxf(red_s[tok_row], red_s[64 + tok_row]),
                                               fmaxf(red_s[128 + tok_row], red_s[192 + tok_row]));
-                        const bool raise = d != -CUDART_INF_F && (j == 0 || d > 8.f);
+                        const bool raise = d != -CUDART_INF_F && (j == 0 || d > kBound);
                         alpha_s[tok_row] = raise && j > 0 ? exp2f(-d) : 1.f;
                         if (raise) nm_s[tok_row] -= d;
                     }
@@ -410,6 +462,7 @@ decode_narrow_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_
                 tc_fence_before();
                 fence_proxy_async();
                 mbar_arrive(&bars->p_full);
+                if (tok_row == 0) NTRACE(9, K);
             }
             if (!ok) break;
             ok = __all_sync(0xffffffffu, wait(&bars->pv_done, (K - 1) & 1));
@@ -522,7 +575,7 @@ decode_narrow_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_
             return true;
         };
         Half s0;
-        Rows x0, x1, x2, x3;               // the step's dim tiles, each loaded when its last was expanded
+        Rows x0, x1, x2, x3;               // the step's dim tiles
         next(s0);
         load(x0, s0, 0);
         load(x1, s0, 1);
@@ -532,13 +585,20 @@ decode_narrow_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_
         for (int K = 0;; ++K) {
             auto part = [&](Rows &x, int c) {
                 if (K > 0 && !__all_sync(0xffffffffu, wait(&bars->empty[c], (K - 1) & 1))) return false;
+                if (tid == 256 && c % 3 == 0) NTRACE(c == 0 ? 10 : 12, K);
                 expand(x, to0 + 2u * c * kCol);
                 fence_proxy_async();
                 mbar_arrive(&bars->full[c]);
-                if (more) load(x, s0, c);
+                if (tid == 256 && c % 3 == 0) NTRACE(c == 0 ? 11 : 13, K);
                 return true;
             };
             if (!part(x0, 0) || !part(x1, 1) || !part(x2, 2) || !part(x3, 3) || !more) break;
+            // all the next step's loads at once, after the last use of this one's (loads share
+            // the few counters that a use waits for)
+            load(x0, s0, 0);
+            load(x1, s0, 1);
+            load(x2, s0, 2);
+            load(x3, s0, 3);
             more = next(s0);
         }
         __syncwarp();
@@ -603,8 +663,25 @@ static cudaError_t launch(const DecodeParams &p, cudaStream_t st) {
 
 bool decode_narrow_supported(const ShapeArgs &s, int32_t q_len) { return is_mx(s.kind) && (long long)q_len * s.H <= 64; }
 
+// A step of this kernel takes 1.26 (32 columns) to 1.5 (64) times the pair kernel's, on one
+// SM instead of two, but its first step costs more. Measured calls, pair / this, at 16 rows:
+// 26.8 / 26.0 us for 32 sequences of 300 tokens, 39.5 / 32.6 of 1250, 87.0 / 62.2 of 5000;
+// one sequence of 169 tokens 18.2 / 20.4. At 64 rows: 28.0 / 33.5 us of 600, 39.5 / 39.9 of
+// 1250, 55.1 / 51.0 of 2500, 85.5 / 72.1 of 5000. So: from one step a CTA on for 32 columns,
+// from four on for 64. The tokens are what the block table has room for (the lengths are on
+// the device).
+bool decode_narrow_wins(const ShapeArgs &s, int32_t q_len, int64_t tokens, int32_t sms) {
+    return tokens >= (int64_t)(q_len * s.H <= 32 ? 1 : 4) * nmx::kStep * sms;
+}
+
 cudaError_t launch_decode_narrow(const DecodeParams &p, cudaStream_t st) {
     return p.q_len * p.s.H <= 32 ? nmx::launch<32>(p, st) : nmx::launch<64>(p, st);
 }
 
 }  // namespace mla
+
+#ifdef MLA_TRACE
+extern "C" int mla_narrow_trace_read(long long *events) {
+    return (int)cudaMemcpyFromSymbol(events, mla::nmx::g_nmtrace, sizeof(mla::nmx::g_nmtrace));
+}
+#endif

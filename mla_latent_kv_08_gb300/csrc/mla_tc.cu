@@ -983,7 +983,7 @@ cudaError_t launch_decode_tc(const DecodeParams &p, int32_t max_work, cudaStream
     // the bf16 and 8-bit caches: two cache blocks per score MMA (mla_wide.cu, mla_wide_mx.cu)
     if (p.s.kind == MLA_KV_BF16) return launch_decode_wide(p, max_work, st);
     if (is_mx(p.s.kind))
-        return decode_narrow_supported(p.s, p.q_len) ? launch_decode_narrow(p, st) : launch_decode_mx(p, max_work, st);
+        return p.narrow ? launch_decode_narrow(p, st) : launch_decode_mx(p, max_work, st);
     tc::TcParams tp;
     tp.p = p;
     tp.row_tiles = (p.q_len * p.s.H + tc::kRows - 1) / tc::kRows;

@@ -194,6 +194,15 @@ def test_read_outside_the_cache_gives_nan_rows(gpu_lib):
 
 # ------------------------------------------------------------------ decode and verify
 
+def _roomy(w):
+    """The same sequences under a block table that has room for long ones: by that room the
+    library takes its kernel for few query rows."""
+    wide = np.full((w.B, 20000 // w.B + 10), -1, np.int32)
+    wide[:, :w.block_table.shape[1]] = w.block_table
+    w.block_table = wide
+    return w
+
+
 def _check(w, out, lse, lat, seqs=None):
     for b in range(w.B) if seqs is None else seqs:
         ro, rl = attention.absorbed(w.q[b], lat[b], w.rope[b], w.W_UV, w.scale)
@@ -201,7 +210,7 @@ def _check(w, out, lse, lat, seqs=None):
         assert np.max(np.abs(lse[b] - rl)) <= gu.BF16_LSE_TOL, (b, np.max(np.abs(lse[b] - rl)))
 
 
-IMPLS = ["auto", "simt"]
+IMPLS = ["auto", "roomy", "simt"]
 
 
 def _impl(mla, name):
@@ -216,6 +225,8 @@ def _impl(mla, name):
 def test_decode_and_verify(gpu_lib, impl, H, q_len, lens):
     import mla_latent_kv_08_gb300 as mla
     w = _workload(20 + H + q_len, lens, H=H, q_len=q_len)
+    if impl == "roomy":
+        _roomy(w)
     shape = _shape(mla, w, impl=_impl(mla, impl))
     cache, _ = gu.fill_cache(w, shape)
     out, lse, ws = gu.attend(w, shape, cache, w.q, q_len=q_len)
@@ -240,6 +251,8 @@ def test_decode_other_shapes(gpu_lib, r, d_rope, d_v, H, bs):
 def test_split_count_does_not_matter(gpu_lib, impl, splits, H):
     import mla_latent_kv_08_gb300 as mla
     w = _workload(50, [2100, 64, 900], H=H)
+    if impl == "roomy":
+        _roomy(w)
     shape = _shape(mla, w, impl=_impl(mla, impl), num_splits_hint=splits)
     cache, _ = gu.fill_cache(w, shape)
     out, lse, ws = gu.attend(w, shape, cache, w.q)
@@ -254,6 +267,8 @@ def test_stale_slots_are_not_read(gpu_lib, impl, H):
     blocks it does not use) leave no trace."""
     import mla_latent_kv_08_gb300 as mla
     w = _workload(51, [1, 63, 65, 190], H=H)
+    if impl == "roomy":
+        _roomy(w)
     shape = _shape(mla, w, impl=_impl(mla, impl))
     cache = mla.Cache.allocate(shape)
     cache.codes.fill_(0x7F), cache.scale_zero.fill_(0xFF), cache.rope.fill_(float("nan"))
@@ -268,11 +283,13 @@ def test_stale_slots_are_not_read(gpu_lib, impl, H):
 def test_bad_lengths_and_blocks_give_nan_rows(gpu_lib, impl, H):
     import mla_latent_kv_08_gb300 as mla
     w = _workload(52, [200, 300, 100, 70], H=H)
+    if impl == "roomy":
+        _roomy(w)
     shape = _shape(mla, w, impl=_impl(mla, impl))
     cache, _ = gu.fill_cache(w, shape)
     lat = _stored(w)
     w.block_table[1, 2] = -5
-    w.seq_lens = np.array([200, 300, 10 ** 6, 0], np.int32)
+    w.seq_lens = np.array([200, 300, 10 ** 7, 0], np.int32)
     out, lse, ws = gu.attend(w, shape, cache, w.q)
     code, flags = mla.mla_get_status(ws)
     assert code == mla.MLA_ERR_BOUNDS and flags & 3 == 3
@@ -280,12 +297,14 @@ def test_bad_lengths_and_blocks_give_nan_rows(gpu_lib, impl, H):
     _check(w, out, lse, lat, [0])
 
 
-@pytest.mark.parametrize("H", [16, 128])
+@pytest.mark.parametrize("H,room", [(16, False), (16, True), (128, False)])
 @pytest.mark.parametrize("k", [1, 3, 700])
-def test_append_decode_is_append_then_decode(gpu_lib, k, H):
+def test_append_decode_is_append_then_decode(gpu_lib, k, H, room):
     import mla_latent_kv_08_gb300 as mla
     import torch
     w = _workload(53, [900, 800, 1000, 750, 801, 720], H=H)
+    if room:
+        _roomy(w)
     shape = _shape(mla, w)
     pos = (w.seq_lens - k).astype(np.int32)
     one, _ = gu.fill_cache(w, shape)
@@ -323,11 +342,14 @@ def test_noalloc_decode(gpu_lib):
     assert np.max(np.abs(lse.cpu().numpy() - lse1)) <= gu.BF16_LSE_TOL
 
 
-def test_decode_captured_and_replayed_on_a_side_stream(gpu_lib):
+@pytest.mark.parametrize("H,room", [(128, False), (32, True)])
+def test_decode_captured_and_replayed_on_a_side_stream(gpu_lib, H, room):
     """A captured step follows its buffers: new codes and lengths under a replay."""
     import mla_latent_kv_08_gb300 as mla
     import torch
-    w = _workload(55, [400, 129], H=128)
+    w = _workload(55, [400, 129], H=H)
+    if room:
+        _roomy(w)
     shape = _shape(mla, w)
     cache, _ = gu.fill_cache(w, shape)
     bf = torch.bfloat16
@@ -354,11 +376,13 @@ def test_decode_captured_and_replayed_on_a_side_stream(gpu_lib):
     _check(w, out.float().cpu().numpy(), lse.cpu().numpy(), lat)
 
 
-@pytest.mark.parametrize("H", [32, 64, 128])
-def test_maxima_that_keep_rising(gpu_lib, H):
+@pytest.mark.parametrize("H,room", [(32, True), (64, True), (64, False), (128, False)])
+def test_maxima_that_keep_rising(gpu_lib, H, room):
     """Scores that grow along the cache: every step raises the running maximum past its bound."""
     import mla_latent_kv_08_gb300 as mla
     w = _workload(56, [1000, 130], H=H)
+    if room:
+        _roomy(w)
     for b, L in enumerate(w.seq_lens):
         ramp = np.linspace(0, 60, L, dtype=np.float32)[:, None]
         w.rope[b] = workloads.bf16_round(np.abs(w.rope[b]) * np.float32(0.1) + ramp / 8)
@@ -375,11 +399,13 @@ def test_maxima_that_keep_rising(gpu_lib, H):
         assert np.max(np.abs(lse[b] - rl)) <= gu.BF16_LSE_TOL
 
 
-@pytest.mark.parametrize("H", [16, 128])
-@pytest.mark.parametrize("scale", [0.0, -0.05])
-def test_scales_of_either_sign(gpu_lib, H, scale):
+@pytest.mark.parametrize("H,room", [(16, True), (16, False), (64, True), (128, False)])
+@pytest.mark.parametrize("scale", [0.0, -0.05, 2.0])
+def test_scales_of_either_sign(gpu_lib, H, room, scale):
     import mla_latent_kv_08_gb300 as mla
     w = _workload(57, [200, 65], H=H)
+    if room:
+        _roomy(w)
     w.scale = scale
     shape = _shape(mla, w)
     cache, _ = gu.fill_cache(w, shape)
@@ -391,8 +417,10 @@ def test_scales_of_either_sign(gpu_lib, H, scale):
 def test_scales_above_one(gpu_lib):
     """Latents whose groups' scales are above 1 and below it take both ways through the expansion."""
     import mla_latent_kv_08_gb300 as mla
-    for H in (16, 128):
+    for H, room in ((16, True), (64, True), (128, False)):
         w = _workload(58, [300, 70], H=H)
+        if room:
+            _roomy(w)
         for c in w.latent:
             c[::7] = workloads.bf16_round(c[::7] * np.float32(2000))
         w.scale = 1e-4
@@ -406,3 +434,42 @@ def test_scales_above_one(gpu_lib):
             ro, rl = attention.absorbed(w.q[b], lat[b], w.rope[b], w.W_UV, w.scale)
             assert gu.rel_err(out[b], ro) <= gu.BF16_REL_TOL
             assert np.max(np.abs(lse[b] - rl)) <= gu.BF16_LSE_TOL
+
+
+def test_low_scores_on_the_few_row_kernel(gpu_lib):
+    """Scores far below 0 at a sequence's start, and a few far above later: both leave the range
+    that the few-row kernel takes without looking for maxima."""
+    import mla_latent_kv_08_gb300 as mla
+    w = _workload(59, [700, 129], H=32)
+    w.q[...] = workloads.bf16_round(np.abs(w.q))
+    for b, L in enumerate(w.seq_lens):
+        w.latent[b] = np.zeros_like(w.latent[b])
+        level = np.where(np.arange(L) < 300, -3.0, -1.0).astype(np.float32)
+        level[L // 2] = 8.0
+        w.rope[b] = workloads.bf16_round(np.repeat(level[:, None], 64, 1) + w.rope[b] * np.float32(0.05))
+        w.latent[b][:, :32] = workloads.bf16_round(np.random.default_rng(b).standard_normal((L, 32)).astype(np.float32))
+    _roomy(w)
+    shape = _shape(mla, w)
+    cache, _ = gu.fill_cache(w, shape)
+    out, lse, ws = gu.attend(w, shape, cache, w.q)
+    assert mla.mla_get_status(ws) == (mla.MLA_OK, 0)
+    lat = _stored(w)
+    for b in range(2):
+        ro, rl = attention.absorbed(w.q[b], lat[b], w.rope[b], w.W_UV, w.scale)
+        assert gu.rel_err(out[b], ro) <= gu.BF16_REL_TOL
+        assert np.max(np.abs(lse[b] - rl)) <= gu.BF16_LSE_TOL
+
+
+def test_few_rows_many_sequences(gpu_lib):
+    """More sequences than CTAs, so that a CTA takes several work items, of all lengths."""
+    import mla_latent_kv_08_gb300 as mla
+    w = _workload(60, [1 + 7 * i % 200 for i in range(400)], H=4)
+    for room in (True, False):
+        if room:
+            _roomy(w)
+        shape = _shape(mla, w)
+        cache, _ = gu.fill_cache(w, shape)
+        out, lse, ws = gu.attend(w, shape, cache, w.q)
+        assert mla.mla_get_status(ws) == (mla.MLA_OK, 0)
+        _check(w, out, lse, _stored(w), range(0, 400, 13))
+        w = _workload(60, [1 + 7 * i % 200 for i in range(400)], H=4)
