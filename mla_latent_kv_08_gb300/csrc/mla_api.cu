@@ -529,7 +529,7 @@ mla_status mla_prefill(const mla_shape *shape, const mla_cache *cache, const int
     p.num_q = num_q;
     p.dn = nope_dim;
     const bool tc = prefill_tc(shape, nope_dim);
-    p.tile_q = tc ? 512 : 16;
+    p.tile_q = tc ? prefill_tc_tile(num_q, B) : 16;
     p.cap_rows = w.cap_rows;
     p.seq_lens = seq_lens;
     p.cu_q = cu_q;

@@ -293,7 +293,9 @@ expand_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_cons
 
 // ============================================================================
 // Attention. A pair of CTAs (a cluster of two) takes up to 512 new tokens of one sequence
-// for one head, as two sub-tiles of 256 rows, CTA r of the pair holding 128 rows of each.
+// for one head, as two sub-tiles of 256 rows, CTA r of the pair holding 128 rows of each
+// (SUBS = 2). For chunks of few tokens it takes one sub-tile (SUBS = 1), in so little shared
+// memory that two pairs share their SMs: their set-ups, waits and outputs overlap.
 // Both sub-tiles go through the same 128-token steps of the cache in turn: while one's
 // warpgroups turn scores into weights, the tensor cores work on the other.
 //
@@ -314,35 +316,39 @@ expand_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_cons
 // Shared memory: Q 96 KB, three stages of key blocks ([64 tokens x 64 dims] each) and a value
 // block ([128 tokens x 64 columns]). Tensor memory: S0, S1, O0, O1, 128 columns each.
 // ============================================================================
-constexpr int kThreads = 384;          // warp 0 copies, 1 products (CTA 0), 4..7 and 8..11 softmax of sub-tiles 0 and 1
-// Registers a thread of the first warpgroup (copies and products) and of the other two
-// (softmax) once they are split again: what the launch had, 3 x 168.
-constexpr int kRegsLaunch = 168, kRegsIssue = 104, kRegsSoftmax = 200;
-static_assert(kRegsIssue + 2 * kRegsSoftmax <= 3 * kRegsLaunch, "register split");
-constexpr int kTileQ = 512;
-constexpr int kStages = 3;
 constexpr uint32_t kKBlock = 64 * 128;                  // 8 KB
 constexpr uint32_t kOffV = 3 * kKBlock;                 // of a stage
 constexpr uint32_t kStage = kOffV + kBlock;             // 40 KB
-constexpr uint32_t kOffQ = 0;
-constexpr uint32_t kOffRing = 6 * kBlock;
-constexpr uint32_t kOffBar = kOffRing + kStages * kStage;
-constexpr uint32_t kSmemBytes = kOffBar + 512 + 1024;
-static_assert(kSmemBytes <= 232448, "shared memory budget");
+constexpr int kMaxStages = 3;
+template <int SUBS> struct Cfg {
+    static constexpr int kThreads = 128 + 128 * SUBS;   // warp 0 copies, 1 products (CTA 0), 4..7 (8..11) softmax
+    // Registers a thread of the first warpgroup (copies and products) and of the others
+    // (softmax) once they are split again: what the launch had.
+    static constexpr int kRegsLaunch = SUBS == 2 ? 168 : 128;
+    static constexpr int kRegsIssue = SUBS == 2 ? 104 : 104, kRegsSoftmax = SUBS == 2 ? 200 : 152;
+    static_assert(kRegsIssue + SUBS * kRegsSoftmax <= (1 + SUBS) * kRegsLaunch, "register split");
+    static constexpr int kTileQ = 256 * SUBS;
+    static constexpr int kStages = SUBS == 2 ? 3 : 1;   // (one: copied while the softmax of the step before runs)
+    static constexpr uint32_t kOffRing = 3 * SUBS * kBlock;             // after Q
+    static constexpr uint32_t kOffBar = kOffRing + kStages * kStage;
+    static constexpr uint32_t kSmemBytes = kOffBar + 256 + 1024;
+    static_assert(kSmemBytes <= 232448 / (3 - SUBS), "shared memory budget");
+    static constexpr uint32_t kTmem = 256 * SUBS;       // S per sub-tile, then O per sub-tile
+};
 
 struct Bars {
     // of CTA 0: both CTAs' copies landed; both CTAs' weights are stored (a warp an arrival)
     uint64_t q_full[2];
-    uint64_t full[kStages];
+    uint64_t full[kMaxStages];
     uint64_t p_full[2];
     // of each CTA, from CTA 0's products
-    uint64_t empty[kStages];
+    uint64_t empty[kMaxStages];
     uint64_t s_full[2];        // scores of the sub-tile's step are there (and its earlier P . V)
     uint64_t o_full[2];
     uint32_t tmem_base;
     int32_t abort_flag;
 };
-static_assert(sizeof(Bars) <= 512, "barriers");
+static_assert(sizeof(Bars) <= 256, "barriers");
 
 // Pipeline timestamps for performance analysis, compiled only with -DMLA_TRACE: clock64 at
 // each hand-off of CTA (0, 0) for its first kTraceSteps steps. Product builds contain none
@@ -361,10 +367,14 @@ __device__ long long g_pftrace[16][kTraceSteps];
     } while (0)
 #endif
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+template <int SUBS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<SUBS>::kThreads, 3 - SUBS)
 prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap rope_map,
                   const PrefillParams p) {
+    using C = Cfg<SUBS>;
+    constexpr int kThreads = C::kThreads, kTileQ = C::kTileQ, kStages = C::kStages;
+    constexpr uint32_t kColO = 128 * SUBS;
     // the last tiles of a sequence see the most: they start first
     const int tiles = p.tile_off[p.B];
     if ((int)(blockIdx.x >> 1) >= tiles) return;         // both CTAs of a pair
@@ -385,14 +395,14 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     }
     const int L = p.seq_lens[b];
     // steps of each sub-tile (0: it has no rows); sub-tile 1 never has fewer than sub-tile 0
-    const int subs = rows_here > 256 ? 2 : 1;
+    const int subs = SUBS == 2 && rows_here > 256 ? 2 : 1;
     const int steps0 = (L - n + i0 + min(256, rows_here) + 127) / 128;
     const int steps1 = subs == 2 ? (L - n + i0 + rows_here + 127) / 128 : 0;
     const int steps = max(steps0, steps1);
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    Bars *bars = (Bars *)(smem + kOffBar);
+    Bars *bars = (Bars *)(smem + C::kOffBar);
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bars->q_full[s], 1);
@@ -411,7 +421,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&bars->tmem_base)),
-                     "r"(512)
+                     "r"(C::kTmem)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
@@ -429,7 +439,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
 
     if (warp == 0) {
         // ================================================= copies
-        reg_dec<kRegsIssue>();
+        reg_dec<C::kRegsIssue>();
         if (lane == 0) {
             const int row0 = p.kv_off[b];
             const int kv0 = hl * p.cap_rows + row0;           // fits: the pass's rows are counted in 32 bits
@@ -437,14 +447,14 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
             auto load_q = [&](int s) {
                 if (r == 0) mbar_expect_tx(&bars->q_full[s], 6 * kBlock);
                 for (int c = 0; c < 3; ++c)
-                    tma_pair_3d(smem + kOffQ + (3 * s + c) * kBlock, &q_map, 64 * c, h, (int)qrow0 + 256 * s + 128 * r,
+                    tma_pair_3d(smem + (3 * s + c) * kBlock, &q_map, 64 * c, h, (int)qrow0 + 256 * s + 128 * r,
                                 leader(&bars->q_full[s]));
             };
             int issued = 0;
             load_q(0);
             for (int u = 0; u <= steps; ++u, ++issued) {
                 const int st = u % kStages;
-                uint8_t *dst = smem + kOffRing + st * kStage;
+                uint8_t *dst = smem + C::kOffRing + st * kStage;
                 if (u >= kStages && !wait(&bars->empty[st], phase_of(u - kStages))) break;
                 if (r == 0) mbar_expect_tx(&bars->full[st], (u < steps ? 6 * kKBlock : 0u) + (u > 0 ? 2 * kBlock : 0u));
                 const uint32_t bar = leader(&bars->full[st]);
@@ -469,12 +479,12 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         // One thread for both sub-tiles, in turn: with a thread each, their products ran side
         // by side, both sub-tiles' scores came at the same time, and the tensor cores waited
         // while both softmaxes ran.
-        reg_dec<kRegsIssue>();
+        reg_dec<C::kRegsIssue>();
         if (lane == 0 && r == 0) {
             constexpr uint32_t kIdS = idesc_bf16(256, 128, false), kIdO = idesc_bf16(256, 128, true);
-            const uint64_t ring = sdesc(smem_u32(smem + kOffRing), 16, 1024);
-            const uint64_t vring = sdesc(smem_u32(smem + kOffRing + kOffV), kBlock, 1024);    // MN-major
-            const uint64_t qd = sdesc(smem_u32(smem + kOffQ), 16, 1024);
+            const uint64_t ring = sdesc(smem_u32(smem + C::kOffRing), 16, 1024);
+            const uint64_t vring = sdesc(smem_u32(smem + C::kOffRing + kOffV), kBlock, 1024);    // MN-major
+            const uint64_t qd = sdesc(smem_u32(smem), 16, 1024);
             const int last = subs - 1;
             auto scores = [&](int s, uint64_t k) {
                 const uint64_t a = qd + (uint64_t)(3 * s * (kBlock >> 4));
@@ -503,7 +513,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                 return mbar_test32(bar, parity) || wait_slow(bar, parity, &bars->abort_flag, p.status);
             };
             int st = 1 % kStages;                              // stage and phase of turn j + 1
-            uint32_t ph = 0;
+            uint32_t ph = phase_of(1);
             for (int j = 0; j < steps && ok; ++j) {
                 ok = there(full0 + 8 * st, ph);
                 PTRACE(3, j);
@@ -517,7 +527,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                     if (!ok) break;
                     PTRACE(8 * s, j);
                     tc_fence_after();
-                    const uint32_t tS = tmem + 128 * s, tO = tmem + 256 + 128 * s;
+                    const uint32_t tS = tmem + 128 * s, tO = tmem + kColO + 128 * s;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) mma2_ts(tO, tS + 8 * e, v + 128 * e, kIdO, (j > 0 || e > 0) ? 1u : 0u);
                     PTRACE(8 * s + 2, j);
@@ -538,13 +548,13 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         __syncwarp();
     } else if (warp >= 4) {
         // ================================================= softmax and output
-        reg_inc<kRegsSoftmax>();
+        reg_inc<C::kRegsSoftmax>();
         const int s = (warp - 4) >> 2, wq = warp & 3;
         const int row = 32 * wq + lane;                        // of the sub-tile
         const int mine = s == 0 ? steps0 : steps1;
         const int i = i0 + 256 * s + 128 * r + row;            // of the sequence's new tokens
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * wq) << 16);
-        const uint32_t tS = lane_addr + 128 * s, tO = lane_addr + 256 + 128 * s;
+        const uint32_t tS = lane_addr + 128 * s, tO = lane_addr + kColO + 128 * s;
         const int seen = L - n + min(i, n - 1) + 1;            // tokens this row sees
         // where the scale is positive the maximum commutes with it: one fma per exponent
         const bool pos_scale = p.scale > 0.f;
@@ -623,7 +633,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
             tc_fence_after();
             // O / l through this warp's part of its sub-tile's Q blocks (read for the last time
             // by the last scores), then rows of 256 bytes
-            uint8_t *stage = smem + kOffQ + 3 * s * kBlock + wq * 32 * 256;
+            uint8_t *stage = smem + 3 * s * kBlock + wq * 32 * 256;
             const float inv = ok ? 1.f / l : CUDART_NAN_F;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
@@ -653,7 +663,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                 p.lse[(qrow0 + first + lane) * H + h] = ok ? (m + log2f(l)) * kLn2 : CUDART_NAN_F;
         }
     } else {
-        reg_dec<kRegsIssue>();
+        reg_dec<C::kRegsIssue>();
     }
     // neither CTA leaves while the other may reach its barriers, its shared memory or its
     // tensor memory
@@ -662,7 +672,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     cluster_sync();
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmem) : "memory");
     }
 }
 
@@ -714,6 +724,10 @@ bool prefill_tc_supported(const ShapeArgs &s, int dn) {
     return (s.kind == MLA_KV_BF16 || is_mx(s.kind)) && s.r == pf::kR && s.dR == pf::kRope && s.dv == pf::kDv && dn == pf::kDn;
 }
 
+int32_t prefill_tc_tile(int32_t num_q, int32_t B) {
+    return (int64_t)num_q <= 256ll * B ? pf::Cfg<1>::kTileQ : pf::Cfg<2>::kTileQ;
+}
+
 cudaError_t launch_prefill_tc(const PrefillParams &p, cudaStream_t st) {
     using namespace pf;
     const uint64_t kv_rows = (uint64_t)p.nh * p.cap_rows;
@@ -725,13 +739,16 @@ cudaError_t launch_prefill_tc(const PrefillParams &p, cudaStream_t st) {
         return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(ex::expand_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ex::kSmemBytes);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(prefill_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    const bool two = p.tile_q == Cfg<2>::kTileQ;
+    auto kern = two ? prefill_tc_kernel<2> : prefill_tc_kernel<1>;
+    const uint32_t smem = two ? Cfg<2>::kSmemBytes : Cfg<1>::kSmemBytes;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     // the register split draws on what the launch has: refuse a build that has less
     cudaFuncAttributes at;
-    e = cudaFuncGetAttributes(&at, prefill_tc_kernel);
+    e = cudaFuncGetAttributes(&at, kern);
     if (e != cudaSuccess) return e;
-    if (at.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
+    if (at.numRegs < (two ? Cfg<2>::kRegsLaunch : Cfg<1>::kRegsLaunch)) return cudaErrorInvalidConfiguration;
     // Heads a pair makes in a row: as many as leave about four pairs' turns for each pair of
     // SMs (the rows are then loaded seldom, and the last turn costs little).
     int dev = 0, sms = 0;
@@ -744,7 +761,7 @@ cudaError_t launch_prefill_tc(const PrefillParams &p, cudaStream_t st) {
     heads += heads & 1;
     ex::expand_tc_kernel<<<dim3((unsigned)(2 * tiles), (unsigned)((p.nh + heads - 1) / heads)), ex::kThreads, ex::kSmemBytes, st>>>(
         rows, uk, uv, p, (int)heads);
-    prefill_tc_kernel<<<dim3(2 * (p.num_q / kTileQ + p.B), p.nh), kThreads, kSmemBytes, st>>>(q, k_ld, v_ld, rope, p);
+    kern<<<dim3(2 * (p.num_q / p.tile_q + p.B), p.nh), two ? Cfg<2>::kThreads : Cfg<1>::kThreads, smem, st>>>(q, k_ld, v_ld, rope, p);
     return cudaGetLastError();
 }
 

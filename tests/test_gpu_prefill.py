@@ -127,7 +127,7 @@ NEW, PAST = [0, 1, 5, 17, 130, 0, 40], [9, 0, 63, 64, 1, 0, 129]
 @pytest.mark.parametrize("impl", [0, 1])
 @pytest.mark.parametrize("new,past,H,bs", [
     (NEW, PAST, 4, 64), ([1], [0], 1, 64), ([256, 257], [0, 255], 3, 64), ([128, 127, 129], [128, 1, 0], 2, 16),
-    ([600], [700], 2, 256), ([2, 2], [1500, 126], 2, 64), ([1] * 40, list(range(40)), 1, 64),
+    ([600], [700], 2, 256), ([513, 100, 700], [0, 400, 63], 2, 64), ([512, 1, 300], [1, 900, 128], 1, 64), ([2, 2], [1500, 126], 2, 64), ([1] * 40, list(range(40)), 1, 64),
 ])
 def test_latent_512(gpu_lib, kind, impl, new, past, H, bs):
     import mla_latent_kv_08_gb300 as mla
