@@ -470,7 +470,7 @@ static mla_status check_prefill(const mla_shape *s, int32_t B, int32_t num_q, in
     if (B < 1 || num_q < 0 || max_tokens < 0 || dn < 8 || dn % 8) return MLA_ERR_INVALID;
     if (is_int2(s->kind) || dn > 512 || s->v_head_dim > 1024) return MLA_ERR_UNSUPPORTED;
     // dense rows and tiles are counted in 32 bits
-    if ((int64_t)max_tokens + 128ll * B > INT32_MAX - 256 || (int64_t)num_q + 512ll * B > INT32_MAX - 256)
+    if ((int64_t)max_tokens + 128ll * B > INT32_MAX - 256 || (int64_t)num_q + 256ll * B > INT32_MAX - 256)
         return MLA_ERR_UNSUPPORTED;
     if (s->impl == MLA_IMPL_TCGEN05 && !prefill_tc(s, dn)) return MLA_ERR_UNSUPPORTED;
     return MLA_OK;
@@ -529,7 +529,7 @@ mla_status mla_prefill(const mla_shape *shape, const mla_cache *cache, const int
     p.num_q = num_q;
     p.dn = nope_dim;
     const bool tc = prefill_tc(shape, nope_dim);
-    p.tile_q = tc ? prefill_tc_tile(num_q, B) : 16;
+    p.tile_q = tc ? kPrefillTcTile : 16;
     p.cap_rows = w.cap_rows;
     p.seq_lens = seq_lens;
     p.cu_q = cu_q;

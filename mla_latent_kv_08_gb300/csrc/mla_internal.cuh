@@ -222,8 +222,7 @@ cudaError_t launch_prefill_plan(const PrefillParams &p, cudaStream_t st);
 cudaError_t launch_prefill_simt(const PrefillParams &p, cudaStream_t st);
 // ---- prefill on the tensor cores (defined in mla_prefill_tc.cu) -------------
 bool prefill_tc_supported(const ShapeArgs &s, int dn);
-// New tokens a tile, by how many a sequence has on average.
-int32_t prefill_tc_tile(int32_t num_q, int32_t B);
+constexpr int32_t kPrefillTcTile = 256;      // new tokens a tile
 cudaError_t launch_prefill_tc(const PrefillParams &p, cudaStream_t st);
 // ---- tensor-core decode (defined in mla_tc.cu) -----------------------------
 bool tc_shape_supported(const ShapeArgs &s);

@@ -292,71 +292,66 @@ expand_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_cons
 }  // namespace ex
 
 // ============================================================================
-// Attention. A pair of CTAs (a cluster of two) takes up to 512 new tokens of one sequence
-// for one head, as two sub-tiles of 256 rows, CTA r of the pair holding 128 rows of each
-// (SUBS = 2). For chunks of few tokens it takes one sub-tile (SUBS = 1), in so little shared
-// memory that two pairs share their SMs: their set-ups, waits and outputs overlap.
-// Both sub-tiles go through the same 128-token steps of the cache in turn: while one's
-// warpgroups turn scores into weights, the tensor cores work on the other.
+// Attention. A pair of CTAs (a cluster of two) takes 256 new tokens of one sequence for one
+// head, 128 rows a CTA, over 128-token steps of the cache:
 //
-//   per step and sub-tile   S[256 x 128] = Q . K^T   12 x M256 N128 K16 over both SMs
-//                           P = 2^(S c - m)          a thread a row: no shuffles
-//                           O[256 x 128] += P . V    8 x M256 N128 K16, P from tensor memory
+//   S[256 x 128] = Q . K^T   12 x M256 N128 K16 over both SMs
+//   P = 2^(S c - m)          a thread a row: no shuffles
+//   O[256 x 128] += P . V    8 x M256 N128 K16, P from tensor memory
+//
+// Two pairs share their SMs: while one's warps turn scores into weights, copy or store, the
+// tensor cores work on the other. (Two sub-tiles of one pair taking turns, with three steps'
+// keys and values in flight, were as fast on long chunks, 5.48 against 5.33 ms for two chunks
+// of 2048 over 18k tokens, and slower on short ones, 176 against 137 us for turns of up to
+// 200: nothing overlapped a tile's set-up and output.)
 //
 // The pair shares the second operand: CTA r copies the keys of tokens 64 r .. 64 r + 63 of a
-// step and value columns 64 r .. 64 r + 63, 40 KB a step instead of the 80 KB that a CTA on
-// its own needs. That leaves room for three steps in flight (a CTA on its own had 1.6, and
-// its tensor cores waited a quarter of the time for keys), halves the reads of L2, and takes
-// the scores' operands (6 KB an MMA and SM, not 8) below the bandwidth of shared memory.
+// step and value columns 64 r .. 64 r + 63, 40 KB a step instead of 80 KB. That halves the
+// reads of L2 and takes the scores' operands (6 KB an MMA and SM, not 8) below the bandwidth
+// of shared memory; with a CTA on its own the products ran at three quarters of this pace.
 //
-// P (bf16) is stored over the scores it came from. The products of one sub-tile are issued
-// in order by one thread of CTA 0, so that the next scores overwrite P only once P . V has
-// read it. m is raised lazily, only when it grows by more than 8 (P <= 2^8).
+// P (bf16) is stored over the scores it came from. The products are issued in order by one
+// thread of CTA 0, so that the next scores overwrite P only once P . V has read it. m is
+// raised lazily, only when it grows by more than 8 (P <= 2^8).
 //
-// Shared memory: Q 96 KB, three stages of key blocks ([64 tokens x 64 dims] each) and a value
-// block ([128 tokens x 64 columns]). Tensor memory: S0, S1, O0, O1, 128 columns each.
+// Shared memory: Q 48 KB, a stage of key blocks ([64 tokens x 64 dims] each) and a value block
+// ([128 tokens x 64 columns]), copied while the softmax of the step before runs. Tensor
+// memory: S, O, 128 columns each.
 // ============================================================================
+constexpr int kThreads = 256;          // warp 0 copies, 1 products (CTA 0), 4..7 softmax
+// Registers a thread of the first warpgroup (copies and products) and of the other (softmax)
+// once they are split again: what the launch had.
+constexpr int kRegsLaunch = 128, kRegsIssue = 104, kRegsSoftmax = 152;
+static_assert(kRegsIssue + kRegsSoftmax <= 2 * kRegsLaunch, "register split");
+constexpr int kTileQ = kPrefillTcTile;
 constexpr uint32_t kKBlock = 64 * 128;                  // 8 KB
-constexpr uint32_t kOffV = 3 * kKBlock;                 // of a stage
-constexpr uint32_t kStage = kOffV + kBlock;             // 40 KB
-constexpr int kMaxStages = 3;
-template <int SUBS> struct Cfg {
-    static constexpr int kThreads = 128 + 128 * SUBS;   // warp 0 copies, 1 products (CTA 0), 4..7 (8..11) softmax
-    // Registers a thread of the first warpgroup (copies and products) and of the others
-    // (softmax) once they are split again: what the launch had.
-    static constexpr int kRegsLaunch = SUBS == 2 ? 168 : 128;
-    static constexpr int kRegsIssue = SUBS == 2 ? 104 : 104, kRegsSoftmax = SUBS == 2 ? 200 : 152;
-    static_assert(kRegsIssue + SUBS * kRegsSoftmax <= (1 + SUBS) * kRegsLaunch, "register split");
-    static constexpr int kTileQ = 256 * SUBS;
-    static constexpr int kStages = SUBS == 2 ? 3 : 1;   // (one: copied while the softmax of the step before runs)
-    static constexpr uint32_t kOffRing = 3 * SUBS * kBlock;             // after Q
-    static constexpr uint32_t kOffBar = kOffRing + kStages * kStage;
-    static constexpr uint32_t kSmemBytes = kOffBar + 256 + 1024;
-    static_assert(kSmemBytes <= 232448 / (3 - SUBS), "shared memory budget");
-    static constexpr uint32_t kTmem = 256 * SUBS;       // S per sub-tile, then O per sub-tile
-};
+constexpr uint32_t kOffK = 3 * kBlock;                  // after Q
+constexpr uint32_t kOffV = kOffK + 3 * kKBlock;
+constexpr uint32_t kOffBar = kOffV + kBlock;
+constexpr uint32_t kSmemBytes = kOffBar + 128 + 1024;
+static_assert(kSmemBytes <= 232448 / 2 - 1024, "shared memory budget of two CTAs");
+constexpr uint32_t kTmem = 256;
+constexpr uint32_t kColS = 0, kColO = 128;
 
 struct Bars {
     // of CTA 0: both CTAs' copies landed; both CTAs' weights are stored (a warp an arrival)
-    uint64_t q_full[2];
-    uint64_t full[kMaxStages];
-    uint64_t p_full[2];
+    uint64_t q_full, full, p_full;
     // of each CTA, from CTA 0's products
-    uint64_t empty[kMaxStages];
-    uint64_t s_full[2];        // scores of the sub-tile's step are there (and its earlier P . V)
-    uint64_t o_full[2];
+    uint64_t empty;            // the turn's keys and values are read
+    uint64_t s_full;           // the step's scores are there (and the P . V before)
+    uint64_t o_full;
     uint32_t tmem_base;
     int32_t abort_flag;
 };
-static_assert(sizeof(Bars) <= 256, "barriers");
+static_assert(sizeof(Bars) <= 128, "barriers");
 
 // Pipeline timestamps for performance analysis, compiled only with -DMLA_TRACE: clock64 at
 // each hand-off of CTA (0, 0) for its first kTraceSteps steps. Product builds contain none
-// of it. Events, 8 s + : 0 weights seen, 1 values landed, 2 P . V issued, 3 keys landed, 4
-// scores issued (MMA), 5 scores seen, 6 maximum agreed, 7 weights stored (softmax)
+// of it. Events: 0 turn landed, 1 weights seen, 2 P . V issued, 3 scores issued (products), 4
+// scores seen, 5 maximum known, 6 weights stored (softmax)
 #ifdef MLA_TRACE
 constexpr int kTraceSteps = 64;
-__device__ long long g_pftrace[16][kTraceSteps];
+__device__ long long g_pftrace[7][kTraceSteps];
 #define PTRACE(ev, step)                                                                  \
     do {                                                                                  \
         if (blockIdx.x == 0 && blockIdx.y == 0 && (step) < kTraceSteps) g_pftrace[ev][step] = clock64(); \
@@ -367,14 +362,10 @@ __device__ long long g_pftrace[16][kTraceSteps];
     } while (0)
 #endif
 
-template <int SUBS>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<SUBS>::kThreads, 3 - SUBS)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 2)
 prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap rope_map,
                   const PrefillParams p) {
-    using C = Cfg<SUBS>;
-    constexpr int kThreads = C::kThreads, kTileQ = C::kTileQ, kStages = C::kStages;
-    constexpr uint32_t kColO = 128 * SUBS;
     // the last tiles of a sequence see the most: they start first
     const int tiles = p.tile_off[p.B];
     if ((int)(blockIdx.x >> 1) >= tiles) return;         // both CTAs of a pair
@@ -394,26 +385,18 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         return;
     }
     const int L = p.seq_lens[b];
-    // steps of each sub-tile (0: it has no rows); sub-tile 1 never has fewer than sub-tile 0
-    const int subs = SUBS == 2 && rows_here > 256 ? 2 : 1;
-    const int steps0 = (L - n + i0 + min(256, rows_here) + 127) / 128;
-    const int steps1 = subs == 2 ? (L - n + i0 + rows_here + 127) / 128 : 0;
-    const int steps = max(steps0, steps1);
+    const int steps = (L - n + i0 + rows_here + 127) / 128;      // of the tile's last row
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    Bars *bars = (Bars *)(smem + C::kOffBar);
+    Bars *bars = (Bars *)(smem + kOffBar);
     if (tid == 0) {
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(&bars->q_full[s], 1);
-            mbar_init(&bars->s_full[s], 1);
-            mbar_init(&bars->p_full[s], 8);
-            mbar_init(&bars->o_full[s], 1);
-        }
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&bars->full[s], 1);
-            mbar_init(&bars->empty[s], 1);
-        }
+        mbar_init(&bars->q_full, 1);
+        mbar_init(&bars->full, 1);
+        mbar_init(&bars->p_full, 8);
+        mbar_init(&bars->empty, 1);
+        mbar_init(&bars->s_full, 1);
+        mbar_init(&bars->o_full, 1);
         bars->abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
@@ -421,7 +404,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&bars->tmem_base)),
-                     "r"(C::kTmem)
+                     "r"(kTmem)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
@@ -433,140 +416,108 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         return mbar_wait_bounded(bar, parity, &bars->abort_flag, p.status, FLAG_TIMEOUT, kTimeoutNs);
     };
+
     // The copies go in turns: turn t brings step t's keys and step t - 1's values, which the
     // products take together (turn 0: keys only; turn `steps`: values only).
-    auto phase_of = [](int t) { return (uint32_t)(t / kStages) & 1u; };
-
     if (warp == 0) {
         // ================================================= copies
-        reg_dec<C::kRegsIssue>();
+        reg_dec<kRegsIssue>();
         if (lane == 0) {
             const int row0 = p.kv_off[b];
             const int kv0 = hl * p.cap_rows + row0;           // fits: the pass's rows are counted in 32 bits
-            auto leader = [&](uint64_t *bar) { return mapa(smem_u32(bar), 0); };
-            auto load_q = [&](int s) {
-                if (r == 0) mbar_expect_tx(&bars->q_full[s], 6 * kBlock);
-                for (int c = 0; c < 3; ++c)
-                    tma_pair_3d(smem + (3 * s + c) * kBlock, &q_map, 64 * c, h, (int)qrow0 + 256 * s + 128 * r,
-                                leader(&bars->q_full[s]));
-            };
-            int issued = 0;
-            load_q(0);
-            for (int u = 0; u <= steps; ++u, ++issued) {
-                const int st = u % kStages;
-                uint8_t *dst = smem + C::kOffRing + st * kStage;
-                if (u >= kStages && !wait(&bars->empty[st], phase_of(u - kStages))) break;
-                if (r == 0) mbar_expect_tx(&bars->full[st], (u < steps ? 6 * kKBlock : 0u) + (u > 0 ? 2 * kBlock : 0u));
-                const uint32_t bar = leader(&bars->full[st]);
-                if (u > 0) tma_pair_2d(dst + kOffV, &v_map, 64 * r, kv0 + 128 * (u - 1), bar);
+            const uint32_t q_bar = mapa(smem_u32(&bars->q_full), 0), bar = mapa(smem_u32(&bars->full), 0);
+            if (r == 0) mbar_expect_tx(&bars->q_full, 6 * kBlock);
+            for (int c = 0; c < 3; ++c)
+                tma_pair_3d(smem + c * kBlock, &q_map, 64 * c, h, (int)qrow0 + 128 * r, q_bar);
+            int u = 0;
+            for (; u <= steps; ++u) {
+                if (u > 0 && !wait(&bars->empty, (u - 1) & 1)) break;
+                if (r == 0) mbar_expect_tx(&bars->full, (u < steps ? 6 * kKBlock : 0u) + (u > 0 ? 2 * kBlock : 0u));
+                if (u > 0) tma_pair_2d(smem + kOffV, &v_map, 64 * r, kv0 + 128 * (u - 1), bar);
                 if (u < steps) {
-                    tma_pair_2d(dst, &k_map, 0, kv0 + 128 * u + 64 * r, bar);
-                    tma_pair_2d(dst + kKBlock, &k_map, 64, kv0 + 128 * u + 64 * r, bar);
-                    tma_pair_2d(dst + 2 * kKBlock, &rope_map, kR, row0 + 128 * u + 64 * r, bar);
+                    tma_pair_2d(smem + kOffK, &k_map, 0, kv0 + 128 * u + 64 * r, bar);
+                    tma_pair_2d(smem + kOffK + kKBlock, &k_map, 64, kv0 + 128 * u + 64 * r, bar);
+                    tma_pair_2d(smem + kOffK + 2 * kKBlock, &rope_map, kR, row0 + 128 * u + 64 * r, bar);
                 }
-                if (u == 0 && subs == 2) load_q(1);
             }
             // Never leave a copy in flight into the pair's shared memory: CTA 0 waits here for
             // both CTAs' copies, CTA 1 for CTA 0 at the end.
             if (r == 0) {
-                for (int s = 0; s < subs; ++s) mbar_drain(&bars->q_full[s], 0);
-                for (int u = max(0, issued - kStages); u < issued; ++u) mbar_drain(&bars->full[u % kStages], phase_of(u));
+                mbar_drain(&bars->q_full, 0);
+                mbar_drain(&bars->full, (u - 1) & 1);
             }
         }
         __syncwarp();
     } else if (warp == 1) {
         // ================================================= products: lane 0 of CTA 0 alone
-        // One thread for both sub-tiles, in turn: with a thread each, their products ran side
-        // by side, both sub-tiles' scores came at the same time, and the tensor cores waited
-        // while both softmaxes ran.
-        reg_dec<C::kRegsIssue>();
+        reg_dec<kRegsIssue>();
         if (lane == 0 && r == 0) {
             constexpr uint32_t kIdS = idesc_bf16(256, 128, false), kIdO = idesc_bf16(256, 128, true);
-            const uint64_t ring = sdesc(smem_u32(smem + C::kOffRing), 16, 1024);
-            const uint64_t vring = sdesc(smem_u32(smem + C::kOffRing + kOffV), kBlock, 1024);    // MN-major
-            const uint64_t qd = sdesc(smem_u32(smem), 16, 1024);
-            const int last = subs - 1;
-            auto scores = [&](int s, uint64_t k) {
-                const uint64_t a = qd + (uint64_t)(3 * s * (kBlock >> 4));
+            const uint64_t qd = sdesc(smem_u32(smem), 16, 1024), kd = sdesc(smem_u32(smem + kOffK), 16, 1024);
+            const uint64_t vd = sdesc(smem_u32(smem + kOffV), kBlock, 1024);                 // MN-major
+            const uint32_t tS = tmem + kColS, tO = tmem + kColO;
+            // Between one product and the next stand as few instructions as can be: the first
+            // probe of a barrier is inline, the bounded wait out of line.
+            const uint32_t full = smem_u32(&bars->full), p_full = smem_u32(&bars->p_full);
+            auto there = [&](uint32_t bar, uint32_t parity) {
+                return mbar_test32(bar, parity) || wait_slow(bar, parity, &bars->abort_flag, p.status);
+            };
+            auto scores = [&]() {
 #pragma unroll
                 for (int c = 0; c < 3; ++c)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const uint64_t ao = a + c * (kBlock >> 4) + 2 * e, ko = k + c * (kKBlock >> 4) + 2 * e;
-                        if (c == 0 && e == 0) mma2_ss<kIdS, 0>(tmem + 128 * s, ao, ko);
-                        else mma2_ss<kIdS, 1>(tmem + 128 * s, ao, ko);
+                        const uint64_t a = qd + c * (kBlock >> 4) + 2 * e, k = kd + c * (kKBlock >> 4) + 2 * e;
+                        if (c == 0 && e == 0) mma2_ss<kIdS, 0>(tS, a, k);
+                        else mma2_ss<kIdS, 1>(tS, a, k);
                     }
-                commit2(&bars->s_full[s]);
+                commit2(&bars->s_full);
             };
-            bool ok = wait(&bars->full[0], 0);
-            for (int s = 0; s < subs && ok; ++s) {
-                ok = wait(&bars->q_full[s], 0);
-                tc_fence_after();
-                if (ok) scores(s, ring);
+            bool ok = wait(&bars->q_full, 0) && wait(&bars->full, 0);
+            tc_fence_after();
+            if (ok) {
+                scores();
+                commit2(&bars->empty);
             }
-            if (ok) commit2(&bars->empty[0]);
-            // Between one product and the next stand as few instructions as can be: the thread's
-            // own pace bounded the kernel (a third of the time, with a barrier for each block
-            // and the general wait inlined everywhere).
-            const uint32_t full0 = smem_u32(&bars->full[0]), p0 = smem_u32(&bars->p_full[0]);
-            auto there = [&](uint32_t bar, uint32_t parity) {
-                return mbar_test32(bar, parity) || wait_slow(bar, parity, &bars->abort_flag, p.status);
-            };
-            int st = 1 % kStages;                              // stage and phase of turn j + 1
-            uint32_t ph = phase_of(1);
             for (int j = 0; j < steps && ok; ++j) {
-                ok = there(full0 + 8 * st, ph);
-                PTRACE(3, j);
-                const uint64_t k = ring + (uint64_t)(st * (kStage >> 4)), v = vring + (uint64_t)(st * (kStage >> 4));
-#pragma unroll 1
-                for (int s = 0; s < subs && ok; ++s) {
-                    const int left = (s == 0 ? steps0 : steps1) - j;     // of the sub-tile's steps
-                    if (left <= 0) continue;
-                    PTRACE(8 * s + 1, j);
-                    ok = there(p0 + 8 * s, j & 1);
-                    if (!ok) break;
-                    PTRACE(8 * s, j);
-                    tc_fence_after();
-                    const uint32_t tS = tmem + 128 * s, tO = tmem + kColO + 128 * s;
+                ok = there(full, (j + 1) & 1);
+                PTRACE(0, j);
+                ok = ok && there(p_full, j & 1);
+                if (!ok) break;
+                PTRACE(1, j);
+                tc_fence_after();
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) mma2_ts(tO, tS + 8 * e, v + 128 * e, kIdO, (j > 0 || e > 0) ? 1u : 0u);
-                    PTRACE(8 * s + 2, j);
-                    if (left > 1) scores(s, k);
-                    else commit2(&bars->o_full[s]);
-                    PTRACE(8 * s + 4, j);
-                }
-                commit2(&bars->empty[st]);
-                if (++st == kStages) {
-                    st = 0;
-                    ph ^= 1;
-                }
+                for (int e = 0; e < 8; ++e) mma2_ts(tO, tS + 8 * e, vd + 128 * e, kIdO, (j > 0 || e > 0) ? 1u : 0u);
+                PTRACE(2, j);
+                if (j + 1 < steps) scores();
+                else commit2(&bars->o_full);
+                commit2(&bars->empty);
+                PTRACE(3, j);
             }
             // products in flight must end before the tensor memory is given back
-            if (!ok) commit2(&bars->o_full[last]);
-            mbar_drain(&bars->o_full[last], 0);
+            if (!ok) commit2(&bars->o_full);
+            mbar_drain(&bars->o_full, 0);
         }
         __syncwarp();
     } else if (warp >= 4) {
         // ================================================= softmax and output
-        reg_inc<C::kRegsSoftmax>();
-        const int s = (warp - 4) >> 2, wq = warp & 3;
-        const int row = 32 * wq + lane;                        // of the sub-tile
-        const int mine = s == 0 ? steps0 : steps1;
-        const int i = i0 + 256 * s + 128 * r + row;            // of the sequence's new tokens
+        reg_inc<kRegsSoftmax>();
+        const int wq = warp & 3, row = 32 * wq + lane;         // of the CTA's rows
+        const int i = i0 + 128 * r + row;                      // of the sequence's new tokens
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * wq) << 16);
-        const uint32_t tS = lane_addr + 128 * s, tO = lane_addr + kColO + 128 * s;
+        const uint32_t tS = lane_addr + kColS, tO = lane_addr + kColO;
         const int seen = L - n + min(i, n - 1) + 1;            // tokens this row sees
         // where the scale is positive the maximum commutes with it: one fma per exponent
         const bool pos_scale = p.scale > 0.f;
         const float c2 = p.scale * kLog2e, cs = pos_scale ? c2 : 1.f;
-        const uint32_t p_bar = mapa(smem_u32(&bars->p_full[s]), 0);
+        const uint32_t p_bar = mapa(smem_u32(&bars->p_full), 0);
         float m = -CUDART_INF_F, l = 0.f;
         bool ok = true;
-        for (int j = 0; j < mine; ++j) {
-            ok = __all_sync(0xffffffffu, wait(&bars->s_full[s], j & 1));
+        for (int j = 0; j < steps; ++j) {
+            ok = __all_sync(0xffffffffu, wait(&bars->s_full, j & 1));
             if (!ok) break;
             tc_fence_after();
-            if (wq == 0 && lane == 0) PTRACE(8 * s + 5, j);
+            if (tid == 128) PTRACE(4, j);
             uint32_t sv[128];
             TMEM_LD32(tS, sv);
             TMEM_LD32(tS + 32, (sv + 32));
@@ -587,7 +538,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
 #pragma unroll
             for (int e = 4; e < 128; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(sv[e]));
             const float m_new = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs);
-            if (wq == 0 && lane == 0) PTRACE(8 * s + 6, j);
+            if (tid == 128) PTRACE(5, j);
             float alpha = 1.f;
             bool rescale = false;
             if (m_new > m + 8.f) {
@@ -607,13 +558,13 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                 sv[e] = *(const uint32_t *)&w;
             }
             l = l * alpha + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
-            // the scores' barrier says that the sub-tile's earlier P . V is done as well
+            // the scores' barrier says that the P . V before is done as well
             if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t ov[32];
                     TMEM_LD32(tO + 32 * c, ov);
-                    tmem_wait_ld();
+                    tmem_wait_ld(ov);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
                     TMEM_ST32(tO + 32 * c, ov);
@@ -625,45 +576,43 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_cluster(p_bar);
-            if (wq == 0 && lane == 0) PTRACE(8 * s + 7, j);
+            if (tid == 128) PTRACE(6, j);
         }
-        if (ok && mine > 0) ok = __all_sync(0xffffffffu, wait(&bars->o_full[s], 0));
+        ok = ok && __all_sync(0xffffffffu, wait(&bars->o_full, 0));
         ok = ok && __all_sync(0xffffffffu, *(volatile int32_t *)&bars->abort_flag == 0);
-        if (mine > 0) {
-            tc_fence_after();
-            // O / l through this warp's part of its sub-tile's Q blocks (read for the last time
-            // by the last scores), then rows of 256 bytes
-            uint8_t *stage = smem + 3 * s * kBlock + wq * 32 * 256;
-            const float inv = ok ? 1.f / l : CUDART_NAN_F;
+        tc_fence_after();
+        // O / l through this warp's part of the Q blocks (read for the last time by the last
+        // scores), then rows of 256 bytes
+        uint8_t *stage = smem + wq * 32 * 256;
+        const float inv = ok ? 1.f / l : CUDART_NAN_F;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                uint32_t ov[32];
-                TMEM_LD32(tO + 32 * c, ov);
-                tmem_wait_ld();
+        for (int c = 0; c < 4; ++c) {
+            uint32_t ov[32];
+            TMEM_LD32(tO + 32 * c, ov);
+            tmem_wait_ld(ov);
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
-                    uint32_t w[4];
+            for (int ch = 0; ch < 4; ++ch) {
+                uint32_t w[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(ov[8 * ch + 2 * e]) * inv,
-                                                                       __uint_as_float(ov[8 * ch + 2 * e + 1]) * inv);
-                        w[e] = *(const uint32_t *)&x;
-                    }
-                    // 16-byte chunks rotated by the row: no two lanes of a store on one bank
-                    *(uint4 *)(stage + lane * 256 + (((4 * c + ch) ^ (lane & 15)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int e = 0; e < 4; ++e) {
+                    const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(ov[8 * ch + 2 * e]) * inv,
+                                                                   __uint_as_float(ov[8 * ch + 2 * e + 1]) * inv);
+                    w[e] = *(const uint32_t *)&x;
                 }
+                // 16-byte chunks rotated by the row: no two lanes of a store on one bank
+                *(uint4 *)(stage + lane * 256 + (((4 * c + ch) ^ (lane & 15)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            __syncwarp();
-            const int first = 256 * s + 128 * r + 32 * wq;     // of the tile
-            for (int rr = lane >> 4; rr < 32; rr += 2)
-                if (first + rr < rows_here)
-                    *(uint4 *)(out + ((qrow0 + first + rr) * H + h) * kDv + 8 * (lane & 15)) =
-                        *(const uint4 *)(stage + rr * 256 + (((lane & 15) ^ (rr & 15)) << 4));
-            if (p.lse && first + lane < rows_here)
-                p.lse[(qrow0 + first + lane) * H + h] = ok ? (m + log2f(l)) * kLn2 : CUDART_NAN_F;
         }
+        __syncwarp();
+        const int first = 128 * r + 32 * wq;                   // of the tile
+        for (int rr = lane >> 4; rr < 32; rr += 2)
+            if (first + rr < rows_here)
+                *(uint4 *)(out + ((qrow0 + first + rr) * H + h) * kDv + 8 * (lane & 15)) =
+                    *(const uint4 *)(stage + rr * 256 + (((lane & 15) ^ (rr & 15)) << 4));
+        if (p.lse && first + lane < rows_here)
+            p.lse[(qrow0 + first + lane) * H + h] = ok ? (m + log2f(l)) * kLn2 : CUDART_NAN_F;
     } else {
-        reg_dec<C::kRegsIssue>();
+        reg_dec<kRegsIssue>();
     }
     // neither CTA leaves while the other may reach its barriers, its shared memory or its
     // tensor memory
@@ -672,7 +621,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     cluster_sync();
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmem) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
     }
 }
 
@@ -724,10 +673,6 @@ bool prefill_tc_supported(const ShapeArgs &s, int dn) {
     return (s.kind == MLA_KV_BF16 || is_mx(s.kind)) && s.r == pf::kR && s.dR == pf::kRope && s.dv == pf::kDv && dn == pf::kDn;
 }
 
-int32_t prefill_tc_tile(int32_t num_q, int32_t B) {
-    return (int64_t)num_q <= 256ll * B ? pf::Cfg<1>::kTileQ : pf::Cfg<2>::kTileQ;
-}
-
 cudaError_t launch_prefill_tc(const PrefillParams &p, cudaStream_t st) {
     using namespace pf;
     const uint64_t kv_rows = (uint64_t)p.nh * p.cap_rows;
@@ -739,16 +684,13 @@ cudaError_t launch_prefill_tc(const PrefillParams &p, cudaStream_t st) {
         return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(ex::expand_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ex::kSmemBytes);
     if (e != cudaSuccess) return e;
-    const bool two = p.tile_q == Cfg<2>::kTileQ;
-    auto kern = two ? prefill_tc_kernel<2> : prefill_tc_kernel<1>;
-    const uint32_t smem = two ? Cfg<2>::kSmemBytes : Cfg<1>::kSmemBytes;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(prefill_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (e != cudaSuccess) return e;
     // the register split draws on what the launch has: refuse a build that has less
     cudaFuncAttributes at;
-    e = cudaFuncGetAttributes(&at, kern);
+    e = cudaFuncGetAttributes(&at, prefill_tc_kernel);
     if (e != cudaSuccess) return e;
-    if (at.numRegs < (two ? Cfg<2>::kRegsLaunch : Cfg<1>::kRegsLaunch)) return cudaErrorInvalidConfiguration;
+    if (at.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
     // Heads a pair makes in a row: as many as leave about four pairs' turns for each pair of
     // SMs (the rows are then loaded seldom, and the last turn costs little).
     int dev = 0, sms = 0;
@@ -761,7 +703,7 @@ cudaError_t launch_prefill_tc(const PrefillParams &p, cudaStream_t st) {
     heads += heads & 1;
     ex::expand_tc_kernel<<<dim3((unsigned)(2 * tiles), (unsigned)((p.nh + heads - 1) / heads)), ex::kThreads, ex::kSmemBytes, st>>>(
         rows, uk, uv, p, (int)heads);
-    kern<<<dim3(2 * (p.num_q / p.tile_q + p.B), p.nh), two ? Cfg<2>::kThreads : Cfg<1>::kThreads, smem, st>>>(q, k_ld, v_ld, rope, p);
+    prefill_tc_kernel<<<dim3(2 * (p.num_q / kTileQ + p.B), p.nh), kThreads, kSmemBytes, st>>>(q, k_ld, v_ld, rope, p);
     return cudaGetLastError();
 }
 
