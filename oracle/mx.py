@@ -39,23 +39,15 @@ def encode(c: np.ndarray):
     """c [n, r] -> codes [n, r] uint8, scale bytes [n, r / 32] uint8."""
     c = np.asarray(c, np.float64)
     g = c.reshape(c.shape[0], -1, GROUP)
-    codes = np.empty(g.shape, np.uint8)
-    scales = np.empty(g.shape[:2], np.uint8)
-    for i in range(g.shape[0]):
-        for j in range(g.shape[1]):
-            x = g[i, j]
-            if not np.all(np.isfinite(x)):
-                scales[i, j], codes[i, j] = 255, 0x7F
-                continue
-            e = -110
-            top = np.max(np.abs(x))
-            if top > 0:
-                e = min(119, max(-110, math.frexp(top)[1] - 10))
-                while e < 119 and top > math.ldexp(448, e):
-                    e += 1
-            scales[i, j] = e + 127
-            codes[i, j] = nearest_code(np.clip(np.ldexp(x, -e), -448, 448))
-    return codes.reshape(c.shape), scales
+    finite = np.isfinite(g).all(-1)
+    g = np.where(finite[..., None], g, 0.0)
+    top = np.abs(g).max(-1)
+    # top = f 2^k with f in [1/2, 1): 448 2^(k - 9) = 0.875 2^k is enough for f <= 0.875
+    f, k = np.frexp(top)
+    e = np.where(top > 0, np.clip(k - 9 + (f > 0.875), -110, 119), -110).astype(np.int64)
+    codes = nearest_code(np.clip(np.ldexp(g, -e[..., None]), -448, 448))
+    codes[~finite] = 0x7F
+    return codes.reshape(c.shape), np.where(finite, e + 127, 255).astype(np.uint8)
 
 
 def decode(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
