@@ -181,8 +181,9 @@ size_t mla_workspace_bytes(const mla_shape *shape, int32_t B, int32_t q_len);
  * MXFP8 encoding per token and group of 32: e is the least exponent with max |c| /
  * 2^e <= 448, within [-110, 119] (a group of zeros: -110); code = the nearest e4m3
  * value to c / 2^e, ties to even (magnitudes above 448 * 2^119 become that).
- * Every value read back is a bf16. A group with an infinity or a NaN in it gets the scale byte 255 and reads
- * back as NaN. R and clip are not used.
+ * Every value read back is a bf16. A group with an infinity or a NaN in it gets the scale
+ * byte 255 and reads back as NaN; query rows that see such a token are NaN, those whose
+ * mask hides it are not touched by it. R and clip are not used.
  *   Source: OSCAR issue #10, maintainer reply (rotated + quantised latent in
  *   the cache, thresholds fit on the rotated latent). */
 mla_status mla_latent_append(const mla_shape *shape, const mla_cache *cache,
@@ -291,7 +292,8 @@ mla_status mla_verify(const mla_shape *shape, const mla_cache *cache,
  *   workspace  at least mla_prefill_workspace_bytes(shape, B, num_q, max_tokens, d_n).
  * New token i of sequence b sees positions 0 .. seq_lens[b] - n_b + i. Keys and values
  * are rounded to bf16 before the products (BF16 and MXFP8 kinds), as a layer that
- * decompresses its cache stores them. Kinds: BF16, FP32, MXFP8; MLA_ERR_UNSUPPORTED
+ * decompresses its cache stores them. A new token that sees a cached one whose latent
+ * holds a NaN or an infinity is NaN; one whose mask hides it is not touched by it. Kinds: BF16, FP32, MXFP8; MLA_ERR_UNSUPPORTED
  * for the INT2 kinds (use mla_verify) and for v_head_dim > 1024. A sequence with a bad
  * length or block gets NaN rows; mla_get_status(workspace) reports the flags. */
 size_t mla_prefill_workspace_bytes(const mla_shape *shape, int32_t B, int32_t num_q, int32_t max_tokens,

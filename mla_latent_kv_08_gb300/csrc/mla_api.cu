@@ -452,7 +452,7 @@ mla_status mla_latent_read(const mla_shape *shape, const mla_cache *cache, const
 
 // ---- prefill ----------------------------------------------------------------
 struct PrefillWs {
-    size_t kv_off, tile_off, bad, rows, k, v, total;
+    size_t kv_off, tile_off, bad, odd, rows, k, v, total;
     int32_t cap_rows;            // every sequence's rows start at a multiple of 128
     int32_t heads;               // heads per pass
 };
@@ -489,6 +489,7 @@ static PrefillWs prefill_ws(const mla_shape *s, int32_t B, int32_t max_tokens, i
     w.kv_off = off;    off = up256(off + sizeof(int32_t) * ((size_t)B + 1));
     w.tile_off = off;  off = up256(off + sizeof(int32_t) * ((size_t)B + 1));
     w.bad = off;       off = up256(off + sizeof(int32_t) * (size_t)B);
+    w.odd = off;       off = up256(off + (size_t)w.cap_rows);
     w.rows = off;      off = up256(off + (size_t)w.cap_rows * (s->kv_lora_rank + s->rope_dim) * es);
     w.k = off;         off = up256(off + (size_t)w.heads * w.cap_rows * dn * ekv);
     w.v = off;         off = up256(off + (size_t)w.heads * w.cap_rows * s->v_head_dim * ekv);
@@ -538,6 +539,7 @@ mla_status mla_prefill(const mla_shape *shape, const mla_cache *cache, const int
     p.bad = (int32_t *)(ws + w.bad);
     p.status = (int32_t *)ws;
     p.rows = ws + w.rows;
+    p.odd = (const uint8_t *)(ws + w.odd);
     p.k = ws + w.k;
     p.v = ws + w.v;
     p.q = q;
@@ -558,6 +560,7 @@ mla_status mla_prefill(const mla_shape *shape, const mla_cache *cache, const int
     r.rows = ws + w.rows;
     r.status = p.status;
     r.bad = p.bad;
+    r.odd = (uint8_t *)(ws + w.odd);
     if (launch_read(r, stream_) != cudaSuccess) return MLA_ERR_CUDA;
     prof_kernels(1);
     for (p.h0 = 0; p.h0 < shape->num_heads; p.h0 += w.heads) {

@@ -154,6 +154,7 @@ struct ReadParams {
     void *rows;
     int32_t *status;
     int32_t *bad;                // prefill: [B], set where a block is out of range; else nullptr
+    uint8_t *odd;                // prefill: [num_rows], 1 where the latent has a NaN or an infinity; else nullptr
 };
 
 // mla_prefill. The new tokens of each sequence are cut into tiles of `tile_q`; the plan
@@ -170,6 +171,7 @@ struct PrefillParams {
     int32_t *bad;                // [B]
     int32_t *status;
     const void *rows;            // [cap_rows, r + d_R]
+    const uint8_t *odd;          // [cap_rows], see ReadParams
     void *k;                     // [nh, cap_rows, d_n]
     void *v;                     // [nh, cap_rows, d_v]
     const void *q, *W_UK, *W_UV;

@@ -62,7 +62,8 @@ constexpr uint32_t kOffQ = kBlocks * kCol;            // 144 KB
 template <int N> struct Lay {
     static constexpr uint32_t kQBlock = N * 128;      // [N rows x 64 dims] bf16
     static constexpr uint32_t kOffStat = kOffQ + kBlocks * kQBlock;   // fp32: -m [64], alpha [64], 1/l [64], per warp [4][64]
-    static constexpr uint32_t kOffBar = kOffStat + 7 * 64 * 4;
+    static constexpr uint32_t kOffNan = kOffStat + 7 * 64 * 4;        // int32 [128]: 1 + the last step where the token was not a number
+    static constexpr uint32_t kOffBar = kOffNan + kStep * 4;
     static constexpr uint32_t kSmemBytes = kOffBar + 256 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
@@ -186,6 +187,7 @@ decode_narrow_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
     }
+    if (tid < kStep) ((int32_t *)(smem + LY::kOffNan))[tid] = 0;
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&bars->tmem_base)),
@@ -372,6 +374,7 @@ decode_narrow_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_
                 const int tok = it.t0 + j * kStep + tok_row;
                 // rows before n_min do not see this token (drafts; or the slot is past the end)
                 const int n_min = tok >= it.t1 ? N : max(0, (tok - (L - p.q_len)) * p.s.H);
+                const bool not_a_number = ((volatile int32_t *)(smem + LY::kOffNan))[tok_row] == K + 1;
                 // exponents of 32 rows, over the rows' m; hidden ones -inf
                 uint32_t sv[32];
                 auto exponents = [&](int h) {
@@ -389,6 +392,11 @@ decode_narrow_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_
 #pragma unroll
                         for (int n = 0; n < 32; ++n)
                             if (32 * h + n < n_min) sv[n] = __float_as_uint(-CUDART_INF_F);
+                    }
+                    if (not_a_number) {
+#pragma unroll
+                        for (int n = 0; n < 32; ++n)
+                            if (32 * h + n >= n_min) sv[n] = 0x7fc00000u;
                     }
                 };
                 float top = -CUDART_INF_F, low = CUDART_INF_F; // the largest and the least visible exponent
@@ -544,14 +552,24 @@ decode_narrow_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_
                 }
             }
         };
-        auto expand = [&](const Rows &x, uint32_t to) {
+        // A group that is not a number becomes zeros (their product with a hidden row's weight 0
+        // stays 0) and its token is noted with `mark`, so that the scores of the rows that see
+        // it become NaN.
+        auto expand = [&](const Rows &x, uint32_t to, int mark) {
             // scales up to 1 take one multiplication
             const bool small = !__any_sync(0xffffffffu, (x.s[0] | x.s[1] | x.s[2] | x.s[3]) & 0x80808080u);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 uint4 o0, o1;
                 if (small) mx_expand16(x.c[q], mx_scale120(x.s[q], p8 >> 1), o0, o1);
-                else mx_expand16(x.c[q], kMx2p120, mx_scale_bf162((x.s[q] >> (8 * (p8 >> 1))) & 0xffu), o0, o1);
+                else {
+                    uint32_t b = mx_scale_bf162((x.s[q] >> (8 * (p8 >> 1))) & 0xffu);
+                    if (b == 0x7fc07fc0u) {
+                        b = 0;
+                        ((volatile int32_t *)(smem + LY::kOffNan))[16 * e + 4 * q + r4] = mark;
+                    }
+                    mx_expand16(x.c[q], kMx2p120, b, o0, o1);
+                }
                 // row 4 q + r4 of the warp's two atoms flips bit 2 of the chunk with q
                 st_shared16(to + 512u * q + (chunk ^ (64u * (q & 1))), o0);
                 st_shared16(to + 512u * q + (chunk ^ (64u * (q & 1)) ^ 16u), o1);
@@ -586,7 +604,7 @@ decode_narrow_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_
             auto part = [&](Rows &x, int c) {
                 if (K > 0 && !__all_sync(0xffffffffu, wait(&bars->empty[c], (K - 1) & 1))) return false;
                 if (tid == 256 && c % 3 == 0) NTRACE(c == 0 ? 10 : 12, K);
-                expand(x, to0 + 2u * c * kCol);
+                expand(x, to0 + 2u * c * kCol, K + 1);
                 fence_proxy_async();
                 mbar_arrive(&bars->full[c]);
                 if (tid == 256 && c % 3 == 0) NTRACE(c == 0 ? 11 : 13, K);

@@ -83,7 +83,9 @@ template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; 
 template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
 
 // y[h][row][j] = sum_k rows[row][k] W[h][j][k] (W_UK: K-major) or W[h][k][j] (W_UV), fp32.
-// A CTA makes a 64 x 64 tile; thread (ty, tx) a 4 x 4 block.
+// A CTA makes a 64 x 64 tile; thread (ty, tx) a 4 x 4 block. A latent with a NaN or an
+// infinity gives NaN keys, so that every new token that sees it is NaN, and zero values, so
+// that those whose mask hides it (weight 0) are as if it were not there.
 template <typename T, bool UK>
 __global__ void __launch_bounds__(256) expand_simt_kernel(PrefillParams p) {
     __shared__ float sA[32][64 + 1], sB[32][64 + 1];
@@ -123,10 +125,13 @@ __global__ void __launch_bounds__(256) expand_simt_kernel(PrefillParams p) {
     }
     float *y = (float *)(UK ? p.k : p.v) + (size_t)blockIdx.z * p.cap_rows * N;
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+    for (int u = 0; u < 4; ++u) {
+        const bool odd = p.odd[m0 + 4 * ty + u];
 #pragma unroll
         for (int v = 0; v < 4; ++v)
-            if (j0 + 4 * tx + v < N) y[(size_t)(m0 + 4 * ty + u) * N + j0 + 4 * tx + v] = acc[u][v];
+            if (j0 + 4 * tx + v < N)
+                y[(size_t)(m0 + 4 * ty + u) * N + j0 + 4 * tx + v] = odd ? (UK ? CUDART_NAN_F : 0.f) : acc[u][v];
+    }
 }
 
 constexpr int kPQ = 16;   // new tokens per CTA

@@ -236,6 +236,9 @@ expand_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_cons
         const int q = warp & 3, hv = (warp - 4) >> 2;
         const int row = m0 + 128 * r + 32 * q;
         uint8_t *box = smem + kOffOut + (warp - 4) * 2048;
+        // A latent with a NaN or an infinity: NaN keys, so that every new token that sees it is
+        // NaN, and zero values, so that those whose mask hides it (weight 0) do not.
+        const bool odd = row < rows_used && p.odd[row + lane], any_odd = __any_sync(0xffffffffu, odd);
         for (int i = 0; i < parts; ++i) {
             const int v = i & 1, hl = hl0 + (i & ~1) + hv;
             if (!__all_sync(0xffffffffu, wait(&bars->acc_full[v], (i >> 1) & 1))) break;
@@ -253,6 +256,10 @@ expand_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_cons
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) arrive_cluster(mapa(smem_u32(&bars->acc_free[v]), 0));
+                }
+                if (any_odd) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = odd ? (v ? 0u : 0x7fc00000u) : x[e];
                 }
                 // rows of 64 bytes, 16-byte chunks rotated by the row pair
 #pragma unroll

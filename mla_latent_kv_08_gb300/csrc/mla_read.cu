@@ -13,6 +13,18 @@ namespace mla {
 
 enum : long long { kSkip = -1, kBadRow = -2, kZeroRow = -3 };
 
+// Whether a 16-byte piece has an infinity or a NaN among its values.
+template <int EL>
+__device__ __forceinline__ bool not_finite(const uint4 &u) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    bool b = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        b |= EL == 4 ? (w[i] & 0x7f800000u) == 0x7f800000u
+                     : (w[i] & 0x7f800000u) == 0x7f800000u || (w[i] & 0x7f80u) == 0x7f80u;
+    return b;
+}
+
 // Rows n[0..N) from token rows tok[0..N) (kSkip: none), by one warp.
 template <int KIND, int N>
 __device__ __forceinline__ void write_rows(const ReadParams &p, const long long (&tok)[N], size_t n0) {
@@ -20,7 +32,8 @@ __device__ __forceinline__ void write_rows(const ReadParams &p, const long long 
     const int r = p.s.r, dR = p.s.dR, D = r + dR;
     if (KIND == MLA_KV_BF16 || KIND == MLA_KV_FP32) {
         constexpr int kEl = KIND == MLA_KV_BF16 ? 2 : 4;
-        const int nv = D * kEl / 16;
+        const int nv = D * kEl / 16, nl = r * kEl / 16;
+        uint32_t odd = 0;                              // bit i: this lane saw one in row i
         for (int v0 = 0; v0 < nv; v0 += 96) {
             uint4 u[N][3];
 #pragma unroll
@@ -37,10 +50,18 @@ __device__ __forceinline__ void write_rows(const ReadParams &p, const long long 
                 for (int k = 0; k < 3; ++k) {
                     const int v = v0 + 32 * k + lane;
                     if (tok[i] >= 0 && v < nv) ((uint4 *)((uint8_t *)p.rows + (n0 + i) * D * kEl))[v] = u[i][k];
+                    if (p.odd && tok[i] >= 0 && v < nl) odd |= (uint32_t)not_finite<kEl>(u[i][k]) << i;
                 }
         }
+        if (p.odd)
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const bool any = __any_sync(0xffffffffu, odd >> i & 1u);
+                if (lane == 0 && tok[i] >= 0) p.odd[n0 + i] = any;
+            }
     } else if (KIND == MLA_KV_MXFP8) {
         const int nv = r / 8, rv = dR / 8;             // eight values at a time
+        uint32_t odd = 0;                              // bit i: this lane saw one in row i
         for (int v0 = 0; v0 < nv; v0 += 64) {
             uint2 c[N][2];
             uint32_t sb[N][2];
@@ -63,11 +84,20 @@ __device__ __forceinline__ void write_rows(const ReadParams &p, const long long 
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const int v = v0 + 32 * k + lane;
-                    if (tok[i] >= 0 && v < nv) dst[v] = mx_expand8(c[i][k], kMx2p120, mx_scale_bf162(sb[i][k]));
+                    if (tok[i] >= 0 && v < nv) {
+                        dst[v] = mx_expand8(c[i][k], kMx2p120, mx_scale_bf162(sb[i][k]));
+                        odd |= (uint32_t)(sb[i][k] == 255u) << i;
+                    }
                 }
                 if (v0 == 0 && tok[i] >= 0 && lane < rv) dst[nv + lane] = rope[i];      // d_R <= 128: 16 lanes
             }
         }
+        if (p.odd)
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const bool any = __any_sync(0xffffffffu, odd >> i & 1u);
+                if (lane == 0 && tok[i] >= 0) p.odd[n0 + i] = any;
+            }
     } else {
 #pragma unroll 1
         for (int i = 0; i < N; ++i) {
@@ -91,6 +121,7 @@ __device__ __forceinline__ void write_rows(const ReadParams &p, const long long 
 template <int KIND>
 __device__ __forceinline__ void fill_row(const ReadParams &p, size_t n, float v) {
     const int lane = threadIdx.x & 31, D = p.s.D();
+    if (p.odd && lane == 0) p.odd[n] = 0;
     if (KIND == MLA_KV_BF16 || KIND == MLA_KV_MXFP8) {
         __nv_bfloat16 *dst = (__nv_bfloat16 *)p.rows + n * D;
         for (int d = lane; d < D; d += 32) dst[d] = __float2bfloat16_rn(v);

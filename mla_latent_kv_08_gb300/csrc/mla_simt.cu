@@ -411,7 +411,7 @@ __device__ __forceinline__ void gather_tile(const DecodeParams &p, int b, int tb
                 const uint32_t w = *((const uint32_t *)(p.codes + row * r) + k);
                 const uint32_t sb = p.mx_scale[row * ng + k / (kMxGroup / 4)];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) dst[e] = mx_value((w >> (8 * e)) & 0xffu, sb);
+                for (int e = 0; e < 4; ++e) dst[e] = sb == 255u ? 0.f : mx_value((w >> (8 * e)) & 0xffu, sb);
             } else {
                 dst[0] = dst[1] = dst[2] = dst[3] = 0.f;
             }
@@ -420,7 +420,15 @@ __device__ __forceinline__ void gather_tile(const DecodeParams &p, int b, int tb
             int tt = idx / dR, d = idx % dR;
             int blk1 = sValid[tt];
             float v = 0.f;
-            if (blk1) v = __bfloat162float(p.rope[((size_t)(blk1 - 1) * bs + (tb + tt) % bs) * dR + d]);
+            if (blk1) {
+                const size_t row = (size_t)(blk1 - 1) * bs + (tb + tt) % bs;
+                v = __bfloat162float(p.rope[row * dR + d]);
+                // a group that is not a number: zeros above (its product with a hidden row's
+                // weight 0 stays 0), and here the NaN for the scores of the rows that see it
+                if (d == 0)
+                    for (int g = 0; g < ng; ++g)
+                        if (p.mx_scale[row * ng + g] == 255u) v = CUDART_NAN_F;
+            }
             sK[tt * Dp + r + d] = v;
         }
     } else {
@@ -588,7 +596,7 @@ __global__ void __launch_bounds__(256) decode_simt_kernel(DecodeParams p) {
         }
         if (tid == 0)
             p.part_lse[(size_t)slot * rows_total + row] =
-                bad ? CUDART_NAN_F : (l > 0.f ? sM[rr] + log2f(l) : -CUDART_INF_F);
+                bad || (KIND == MLA_KV_MXFP8 && l != l) ? CUDART_NAN_F : (l > 0.f ? sM[rr] + log2f(l) : -CUDART_INF_F);
     }
 }
 

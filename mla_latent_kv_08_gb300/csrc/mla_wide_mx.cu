@@ -62,7 +62,8 @@ constexpr uint32_t kOffBuf = 0;
 constexpr uint32_t kOffQ = kOffBuf + kBlocks * kCol;          // 144 KB
 constexpr uint32_t kOffBar = kOffQ + kQSmemBlocks * kQBlock;   // 224 KB
 constexpr uint32_t kOffXchg = kOffBar + 512;                   // [2][128] fp32 row values
-constexpr uint32_t kSmemBytes = kOffXchg + 1024 + 1024;        // + alignment slack
+constexpr uint32_t kOffNan = kOffXchg + 1024;                  // int32 [128], see Bars::nan_step
+constexpr uint32_t kSmemBytes = kOffNan + 512 + 1024;          // + alignment slack
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 384;
 constexpr uint32_t kEpiBoxBytes = 32 * 128;           // epilogue box: [32 rows x 64 dims] bf16
@@ -122,6 +123,10 @@ struct Bars {
     uint64_t xchg_read[4];    // lane quarter q: both halves read the other's value
     uint32_t tmem_base;
     int32_t abort_flag;
+    // 1 + the last step with a group that is not a number. Such a group is expanded to zeros
+    // (its product with a hidden row's weight 0 stays 0); the scores of the tokens at kOffNan
+    // that hold this step become NaN for the rows that see them.
+    int32_t nan_step;
 };
 static_assert(sizeof(Bars) <= 512, "barriers must fit below the exchange area");
 
@@ -171,9 +176,11 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
             mbar_init(&bars->xchg_read[q], 64);
         }
         bars->abort_flag = 0;
+        bars->nan_step = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
     }
+    if (tid < kStep) ((int32_t *)(smem + kOffNan))[tid] = 0;
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&bars->tmem_base)),
@@ -445,6 +452,7 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
                 }
                 tc_fence_after();
                 if (tid == 128) WTRACE(8, K);
+                const int32_t nan_step = *(volatile int32_t *)&bars->nan_step;
                 uint32_t sv[64];
                 TMEM_LD32(lane_addr + kColS + 64 * hs, sv);
                 TMEM_LD32(lane_addr + kColS + 64 * hs + 32, (sv + 32));
@@ -455,10 +463,12 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
                 // with the scaling and each exponent argument is one fma. Hidden slots -> -inf.
                 const bool pos_scale = p.scale_log2 > 0.f;
                 const float cs = pos_scale ? p.scale_log2 : 1.f;
-                if (!pos_scale || __any_sync(0xffffffffu, n_vis < kTile)) {
+                if (!pos_scale || __any_sync(0xffffffffu, n_vis < kTile || nan_step == K + 1)) {
+                    const volatile int32_t *at = (const volatile int32_t *)(smem + kOffNan) + kTile * hs;
 #pragma unroll
                     for (int jj = 0; jj < 64; ++jj) {
-                        const float v = pos_scale ? __uint_as_float(sv[jj]) : __uint_as_float(sv[jj]) * p.scale_log2;
+                        float v = pos_scale ? __uint_as_float(sv[jj]) : __uint_as_float(sv[jj]) * p.scale_log2;
+                        if (at[jj] == K + 1) v = CUDART_NAN_F;
                         sv[jj] = __float_as_uint(jj < n_vis ? v : -CUDART_INF_F);
                     }
                 }
@@ -576,7 +586,7 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
             ++uses;
             if (row_valid && half == 0 && hs == 0)
                 p.part_lse[(size_t)i * rows_seq + row_seq] =
-                    bad ? CUDART_NAN_F : (l_row > 0.f ? m_used + log2f(l_row) : -CUDART_INF_F);
+                    bad || l_row != l_row ? CUDART_NAN_F : (l_row > 0.f ? m_used + log2f(l_row) : -CUDART_INF_F);
             tc_fence_before();     // O reads complete before the next item's first PV
             if (ok && have_next) ok = __all_sync(0xffffffffu, issue_q(i + 1, 1));
         }
@@ -620,7 +630,8 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
                 }
             }
         };
-        auto expand = [&](const Rows &x, uint32_t to) {
+        // `mark`: where not 0, the step (+ 1) to note for groups that are not a number; u: the tile
+        auto expand = [&](const Rows &x, uint32_t to, int mark, int u) {
             // scales up to 1 take one multiplication
             const uint32_t any = x.s[0].x | x.s[0].y | x.s[1].x | x.s[1].y;
             const bool small = !__any_sync(0xffffffffu, any & 0x80808080u);
@@ -631,7 +642,15 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
                     const uint32_t sw = w ? x.s[q].y : x.s[q].x;
                     uint4 o0, o1;
                     if (small) mx_expand16(x.c[q][w], mx_scale120(sw, p8 >> 1), o0, o1);
-                    else mx_expand16(x.c[q][w], kMx2p120, mx_scale_bf162((sw >> (8 * (p8 >> 1))) & 0xffu), o0, o1);
+                    else {
+                        uint32_t b = mx_scale_bf162((sw >> (8 * (p8 >> 1))) & 0xffu);
+                        if (mark && b == 0x7fc07fc0u) {
+                            b = 0;
+                            ((volatile int32_t *)(smem + kOffNan))[kTile * u + 8 * e + 4 * q + r4] = mark;
+                            *(volatile int32_t *)&bars->nan_step = mark;
+                        }
+                        mx_expand16(x.c[q][w], kMx2p120, b, o0, o1);
+                    }
                     // row 4 q + r4 of the warp's atom flips bit 2 of the chunk with q
                     const uint32_t at = to + 512u * q + 2u * w * kCol;
                     st_shared16(at + (chunk ^ (64u * q)), o0);
@@ -680,7 +699,7 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
                 ok = K == 0 || (!own && u) || __all_sync(0xffffffffu, mbar_wait(bar, (K - 1) & 1, bars, p.status));
                 if (!ok) break;
                 WTRACE_E(own ? 14 : 12);
-                expand(x, to + 8192u * u);
+                expand(x, to + 8192u * u, own ? K + 1 : 0, u);
                 if (u == 0) x = y;
             }
             if (!ok) break;

@@ -278,6 +278,39 @@ def test_stale_slots_are_not_read(gpu_lib, impl, H):
     _check(w, out, lse, _stored(w))
 
 
+@pytest.mark.parametrize("impl", IMPLS)
+@pytest.mark.parametrize("H,q_len", [(16, 1), (16, 2), (16, 4), (64, 1), (128, 1), (128, 3), (40, 6)])
+def test_not_a_number_in_a_draft(gpu_lib, impl, H, q_len):
+    """A cached token with a NaN or an infinity makes the rows that see it NaN and leaves
+    those whose mask hides it as they are."""
+    import mla_latent_kv_08_gb300 as mla
+    lens = [200, 129, 66, 700, 385, 30]
+    w = _workload(55, lens, H=H, q_len=q_len)
+    if impl == "roomy":
+        _roomy(w)
+    at = [199, 128 - (q_len > 1), 65, 350, 385 - q_len, None]           # the token, of each sequence
+    dim = [0, 511, 255, 100, 290, None]
+    for b, (t, d) in enumerate(zip(at, dim)):
+        if t is not None:
+            w.latent[b][t, d] = [np.nan, np.inf, -np.inf][b % 3]
+    w.rope[5][29, 63] = np.nan                                          # and in a rope key
+    at[5] = 29
+    shape = _shape(mla, w, impl=_impl(mla, impl), num_splits_hint=5)
+    cache, _ = gu.fill_cache(w, shape)
+    out, lse, ws = gu.attend(w, shape, cache, w.q, q_len=q_len)
+    assert mla.mla_get_status(ws) == (mla.MLA_OK, 0)
+    for b, (t, L) in enumerate(zip(at, lens)):
+        w.latent[b][t], w.rope[b][t] = 0, 0                             # hidden from the rows that are held to it
+    lat = _stored(w)
+    for b, (t, L) in enumerate(zip(at, lens)):
+        sees = L - q_len + np.arange(q_len) >= t
+        assert np.isnan(out[b][sees]).all() and np.isnan(lse[b][sees]).all(), b
+        if not sees.all():
+            ro, rl = attention.absorbed(w.q[b], lat[b], w.rope[b], w.W_UV, w.scale)
+            assert gu.rel_err(out[b][~sees], ro[~sees]) <= gu.BF16_REL_TOL, b
+            assert np.max(np.abs(lse[b][~sees] - rl[~sees])) <= gu.BF16_LSE_TOL, b
+
+
 @pytest.mark.parametrize("H", [16, 128])
 @pytest.mark.parametrize("impl", IMPLS)
 def test_bad_lengths_and_blocks_give_nan_rows(gpu_lib, impl, H):

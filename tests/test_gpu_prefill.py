@@ -272,6 +272,29 @@ def test_capture_and_replay_with_other_lengths(gpu_lib):
     assert np.isnan(out[60:]).all() and mla.mla_get_status(a["workspace"])[0] == mla.MLA_ERR_BOUNDS
 
 
+@pytest.mark.parametrize("kind,impl", [("bf16", 0), ("bf16", 1), ("mxfp8", 0), ("mxfp8", 1), ("fp32", 1)])
+def test_not_a_number_in_a_later_token(gpu_lib, kind, impl):
+    """A cached token with a NaN or an infinity makes the new tokens that see it NaN and leaves
+    those before it as they are."""
+    import mla_latent_kv_08_gb300 as mla
+    case = Case(102, [300, 130, 40, 200, 9], [50, 0, 100, 250, 30], H=3, kind=kind)
+    at = [349, 1, 139, 300, 38]                                          # the token, of each sequence
+    for b, t in enumerate(at):
+        if b < 4:
+            case.lat[b][t, [0, 511, 255, 100][b]] = [np.nan, np.inf, -np.inf, np.nan][b]
+        else:
+            case.rope[b][t, 63] = np.nan
+    out, lse, status = _run(mla, case, case.shape(mla, impl=impl))
+    assert status == (mla.MLA_OK, 0)
+    for b, t in enumerate(at):
+        case.lat[b][t], case.rope[b][t] = 0, 0                           # hidden from the rows that are held to it
+        n, L = int(case.new[b]), int(case.L[b])
+        first = t - (L - n)                                              # the first new token that sees it
+        mine = slice(int(case.cu[b]) + first, int(case.cu[b]) + n)
+        assert np.isnan(out[mine]).all() and np.isnan(lse[mine]).all(), b
+        case.check(out, lse, seqs=[b], rows=np.arange(first))
+
+
 # ------------------------------------------------------------------ as they are used together
 
 def test_prompt_then_steps(gpu_lib):
