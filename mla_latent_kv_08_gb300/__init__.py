@@ -151,9 +151,10 @@ def _check(code: int, where: str) -> None:
 # ---------------------------------------------------------------- shapes
 
 @functools.lru_cache(maxsize=256)
-def _shape_struct(*fields) -> mla_shape:
-    """The C struct of these fields (the library only reads it)."""
-    return mla_shape(*fields)
+def _shape_ref(*fields):
+    """A reference to the C struct of these fields, for the calls below (the library only
+    reads it), by value: a shape that changes gets another."""
+    return ctypes.byref(mla_shape(*fields))
 
 
 @dataclasses.dataclass
@@ -173,10 +174,15 @@ class Shape:
     index_dim: int = 0
     flags: int = 0
 
+    def _fields(self) -> tuple:
+        return (self.num_heads, self.kv_lora_rank, self.rope_dim, self.v_head_dim, self.block_size, self.num_blocks,
+                self.group_size, self.kind, self.impl, self.num_splits_hint, self.index_dim, self.flags)
+
     def c(self) -> mla_shape:
-        return _shape_struct(self.num_heads, self.kv_lora_rank, self.rope_dim, self.v_head_dim,
-                         self.block_size, self.num_blocks, self.group_size, self.kind, self.impl,
-                         self.num_splits_hint, self.index_dim, self.flags)
+        return mla_shape(*self._fields())
+
+    def _ref(self):
+        return _shape_ref(*self._fields())
 
     @property
     def D(self) -> int:
@@ -252,7 +258,7 @@ class Cache:
 # ---------------------------------------------------------------- entry points
 
 def mla_workspace_bytes(shape: Shape, B: int, q_len: int = 1) -> int:
-    n = load_library().mla_workspace_bytes(ctypes.byref(shape.c()), int(B), int(q_len))
+    n = load_library().mla_workspace_bytes(shape._ref(), int(B), int(q_len))
     if n == 0:
         raise MlaError(MLA_ERR_INVALID, "mla_workspace_bytes")
     return int(n)
@@ -268,7 +274,7 @@ def mla_latent_append(cache: Cache, block_table, start_pos, cu_new, c_kv, k_rope
     """Write len(c_kv) new tokens into the paged cache (see include/mla.h)."""
     lib = load_library()
     B = int(start_pos.shape[0])
-    code = lib.mla_latent_append(ctypes.byref(cache.shape.c()), ctypes.byref(cache.c()), _ptr(block_table),
+    code = lib.mla_latent_append(cache.shape._ref(), ctypes.byref(cache.c()), _ptr(block_table),
                                  int(block_table.shape[1]), B, _ptr(start_pos), _ptr(cu_new),
                                  int(c_kv.shape[0]), _ptr(c_kv), _ptr(k_rope), _ptr(R), _ptr(clip),
                                  _ptr(status), _stream(stream))
@@ -279,7 +285,7 @@ def mla_latent_append_index(cache: Cache, block_table, start_pos, cu_new, index_
                             stream=None) -> None:
     """Write the extra per-token key of len(index_key) tokens (see include/mla.h)."""
     lib = load_library()
-    code = lib.mla_latent_append_index(ctypes.byref(cache.shape.c()), ctypes.byref(cache.c()), _ptr(block_table),
+    code = lib.mla_latent_append_index(cache.shape._ref(), ctypes.byref(cache.c()), _ptr(block_table),
                                        int(block_table.shape[1]), int(start_pos.shape[0]), _ptr(start_pos),
                                        _ptr(cu_new), int(index_key.shape[0]), _ptr(index_key), _ptr(status),
                                        _stream(stream))
@@ -290,14 +296,14 @@ def mla_latent_read(cache: Cache, block_table, start_pos, cu_rows, rows, status=
     """Cached tokens back as dense rows [len(rows), r + d_R] (see include/mla.h): bf16 for
     the BF16 and MXFP8 kinds, fp32 for the others."""
     lib = load_library()
-    code = lib.mla_latent_read(ctypes.byref(cache.shape.c()), ctypes.byref(cache.c()), _ptr(block_table),
+    code = lib.mla_latent_read(cache.shape._ref(), ctypes.byref(cache.c()), _ptr(block_table),
                                int(block_table.shape[1]), int(start_pos.shape[0]), _ptr(start_pos), _ptr(cu_rows),
                                int(rows.shape[0]), _ptr(rows), _ptr(status), _stream(stream))
     _check(code, "mla_latent_read")
 
 
 def mla_prefill_workspace_bytes(shape: Shape, B: int, num_q: int, max_tokens: int, nope_dim: int) -> int:
-    n = load_library().mla_prefill_workspace_bytes(ctypes.byref(shape.c()), int(B), int(num_q), int(max_tokens),
+    n = load_library().mla_prefill_workspace_bytes(shape._ref(), int(B), int(num_q), int(max_tokens),
                                                    int(nope_dim))
     if n == 0:
         raise MlaError(MLA_ERR_INVALID, "mla_prefill_workspace_bytes")
@@ -315,7 +321,7 @@ def mla_prefill(cache: Cache, block_table, seq_lens, cu_q, q, W_UK, W_UV, scale:
     """Attention of chunks of new tokens, q [num_q, H, d_n + d_R] (not absorbed), over the
     cache that holds them already -> out [num_q, H, d_v], lse [num_q, H] (see include/mla.h)."""
     lib = load_library()
-    code = lib.mla_prefill(ctypes.byref((shape or cache.shape).c()), ctypes.byref(cache.c()), _ptr(block_table),
+    code = lib.mla_prefill((shape or cache.shape)._ref(), ctypes.byref(cache.c()), _ptr(block_table),
                            int(block_table.shape[1]), _ptr(seq_lens), _ptr(cu_q), int(seq_lens.shape[0]),
                            int(q.shape[0]), int(max_tokens), int(W_UK.shape[1]), _ptr(q), _ptr(W_UK), _ptr(W_UV),
                            float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
@@ -328,7 +334,7 @@ def mla_decode(cache: Cache, block_table, seq_lens, q, W_UV, scale: float, out, 
     """Decode attention, q [B, 1, H, r + d_R] -> out [B, 1, H, d_v], lse [B, 1, H].
     ``shape`` overrides ``cache.shape`` (e.g. to set flags for this call)."""
     lib = load_library()
-    code = lib.mla_decode(ctypes.byref((shape or cache.shape).c()), ctypes.byref(cache.c()), _ptr(block_table),
+    code = lib.mla_decode((shape or cache.shape)._ref(), ctypes.byref(cache.c()), _ptr(block_table),
                           int(block_table.shape[1]), _ptr(seq_lens), int(seq_lens.shape[0]), _ptr(q),
                           _ptr(W_UV), _ptr(R), float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
                           int(workspace.numel() * workspace.element_size()), _stream(stream))
@@ -341,7 +347,7 @@ def mla_append_decode(cache: Cache, block_table, start_pos, cu_new, c_kv, k_rope
     """mla_latent_append of len(c_kv) new tokens, then mla_decode over the cache that
     holds them, in one call (see include/mla.h)."""
     lib = load_library()
-    code = lib.mla_append_decode(ctypes.byref((shape or cache.shape).c()), ctypes.byref(cache.c()),
+    code = lib.mla_append_decode((shape or cache.shape)._ref(), ctypes.byref(cache.c()),
                                  _ptr(block_table), int(block_table.shape[1]), int(seq_lens.shape[0]),
                                  _ptr(start_pos), _ptr(cu_new), int(c_kv.shape[0]), _ptr(c_kv), _ptr(k_rope),
                                  _ptr(clip), _ptr(append_status), _ptr(seq_lens), _ptr(q), _ptr(W_UV), _ptr(R),
@@ -354,7 +360,7 @@ def mla_verify(cache: Cache, block_table, seq_lens, q, W_UV, scale: float, out, 
                R=None, stream=None, shape: Optional[Shape] = None) -> None:
     """Speculative verify, q [B, q_len, H, r + d_R] with the causal draft window."""
     lib = load_library()
-    code = lib.mla_verify(ctypes.byref((shape or cache.shape).c()), ctypes.byref(cache.c()), _ptr(block_table),
+    code = lib.mla_verify((shape or cache.shape)._ref(), ctypes.byref(cache.c()), _ptr(block_table),
                           int(block_table.shape[1]), _ptr(seq_lens), int(seq_lens.shape[0]), int(q.shape[1]),
                           _ptr(q), _ptr(W_UV), _ptr(R), float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
                           int(workspace.numel() * workspace.element_size()), _stream(stream))
@@ -364,7 +370,7 @@ def mla_verify(cache: Cache, block_table, seq_lens, q, W_UV, scale: float, out, 
 def mla_fold_rotation(shape: Shape, R, W_UV, W_folded, stream=None) -> None:
     """W_folded[h] = R^T . W_UV[h] (bf16), for decode with MLA_FLAG_WUV_FOLDED (see include/mla.h)."""
     lib = load_library()
-    _check(lib.mla_fold_rotation(ctypes.byref(shape.c()), _ptr(R), _ptr(W_UV), _ptr(W_folded), _stream(stream)),
+    _check(lib.mla_fold_rotation(shape._ref(), _ptr(R), _ptr(W_UV), _ptr(W_folded), _stream(stream)),
            "mla_fold_rotation")
 
 
@@ -374,7 +380,7 @@ def mla_decode_noalloc(cache: Cache, block_table, seq_lens, q, W_UV, scale: floa
     workspace, for callers that cannot allocate device memory at call time (see
     include/mla.h for the size limit and the ordering rule)."""
     lib = load_library()
-    code = lib.mla_decode_noalloc(ctypes.byref(cache.shape.c()), ctypes.byref(cache.c()), _ptr(block_table),
+    code = lib.mla_decode_noalloc(cache.shape._ref(), ctypes.byref(cache.c()), _ptr(block_table),
                                   int(block_table.shape[1]), _ptr(seq_lens), int(seq_lens.shape[0]), _ptr(q),
                                   _ptr(W_UV), _ptr(R), float(scale), _ptr(out), _ptr(lse), _ptr(status),
                                   _stream(stream))
@@ -401,7 +407,7 @@ def mla_selftest_wait_timeout(timeout_ns: int, status, stream=None) -> None:
 
 
 def mla_resolve_impl(shape: Shape, q_len: int = 1) -> int:
-    return int(load_library().mla_resolve_impl(ctypes.byref(shape.c()), int(q_len)))
+    return int(load_library().mla_resolve_impl(shape._ref(), int(q_len)))
 
 
 def mla_version() -> int:

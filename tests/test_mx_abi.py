@@ -80,6 +80,19 @@ def test_shapes(lib):
         assert mla.mla_resolve_impl(_shape(**bad)) == mla.MLA_ERR_INVALID, bad
 
 
+def test_a_changed_shape_counts(lib):
+    """Calls go by the shape's fields at the time, and a struct handed out is the caller's own."""
+    import mla_latent_kv_08_gb300 as mla
+    s = _shape()
+    before = mla.mla_workspace_bytes(s, 4)
+    s.c().num_heads = 1
+    assert mla.mla_workspace_bytes(s, 4) == before
+    s.kv_lora_rank = 520
+    assert mla.mla_resolve_impl(s) == mla.MLA_ERR_INVALID
+    s.kv_lora_rank = 512
+    assert mla.mla_workspace_bytes(s, 4) == before
+
+
 FAKE = ctypes.c_void_p(4096)         # never dereferenced: every call here is refused on the host
 ODD = ctypes.c_void_p(4100)
 
