@@ -484,6 +484,7 @@ static PrefillWs prefill_ws(const mla_shape *s, int32_t B, int32_t max_tokens, i
     const size_t ekv = prefill_tc(s, dn) ? 2 : 4;        // the CUDA-core path keeps fp32 keys and values
     const size_t head = (size_t)w.cap_rows * (size_t)(dn + s->v_head_dim) * ekv;
     size_t n = kPrefillKvBytes / head;
+    if (n > 65535) n = 65535;    // a dimension of the grids
     w.heads = (int32_t)(n < 1 ? 1 : n > (size_t)s->num_heads ? (size_t)s->num_heads : n);
     size_t off = 256;            // the flags word
     w.kv_off = off;    off = up256(off + sizeof(int32_t) * ((size_t)B + 1));

@@ -13,6 +13,7 @@
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
+#include <limits.h>
 #include <math_constants.h>
 #include <string.h>
 
@@ -698,16 +699,22 @@ cudaError_t launch_prefill_tc(const PrefillParams &p, cudaStream_t st) {
     e = cudaFuncGetAttributes(&at, prefill_tc_kernel);
     if (e != cudaSuccess) return e;
     if (at.numRegs < kRegsLaunch) return cudaErrorInvalidConfiguration;
-    // Heads a pair makes in a row: as many as leave about four pairs' turns for each pair of
-    // SMs (the rows are then loaded seldom, and the last turn costs little).
+    // Heads a pair of CTAs makes in a row: those that give the least rounds x (heads + what a
+    // pair's start and end cost, about 2.5 heads' time). The rows that the sequences' ends
+    // leave of their last 128 are counted half.
     int dev = 0, sms = 0;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess ||
         (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
         return e;
-    const long long tiles = (p.cap_rows + 255) / 256;
-    long long heads = p.nh * tiles / (2ll * sms);
-    heads = heads < 2 ? 2 : heads > p.nh ? p.nh : heads;
-    heads += heads & 1;
+    const long long tiles = (p.cap_rows + 255) / 256, likely = (p.cap_rows - 64ll * p.B + 255) / 256;
+    long long heads = 2, least = LLONG_MAX;
+    for (int n = 2; n < p.nh + 2; n += 2) {
+        const long long cost = (2 * n + 5) * ((likely * ((p.nh + n - 1) / n) + sms / 2 - 1) / (sms / 2));
+        if (cost < least) {
+            least = cost;
+            heads = n;
+        }
+    }
     ex::expand_tc_kernel<<<dim3((unsigned)(2 * tiles), (unsigned)((p.nh + heads - 1) / heads)), ex::kThreads, ex::kSmemBytes, st>>>(
         rows, uk, uv, p, (int)heads);
     prefill_tc_kernel<<<dim3(2 * (p.num_q / kTileQ + p.B), p.nh), kThreads, kSmemBytes, st>>>(q, k_ld, v_ld, rope, p);
