@@ -36,6 +36,7 @@ __device__ __forceinline__ long long scan1024(long long v, long long *s_warp, lo
 
 __global__ void __launch_bounds__(1024) prefill_plan_kernel(PrefillParams p) {
     __shared__ long long s_warp[32];
+    pdl_trigger();
     if (threadIdx.x == 0) p.status[0] = 0;
     __syncthreads();
     const long long cap_tokens = (long long)p.max_blocks * p.s.bs;

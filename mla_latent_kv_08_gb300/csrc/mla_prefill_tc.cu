@@ -125,6 +125,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 expand_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_constant__ CUtensorMap uk_map,
                  const __grid_constant__ CUtensorMap uv_map, const PrefillParams p, int heads) {
     const int r = (int)cluster_ctarank(), m0 = (blockIdx.x >> 1) * 256;
+    pdl_trigger();
+    pdl_wait();
     const int rows_used = p.kv_off[p.B];
     if (m0 >= rows_used) return;                       // both CTAs of a pair
     const int hl0 = blockIdx.y * heads, nh = min(heads, p.nh - hl0);     // heads of this pass (`heads` is even)
@@ -374,6 +376,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 2)
 prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap rope_map,
                   const PrefillParams p) {
+    pdl_trigger();
+    pdl_wait();
     // the last tiles of a sequence see the most: they start first
     const int tiles = p.tile_off[p.B];
     if ((int)(blockIdx.x >> 1) >= tiles) return;         // both CTAs of a pair
@@ -715,10 +719,10 @@ cudaError_t launch_prefill_tc(const PrefillParams &p, cudaStream_t st) {
             heads = n;
         }
     }
-    ex::expand_tc_kernel<<<dim3((unsigned)(2 * tiles), (unsigned)((p.nh + heads - 1) / heads)), ex::kThreads, ex::kSmemBytes, st>>>(
-        rows, uk, uv, p, (int)heads);
-    prefill_tc_kernel<<<dim3(2 * (p.num_q / kTileQ + p.B), p.nh), kThreads, kSmemBytes, st>>>(q, k_ld, v_ld, rope, p);
-    return cudaGetLastError();
+    e = launch_pdl(ex::expand_tc_kernel, dim3((unsigned)(2 * tiles), (unsigned)((p.nh + heads - 1) / heads)), dim3(ex::kThreads),
+                   ex::kSmemBytes, st, rows, uk, uv, p, (int)heads);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(prefill_tc_kernel, dim3(2 * (p.num_q / kTileQ + p.B), p.nh), dim3(kThreads), kSmemBytes, st, q, k_ld, v_ld, rope, p);
 }
 
 }  // namespace mla

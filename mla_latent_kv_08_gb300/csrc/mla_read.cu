@@ -155,6 +155,8 @@ __device__ __forceinline__ long long find_token(const ReadParams &p, int n) {
 template <int KIND, int N>              // N rows a warp, two at a time
 __global__ void __launch_bounds__(256, KIND == MLA_KV_MXFP8 || KIND == MLA_KV_BF16 ? 5 : 4) read_kernel(ReadParams p) {
     const int lane = threadIdx.x & 31;
+    pdl_trigger();
+    pdl_wait();
     const long long n0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * N;
     if (n0 >= p.num_rows) return;
     const long long mine = lane < N ? find_token(p, (int)min(n0 + lane, (long long)INT32_MAX)) : kSkip;
@@ -173,23 +175,24 @@ __global__ void __launch_bounds__(256, KIND == MLA_KV_MXFP8 || KIND == MLA_KV_BF
 }
 
 template <int KIND>
-static void launch_kind(const ReadParams &p, cudaStream_t st) {
+static cudaError_t launch_kind(const ReadParams &p, cudaStream_t st) {
     // a warp a row while that leaves SMs free, else eight rows a warp
-    if (p.num_rows > 4096)
-        read_kernel<KIND, 8><<<(unsigned)((p.num_rows + 63ll) / 64), 256, 0, st>>>(p);
-    else
-        read_kernel<KIND, 1><<<(unsigned)((p.num_rows + 7ll) / 8), 256, 0, st>>>(p);
+    const bool many = p.num_rows > 4096;
+    const auto kern = many ? read_kernel<KIND, 8> : read_kernel<KIND, 1>;
+    const dim3 grid((unsigned)(many ? (p.num_rows + 63ll) / 64 : (p.num_rows + 7ll) / 8));
+    if (p.lens) return launch_pdl(kern, grid, dim3(256), 0, st, p);      // behind the prefill's plan
+    kern<<<grid, 256, 0, st>>>(p);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_read(const ReadParams &p, cudaStream_t st) {
     if (p.num_rows == 0) return cudaSuccess;
     switch (p.s.kind) {
-        case MLA_KV_BF16: launch_kind<MLA_KV_BF16>(p, st); break;
-        case MLA_KV_FP32: launch_kind<MLA_KV_FP32>(p, st); break;
-        case MLA_KV_MXFP8: launch_kind<MLA_KV_MXFP8>(p, st); break;
-        default: launch_kind<MLA_KV_INT2_ROT>(p, st); break;
+        case MLA_KV_BF16: return launch_kind<MLA_KV_BF16>(p, st);
+        case MLA_KV_FP32: return launch_kind<MLA_KV_FP32>(p, st);
+        case MLA_KV_MXFP8: return launch_kind<MLA_KV_MXFP8>(p, st);
+        default: return launch_kind<MLA_KV_INT2_ROT>(p, st);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace mla
