@@ -336,18 +336,19 @@ static_assert(kRegsIssue + kRegsSoftmax <= 2 * kRegsLaunch, "register split");
 constexpr int kTileQ = kPrefillTcTile;
 constexpr uint32_t kKBlock = 64 * 128;                  // 8 KB
 constexpr uint32_t kOffK = 3 * kBlock;                  // after Q
-constexpr uint32_t kOffV = kOffK + 3 * kKBlock;
+constexpr uint32_t kStageK = 3 * kKBlock;               // two of them
+constexpr uint32_t kOffV = kOffK + 2 * kStageK;
 constexpr uint32_t kOffBar = kOffV + kBlock;
-constexpr uint32_t kSmemBytes = kOffBar + 128 + 1024;
-static_assert(kSmemBytes <= 232448 / 2 - 1024, "shared memory budget of two CTAs");
+constexpr uint32_t kSmemBytes = kOffBar + 128;          // (no slack: the kernel checks its base)
+static_assert(kSmemBytes <= 228 * 1024 / 2 - 1024, "shared memory budget of two CTAs");
 constexpr uint32_t kTmem = 256;
 constexpr uint32_t kColS = 0, kColO = 128;
 
 struct Bars {
     // of CTA 0: both CTAs' copies landed; both CTAs' weights are stored (a warp an arrival)
-    uint64_t q_full, full, p_full;
+    uint64_t q_full, full[2], p_full;
     // of each CTA, from CTA 0's products
-    uint64_t empty;            // the turn's keys and values are read
+    uint64_t empty;            // a step's P . V is done
     uint64_t s_full;           // the step's scores are there (and the P . V before)
     uint64_t o_full;
     uint32_t tmem_base;
@@ -399,12 +400,16 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     const int L = p.seq_lens[b];
     const int steps = (L - n + i0 + rows_here + 127) / 128;      // of the tile's last row
 
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023u) {          // both CTAs: the swizzled blocks need it
+        raise_flag(p.status, FLAG_TIMEOUT);
+        return;
+    }
     Bars *bars = (Bars *)(smem + kOffBar);
     if (tid == 0) {
         mbar_init(&bars->q_full, 1);
-        mbar_init(&bars->full, 1);
+        mbar_init(&bars->full[0], 1);
+        mbar_init(&bars->full[1], 1);
         mbar_init(&bars->p_full, 8);
         mbar_init(&bars->empty, 1);
         mbar_init(&bars->s_full, 1);
@@ -430,33 +435,37 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     };
 
     // The copies go in turns: turn t brings step t's keys and step t - 1's values, which the
-    // products take together (turn 0: keys only; turn `steps`: values only).
+    // products take one after the other (turn 0: keys only; turn `steps`: values only). Two
+    // turns are on their way at a time: turn t starts when the P . V of step t - 2 is done,
+    // which read the values that stood in its place, its scores before it the keys.
     if (warp == 0) {
         // ================================================= copies
         reg_dec<kRegsIssue>();
         if (lane == 0) {
             const int row0 = p.kv_off[b];
             const int kv0 = hl * p.cap_rows + row0;           // fits: the pass's rows are counted in 32 bits
-            const uint32_t q_bar = mapa(smem_u32(&bars->q_full), 0), bar = mapa(smem_u32(&bars->full), 0);
+            const uint32_t q_bar = mapa(smem_u32(&bars->q_full), 0);
             if (r == 0) mbar_expect_tx(&bars->q_full, 6 * kBlock);
             for (int c = 0; c < 3; ++c)
                 tma_pair_3d(smem + c * kBlock, &q_map, 64 * c, h, (int)qrow0 + 128 * r, q_bar);
             int u = 0;
             for (; u <= steps; ++u) {
-                if (u > 0 && !wait(&bars->empty, (u - 1) & 1)) break;
-                if (r == 0) mbar_expect_tx(&bars->full, (u < steps ? 6 * kKBlock : 0u) + (u > 0 ? 2 * kBlock : 0u));
+                if (u > 1 && !wait(&bars->empty, u & 1)) break;
+                const uint32_t bar = mapa(smem_u32(&bars->full[u & 1]), 0);
+                if (r == 0) mbar_expect_tx(&bars->full[u & 1], (u < steps ? 6 * kKBlock : 0u) + (u > 0 ? 2 * kBlock : 0u));
                 if (u > 0) tma_pair_2d(smem + kOffV, &v_map, 64 * r, kv0 + 128 * (u - 1), bar);
                 if (u < steps) {
-                    tma_pair_2d(smem + kOffK, &k_map, 0, kv0 + 128 * u + 64 * r, bar);
-                    tma_pair_2d(smem + kOffK + kKBlock, &k_map, 64, kv0 + 128 * u + 64 * r, bar);
-                    tma_pair_2d(smem + kOffK + 2 * kKBlock, &rope_map, kR, row0 + 128 * u + 64 * r, bar);
+                    uint8_t *k = smem + kOffK + (u & 1) * kStageK;
+                    tma_pair_2d(k, &k_map, 0, kv0 + 128 * u + 64 * r, bar);
+                    tma_pair_2d(k + kKBlock, &k_map, 64, kv0 + 128 * u + 64 * r, bar);
+                    tma_pair_2d(k + 2 * kKBlock, &rope_map, kR, row0 + 128 * u + 64 * r, bar);
                 }
             }
             // Never leave a copy in flight into the pair's shared memory: CTA 0 waits here for
             // both CTAs' copies, CTA 1 for CTA 0 at the end.
             if (r == 0) {
                 mbar_drain(&bars->q_full, 0);
-                mbar_drain(&bars->full, (u - 1) & 1);
+                for (int v = max(0, u - 2); v < u; ++v) mbar_drain(&bars->full[v & 1], (v >> 1) & 1);
             }
         }
         __syncwarp();
@@ -470,29 +479,28 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
             const uint32_t tS = tmem + kColS, tO = tmem + kColO;
             // Between one product and the next stand as few instructions as can be: the first
             // probe of a barrier is inline, the bounded wait out of line.
-            const uint32_t full = smem_u32(&bars->full), p_full = smem_u32(&bars->p_full);
+            const uint32_t full = smem_u32(bars->full), p_full = smem_u32(&bars->p_full);
             auto there = [&](uint32_t bar, uint32_t parity) {
                 return mbar_test32(bar, parity) || wait_slow(bar, parity, &bars->abort_flag, p.status);
             };
-            auto scores = [&]() {
+            auto scores = [&](uint32_t stage) {
+                const uint64_t ks = kd + stage * (kStageK >> 4);
 #pragma unroll
                 for (int c = 0; c < 3; ++c)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const uint64_t a = qd + c * (kBlock >> 4) + 2 * e, k = kd + c * (kKBlock >> 4) + 2 * e;
+                        const uint64_t a = qd + c * (kBlock >> 4) + 2 * e, k = ks + c * (kKBlock >> 4) + 2 * e;
                         if (c == 0 && e == 0) mma2_ss<kIdS, 0>(tS, a, k);
                         else mma2_ss<kIdS, 1>(tS, a, k);
                     }
                 commit2(&bars->s_full);
             };
-            bool ok = wait(&bars->q_full, 0) && wait(&bars->full, 0);
+            bool ok = wait(&bars->q_full, 0) && wait(&bars->full[0], 0);
             tc_fence_after();
-            if (ok) {
-                scores();
-                commit2(&bars->empty);
-            }
+            if (ok) scores(0);
             for (int j = 0; j < steps && ok; ++j) {
-                ok = there(full, (j + 1) & 1);
+                const uint32_t s = (j + 1) & 1;                // of turn j + 1
+                ok = there(full + 8 * s, ((j + 1) >> 1) & 1);
                 PTRACE(0, j);
                 ok = ok && there(p_full, j & 1);
                 if (!ok) break;
@@ -500,10 +508,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
                 tc_fence_after();
 #pragma unroll
                 for (int e = 0; e < 8; ++e) mma2_ts(tO, tS + 8 * e, vd + 128 * e, kIdO, (j > 0 || e > 0) ? 1u : 0u);
-                PTRACE(2, j);
-                if (j + 1 < steps) scores();
-                else commit2(&bars->o_full);
                 commit2(&bars->empty);
+                PTRACE(2, j);
+                if (j + 1 < steps) scores(s);
+                else commit2(&bars->o_full);
                 PTRACE(3, j);
             }
             // products in flight must end before the tensor memory is given back
