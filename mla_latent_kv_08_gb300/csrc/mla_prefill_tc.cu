@@ -58,6 +58,13 @@ __device__ __forceinline__ void mma2_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
         ::"r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
+__device__ __forceinline__ void prefetch_2d(const CUtensorMap *map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"((uint64_t)map), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void prefetch_3d(const CUtensorMap *map, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"((uint64_t)map), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
 // Arrives, once the products issued so far are done, on this barrier of both CTAs.
 __device__ __forceinline__ void commit2(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
@@ -406,6 +413,15 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         return;
     }
     Bars *bars = (Bars *)(smem + kOffBar);
+    const int row0 = p.kv_off[b];
+    const int kv0 = hl * p.cap_rows + row0;               // fits: the pass's rows are counted in 32 bits
+    if (tid == 64) {                       // an idle warp: the first step's operands into L2 during the set-up
+        for (int c = 0; c < 3; ++c) prefetch_3d(&q_map, 64 * c, h, (int)qrow0 + 128 * r);
+        prefetch_2d(&k_map, 0, kv0 + 64 * r);
+        prefetch_2d(&k_map, 64, kv0 + 64 * r);
+        prefetch_2d(&rope_map, kR, row0 + 64 * r);
+        prefetch_2d(&v_map, 64 * r, kv0);
+    }
     if (tid == 0) {
         mbar_init(&bars->q_full, 1);
         mbar_init(&bars->full[0], 1);
@@ -442,8 +458,6 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
         // ================================================= copies
         reg_dec<kRegsIssue>();
         if (lane == 0) {
-            const int row0 = p.kv_off[b];
-            const int kv0 = hl * p.cap_rows + row0;           // fits: the pass's rows are counted in 32 bits
             const uint32_t q_bar = mapa(smem_u32(&bars->q_full), 0);
             if (r == 0) mbar_expect_tx(&bars->q_full, 6 * kBlock);
             for (int c = 0; c < 3; ++c)
