@@ -19,6 +19,12 @@
 // reduction; one that does not finds the rows' maxima and moves m there. Row sums stay a
 // thread's own until the end of a work item.
 //
+// Measured, 64 heads over two sequences of 52k and 75k tokens: 54 us
+// (the pair kernel: 64 us), bytes at the copy rate 12.4 us. The tensor pipe is busy for
+// 14 % of the time: a product whose first operand lies MN-major in shared memory takes 139
+// cycles, twice a K-major one, and a step's scores wait for its expansion. Taking V^T from
+// a second, transposed copy would cost the room of the step after.
+//
 // Shared memory: nine 16 KB column blocks of a step (the rope block, done with after the
 // scores, then holds P^T), Q, statistics. The blocks of dim tile c are written again for the
 // next step as soon as its P . V is done, while the other tiles' run, by eight warps that

@@ -106,6 +106,10 @@ template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setma
 // columns). Keys and values have accumulators of their own, the whole of tensor memory, so
 // that one is rounded and stored while the other is made. W_UK[h] is K-major as it lies
 // ([d_n, r]), W_UV[h] MN-major ([r, d_v]).
+//
+// They are rounded to bf16, the type of the next products' operands. Measured: 37k rows on
+// 128 heads 0.81 ms, 1.53 PFLOP/s (cuBLAS in a loop of seconds 1.74); 28k rows on 16 heads
+// 89 us. Without pairs 1.21 ms. Bound by the tensor pipe and, on long ones, the power cap.
 // ============================================================================
 namespace ex {
 constexpr int kThreads = 384;                          // warp 0 copies, 1 products (CTA 0), 4..11 output
@@ -316,6 +320,15 @@ expand_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_cons
 //   P = 2^(S c - m)          a thread a row: no shuffles
 //   O[256 x 128] += P . V    8 x M256 N128 K16, P from tensor memory
 //
+// Measured: two chunks of 2048 over 18k tokens on 128 heads 4.45 ms for 5.8 TFLOP, 1.30
+// PFLOP/s; 4 prompts of 2100 to 3400 tokens 1.19 ms, 1.01 PFLOP/s; 6 turns of up to 200 tokens
+// 66 us. A step of both pairs of an SM takes 3000 cycles, the products' own pace, while they
+// take turns at the tensor cores, and up to 4300 while both queue products and then both
+// exponentials at the same time; the pairs know nothing of each other, and holding one back
+// when its products took longer than they do alone gave 4 % on short chunks and lost as much
+// on long ones. A tile's set-up, first copies and output cost about 12000 cycles, which
+// bounds turns.
+//
 // Two pairs share their SMs: while one's warps turn scores into weights, copy or store, the
 // tensor cores work on the other. (Two sub-tiles of one pair taking turns, with three steps'
 // keys and values in flight, were as fast on long chunks, 5.48 against 5.33 ms for two chunks
@@ -331,9 +344,9 @@ expand_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_cons
 // thread of CTA 0, so that the next scores overwrite P only once P . V has read it. m is
 // raised lazily, only when it grows by more than 8 (P <= 2^8).
 //
-// Shared memory: Q 48 KB, a stage of key blocks ([64 tokens x 64 dims] each) and a value block
-// ([128 tokens x 64 columns]), copied while the softmax of the step before runs. Tensor
-// memory: S, O, 128 columns each.
+// Shared memory: Q 48 KB, two steps' key blocks ([64 tokens x 64 dims] each) and a value block
+// ([128 tokens x 64 columns]), copied two steps ahead (keys) and while the softmax runs
+// (values). Tensor memory: S, O, 128 columns each.
 // ============================================================================
 constexpr int kThreads = 256;          // warp 0 copies, 1 products (CTA 0), 4..7 softmax
 // Registers a thread of the first warpgroup (copies and products) and of the other (softmax)
