@@ -57,25 +57,15 @@ __device__ __forceinline__ void mx_place4(uint32_t w, uint32_t &o0, uint32_t &o1
     o0 = (lo << 4) & 0x87f087f0u;
     o1 = (hi << 4) & 0x87f087f0u;
 }
-// Eight codes (memory order) as bf16: `first` times their placed values, where no scale is
-// above 1 the scale and 2^120 in one (mx_scale120), else 2^120 and then `second`. Every
-// product is exact.
-__device__ __forceinline__ uint4 mx_expand8(uint2 c, uint32_t first) {
+// Eight codes (memory order) as bf16. Both products are exact.
+__device__ __forceinline__ uint4 mx_expand8(uint2 c, uint32_t scale) {
     uint4 o;
     mx_place4(c.x, o.x, o.y);
     mx_place4(c.y, o.z, o.w);
-    o.x = mul_bf162(o.x, first);
-    o.y = mul_bf162(o.y, first);
-    o.z = mul_bf162(o.z, first);
-    o.w = mul_bf162(o.w, first);
-    return o;
-}
-__device__ __forceinline__ uint4 mx_expand8(uint2 c, uint32_t first, uint32_t second) {
-    uint4 o = mx_expand8(c, first);
-    o.x = mul_bf162(o.x, second);
-    o.y = mul_bf162(o.y, second);
-    o.z = mul_bf162(o.z, second);
-    o.w = mul_bf162(o.w, second);
+    o.x = mul_bf162(mul_bf162(o.x, kMx2p120), scale);
+    o.y = mul_bf162(mul_bf162(o.y, kMx2p120), scale);
+    o.z = mul_bf162(mul_bf162(o.z, kMx2p120), scale);
+    o.w = mul_bf162(mul_bf162(o.w, kMx2p120), scale);
     return o;
 }
 // Sixteen codes (memory order) as bf16: `first` times their placed values, where no scale

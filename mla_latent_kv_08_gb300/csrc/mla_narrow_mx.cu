@@ -372,7 +372,7 @@ decode_narrow_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_
 #pragma unroll
             for (int n = 0; n < N; ++n) l[n] = 0.f;
             if (tok_row < 64) nm_s[tok_row] = 0.f;             // m = 0 until the first scores
-            if (soft_any(false)) {}
+            soft_any(false);
             for (int j = 0; j < ns; ++j, ++K) {
                 const bool mine_ok = __all_sync(0xffffffffu, wait(&bars->s_full, K & 1));
                 tc_fence_after();

@@ -725,8 +725,7 @@ cudaError_t launch_prefill_tc(const PrefillParams &p, cudaStream_t st) {
     const uint64_t kv_rows = (uint64_t)p.nh * p.cap_rows;
     CUtensorMap rows, uk, uv, q, k_ld, v_ld, rope;
     if (!map2d(&rows, p.rows, p.cap_rows, kR + kRope, 128) || !map2d(&uk, p.W_UK, (uint64_t)p.s.H * kDn, kR, 128) ||
-        !map2d(&uv, p.W_UV, (uint64_t)p.s.H * kR, kDv, 64) || 
-        !map2d(&k_ld, p.k, kv_rows, kDn, 64) ||
+        !map2d(&uv, p.W_UV, (uint64_t)p.s.H * kR, kDv, 64) || !map2d(&k_ld, p.k, kv_rows, kDn, 64) ||
         !map2d(&v_ld, p.v, kv_rows, kDv, 128) || !map2d(&rope, p.rows, p.cap_rows, kR + kRope, 64) || !map_q(&q, p.q, p.num_q, p.s.H))
         return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(ex::expand_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ex::kSmemBytes);

@@ -87,7 +87,7 @@ __device__ __forceinline__ void write_rows(const ReadParams &p, const long long 
                 for (int k = 0; k < 2; ++k) {
                     const int v = v0 + 32 * k + lane;
                     if (tok[i] >= 0 && v < nv) {
-                        dst[v] = mx_expand8(c[i][k], kMx2p120, mx_scale_bf162(sb[i][k]));
+                        dst[v] = mx_expand8(c[i][k], mx_scale_bf162(sb[i][k]));
                         odd |= (uint32_t)(sb[i][k] == 255u) << i;
                     }
                 }
