@@ -111,6 +111,10 @@ int32_t resolve_impl(const mla_shape *s, int32_t q_len) {
 // to two 128-token steps of the bf16 decode that scores two blocks per MMA).
 constexpr int kItemCostTc = 3;
 constexpr int kItemCostWide = 2;
+// The 8-bit kernels' steps are longer: over 32 batches of 8 to 100 sequences, 128 heads, a call
+// took 61.2 us on (geometric) average with 1, 62.6 with 2, 63.9 with 3; at 8 to 64 heads 78.9,
+// 80.8, 81.7 and with 0 82.2.
+constexpr int kItemCostMx = 1;
 // mla_append_decode: new tokens up to this count are copied by the planner's launch
 constexpr int32_t kFusedAppendMax = 4096;
 
@@ -211,7 +215,7 @@ static mla_status run_attention(const mla_shape *s, const mla_cache *cache, cons
     // the bf16 decode that scores two blocks per MMA plans in 128-token steps, so that
     // only a sequence's last work item can end with an unpaired block
     const bool wide = impl == MLA_IMPL_TCGEN05 && (s->kind == MLA_KV_BF16 || mx);
-    p.item_cost = impl == MLA_IMPL_TCGEN05 ? (wide ? kItemCostWide : kItemCostTc) : 0;
+    p.item_cost = impl == MLA_IMPL_TCGEN05 ? (mx ? kItemCostMx : wide ? kItemCostWide : kItemCostTc) : 0;
     p.plan_tile = wide ? 128 : 64;
     p.work = (const WorkItem *)(ws + w.work);
     p.split_start = (const int32_t *)(ws + w.split_start);
