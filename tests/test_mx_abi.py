@@ -165,7 +165,7 @@ def test_prefill_workspace(lib):
     import mla_latent_kv_08_gb300 as mla
     small = mla.mla_prefill_workspace_bytes(_shape(), 1, 1, 1, 128)
     big = mla.mla_prefill_workspace_bytes(_shape(), 4, 4096, 100000, 128)
-    assert 0 < small < big < 3 << 30          # keys and values of some heads at a time
+    assert 0 < small < big < 5 << 30          # keys and values of some heads at a time
     for bad in (dict(B=0), dict(num_q=-1), dict(nope_dim=7)):
         a = dict(B=1, num_q=1, max_tokens=1, nope_dim=128)
         a.update(bad)
