@@ -12,8 +12,8 @@
 
 namespace mla {
 
-// Block-wide exclusive scan over 1024 threads of a 64-bit value; `total` to all.
-__device__ __forceinline__ long long scan1024(long long v, long long *s_warp, long long &total) {
+// Block-wide exclusive scan of a 64-bit value; `total` to all.
+__device__ __forceinline__ long long scan_block(long long v, long long *s_warp, long long &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long incl = v;
 #pragma unroll
@@ -24,7 +24,7 @@ __device__ __forceinline__ long long scan1024(long long v, long long *s_warp, lo
     if (lane == 31) s_warp[warp] = incl;
     __syncthreads();
     long long before = 0, all = 0;
-    for (int w = 0; w < 32; ++w) {
+    for (int w = 0; w < (int)blockDim.x / 32; ++w) {
         const long long x = s_warp[w];
         if (w < warp) before += x;
         all += x;
@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(PrefillParams p) {
     __syncthreads();
     const long long cap_tokens = (long long)p.max_blocks * p.s.bs;
     long long rows0 = 0, tiles0 = 0;
-    for (int base = 0; base < p.B; base += 1024) {
+    for (int base = 0; base < p.B; base += blockDim.x) {
         const int b = base + threadIdx.x;
         long long rows = 0, tiles = 0;
         bool bad = false;
@@ -56,8 +56,8 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(PrefillParams p) {
             }
         }
         long long tot_rows, tot_tiles;
-        const long long r0 = rows0 + scan1024(rows, s_warp, tot_rows);
-        const long long t0 = tiles0 + scan1024(tiles, s_warp, tot_tiles);
+        const long long r0 = rows0 + scan_block(rows, s_warp, tot_rows);
+        const long long t0 = tiles0 + scan_block(tiles, s_warp, tot_tiles);
         if (b < p.B) {
             bad = bad || r0 + rows > p.cap_rows;
             p.kv_off[b] = (int)min(r0, (long long)p.cap_rows);
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(1024) prefill_plan_kernel(PrefillParams p) {
 }
 
 cudaError_t launch_prefill_plan(const PrefillParams &p, cudaStream_t st) {
-    prefill_plan_kernel<<<1, 1024, 0, st>>>(p);
+    prefill_plan_kernel<<<1, p.B >= 1024 ? 1024 : (p.B + 31) / 32 * 32, 0, st>>>(p);
     return cudaGetLastError();
 }
 

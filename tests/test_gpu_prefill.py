@@ -272,6 +272,17 @@ def test_capture_and_replay_with_other_lengths(gpu_lib):
     assert np.isnan(out[60:]).all() and mla.mla_get_status(a["workspace"])[0] == mla.MLA_ERR_BOUNDS
 
 
+@pytest.mark.parametrize("B", [31, 33, 1023, 1024, 1100])
+def test_many_sequences(gpu_lib, B):
+    """Numbers of sequences about the plan's warp and block sizes, some without new tokens."""
+    import mla_latent_kv_08_gb300 as mla
+    new = [(i * 7) % 5 for i in range(B)]
+    case = Case(103, new, [i % 40 + (k == 0) for i, k in enumerate(new)], H=1, r=64, dR=16, dn=32, dv=32, bs=16)
+    out, lse, status = _run(mla, case)
+    assert status == (mla.MLA_OK, 0)
+    case.check(out, lse, seqs=sorted({*range(0, B, 37), *range(max(0, B - 80), B)}))
+
+
 @pytest.mark.parametrize("kind,impl", [("bf16", 0), ("bf16", 1), ("mxfp8", 0), ("mxfp8", 1), ("fp32", 1)])
 def test_not_a_number_in_a_later_token(gpu_lib, kind, impl):
     """A cached token with a NaN or an infinity makes the new tokens that see it NaN and leaves
