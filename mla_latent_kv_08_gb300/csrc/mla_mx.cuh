@@ -103,7 +103,7 @@ __device__ __forceinline__ float mx_value(uint32_t code, uint32_t scale_byte) {
     return __uint_as_float(h << 16) * 0x1p120f * mx_scale_f32(scale_byte);
 }
 
-// Memory bound: 1152 bytes in and 656 out a token (51k tokens: 20.2 us, 4.6 TB/s).
+// Memory bound: 1152 bytes in and 656 out a token (51k tokens: 19.6 us, 4.7 TB/s).
 // A new token's codes, by one warp: a lane takes 16 values (two lanes a group), 512 a pass.
 // `row()` gives the token row of the cache, or below 0 for none; it is asked for once the
 // loads are on their way, which do not depend on it (with the look-up first, its chain of
@@ -129,23 +129,25 @@ __device__ __forceinline__ void mx_write_token(const AppendParams &p, const __nv
             if (at < 0) return;
         }
         const uint32_t *w = (const uint32_t *)u;
-        uint32_t m = 0;
+        __nv_bfloat162 mm = __habs2(*(const __nv_bfloat162 *)&w[0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+        for (int i = 1; i < 8; ++i) mm = __hmax2_nan(mm, __habs2(*(const __nv_bfloat162 *)&w[i]));
+        uint32_t m = *(const uint32_t *)&mm;
         m = max(m & 0xffffu, m >> 16);
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
         const uint32_t sb = mx_scale_byte(m);
         if (!act) continue;
-        // 2^-e: exponent field 127 - e = 254 - sb, normal for every e of the range
-        const float inv = __uint_as_float((254u - min(sb, 254u)) << 23);
+        // 2^-e: exponent field 127 - e = 254 - sb, normal for every e of the range. The products
+        // are exact in bf16, but for those below 2^-126, whose code is 0 either way.
+        const uint32_t inv = ((254u - min(sb, 254u)) << 7) * 0x10001u;
         uint32_t o[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float2 x = make_float2(__uint_as_float(w[2 * i] << 16) * inv, __uint_as_float(w[2 * i] & 0xffff0000u) * inv);
-            const float2 y = make_float2(__uint_as_float(w[2 * i + 1] << 16) * inv,
-                                         __uint_as_float(w[2 * i + 1] & 0xffff0000u) * inv);
-            o[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3) |
-                   ((uint32_t)__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3) << 16);
+            const uint32_t x = mul_bf162(w[2 * i], inv), y = mul_bf162(w[2 * i + 1], inv);
+            o[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)),
+                                                      __NV_SATFINITE, __NV_E4M3) |
+                   ((uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(__uint_as_float(y << 16), __uint_as_float(y & 0xffff0000u)),
+                                                       __NV_SATFINITE, __NV_E4M3) << 16);
             if (sb == 255u) o[i] = 0x7f7f7f7fu;
         }
         *(uint4 *)(p.codes + (size_t)at * r + g * kMxGroup + 16 * (lane & 1)) = make_uint4(o[0], o[1], o[2], o[3]);
