@@ -171,3 +171,40 @@ def test_bounds_above_what_is_used(gpu_lib):
     out, lse = a["out"].double().cpu().numpy(), a["lse"].cpu().numpy()
     assert (out[n:] == 7.0).all() and (lse[n:] == 7.0).all()
     case.check(out[:n], lse[:n])
+
+
+def test_blocks_past_32_bits(gpu_lib):
+    """A pool whose codes are more than 2^32 bytes, its last blocks in use: as in a small pool."""
+    import mla_latent_kv_08_gb300 as mla
+    import torch
+    big = 140000
+    for H, room in ((16, True), (128, False)):
+        w = _workload(77, [300, 65], H=H)
+        if room:
+            _roomy(w)
+        got = []
+        for blocks in (w.num_blocks, big):
+            shape = _shape(mla, w, num_blocks=blocks)
+            cache = mla.Cache.allocate(shape, zero=False)
+            table = w.block_table
+            w.block_table = np.where(table >= 0, table + blocks - w.num_blocks, -1).astype(np.int32)
+            gu.append_tokens(cache, w, w.latent, w.rope, np.zeros(2, np.int32))
+            out, lse, ws = gu.attend(w, shape, cache, w.q)
+            assert mla.mla_get_status(ws) == (mla.MLA_OK, 0)
+            rows = torch.zeros((365, 576), dtype=torch.bfloat16, device="cuda")
+            bt = gu.dev(w.block_table)
+            cu = gu.dev(np.array([0, 300, 365], np.int32))
+            mla.mla_latent_read(cache, bt, gu.dev(np.zeros(2, np.int32)), cu, rows)
+            case = Case(78, [40, 65], [260, 0], H=2, kind="mxfp8")
+            pshape = case.shape(mla)
+            pshape.num_blocks = blocks
+            a = case.args(mla, pshape)
+            a["block_table"] = bt
+            mla.mla_prefill(cache, shape=pshape, **a)
+            torch.cuda.synchronize()
+            got.append((out, lse, rows.float().cpu().numpy(), a["out"].float().cpu().numpy()))
+            w.block_table = table
+            del cache
+        for small, large in zip(*got):
+            np.testing.assert_array_equal(small, large)
+        _check(w, got[1][0], got[1][1], _stored(w))
