@@ -108,7 +108,7 @@ template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setma
 // ([d_n, r]), W_UV[h] MN-major ([r, d_v]).
 //
 // They are rounded to bf16, the type of the next products' operands. Measured: 37k rows on
-// 128 heads 0.81 ms, 1.53 PFLOP/s (cuBLAS in a loop of seconds 1.74); 28k rows on 16 heads
+// 128 heads 0.78 ms, 1.57 PFLOP/s (cuBLAS in a loop of seconds 1.74); 28k rows on 16 heads
 // 89 us. Without pairs 1.21 ms. Bound by the tensor pipe and, on long ones, the power cap.
 // ============================================================================
 namespace ex {
@@ -320,7 +320,7 @@ expand_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_cons
 //   P = 2^(S c - m)          a thread a row: no shuffles
 //   O[256 x 128] += P . V    8 x M256 N128 K16, P from tensor memory
 //
-// Measured: two chunks of 2048 over 18k tokens on 128 heads 4.45 ms for 5.8 TFLOP, 1.30
+// Measured: two chunks of 2048 over 18k tokens on 128 heads 4.3 ms for 5.8 TFLOP, 1.35
 // PFLOP/s; 4 prompts of 2100 to 3400 tokens 1.19 ms, 1.01 PFLOP/s; 6 turns of up to 200 tokens
 // 66 us. A step of both pairs of an SM takes 3000 cycles, the products' own pace, while they
 // take turns at the tensor cores, and up to 4300 while both queue products and then both

@@ -20,7 +20,7 @@
 // warps waited for instruction fetches more than for anything else (3.9 warps an issue
 // slot), so the expansion is one loop body for all parts.
 //
-// Measured, 32 sequences of 1024 to 8192 tokens (156k in all), 128 heads: 76 us, of which
+// Measured, 32 sequences of 1024 to 8192 tokens (156k in all), 128 heads: 74 us, of which
 // the codes' bytes at the copy rate are 15 us and the products at the cuBLAS rate 23 us;
 // 16 sequences of 4096 to 32768 tokens with 8 drafts: 760 us against 272 us of products.
 // The tensor pipe is busy for 41 % of the time. What bounds it is the chain of a step, one
