@@ -362,7 +362,9 @@ decode_narrow_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_
                 if (tok_row == 0) NTRACE(7, K);
                 const int tok = it.t0 + j * kStep + tok_row;
                 // rows before n_min do not see this token (drafts; or the slot is past the end)
-                const int n_min = tok >= it.t1 ? N : max(0, (tok - (L - p.q_len)) * p.s.H);
+                // (clamped before the product: at most q_len * H, where a long cache's tokens times
+                // heads pass 2^31)
+                const int n_min = tok >= it.t1 ? N : max(0, tok - (L - p.q_len)) * p.s.H;
                 const bool not_a_number = ((volatile int32_t *)(smem + LY::kOffNan))[tok_row] == K + 1;
                 // exponents of 32 rows, over the rows' m; hidden ones -inf
                 uint32_t sv[32];

@@ -1,0 +1,45 @@
+"""Decode, verify and reading of the 8-bit cache at the ends of their ranges. Tolerances are
+the framework's bars for bf16 caches, but for what is exact."""
+import numpy as np
+import pytest
+
+from tests import gpu_util as gu
+from tests.test_gpu_mx import _shape, _stored, _workload
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("H,q_len,blocks", [(64, 1, 625000), (16, 4, 2200000), (128, 1, 625000), (32, 2, 1100001)])
+def test_tokens_times_heads_past_31_bits(gpu_lib, H, q_len, blocks):
+    """A table that repeats two blocks of the cache, the first one over the sequence's oldest
+    eighth: as the softmax over their 128 tokens, each counted as often as it stands there."""
+    import mla_latent_kv_08_gb300 as mla
+    import torch
+    w = _workload(80 + H, [128], H=H, q_len=q_len)
+    shape = _shape(mla, w)
+    cache, _ = gu.fill_cache(w, shape)
+    a, b = (int(x) for x in w.block_table[0, :2])
+    L = 64 * blocks
+    assert (L - q_len) * H > 2 ** 31
+    old = blocks // 8
+    table = np.full((1, blocks), b, np.int32)
+    table[0, :old] = a
+    bf = torch.bfloat16
+    out = torch.empty((1, q_len, H, 128), dtype=bf, device="cuda")
+    lse = torch.empty((1, q_len, H), dtype=torch.float32, device="cuda")
+    ws = mla.alloc_workspace(shape, 1, q_len)
+    call = mla.mla_decode if q_len == 1 else mla.mla_verify
+    call(cache, gu.dev(table), gu.dev(np.array([L], np.int32)), gu.dev(w.q, bf), gu.dev(w.W_UV, bf), w.scale, out, lse, ws)
+    torch.cuda.synchronize()
+    assert mla.mla_get_status(ws) == (mla.MLA_OK, 0)
+    c = _stored(w)[0]
+    s = w.scale * w.q[0].astype(np.float64) @ np.concatenate([c, w.rope[0].astype(np.float64)], 1).T        # [q_len, H, 128]
+    count = np.repeat([[old] * 64 + [blocks - old] * 64], q_len, 0).astype(np.float64)
+    for i in range(q_len):
+        count[i, 128 - (q_len - 1 - i):] -= 1                    # hidden from this draft's row
+    m = s.max(-1, keepdims=True)
+    e = count[:, None, :] * np.exp(s - m)
+    l = e.sum(-1, keepdims=True)
+    want = np.einsum("qhr,hrv->qhv", e / l @ c, w.W_UV.astype(np.float64))
+    assert gu.rel_err(out[0].float().cpu().numpy(), want) <= gu.BF16_REL_TOL
+    assert np.max(np.abs(lse[0].cpu().numpy() - (m + np.log(l))[..., 0])) <= gu.BF16_LSE_TOL
