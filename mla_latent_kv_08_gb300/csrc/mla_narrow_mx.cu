@@ -16,8 +16,9 @@
 // The row maxima run across threads here, and any m will do that keeps the weights in the
 // range of their types. So m starts at 0, and a step whose exponents all stay below 2^20
 // (and, at an item's first, above 2^-20) takes one vote of the four softmax warps and no
-// reduction; one that does not finds the rows' maxima and moves m there. Row sums stay a
-// thread's own until the end of a work item.
+// reduction; one that does not finds the rows' maxima and moves m there. A row that has
+// seen nothing but scores of minus infinity has no maximum yet, and its first one counts as
+// an item's first. Row sums stay a thread's own until the end of a work item.
 //
 // Measured, 64 heads over two sequences of 52k and 75k tokens: 54 us
 // (the pair kernel: 64 us), bytes at the copy rate 12.4 us. The tensor pipe is busy for
@@ -355,6 +356,9 @@ decode_narrow_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_
 #pragma unroll
             for (int n = 0; n < N; ++n) l[n] = 0.f;
             if (tok_row < 64) nm_s[tok_row] = 0.f;             // m = 0 until the first scores
+            // whether row tok_row has its m (a row that does not see the item's first token sees
+            // none of it and needs none), and whether a row is still without
+            bool set = tok_row >= N || tok_row < max(0, it.t0 - (L - p.q_len)) * p.s.H, first = true;
             soft_any(false);
             for (int j = 0; j < ns; ++j, ++K) {
                 const bool mine_ok = __all_sync(0xffffffffu, wait(&bars->s_full, K & 1));
@@ -396,18 +400,17 @@ decode_narrow_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_
                     exponents(h);
 #pragma unroll
                     for (int n = 0; n < 32; ++n) top = fmaxf(top, __uint_as_float(sv[n]));
-                    if (j == 0)
+                    if (first)
 #pragma unroll
-                        for (int n = 0; n < 32; ++n)
-                            low = fminf(low, __uint_as_float(sv[n]) == -CUDART_INF_F ? 0.f : __uint_as_float(sv[n]));
+                        for (int n = 0; n < 32; ++n) low = fminf(low, 32 * h + n < n_min ? 0.f : __uint_as_float(sv[n]));
                 }
-                const bool slow = soft_any(top > kBound || (j == 0 && low < -kBound) || !mine_ok);
+                const bool slow = soft_any(top > kBound || (first && low < -kBound) || !mine_ok);
                 if (tok_row == 0) NTRACE(8, K);
                 if (slow) {
                     ok = !soft_any(!mine_ok);
                     if (!ok) break;
-                    // The maxima of every row over the step's tokens; m becomes them at the item's
-                    // first step, and rises to them later where they are past the bound.
+                    // The maxima of every row over the step's tokens; m becomes them where the row
+                    // has none yet, and rises to them later where they are past the bound.
 #pragma unroll 1
                     for (int h = 0; h < N / 32; ++h) {
                         exponents(h);
@@ -417,11 +420,14 @@ decode_narrow_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_
                     if (tok_row < N) {
                         const float d = fmaxf(fmaxf(red_s[tok_row], red_s[64 + tok_row]),
                                               fmaxf(red_s[128 + tok_row], red_s[192 + tok_row]));
-                        const bool raise = d != -CUDART_INF_F && (j == 0 || d > kBound);
-                        alpha_s[tok_row] = raise && j > 0 ? exp2f(-d) : 1.f;
-                        if (raise) nm_s[tok_row] -= d;
+                        const bool raise = d != -CUDART_INF_F && (!set || d > kBound);
+                        alpha_s[tok_row] = raise && set ? exp2f(-d) : 1.f;
+                        if (raise) {
+                            nm_s[tok_row] -= d;
+                            set = true;
+                        }
                     }
-                    soft_any(false);
+                    first = soft_any(!set);
 #pragma unroll
                     for (int n = 0; n < N; ++n) l[n] *= alpha_s[n];
                     // O^T *= alpha: the scores' barrier says that the P . V before is done
@@ -438,6 +444,9 @@ decode_narrow_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_
                         }
                         tmem_wait_st();
                     }
+                } else {
+                    set = true;
+                    first = false;
                 }
                 // weights (bf16) into the token's row of P^T, 16-byte chunks swizzled as an
                 // MN-major operand; sums of the unrounded ones

@@ -3,8 +3,9 @@ the framework's bars for bf16 caches, but for what is exact."""
 import numpy as np
 import pytest
 
+from oracle import attention
 from tests import gpu_util as gu
-from tests.test_gpu_mx import _shape, _stored, _workload
+from tests.test_gpu_mx import _impl, _roomy, _shape, _stored, _workload
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +44,29 @@ def test_tokens_times_heads_past_31_bits(gpu_lib, H, q_len, blocks):
     want = np.einsum("qhr,hrv->qhv", e / l @ c, w.W_UV.astype(np.float64))
     assert gu.rel_err(out[0].float().cpu().numpy(), want) <= gu.BF16_REL_TOL
     assert np.max(np.abs(lse[0].cpu().numpy() - (m + np.log(l))[..., 0])) <= gu.BF16_LSE_TOL
+
+
+@pytest.mark.parametrize("impl", ["auto", "roomy"])
+@pytest.mark.parametrize("H,q_len", [(16, 1), (16, 4), (64, 1), (8, 3), (128, 1), (128, 2)])
+def test_scores_of_minus_infinity(gpu_lib, impl, H, q_len):
+    """A sequence's first tokens score past the 32-bit range, and the others far below 0: weight
+    0 for the former, the softmax over the latter."""
+    import mla_latent_kv_08_gb300 as mla
+    lens, gone = [700, 128 + q_len, q_len], [400, 128, 0]
+    w = _workload(83, lens, H=H, q_len=q_len)
+    w.q[..., 512], w.q[..., 513] = np.float32(2.0 ** 100), 30
+    for b, n in enumerate(gone):
+        w.rope[b][:, 0] = 0
+        w.rope[b][:n, 0] = -np.float32(2.0 ** 60)
+        w.rope[b][:, 1] = -500
+    if impl == "roomy":
+        _roomy(w)
+    shape = _shape(mla, w, impl=_impl(mla, impl), num_splits_hint=1)
+    cache, _ = gu.fill_cache(w, shape)
+    out, lse, ws = gu.attend(w, shape, cache, w.q, q_len=q_len)
+    assert mla.mla_get_status(ws) == (mla.MLA_OK, 0)
+    lat = _stored(w)
+    for b in range(3):
+        ro, rl = attention.absorbed(w.q[b], lat[b], w.rope[b], w.W_UV, w.scale)
+        assert gu.rel_err(out[b], ro) <= gu.BF16_REL_TOL, b
+        assert np.max(np.abs(lse[b] - rl)) <= gu.BF16_LSE_TOL, b
