@@ -204,7 +204,8 @@ __global__ void __launch_bounds__(256) prefill_simt_kernel(PrefillParams p) {
             const bool vis = rr < rows_here && t0 + lane <= L - n + i0 + rr;
             const float s2 = vis ? sc[j] * c2 : -CUDART_INF_F;
             const float m_new = fmaxf(m_run[j], warp_max(s2));
-            const float pr = vis ? exp2f(s2 - m_new) : 0.f;
+            // (a score of minus infinity weighs 0, also while there is no other: m_new is it too)
+            const float pr = s2 != -CUDART_INF_F ? exp2f(s2 - m_new) : 0.f;
             const float alpha = m_new == -CUDART_INF_F ? 1.f : exp2f(m_run[j] - m_new);
             l_run[j] = l_run[j] * alpha + warp_sum(pr);
             m_run[j] = m_new;

@@ -5,7 +5,7 @@ import pytest
 
 from oracle import attention
 from tests import gpu_util as gu
-from tests.test_gpu_mx import _impl, _roomy, _shape, _stored, _workload
+from tests.test_gpu_mx import IMPLS, _impl, _roomy, _shape, _stored, _workload
 
 pytestmark = pytest.mark.gpu
 
@@ -46,7 +46,7 @@ def test_tokens_times_heads_past_31_bits(gpu_lib, H, q_len, blocks):
     assert np.max(np.abs(lse[0].cpu().numpy() - (m + np.log(l))[..., 0])) <= gu.BF16_LSE_TOL
 
 
-@pytest.mark.parametrize("impl", ["auto", "roomy"])
+@pytest.mark.parametrize("impl", IMPLS)
 @pytest.mark.parametrize("H,q_len", [(16, 1), (16, 4), (64, 1), (8, 3), (128, 1), (128, 2)])
 def test_scores_of_minus_infinity(gpu_lib, impl, H, q_len):
     """A sequence's first tokens score past the 32-bit range, and the others far below 0: weight
