@@ -140,10 +140,13 @@ typedef enum {
  *                          fp16, as above over the row [c . R ; k_R]; rope unused
  *   INT2_JOINT: codes and scale_zero as INT2_ROT_QR, over the row [c ; k_R] . R_j
  *   MXFP8:      codes      [num_blocks, block_size, r]        uint8, e4m3 (sign, 4
- *               exponent bits of bias 7, 3 fraction bits)
+ *               exponent bits of bias 7, 3 fraction bits; 0x7f and 0xff are not a number)
  *               scale_zero [num_blocks, block_size, r / 32]   uint8, the biased
- *               exponent e + 127 of the group's scale 2^e; value = code * 2^e
+ *               exponent e + 127 of the group's scale 2^e, 17 to 246, or 255: the group is
+ *               not a number; value = code * 2^e
  *               rope       [num_blocks, block_size, d_R]      bf16
+ *               (Another writer's cache has to keep to these scales: with others, values
+ *               would leave the range of bf16.)
  * Unused members are NULL. */
 typedef struct {
     void *latent;
@@ -183,7 +186,8 @@ size_t mla_workspace_bytes(const mla_shape *shape, int32_t B, int32_t q_len);
  * value to c / 2^e, ties to even (magnitudes above 448 * 2^119 become that).
  * Every value read back is a bf16. A group with an infinity or a NaN in it gets the scale
  * byte 255 and reads back as NaN; query rows that see such a token are NaN, those whose
- * mask hides it are not touched by it. R and clip are not used.
+ * mask hides it are not touched by it. The same holds for a token with a code that is not
+ * a number, which this call writes under the scale byte 255 alone. R and clip are not used.
  *   Source: OSCAR issue #10, maintainer reply (rotated + quantised latent in
  *   the cache, thresholds fit on the rotated latent). */
 mla_status mla_latent_append(const mla_shape *shape, const mla_cache *cache,

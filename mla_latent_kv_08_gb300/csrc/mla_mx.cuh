@@ -57,6 +57,18 @@ __device__ __forceinline__ void mx_place4(uint32_t w, uint32_t &o0, uint32_t &o1
     o0 = (lo << 4) & 0x87f087f0u;
     o1 = (hi << 4) & 0x87f087f0u;
 }
+// Codes 0x7f and 0xff are not a number. Bit 7 of each byte of a word of four: whether it is
+// one.
+__device__ __forceinline__ uint32_t mx_nan4(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+// Whether any of several is one, in fewer steps: adding 1 to a byte changes its bit 7 where the
+// seven below are ones. (Of bytes, only 0xff carries into the next, and that is one itself.) The
+// check takes 2 to 3 % of a decode or verify call (32 sequences, 156k tokens, 128 heads: 92.3
+// -> 94.7 us; ahead of the expanding warps' waits it took as much).
+__device__ __forceinline__ uint32_t mx_bit7(uint32_t w) { return (w + 0x01010101u) ^ w; }
+__device__ __forceinline__ bool mx_any_nan(uint2 c) { return ((mx_bit7(c.x) | mx_bit7(c.y)) & 0x80808080u) != 0; }
+__device__ __forceinline__ uint32_t mx_nan16(const uint4 &c) {
+    return (mx_bit7(c.x) | mx_bit7(c.y) | mx_bit7(c.z) | mx_bit7(c.w)) & 0x80808080u;
+}
 // Eight codes (memory order) as bf16. Both products are exact.
 __device__ __forceinline__ uint4 mx_expand8(uint2 c, uint32_t scale) {
     uint4 o;
@@ -66,11 +78,20 @@ __device__ __forceinline__ uint4 mx_expand8(uint2 c, uint32_t scale) {
     o.y = mul_bf162(mul_bf162(o.y, kMx2p120), scale);
     o.z = mul_bf162(mul_bf162(o.z, kMx2p120), scale);
     o.w = mul_bf162(mul_bf162(o.w, kMx2p120), scale);
+    if (mx_any_nan(c)) {
+        uint32_t *w = (uint32_t *)&o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t n = mx_nan4(i < 2 ? c.x : c.y) >> (16 * (i & 1));
+            if (n & 0x80u) w[i] = (w[i] & 0xffff0000u) | 0x7fc0u;
+            if (n & 0x8000u) w[i] = (w[i] & 0xffffu) | 0x7fc00000u;
+        }
+    }
     return o;
 }
 // Sixteen codes (memory order) as bf16: `first` times their placed values, where no scale
 // is above 1 the scale and 2^120 in one (mx_scale120), else 2^120 and then `second`. Every
-// product is exact.
+// product is exact. (Codes that are not a number come out as +-480: mx_nan16 finds them.)
 __device__ __forceinline__ void mx_expand16(const uint4 &c, uint32_t first, uint4 &o0, uint4 &o1) {
     mx_place4(c.x, o0.x, o0.y);
     mx_place4(c.y, o0.z, o0.w);
@@ -97,7 +118,7 @@ __device__ __forceinline__ void mx_expand16(const uint4 &c, uint32_t first, uint
 __device__ __forceinline__ uint32_t mx_scale120(uint32_t bytes, uint32_t sel) {
     return __byte_perm(bytes, 0u, 0x4040u | sel | (sel << 8)) * 128u + 0x3c003c00u;
 }
-// One code and its scale byte in fp32 (the CUDA-core kernels).
+// One code, a number, and its scale byte in fp32 (the CUDA-core kernels).
 __device__ __forceinline__ float mx_value(uint32_t code, uint32_t scale_byte) {
     const uint32_t h = ((code & 0x7fu) << 4) | ((code & 0x80u) << 8);
     return __uint_as_float(h << 16) * 0x1p120f * mx_scale_f32(scale_byte);

@@ -552,19 +552,24 @@ decode_narrow_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_
                 }
             }
         };
-        // A group that is not a number becomes zeros (their product with a hidden row's weight 0
-        // stays 0) and its token is noted with `mark`, so that the scores of the rows that see
-        // it become NaN.
-        auto expand = [&](const Rows &x, uint32_t to, int mark) {
-            // scales up to 1 take one multiplication
-            const bool small = !__any_sync(0xffffffffu, (x.s[0] | x.s[1] | x.s[2] | x.s[3]) & 0x80808080u);
+        // Whether every scale is at most 1 (they take one multiplication) and every code a number.
+        auto plain = [&](const Rows &x) {
+            uint32_t odd = (x.s[0] | x.s[1] | x.s[2] | x.s[3]) & 0x80808080u;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) odd |= mx_nan16(x.c[q]);
+            return !__any_sync(0xffffffffu, odd);
+        };
+        // A group that is not a number, or a lane's codes with one that is not, become zeros
+        // (their product with a hidden row's weight 0 stays 0) and their token is noted with
+        // `mark`, so that the scores of the rows that see it become NaN.
+        auto expand = [&](const Rows &x, uint32_t to, int mark, bool small) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 uint4 o0, o1;
                 if (small) mx_expand16(x.c[q], mx_scale120(x.s[q], p8 >> 1), o0, o1);
                 else {
                     uint32_t b = mx_scale_bf162((x.s[q] >> (8 * (p8 >> 1))) & 0xffu);
-                    if (b == 0x7fc07fc0u) {
+                    if (b == 0x7fc07fc0u || mx_nan16(x.c[q])) {
                         b = 0;
                         ((volatile int32_t *)(smem + LY::kOffNan))[16 * e + 4 * q + r4] = mark;
                     }
@@ -604,7 +609,7 @@ decode_narrow_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_
             auto part = [&](Rows &x, int c) {
                 if (K > 0 && !__all_sync(0xffffffffu, wait(&bars->empty[c], (K - 1) & 1))) return false;
                 if (tid == 256 && c % 3 == 0) NTRACE(c == 0 ? 10 : 12, K);
-                expand(x, to0 + 2u * c * kCol, K + 1);
+                expand(x, to0 + 2u * c * kCol, K + 1, plain(x));
                 fence_proxy_async();
                 mbar_arrive(&bars->full[c]);
                 if (tid == 256 && c % 3 == 0) NTRACE(c == 0 ? 11 : 13, K);

@@ -88,7 +88,7 @@ __device__ __forceinline__ void write_rows(const ReadParams &p, const long long 
                     const int v = v0 + 32 * k + lane;
                     if (tok[i] >= 0 && v < nv) {
                         dst[v] = mx_expand8(c[i][k], mx_scale_bf162(sb[i][k]));
-                        odd |= (uint32_t)(sb[i][k] == 255u) << i;
+                        odd |= (uint32_t)(sb[i][k] == 255u || mx_any_nan(c[i][k])) << i;
                     }
                 }
                 if (v0 == 0 && tok[i] >= 0 && lane < rv) dst[nv + lane] = rope[i];      // d_R <= 128: 16 lanes

@@ -354,7 +354,7 @@ constexpr int kTT = 32;   // tokens per tile
 
 template <int KIND>
 __device__ __forceinline__ void gather_tile(const DecodeParams &p, int b, int tb, int t1, float *sK,
-                                            int Dp, int *sValid) {
+                                            int Dp, int *sValid, int *sNan) {
     const int D = p.s.D(), r = p.s.r, dR = p.s.dR, bs = p.s.bs;
     if (threadIdx.x < kTT) {
         int t = tb + threadIdx.x;
@@ -366,6 +366,7 @@ __device__ __forceinline__ void gather_tile(const DecodeParams &p, int b, int tb
             else raise_flag(p.status, FLAG_BAD_BLOCK);
         }
         sValid[threadIdx.x] = ok;
+        if (KIND == MLA_KV_MXFP8) sNan[threadIdx.x] = 0;
     }
     __syncthreads();
     if (KIND == MLA_KV_BF16) {
@@ -400,7 +401,9 @@ __device__ __forceinline__ void gather_tile(const DecodeParams &p, int b, int tb
             }
         }
     } else if (KIND == MLA_KV_MXFP8) {
-        // four codes per thread step, then the bf16 rope key
+        // four codes per thread step, then the bf16 rope key. Groups and codes that are not a
+        // number become zeros (their product with a hidden row's weight 0 stays 0) and their
+        // token is noted, for the scores of the rows that see it.
         const int nw = r / 4, ng = r / kMxGroup;
         for (int idx = threadIdx.x; idx < kTT * nw; idx += blockDim.x) {
             int tt = idx / nw, k = idx % nw;
@@ -410,8 +413,10 @@ __device__ __forceinline__ void gather_tile(const DecodeParams &p, int b, int tb
                 size_t row = (size_t)(blk1 - 1) * bs + (tb + tt) % bs;
                 const uint32_t w = *((const uint32_t *)(p.codes + row * r) + k);
                 const uint32_t sb = p.mx_scale[row * ng + k / (kMxGroup / 4)];
+                const uint32_t nan = sb == 255u ? 0x80808080u : mx_nan4(w);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) dst[e] = sb == 255u ? 0.f : mx_value((w >> (8 * e)) & 0xffu, sb);
+                for (int e = 0; e < 4; ++e) dst[e] = (nan >> (8 * e)) & 0x80u ? 0.f : mx_value((w >> (8 * e)) & 0xffu, sb);
+                if (nan) sNan[tt] = 1;
             } else {
                 dst[0] = dst[1] = dst[2] = dst[3] = 0.f;
             }
@@ -419,17 +424,7 @@ __device__ __forceinline__ void gather_tile(const DecodeParams &p, int b, int tb
         for (int idx = threadIdx.x; idx < kTT * dR; idx += blockDim.x) {
             int tt = idx / dR, d = idx % dR;
             int blk1 = sValid[tt];
-            float v = 0.f;
-            if (blk1) {
-                const size_t row = (size_t)(blk1 - 1) * bs + (tb + tt) % bs;
-                v = __bfloat162float(p.rope[row * dR + d]);
-                // a group that is not a number: zeros above (its product with a hidden row's
-                // weight 0 stays 0), and here the NaN for the scores of the rows that see it
-                if (d == 0)
-                    for (int g = 0; g < ng; ++g)
-                        if (p.mx_scale[row * ng + g] == 255u) v = CUDART_NAN_F;
-            }
-            sK[tt * Dp + r + d] = v;
+            sK[tt * Dp + r + d] = blk1 ? __bfloat162float(p.rope[((size_t)(blk1 - 1) * bs + (tb + tt) % bs) * dR + d]) : 0.f;
         }
     } else {
         // INT2: one thread per code byte (4 dims), then the bf16 rope key (INT2_ROT_QR:
@@ -487,7 +482,7 @@ __global__ void __launch_bounds__(256) decode_simt_kernel(DecodeParams p) {
     float *sL = sA + kRB;                 // [kRB]
     float *sM = sL + kRB;                 // [kRB]
     int *sValid = (int *)(sM + kRB);      // [kTT]
-    __shared__ int s_bad;
+    __shared__ int s_bad, s_nan[kTT];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) s_bad = 0;
@@ -518,7 +513,7 @@ __global__ void __launch_bounds__(256) decode_simt_kernel(DecodeParams p) {
 
     for (int tb = t0; tb < t1; tb += kTT) {
         __syncthreads();                  // previous tile fully consumed
-        gather_tile<KIND>(p, b, tb, t1, sK, Dp, sValid);
+        gather_tile<KIND>(p, b, tb, t1, sK, Dp, sValid, s_nan);
         __syncthreads();
         if (tid < kTT && tb + tid < t1 && !sValid[tid]) s_bad = 1;
         float sc[2];
@@ -539,7 +534,7 @@ __global__ void __launch_bounds__(256) decode_simt_kernel(DecodeParams p) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int rr = warp + 8 * j;
-            const float s = sc[j];
+            const float s = KIND == MLA_KV_MXFP8 && s_nan[lane] ? CUDART_NAN_F : sc[j];
             const int t = tb + lane;
             const bool vis = (t < t1) && (t <= last_vis[j]) && sValid[lane];
             const float s2 = vis ? s * p.scale_log2 : -CUDART_INF_F;

@@ -126,9 +126,9 @@ struct Bars {
     uint64_t xchg_read[4];    // lane quarter q: both halves read the other's value
     uint32_t tmem_base;
     int32_t abort_flag;
-    // 1 + the last step with a group that is not a number. Such a group is expanded to zeros
-    // (its product with a hidden row's weight 0 stays 0); the scores of the tokens at kOffNan
-    // that hold this step become NaN for the rows that see them.
+    // 1 + the last step with own dims that are not a number (a group's scale, or a code). They
+    // are expanded to zeros (their product with a hidden row's weight 0 stays 0); the scores of
+    // the tokens at kOffNan that hold this step become NaN for the rows that see them.
     int32_t nan_step;
 };
 static_assert(sizeof(Bars) <= 512, "barriers must fit below the exchange area");
@@ -636,11 +636,16 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
                 }
             }
         };
-        // `mark`: where not 0, the step (+ 1) to note for groups that are not a number; u: the tile
-        auto expand = [&](const Rows &x, uint32_t to, int mark, int u) {
-            // scales up to 1 take one multiplication
-            const uint32_t any = x.s[0].x | x.s[0].y | x.s[1].x | x.s[1].y;
-            const bool small = !__any_sync(0xffffffffu, any & 0x80808080u);
+        // Whether every scale is at most 1 (they take one multiplication) and every code a number.
+        auto plain = [&](const Rows &x) {
+            uint32_t odd = (x.s[0].x | x.s[0].y | x.s[1].x | x.s[1].y) & 0x80808080u;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) odd |= mx_nan16(x.c[q][0]) | mx_nan16(x.c[q][1]);
+            return !__any_sync(0xffffffffu, odd);
+        };
+        // `mark`: of own dims, the step (+ 1) to note for what is not a number; 0: of score-only
+        // dims, where it is expanded to NaN; u: the tile
+        auto expand = [&](const Rows &x, uint32_t to, int mark, int u, bool small) {
 #pragma unroll
             for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -650,10 +655,13 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
                     if (small) mx_expand16(x.c[q][w], mx_scale120(sw, p8 >> 1), o0, o1);
                     else {
                         uint32_t b = mx_scale_bf162((sw >> (8 * (p8 >> 1))) & 0xffu);
-                        if (mark && b == 0x7fc07fc0u) {
-                            b = 0;
-                            ((volatile int32_t *)(smem + kOffNan))[kTile * u + 8 * e + 4 * q + r4] = mark;
-                            *(volatile int32_t *)&bars->nan_step = mark;
+                        if (b == 0x7fc07fc0u || mx_nan16(x.c[q][w])) {
+                            b = 0x7fc07fc0u;
+                            if (mark) {
+                                b = 0;
+                                ((volatile int32_t *)(smem + kOffNan))[kTile * u + 8 * e + 4 * q + r4] = mark;
+                                *(volatile int32_t *)&bars->nan_step = mark;
+                            }
                         }
                         mx_expand16(x.c[q][w], kMx2p120, b, o0, o1);
                     }
@@ -705,7 +713,7 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
                 ok = K == 0 || (!own && u) || __all_sync(0xffffffffu, mbar_wait(bar, (K - 1) & 1, bars, p.status));
                 if (!ok) break;
                 WTRACE_E(own ? 14 : 12);
-                expand(x, to + 8192u * u, own ? K + 1 : 0, u);
+                expand(x, to + 8192u * u, own ? K + 1 : 0, u, plain(x));
                 if (u == 0) x = y;
             }
             if (!ok) break;

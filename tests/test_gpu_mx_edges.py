@@ -70,3 +70,53 @@ def test_scores_of_minus_infinity(gpu_lib, impl, H, q_len):
         ro, rl = attention.absorbed(w.q[b], lat[b], w.rope[b], w.W_UV, w.scale)
         assert gu.rel_err(out[b], ro) <= gu.BF16_REL_TOL, b
         assert np.max(np.abs(lse[b] - rl)) <= gu.BF16_LSE_TOL, b
+
+
+def _nan_codes(w, cache, at):
+    """Codes that are not a number at (sequence, token, latent dim); `_stored` with them."""
+    lat = _stored(w)
+    for i, (b, t, d) in enumerate(at):
+        cache.codes[int(w.block_table[b, t // 64]), t % 64, d] = (0x7F, 0xFF)[i % 2]
+        lat[b][t, d] = np.nan
+    return lat
+
+
+def test_a_code_that_is_not_a_number_reads_as_one(gpu_lib):
+    import mla_latent_kv_08_gb300 as mla
+    import torch
+    w = _workload(81, [130, 4200], H=1)
+    shape = _shape(mla, w)
+    cache, _ = gu.fill_cache(w, shape)
+    lat = _nan_codes(w, cache, [(0, 0, 0), (0, 129, 511), (1, 7, 31), (1, 7, 32), (1, 4199, 300)])
+    for b, L in enumerate((130, 4200)):                          # few rows, many rows
+        rows = torch.empty((L, 576), dtype=torch.bfloat16, device="cuda")
+        mla.mla_latent_read(cache, gu.dev(w.block_table[b:b + 1]), gu.dev(np.zeros(1, np.int32)),
+                            gu.dev(np.array([0, L], np.int32)), rows)
+        np.testing.assert_array_equal(rows.double().cpu().numpy(), np.concatenate([lat[b], w.rope[b]], 1))
+
+
+@pytest.mark.parametrize("impl", IMPLS)
+@pytest.mark.parametrize("H,q_len", [(16, 1), (16, 4), (64, 1), (128, 1), (128, 3)])
+def test_a_code_that_is_not_a_number_in_a_draft(gpu_lib, impl, H, q_len):
+    """It makes the rows that see it NaN and leaves those whose mask hides it as they are."""
+    import mla_latent_kv_08_gb300 as mla
+    lens = [200, 129, 66, 700, 385]
+    w = _workload(82, lens, H=H, q_len=q_len)
+    if impl == "roomy":
+        _roomy(w)
+    at = [(0, 199, 0), (1, 128 - (q_len > 1), 511), (2, 65, 255), (3, 350, 256), (4, 385 - q_len, 100)]
+    shape = _shape(mla, w, impl=_impl(mla, impl), num_splits_hint=5)
+    cache, _ = gu.fill_cache(w, shape)
+    _nan_codes(w, cache, at)
+    out, lse, ws = gu.attend(w, shape, cache, w.q, q_len=q_len)
+    assert mla.mla_get_status(ws) == (mla.MLA_OK, 0)
+    for b, t, _ in at:
+        w.latent[b][t], w.rope[b][t] = 0, 0                      # hidden from the rows that are held to it
+    lat = _stored(w)
+    for b, t, _ in at:
+        sees = lens[b] - q_len + np.arange(q_len) >= t
+        assert np.isnan(out[b][sees]).all() and np.isnan(lse[b][sees]).all(), b
+        if not sees.all():
+            ro, rl = attention.absorbed(w.q[b], lat[b], w.rope[b], w.W_UV, w.scale)
+            assert gu.rel_err(out[b][~sees], ro[~sees]) <= gu.BF16_REL_TOL, b
+            assert np.max(np.abs(lse[b][~sees] - rl[~sees])) <= gu.BF16_LSE_TOL, b

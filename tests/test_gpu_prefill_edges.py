@@ -21,3 +21,26 @@ def test_scores_of_minus_infinity(gpu_lib, kind, impl):
     out, lse, status = _run(mla, case, case.shape(mla, impl=impl))
     assert status == (mla.MLA_OK, 0)
     case.check(out, lse)
+
+
+@pytest.mark.parametrize("impl", [0, 1])
+def test_a_code_that_is_not_a_number(gpu_lib, impl):
+    """New tokens that see such a code are NaN; those before it stay as they are."""
+    import mla_latent_kv_08_gb300 as mla
+    import torch
+    case = Case(114, [300, 130, 40], [50, 0, 100], H=3, kind="mxfp8")
+    at = [(0, 349, 0, 0x7F), (1, 1, 511, 0xFF), (2, 120, 255, 0x7F)]
+    shape = case.shape(mla, impl=impl)
+    cache, a = case.cache(mla, shape), case.args(mla, shape)
+    for b, t, d, code in at:
+        cache.codes[int(case.table[b, t // 64]), t % 64, d] = code
+    mla.mla_prefill(cache, **a)
+    torch.cuda.synchronize()
+    assert mla.mla_get_status(a["workspace"]) == (mla.MLA_OK, 0)
+    out, lse = a["out"].double().cpu().numpy(), a["lse"].cpu().numpy()
+    for b, t, _, _ in at:
+        first = t - int(case.L[b] - case.new[b])                         # the first new token that sees it
+        mine = slice(int(case.cu[b]) + first, int(case.cu[b + 1]))
+        assert np.isnan(out[mine]).all() and np.isnan(lse[mine]).all(), b
+        case.lat[b][t], case.rope[b][t] = 0, 0                           # hidden from the rows that are held to it
+        case.check(out, lse, seqs=[b], rows=np.arange(first))
