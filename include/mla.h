@@ -218,7 +218,7 @@ mla_status mla_latent_read(const mla_shape *shape, const mla_cache *cache, const
                            void *stream);
 
 /* Decode attention, one query row per sequence (q_len = 1).
- *   seq_lens   [B] int32: tokens in the cache per sequence (>= 1).
+ *   seq_lens   [B] int32: tokens in the cache per sequence (>= 1, at most 2^31 - 256).
  *   q          [B, 1, H, r + d_R] absorbed query, bf16 (FP32 kind: fp32).
  *   W_UV       [H, r, d_v] bf16 (FP32 kind: fp32).
  *   R          INT2 kinds: [r, r] fp32 (as in append; INT2_JOINT: [r + d_R,

@@ -15,7 +15,7 @@ namespace mla {
 // Device status flags (OR-ed into the status word).
 enum : int32_t {
     FLAG_BAD_BLOCK = 1,      // a block id outside [0, num_blocks) or a logical block past the table
-    FLAG_BAD_LENGTH = 2,     // a sequence length outside [q_len, max_blocks * block_size]
+    FLAG_BAD_LENGTH = 2,     // a sequence length outside [q_len, max_blocks * block_size], or above 2^31 - 256
     FLAG_TIMEOUT = 4,        // a bounded wait gave up
 };
 

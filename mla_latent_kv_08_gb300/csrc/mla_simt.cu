@@ -91,7 +91,9 @@ __device__ __forceinline__ void plan_body(const DecodeParams &p, int32_t max_wor
     if (threadIdx.x == 0) g_plan_time[1] = ptx_globaltimer();
 #endif
     const int tid = threadIdx.x;
-    const int64_t cap = (int64_t)p.max_blocks * p.s.bs;
+    // the longest sequence: the table's room; and positions rounded up to a step of any kernel
+    // stay within 31 bits
+    const int64_t cap = min((int64_t)p.max_blocks * p.s.bs, (int64_t)INT32_MAX - 255);
     const int P = p.streams;
     if (tid == 0) { s_tiles = 0; p.status[0] = 0; }
     __syncthreads();

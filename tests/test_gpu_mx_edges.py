@@ -46,6 +46,35 @@ def test_tokens_times_heads_past_31_bits(gpu_lib, H, q_len, blocks):
     assert np.max(np.abs(lse[0].cpu().numpy() - (m + np.log(l))[..., 0])) <= gu.BF16_LSE_TOL
 
 
+@pytest.mark.parametrize("kind,H", [("mxfp8", 16), ("mxfp8", 128), ("bf16", 128)])
+@pytest.mark.parametrize("over", [0, 254])
+def test_a_length_at_the_end_of_31_bits_is_refused(gpu_lib, kind, H, over):
+    """2^31 - 255 tokens and more, under a table with room for them: the flag and NaN rows; the
+    sequence beside it as it is."""
+    import mla_latent_kv_08_gb300 as mla
+    import torch
+    w = _workload(84, [64, 70], H=H)
+    shape = _shape(mla, w, kind=mla.MLA_KV_MXFP8 if kind == "mxfp8" else mla.MLA_KV_BF16)
+    cache, _ = gu.fill_cache(w, shape)
+    table = torch.full((2, 2 ** 25), -1, dtype=torch.int32, device="cuda")
+    table[0] = int(w.block_table[0, 0])
+    table[1, :2] = gu.dev(w.block_table[1, :2])
+    bf = torch.bfloat16
+    out = torch.empty((2, 1, H, 128), dtype=bf, device="cuda")
+    lse = torch.empty((2, 1, H), dtype=torch.float32, device="cuda")
+    ws = mla.alloc_workspace(shape, 2, 1)
+    mla.mla_decode(cache, table, gu.dev(np.array([2 ** 31 - 255 + over, 70], np.int32)), gu.dev(w.q, bf), gu.dev(w.W_UV, bf),
+                   w.scale, out, lse, ws)
+    torch.cuda.synchronize()
+    code, flags = mla.mla_get_status(ws)
+    assert code == mla.MLA_ERR_BOUNDS and flags == 2            # a length
+    assert torch.isnan(out[0]).all() and torch.isnan(lse[0]).all()
+    lat = _stored(w) if kind == "mxfp8" else w.latent
+    ro, rl = attention.absorbed(w.q[1], lat[1], w.rope[1], w.W_UV, w.scale)
+    assert gu.rel_err(out[1].float().cpu().numpy(), ro) <= gu.BF16_REL_TOL
+    assert np.max(np.abs(lse[1].cpu().numpy() - rl)) <= gu.BF16_LSE_TOL
+
+
 @pytest.mark.parametrize("impl", IMPLS)
 @pytest.mark.parametrize("H,q_len", [(16, 1), (16, 4), (64, 1), (8, 3), (128, 1), (128, 2)])
 def test_scores_of_minus_infinity(gpu_lib, impl, H, q_len):
