@@ -8,6 +8,32 @@ from tests.test_gpu_prefill import Case, _run
 pytestmark = pytest.mark.gpu
 
 
+@pytest.mark.parametrize("kind,impl,dims,bound", [
+    ("mxfp8", 0, {}, 3500000), ("bf16", 0, {}, 3500000), ("mxfp8", 1, {}, 1800000),
+    ("fp32", 1, dict(r=64, dR=16, dn=32, dv=32, bs=16), 7000000)])
+def test_several_passes_over_the_heads(gpu_lib, kind, impl, dims, bound):
+    """Keys and values of two heads fill the library's 4 GiB under a bound of so many cached
+    tokens, so five heads take three passes, the last one a head short. The workspace starts as
+    NaN, and two calls follow one another."""
+    import mla_latent_kv_08_gb300 as mla
+    import torch
+    case = Case(110, [300, 0, 140, 7], [200, 9, 0, 600], H=5, kind=kind, **dims)
+    shape = case.shape(mla, impl=impl)
+    head = (case.dn + case.dv) * (2 if impl == 0 else 4) * bound
+    assert 2 * head <= 4 << 30 < 3 * head
+    cache, a = case.cache(mla, shape, poison=True), case.args(mla, shape)
+    a["max_tokens"] = bound
+    a["workspace"] = mla.alloc_prefill_workspace(shape, 4, int(case.cu[-1]), bound, case.dn)
+    a["workspace"].fill_(0xFF)
+    for _ in range(2):
+        a["out"].fill_(float("nan")), a["lse"].fill_(float("nan"))
+        mla.mla_prefill(cache, **a)
+        mla.mla_prefill(cache, **a)
+        torch.cuda.synchronize()
+        assert mla.mla_get_status(a["workspace"]) == (mla.MLA_OK, 0)
+        case.check(a["out"].double().cpu().numpy(), a["lse"].cpu().numpy())
+
+
 @pytest.mark.parametrize("kind,impl", [("mxfp8", 0), ("mxfp8", 1), ("fp32", 1)])
 def test_scores_of_minus_infinity(gpu_lib, kind, impl):
     """The first cached tokens score past the 32-bit range: weight 0, and the softmax over the
