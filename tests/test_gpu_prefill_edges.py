@@ -34,6 +34,24 @@ def test_several_passes_over_the_heads(gpu_lib, kind, impl, dims, bound):
         case.check(a["out"].double().cpu().numpy(), a["lse"].cpu().numpy())
 
 
+@pytest.mark.parametrize("above", [False, True])
+def test_either_order_of_the_tiles(gpu_lib, above):
+    """Chunks of unequal lengths, some empty, on as many heads as give just below and just
+    above eight tiles (at their bound) for each SM: sequence by sequence, and head by head."""
+    import mla_latent_kv_08_gb300 as mla
+    import torch
+    new, past = [1500, 0, 700, 1, 0, 900, 257], [100, 30, 0, 2000, 0, 129, 0]
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    tiles = sum(new) // 256 + len(new)
+    H = (8 * sms - 1) // tiles + above
+    case = Case(111 + above, new, past, H=H, kind="mxfp8")
+    out, lse, status = _run(mla, case)
+    assert status == (mla.MLA_OK, 0)
+    assert np.isfinite(out).all() and np.isfinite(lse).all() and not (lse == 5.0).any()
+    case.check(out, lse, heads=sorted({0, 1, H // 2, H - 2, H - 1}),
+               rows=[0, 1, 127, 128, 255, 256, 257, 511, 512, 699, 899, 1023, 1280, 1499])
+
+
 @pytest.mark.parametrize("kind,impl", [("mxfp8", 0), ("mxfp8", 1), ("fp32", 1)])
 def test_scores_of_minus_infinity(gpu_lib, kind, impl):
     """The first cached tokens score past the 32-bit range: weight 0, and the softmax over the
