@@ -299,7 +299,8 @@ mla_status mla_verify(const mla_shape *shape, const mla_cache *cache,
  * decompresses its cache stores them. A new token that sees a cached one whose latent
  * holds a NaN or an infinity is NaN; one whose mask hides it is not touched by it. Kinds: BF16, FP32, MXFP8; MLA_ERR_UNSUPPORTED
  * for the INT2 kinds (use mla_verify) and for v_head_dim > 1024. A sequence with a bad
- * length or block gets NaN rows; mla_get_status(workspace) reports the flags. */
+ * length or block gets NaN rows, and a wait on the device that gave up makes rows NaN;
+ * mla_get_status(workspace) reports the flags. */
 size_t mla_prefill_workspace_bytes(const mla_shape *shape, int32_t B, int32_t num_q, int32_t max_tokens,
                                    int32_t nope_dim);
 mla_status mla_prefill(const mla_shape *shape, const mla_cache *cache, const int32_t *block_table,
@@ -377,6 +378,14 @@ mla_status mla_profile_read(double *attention_ms, int32_t *attention_launches,
  * timeout_ns must be in [1000, 100000000] (1 us .. 100 ms), else
  * MLA_ERR_INVALID; MLA_ERR_CUDA if the launch fails. */
 mla_status mla_selftest_wait_timeout(uint64_t timeout_ns, int32_t *status, void *stream);
+
+/* Self-test of what mla_prefill does about a wait that gave up: the next `calls` (0 .. 16,
+ * else MLA_ERR_INVALID) mla_prefill calls of the process that launch something start with
+ * the words set that its tensor-core kernel that makes keys and values sets then. No wait
+ * runs out, every kernel runs as ever. On the tensor-core path all rows of such a call are
+ * NaN and mla_get_status(workspace) reports MLA_ERR_TIMEOUT; the CUDA-core path has no
+ * waits and reports it alone. */
+mla_status mla_selftest_prefill_timeout(int32_t calls);
 
 /* Write the extra per-token key (shape->index_dim elements, the caller's dtype:
  * bf16, or fp32 for the FP32 kind) of the tokens described exactly as for

@@ -2,6 +2,7 @@
 // choice and the launch sequence of append, decode and verify.
 #include "mla_internal.cuh"
 
+#include <atomic>
 #include <string.h>
 
 namespace mla {
@@ -467,6 +468,15 @@ struct PrefillWs {
 // 1.5 % of the memory.
 constexpr size_t kPrefillKvBytes = (size_t)4 << 30;
 
+// mla_selftest_prefill_timeout's calls to go
+static std::atomic<int32_t> g_prefill_gave_up{0};
+
+mla_status mla_selftest_prefill_timeout(int32_t calls) {
+    if (calls < 0 || calls > 16) return MLA_ERR_INVALID;
+    g_prefill_gave_up = calls;
+    return MLA_OK;
+}
+
 static bool prefill_tc(const mla_shape *s, int32_t dn) {
     return s->impl != MLA_IMPL_SIMT && prefill_tc_supported(shape_args(s), dn);
 }
@@ -557,6 +567,7 @@ mla_status mla_prefill(const mla_shape *shape, const mla_cache *cache, const int
     p.scale = scale;
     p.out = out;
     p.lse = lse;
+    if (g_prefill_gave_up > 0) p.gave_up = g_prefill_gave_up.fetch_sub(1) > 0;
     if (launch_prefill_plan(p, stream_) != cudaSuccess) return MLA_ERR_CUDA;
     prof_kernels(1);
     if (num_q == 0) return MLA_OK;

@@ -169,7 +169,8 @@ struct PrefillParams {
     int32_t *kv_off;             // [B + 1]
     int32_t *tile_off;           // [B + 1]
     int32_t *bad;                // [B]
-    int32_t *status;
+    int32_t *status;             // [2]: the flags; whether a wait of expand_tc_kernel gave up
+    int32_t gave_up;             // self-test: that word starts as this
     const void *rows;            // [cap_rows, r + d_R]
     const uint8_t *odd;          // [cap_rows], see ReadParams
     void *k;                     // [nh, cap_rows, d_n]

@@ -37,7 +37,10 @@ __device__ __forceinline__ long long scan_block(long long v, long long *s_warp, 
 __global__ void __launch_bounds__(1024) prefill_plan_kernel(PrefillParams p) {
     __shared__ long long s_warp[32];
     pdl_trigger();
-    if (threadIdx.x == 0) p.status[0] = 0;
+    if (threadIdx.x == 0) {
+        p.status[0] = p.gave_up ? FLAG_TIMEOUT : 0;
+        p.status[1] = p.gave_up;
+    }
     __syncthreads();
     const long long cap_tokens = (long long)p.max_blocks * p.s.bs;
     long long rows0 = 0, tiles0 = 0;

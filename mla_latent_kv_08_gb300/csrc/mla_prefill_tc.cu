@@ -7,7 +7,8 @@
 //                     rope keys in the dense rows
 //
 // Every wait is bounded (2 s): one that gives up records FLAG_TIMEOUT and the CTA winds
-// down without trapping.
+// down without trapping. The attention's own rows become NaN then; after one of the
+// expansion's, whose keys and values are what was in the workspace, all rows do.
 #include "mla_internal.cuh"
 #include "mla_ptx.cuh"
 
@@ -305,6 +306,7 @@ expand_tc_kernel(const __grid_constant__ CUtensorMap rows_map, const __grid_cons
     tc_fence_before();
     __syncthreads();
     cluster_sync();
+    if (tid == 0 && bars->abort_flag) p.status[1] = 1;
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
@@ -400,7 +402,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     pdl_trigger();
     pdl_wait();
     // The last tiles of a sequence see the most: they start first.
-    const int tiles = p.tile_off[p.B], r = (int)cluster_ctarank(), H = p.s.H;
+    const int tiles = p.tile_off[p.B], gave_up = p.status[1], r = (int)cluster_ctarank(), H = p.s.H;
     int b, hl, i0;
     if (by_seq) {                                        // sequence, head, tile
         const int at = blockIdx.y * (gridDim.x >> 1) + (blockIdx.x >> 1), pos = tiles * p.nh - 1 - at;
@@ -421,7 +423,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     const int rows_here = min(kTileQ, n - i0);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     __nv_bfloat16 *out = (__nv_bfloat16 *)p.out;
-    if (p.bad[b]) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const bool misaligned = smem_u32(smem) & 1023u;      // of both CTAs: the swizzled blocks need it
+    if (misaligned) raise_flag(p.status, FLAG_TIMEOUT);
+    // (gave_up is the expansion's, which is complete: every thread of the pair read the same)
+    if (p.bad[b] | gave_up | misaligned) {
         for (int e = r * kThreads + tid; e < rows_here * kDv; e += 2 * kThreads)
             out[((qrow0 + e / kDv) * H + h) * kDv + e % kDv] = __float2bfloat16_rn(CUDART_NAN_F);
         if (p.lse)
@@ -430,12 +436,6 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_consta
     }
     const int L = p.seq_lens[b];
     const int steps = (L - n + i0 + rows_here + 127) / 128;      // of the tile's last row
-
-    extern __shared__ __align__(1024) uint8_t smem[];
-    if (smem_u32(smem) & 1023u) {          // both CTAs: the swizzled blocks need it
-        raise_flag(p.status, FLAG_TIMEOUT);
-        return;
-    }
     Bars *bars = (Bars *)(smem + kOffBar);
     const int row0 = p.kv_off[b];
     const int kv0 = hl * p.cap_rows + row0;               // fits: the pass's rows are counted in 32 bits

@@ -88,3 +88,22 @@ def test_a_code_that_is_not_a_number(gpu_lib, impl):
         assert np.isnan(out[mine]).all() and np.isnan(lse[mine]).all(), b
         case.lat[b][t], case.rope[b][t] = 0, 0                           # hidden from the rows that are held to it
         case.check(out, lse, seqs=[b], rows=np.arange(first))
+
+
+@pytest.mark.parametrize("kind,lse", [("mxfp8", True), ("bf16", False)])
+def test_rows_are_nan_after_an_expansion_that_gave_up(gpu_lib, kind, lse):
+    """As if a wait of the kernel that makes keys and values had given up: NaN in every new
+    token's rows, the flag, and the next call as ever."""
+    import mla_latent_kv_08_gb300 as mla
+    case = Case(115, [300, 0, 40, 1], [50, 9, 100, 700], H=3, kind=kind)
+    change = {} if lse else {"lse": None}
+    mla.mla_selftest_prefill_timeout(1)
+    try:
+        out, got, status = _run(mla, case, **change)
+    finally:
+        mla.mla_selftest_prefill_timeout(0)
+    assert status == (mla.MLA_ERR_TIMEOUT, 4)
+    assert np.isnan(out).all() and (got is None or np.isnan(got).all())
+    out, got, status = _run(mla, case)
+    assert status == (mla.MLA_OK, 0)
+    case.check(out, got)

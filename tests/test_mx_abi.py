@@ -171,3 +171,10 @@ def test_prefill_workspace(lib):
         a.update(bad)
         with pytest.raises(mla.MlaError):
             mla.mla_prefill_workspace_bytes(_shape(), **a)
+
+
+def test_prefill_selftest_arguments(lib):
+    import mla_latent_kv_08_gb300 as mla
+    for calls in (-1, 17):
+        assert lib.mla_selftest_prefill_timeout(calls) == mla.MLA_ERR_INVALID
+    mla.mla_selftest_prefill_timeout(0)
