@@ -379,13 +379,13 @@ mla_status mla_profile_read(double *attention_ms, int32_t *attention_launches,
  * MLA_ERR_INVALID; MLA_ERR_CUDA if the launch fails. */
 mla_status mla_selftest_wait_timeout(uint64_t timeout_ns, int32_t *status, void *stream);
 
-/* Self-test of what mla_prefill does about a wait that gave up: the next `calls` (0 .. 16,
- * else MLA_ERR_INVALID) mla_prefill calls of the process that launch something start with
- * the words set that its tensor-core kernel that makes keys and values sets then. No wait
- * runs out, every kernel runs as ever. On the tensor-core path all rows of such a call are
- * NaN and mla_get_status(workspace) reports MLA_ERR_TIMEOUT; the CUDA-core path has no
- * waits and reports it alone. */
-mla_status mla_selftest_prefill_timeout(int32_t calls);
+/* Self-test of what a call does about a wait on the device that gave up: the next `calls`
+ * (0 .. 16, else MLA_ERR_INVALID) calls of the process to mla_decode, mla_verify,
+ * mla_append_decode, mla_decode_noalloc or mla_prefill that launch something start with the
+ * words set that a kernel of theirs sets then. No wait runs out and every kernel runs as
+ * ever; all rows of such a call are NaN and mla_get_status(workspace) reports
+ * MLA_ERR_TIMEOUT. (mla_prefill on the CUDA cores has no waits: it reports the flag alone.) */
+mla_status mla_selftest_gave_up(int32_t calls);
 
 /* Write the extra per-token key (shape->index_dim elements, the caller's dtype:
  * bf16, or fp32 for the FP32 kind) of the tokens described exactly as for

@@ -49,7 +49,7 @@ EXPORTED = (
     "mla_latent_append_index", "mla_fold_rotation", "mla_append_decode",
     "mla_calib_covariance", "mla_calib_projection_energy", "mla_calib_eigh", "mla_calib_eigh_weighted",
     "mla_calib_project_abs", "mla_calib_thresholds",
-    "mla_latent_read", "mla_prefill", "mla_prefill_workspace_bytes", "mla_selftest_prefill_timeout",
+    "mla_latent_read", "mla_prefill", "mla_prefill_workspace_bytes", "mla_selftest_gave_up",
 )
 
 
@@ -112,8 +112,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mla_decode_noalloc.restype = i32
     lib.mla_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp, vp]
     lib.mla_selftest_wait_timeout.restype = i32
-    lib.mla_selftest_prefill_timeout.argtypes = [i32]
-    lib.mla_selftest_prefill_timeout.restype = i32
+    lib.mla_selftest_gave_up.argtypes = [i32]
+    lib.mla_selftest_gave_up.restype = i32
     lib.mla_fold_rotation.argtypes = [sp, vp, vp, vp, vp]
     lib.mla_fold_rotation.restype = i32
     i64 = ctypes.c_int64
@@ -408,9 +408,9 @@ def mla_selftest_wait_timeout(timeout_ns: int, status, stream=None) -> None:
            "mla_selftest_wait_timeout")
 
 
-def mla_selftest_prefill_timeout(calls: int) -> None:
-    """The next ``calls`` mla_prefill calls behave as if a wait on the device had given up (see mla.h)."""
-    _check(load_library().mla_selftest_prefill_timeout(int(calls)), "mla_selftest_prefill_timeout")
+def mla_selftest_gave_up(calls: int) -> None:
+    """The next ``calls`` attention calls behave as if a wait on the device had given up (see mla.h)."""
+    _check(load_library().mla_selftest_gave_up(int(calls)), "mla_selftest_gave_up")
 
 
 def mla_resolve_impl(shape: Shape, q_len: int = 1) -> int:

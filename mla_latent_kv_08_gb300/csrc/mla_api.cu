@@ -21,6 +21,10 @@ static bool mx_cache_ok(const mla_cache *c) {
     return c->codes && c->scale_zero && c->rope && aligned16(c->codes) && aligned16(c->scale_zero) && aligned16(c->rope);
 }
 
+// mla_selftest_gave_up: its calls to go, and whether this is one of them
+static std::atomic<int32_t> g_gave_up{0};
+static int32_t take_gave_up() { return g_gave_up > 0 && g_gave_up.fetch_sub(1) > 0; }
+
 // ---- benchmarking diagnostics (see mla_profile_enable) ----------------------
 struct Profile {
     bool on = false;
@@ -212,6 +216,7 @@ static mla_status run_attention(const mla_shape *s, const mla_cache *cache, cons
     p.q_prep = int2 ? (const float *)(ws + w.q_prep) : nullptr;
     p.scale_log2 = scale * kLog2e;
     p.status = (int32_t *)(ws + w.status);
+    p.gave_up = take_gave_up();
     p.num_work = (const int32_t *)(ws + w.status + sizeof(int32_t));
     // the bf16 decode that scores two blocks per MMA plans in 128-token steps, so that
     // only a sequence's last work item can end with an unpaired block
@@ -280,6 +285,7 @@ static mla_status run_attention(const mla_shape *s, const mla_cache *cache, cons
     c.s = p.s;
     c.B = B;
     c.q_len = q_len;
+    c.status = p.status;
     c.split_start = p.split_start;
     c.part_bf16 = impl == MLA_IMPL_TCGEN05;   // the tensor-core decode writes bf16 partials
     c.part_o = p.part_o;
@@ -326,6 +332,12 @@ static mla_status run_attention(const mla_shape *s, const mla_cache *cache, cons
 using namespace mla;
 
 extern "C" {
+
+mla_status mla_selftest_gave_up(int32_t calls) {
+    if (calls < 0 || calls > 16) return MLA_ERR_INVALID;
+    g_gave_up = calls;
+    return MLA_OK;
+}
 
 size_t mla_workspace_bytes(const mla_shape *shape, int32_t B, int32_t q_len) {
     if (check_shape(shape) != MLA_OK || B < 1 || q_len < 1) return 0;
@@ -468,15 +480,6 @@ struct PrefillWs {
 // 1.5 % of the memory.
 constexpr size_t kPrefillKvBytes = (size_t)4 << 30;
 
-// mla_selftest_prefill_timeout's calls to go
-static std::atomic<int32_t> g_prefill_gave_up{0};
-
-mla_status mla_selftest_prefill_timeout(int32_t calls) {
-    if (calls < 0 || calls > 16) return MLA_ERR_INVALID;
-    g_prefill_gave_up = calls;
-    return MLA_OK;
-}
-
 static bool prefill_tc(const mla_shape *s, int32_t dn) {
     return s->impl != MLA_IMPL_SIMT && prefill_tc_supported(shape_args(s), dn);
 }
@@ -567,7 +570,7 @@ mla_status mla_prefill(const mla_shape *shape, const mla_cache *cache, const int
     p.scale = scale;
     p.out = out;
     p.lse = lse;
-    if (g_prefill_gave_up > 0) p.gave_up = g_prefill_gave_up.fetch_sub(1) > 0;
+    p.gave_up = take_gave_up();
     if (launch_prefill_plan(p, stream_) != cudaSuccess) return MLA_ERR_CUDA;
     prof_kernels(1);
     if (num_q == 0) return MLA_OK;

@@ -117,6 +117,7 @@ combine_tc_kernel(const __grid_constant__ CUtensorMap w_map, const CombTcParams 
     pdl_wait();                      // the split partials are complete from here on
     COMB_TRACE(1);
     if (!c.ranges_early) read_ranges();
+    const bool gave_up = c.status[0] & FLAG_TIMEOUT;
     __syncthreads();
     // Rows of 8 or fewer: each row's splits are dealt to wpr = 16 / rows warps (split
     // sb + wpr k to warp sub of the row), each merging its share; the row's warp then
@@ -212,7 +213,7 @@ combine_tc_kernel(const __grid_constant__ CUtensorMap w_map, const CombTcParams 
             const int i = grow % c.q_len;
             const int2 sr = s_range[rr];
             const int row = i * H + h;
-            bool nan = sr.y <= sr.x;
+            bool nan = sr.y <= sr.x || gave_up;
             float M = -CUDART_INF_F, tot = 0.f;
             if (wpr == 1) {
                 merge_splits(row, sr.x, sr.y, 1, M, tot, acc, nan);

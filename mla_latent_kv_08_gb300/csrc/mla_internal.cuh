@@ -98,6 +98,7 @@ struct DecodeParams {
     int32_t streams;
     int32_t item_cost;           // planner: units charged per sequence start (its Q load, epilogue)
     int32_t plan_tile;           // planner: tokens per cost unit; work items start at multiples of it
+    int32_t gave_up;             // self-test: the flags start with FLAG_TIMEOUT
     int32_t narrow;              // MXFP8 on the tensor cores: the kernel for few query rows, a CTA a stream
     float *part_o;
     float *part_lse;
@@ -107,6 +108,8 @@ struct CombineParams {
     ShapeArgs s;
     int32_t B, q_len;
     int32_t part_bf16;           // part_o holds bf16 values (else fp32)
+    const int32_t *status;       // the call's flags: FLAG_TIMEOUT makes every row NaN (an attention
+                                 // kernel whose wait gave up leaves partials as the workspace had them)
     const int32_t *split_start;
     const void *part_o;
     const float *part_lse;

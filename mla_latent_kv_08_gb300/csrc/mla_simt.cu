@@ -95,7 +95,7 @@ __device__ __forceinline__ void plan_body(const DecodeParams &p, int32_t max_wor
     // stay within 31 bits
     const int64_t cap = min((int64_t)p.max_blocks * p.s.bs, (int64_t)INT32_MAX - 255);
     const int P = p.streams;
-    if (tid == 0) { s_tiles = 0; p.status[0] = 0; }
+    if (tid == 0) { s_tiles = 0; p.status[0] = p.gave_up ? FLAG_TIMEOUT : 0; }
     __syncthreads();
     // Cost axis: each sequence is charged item_cost units for its start (the query
     // load and epilogue of a new work item) followed by one unit per tile; streams
@@ -659,7 +659,7 @@ __global__ void __launch_bounds__(256) combine_kernel(CombineParams p) {
             const int s0 = p.split_start[b], s1 = p.split_start[b + 1];
             const int row = i * H + h;
             float M = -CUDART_INF_F;
-            bool nan = (s1 <= s0);
+            bool nan = s1 <= s0 || (p.status[0] & FLAG_TIMEOUT);
             for (int s = s0; s < s1; ++s) {
                 float v = p.part_lse[(size_t)s * rows_total + row];
                 if (isnan(v)) nan = true;

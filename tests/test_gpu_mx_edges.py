@@ -149,3 +149,31 @@ def test_a_code_that_is_not_a_number_in_a_draft(gpu_lib, impl, H, q_len):
             ro, rl = attention.absorbed(w.q[b], lat[b], w.rope[b], w.W_UV, w.scale)
             assert gu.rel_err(out[b][~sees], ro[~sees]) <= gu.BF16_REL_TOL, b
             assert np.max(np.abs(lse[b][~sees] - rl[~sees])) <= gu.BF16_LSE_TOL, b
+
+
+@pytest.mark.parametrize("kind,impl,H,q_len", [("mxfp8", "auto", 128, 1), ("mxfp8", "roomy", 16, 2), ("mxfp8", "simt", 16, 1),
+                                               ("bf16", "auto", 128, 1), ("bf16", "auto", 20, 3), ("int2", "auto", 128, 1)])
+def test_rows_are_nan_after_a_wait_that_gave_up(gpu_lib, kind, impl, H, q_len):
+    """As if a wait of a call's kernel had given up: NaN in every row, the flag, and the next
+    call on the same workspace as ever."""
+    import mla_latent_kv_08_gb300 as mla
+    import torch
+    w = _workload(85, [700, 64, 129], H=H, q_len=q_len)
+    if impl == "roomy":
+        _roomy(w)
+    kinds = {"mxfp8": mla.MLA_KV_MXFP8, "bf16": mla.MLA_KV_BF16, "int2": mla.MLA_KV_INT2_ROT}
+    shape = _shape(mla, w, kind=kinds[kind], impl=_impl(mla, impl))
+    R, T = (np.eye(512, dtype=np.float32), np.full(16, 4.0, np.float32)) if kind == "int2" else (None, None)
+    cache, _ = gu.fill_cache(w, shape, R, T)
+    want, want_l, _ = gu.attend(w, shape, cache, w.q, R=R, q_len=q_len)
+    mla.mla_selftest_gave_up(1)
+    try:
+        out, lse, ws = gu.attend(w, shape, cache, w.q, R=R, q_len=q_len)
+    finally:
+        mla.mla_selftest_gave_up(0)
+    assert mla.mla_get_status(ws) == (mla.MLA_ERR_TIMEOUT, 4)
+    assert np.isnan(out).all() and np.isnan(lse).all()
+    out, lse, ws = gu.attend(w, shape, cache, w.q, R=R, q_len=q_len)
+    assert mla.mla_get_status(ws) == (mla.MLA_OK, 0)
+    np.testing.assert_array_equal(out, want)
+    np.testing.assert_array_equal(lse, want_l)

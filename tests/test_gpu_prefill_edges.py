@@ -97,11 +97,11 @@ def test_rows_are_nan_after_an_expansion_that_gave_up(gpu_lib, kind, lse):
     import mla_latent_kv_08_gb300 as mla
     case = Case(115, [300, 0, 40, 1], [50, 9, 100, 700], H=3, kind=kind)
     change = {} if lse else {"lse": None}
-    mla.mla_selftest_prefill_timeout(1)
+    mla.mla_selftest_gave_up(1)
     try:
         out, got, status = _run(mla, case, **change)
     finally:
-        mla.mla_selftest_prefill_timeout(0)
+        mla.mla_selftest_gave_up(0)
     assert status == (mla.MLA_ERR_TIMEOUT, 4)
     assert np.isnan(out).all() and (got is None or np.isnan(got).all())
     out, got, status = _run(mla, case)

@@ -176,5 +176,5 @@ def test_prefill_workspace(lib):
 def test_prefill_selftest_arguments(lib):
     import mla_latent_kv_08_gb300 as mla
     for calls in (-1, 17):
-        assert lib.mla_selftest_prefill_timeout(calls) == mla.MLA_ERR_INVALID
-    mla.mla_selftest_prefill_timeout(0)
+        assert lib.mla_selftest_gave_up(calls) == mla.MLA_ERR_INVALID
+    mla.mla_selftest_gave_up(0)
