@@ -294,11 +294,14 @@ mla_status mla_verify(const mla_shape *shape, const mla_cache *cache,
  *   out        [num_q, H, d_v] bf16 (FP32 kind: fp32).
  *   lse        [num_q, H] fp32 natural-log softmax denominators, or NULL.
  *   workspace  at least mla_prefill_workspace_bytes(shape, B, num_q, max_tokens, d_n).
- * New token i of sequence b sees positions 0 .. seq_lens[b] - n_b + i. Keys and values
- * are rounded to bf16 before the products (BF16 and MXFP8 kinds), as a layer that
- * decompresses its cache stores them. A new token that sees a cached one whose latent
- * holds a NaN or an infinity is NaN; one whose mask hides it is not touched by it. Kinds: BF16, FP32, MXFP8; MLA_ERR_UNSUPPORTED
- * for the INT2 kinds (use mla_verify) and for v_head_dim > 1024. A sequence with a bad
+ * New token i of sequence b sees positions 0 .. seq_lens[b] - n_b + i. On the tensor cores
+ * (BF16 and MXFP8 kinds with r 512, d_R 64, d_n 128 and d_v 128, unless MLA_IMPL_SIMT asks
+ * otherwise) keys and values are rounded to bf16 before the products, as a layer that
+ * decompresses its cache stores them, and so are the softmax weights; on the CUDA cores,
+ * which take every other shape, all three stay fp32. A new token that sees a cached one
+ * whose latent holds a NaN or an infinity is NaN; one whose mask hides it is not touched
+ * by it. Kinds: BF16, FP32, MXFP8; MLA_ERR_UNSUPPORTED for the INT2 kinds (use mla_verify)
+ * and for v_head_dim > 1024. A sequence with a bad
  * length or block gets NaN rows, and a wait on the device that gave up makes rows NaN;
  * mla_get_status(workspace) reports the flags. */
 size_t mla_prefill_workspace_bytes(const mla_shape *shape, int32_t B, int32_t num_q, int32_t max_tokens,
