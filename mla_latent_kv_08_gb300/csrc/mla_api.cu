@@ -476,7 +476,8 @@ struct PrefillWs {
 
 // Keys and values of `heads` heads are held at a time: as many as fit into this, spread evenly
 // over the passes. Each pass ends with SMs that wait for its last tiles: two chunks of 2048
-// over 37k tokens took 5.32 ms in three passes (1 GiB), 5.13 in two, 4.97 in one. 4 GiB are
+// over 37k tokens took 5.43 ms in three passes (1 GiB), 5.17 in two, 4.97 in one (replays in
+// turn, idle between them; back to back, under the power cap, one pass takes 5.15). 4 GiB are
 // 1.5 % of the memory.
 constexpr size_t kPrefillKvBytes = (size_t)4 << 30;
 

@@ -20,7 +20,7 @@
 // seen nothing but scores of minus infinity has no maximum yet, and its first one counts as
 // an item's first. Row sums stay a thread's own until the end of a work item.
 //
-// Measured, 64 heads over two sequences of 52k and 75k tokens: 54 us
+// Measured, 64 heads over two sequences of 52k and 75k tokens: 55 us
 // (the pair kernel: 64 us), bytes at the copy rate 12.4 us. The tensor pipe is busy for
 // 14 % of the time: a product whose first operand lies MN-major in shared memory takes 139
 // cycles, twice a K-major one, and a step's scores wait for its expansion. Taking V^T from
@@ -477,7 +477,8 @@ decode_narrow_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_
             ok = !soft_any(!ok);
             if (!ok) break;
             tc_fence_after();
-            // row sums over the tokens, then O^T / l into the item's partial slot
+            // row sums over the tokens, then O^T / l into the item's partial slot, rounded to bf16
+            // as the pair kernel's (half of the bytes that the combine waits for)
 #pragma unroll
             for (int h = 0; h < N / 32; ++h) {
                 uint32_t v[32];
@@ -692,7 +693,10 @@ bool decode_narrow_supported(const ShapeArgs &s, int32_t q_len) { return is_mx(s
 // one sequence of 169 tokens 18.2 / 20.4. At 64 rows: 28.0 / 33.5 us of 600, 39.5 / 39.9 of
 // 1250, 55.1 / 51.0 of 2500, 85.5 / 72.1 of 5000. So: from one step a CTA on for 32 columns,
 // from four on for 64. The tokens are what the block table has room for (the lengths are on
-// the device).
+// the device); the figures are of tables as wide as the longest sequence. Under a wider one, as
+// a server has for its longest context, the rule takes this kernel for shorter sequences too,
+// at the cost that the figures show (5.5 us of 28 for those of 600 tokens), and the same
+// sequences may then round differently.
 bool decode_narrow_wins(const ShapeArgs &s, int32_t q_len, int64_t tokens, int32_t sms) {
     return tokens >= (int64_t)(q_len * s.H <= 32 ? 1 : 4) * nmx::kStep * sms;
 }

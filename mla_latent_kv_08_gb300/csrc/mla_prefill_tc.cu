@@ -769,9 +769,12 @@ cudaError_t launch_prefill_tc(const PrefillParams &p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     // The order of the tiles. Head by head the heaviest sequence's tiles are among the last to
     // start too, so where there are few rounds the sequences go one after the other instead: 8
-    // chunks of 1025 to 1992 tokens on 16 heads (6 rounds of the pairs that fit) 436 us instead
-    // of 459, 8 of 256 on 64 heads (3) 266 instead of 272, but 4 prompts on 128 heads (35) 1449
-    // instead of 1432, 8 chunks of 768 on 64 heads (10) 534 instead of 529.
+    // chunks of 1025 to 1992 tokens on 16 heads (6 rounds of the pairs that fit) 439 us instead
+    // of 464, 8 of 256 on 64 heads (3) 266 instead of 272, but 4 prompts on 128 heads (37) 1452
+    // instead of 1443, 8 chunks of 768 on 64 heads (10) 534 instead of 529. Between them it
+    // depends on the lengths, and the border is low: chunks of 1000 to 2000 tokens gain 3.9 % at
+    // 9 rounds, 2.3 % at 14; prompts of 1000 to 4000 1.9 % at 9, 0.6 % at 19; chunks of 1 to 1500
+    // 1.4 % at 16, 1.0 % at 21, 0.3 % at 32.
     const int pairs = p.num_q / kTileQ + p.B, by_seq = (long long)pairs * p.nh < 8ll * sms;
     return launch_pdl(prefill_tc_kernel, dim3(2 * pairs, p.nh), dim3(kThreads), kSmemBytes, st, q, k_ld, v_ld, rope, p, by_seq);
 }

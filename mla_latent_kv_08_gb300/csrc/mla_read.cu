@@ -4,8 +4,9 @@
 // stored bytes in, its row out (MXFP8 of the DeepSeek-V3 shape: 656 in, 1152 out). The lanes
 // of a warp look the tokens of its eight rows up side by side (a chain of dependent loads
 // that a warp a row would pay for each), then the warp moves two rows at a time. 133k MXFP8
-// tokens: 42.7 us, 5.65 TB/s of the copy rate's 6.75 (a warp a row: 55 us); up to 4096 rows a
-// warp a row fills more SMs (1000 tokens: 2.6 us).
+// tokens: 43.9 us, 5.5 TB/s of the copy rate's 6.8 (a warp a row: 55 us; without the look for
+// codes that are not a number 42.7); up to 4096 rows a warp a row fills more SMs (1000 tokens:
+// 2.7 us).
 #include "mla_internal.cuh"
 #include "mla_mx.cuh"
 

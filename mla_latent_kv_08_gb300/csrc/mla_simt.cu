@@ -785,9 +785,9 @@ __device__ __forceinline__ void copy_token(const AppendParams &p, int n) {
     for (int v = lane; v < dR / E; v += 32) dst[r / E + v] = src_r[v];
 }
 
-// The 8-bit kind: one warp quantises its token as it writes it. Memory bound, 1152 bytes in
-// and 656 out a token; eight tokens a warp with their slots looked up side by side took
-// longer (25 to 32 us for 51312 tokens): the chain of loads hides behind the other warps'.
+// The 8-bit kind: one warp quantises its token as it writes it (mx_write_token). Eight tokens a
+// warp with their slots looked up side by side took longer (25 to 32 us for 51312 tokens): the
+// chain of loads hides behind the other warps'.
 struct MxToken {};
 template <>
 __device__ __forceinline__ void copy_token<MxToken>(const AppendParams &p, int n) {

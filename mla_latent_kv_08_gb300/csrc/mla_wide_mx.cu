@@ -20,10 +20,10 @@
 // warps waited for instruction fetches more than for anything else (3.9 warps an issue
 // slot), so the expansion is one loop body for all parts.
 //
-// Measured, 32 sequences of 1024 to 8192 tokens (156k in all), 128 heads: 74 us, of which
+// Measured, 32 sequences of 1024 to 8192 tokens (156k in all), 128 heads: 76 us, of which
 // the codes' bytes at the copy rate are 15 us and the products at the cuBLAS rate 23 us;
-// 16 sequences of 4096 to 32768 tokens with 8 drafts: 760 us against 272 us of products.
-// The tensor pipe is busy for 41 % of the time. What bounds it is the chain of a step, one
+// 16 sequences of 4096 to 32768 tokens with 8 drafts: 780 us against 272 us of products.
+// The tensor pipe is busy for 39 % of the time. What bounds it is the chain of a step, one
 // buffer deep: expand, score, softmax, P . V, and the scores that both CTAs of a pair make.
 //
 // Tensor memory: O [0,256), S / P [256,384), Q's other half of the latent dims [384,512).
@@ -104,10 +104,9 @@ __device__ long long g_mxtrace[16][kTraceSteps];
     do {                                      \
         if (warp == 12 && lane == 0) WTRACE(ev, K); \
     } while (0)
-// events: 0 score-only boxes issued, 1 own boxes issued (producer), 2 score-only blocks
-// landed, 3 part 1 issued, 4 own blocks landed, 5 QK committed, 6 P seen, 7 PV issued
-// (MMA), 8 S seen, 9 row max agreed, 10 P stored (softmax), 11 entry, 12 score-only blocks
-// free, 13 expanded, 14 own blocks free, 15 expanded (warp 2 of the 8-bit kind)
+// events: 2 score-only blocks there, 3 part 1 issued, 4 own blocks there, 5 QK committed, 6 P
+// seen, 7 PV issued (MMA), 8 S seen, 9 row max agreed, 10 P stored (softmax), 11 entry, 12
+// score-only blocks free, 13 expanded, 14 own blocks free, 15 expanded (warp 12)
 
 struct Bars {
     uint64_t full_a;          // the step's score-only blocks are there
@@ -544,7 +543,8 @@ decode_mx_kernel(const __grid_constant__ CUtensorMap rope_map, const __grid_cons
             if (ok && have_next)
                 ok = __all_sync(0xffffffffu, mbar_wait(&bars->qreg_free, (uses - 1) & 1, bars, p.status));
             const bool bad = aborted(bars) || !ok || bad_item;
-            // Epilogue: O / l -> partial slot i, rounded to bf16; [32 rows x 64 dims] boxes
+            // Epilogue: O / l -> partial slot i, rounded to bf16 as the bf16 cache's (half of the
+            // bytes that the combine waits for; the output is rounded as far); [32 rows x 64 dims] boxes
             // (128B-swizzled) through the region, one TMA store each; rows past the
             // sequence's rows are clipped by the tensor map.
             if (ok) {
