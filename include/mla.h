@@ -44,9 +44,11 @@
  *     must be 16-byte aligned.
  *   - Host-side argument errors return before anything is launched. Device-side
  *     problems (a block id outside [0, num_blocks), a sequence length outside
- *     [q_len, max_blocks_per_seq * block_size]) never trap: the kernel records
- *     a flag, skips the bad work and writes NaN to the affected output rows;
- *     mla_get_status reports the flags.
+ *     [q_len, max_blocks_per_seq * block_size] or above 2^31 - 256) never trap:
+ *     the kernel records a flag, skips the bad work and writes NaN to the
+ *     affected output rows; mla_get_status reports the flags. A wait on the
+ *     device that gave up is recorded too, and makes NaN of every row of a
+ *     decode or verify call.
  */
 #ifndef MLA_GB300_H
 #define MLA_GB300_H
@@ -301,9 +303,9 @@ mla_status mla_verify(const mla_shape *shape, const mla_cache *cache,
  * which take every other shape, all three stay fp32. A new token that sees a cached one
  * whose latent holds a NaN or an infinity is NaN; one whose mask hides it is not touched
  * by it. Kinds: BF16, FP32, MXFP8; MLA_ERR_UNSUPPORTED for the INT2 kinds (use mla_verify)
- * and for v_head_dim > 1024. A sequence with a bad
- * length or block gets NaN rows, and a wait on the device that gave up makes rows NaN;
- * mla_get_status(workspace) reports the flags. */
+ * and for v_head_dim > 1024. A sequence with a bad length or block gets NaN rows, and a wait
+ * on the device that gave up makes NaN of the rows behind it; mla_get_status(workspace)
+ * reports the flags. */
 size_t mla_prefill_workspace_bytes(const mla_shape *shape, int32_t B, int32_t num_q, int32_t max_tokens,
                                    int32_t nope_dim);
 mla_status mla_prefill(const mla_shape *shape, const mla_cache *cache, const int32_t *block_table,
