@@ -67,7 +67,10 @@ typedef enum {
     MLA_ERR_BOUNDS = -3,       /* device flag: block id or length out of range     */
     MLA_ERR_WORKSPACE = -4,    /* workspace smaller than mla_workspace_bytes()     */
     MLA_ERR_CUDA = -5,         /* a CUDA launch or runtime call failed             */
-    MLA_ERR_TIMEOUT = -6       /* device flag: a bounded wait gave up              */
+    MLA_ERR_TIMEOUT = -6,      /* device flag: a bounded wait gave up              */
+    MLA_ERR_FULL = -7,         /* device flag: too few free blocks in the pool     */
+    MLA_ERR_VALUE = -8         /* device flag: a probability, random number or
+                                  drafted token out of range                       */
 } mla_status;
 
 typedef enum {
@@ -349,7 +352,8 @@ mla_status mla_decode_noalloc(const mla_shape *shape, const mla_cache *cache,
  * raw_flags is not NULL it receives the raw flag word (host int). */
 mla_status mla_get_status(const void *workspace, int32_t *raw_flags, void *stream);
 
-/* Read a device status word written by mla_latent_append (same meaning). */
+/* Read a device status word written by mla_latent_append or another call that takes one (same
+ * meaning; also MLA_ERR_FULL and MLA_ERR_VALUE, which mla_pool_* and mla_draft_accept raise). */
 mla_status mla_read_status_word(const int32_t *status, int32_t *raw_flags, void *stream);
 
 /* Static description of a status code. */
@@ -402,6 +406,113 @@ mla_status mla_latent_append_index(const mla_shape *shape, const mla_cache *cach
                                    int32_t max_blocks_per_seq, int32_t B, const int32_t *start_pos,
                                    const int32_t *cu_new, int32_t num_new, const void *index_key,
                                    int32_t *status, void *stream);
+
+/* ---- The pool's books: which blocks of the cache each sequence holds.
+ * One set of books serves the caches of all layers, which share a block table. The calls
+ * below work on device memory alone, in stream order, so that a serving loop needs no copy
+ * of the books on the host. A sequence of length L (seq_lens[b]) holds the first
+ * ceil(L / block_size) entries of its row of the block table; the others are -1. A block that
+ * several sequences hold (after mla_pool_fork) is full of tokens common to all of them: the
+ * block that a sequence's next token goes to is always its own, so that mla_latent_append
+ * needs no care.
+ * Books begin as block_table -1, seq_lens 0, ref_count 0 throughout, and are changed by these
+ * calls alone. block_table and seq_lens are what the attention calls take. */
+typedef struct {
+    int32_t *block_table;      /* [max_seqs, max_blocks_per_seq]                   */
+    int32_t *seq_lens;         /* [max_seqs]                                       */
+    int32_t *ref_count;        /* [shape->num_blocks]: table entries that hold the
+                                  block; 0: it is free                             */
+    int32_t max_seqs;          /* at most 16384                                    */
+    int32_t max_blocks_per_seq;
+} mla_pool;
+
+/* Each of the three pool calls
+ *   - changes all that it is asked to, or nothing: where something is out of range or there
+ *     are too few free blocks, it raises flags in `status` (optional [1] int32 device word;
+ *     mla_read_status_word gives MLA_ERR_BOUNDS or MLA_ERR_FULL), leaves the books as they
+ *     were and lists no copies;
+ *   - takes the blocks that were free before the call, lowest first, in the order of sequences
+ *     (forks) and of their blocks; those that it gives back are free for the next call;
+ *   - lists in `copies` [room, 4] int32 (16-byte aligned) which cached rows have to move
+ *     because of it: (source block, destination block, first row, rows), from entry 0 on, and
+ *     in num_copies [1] int32 (device) how many entries there are; those behind are left as
+ *     they were. Run mla_cache_copy on every layer's cache before the next call that appends
+ *     to or reads the caches, or changes the books;
+ *   - is one launch, without a workspace.
+ * MLA_ERR_UNSUPPORTED where max_seqs * max_blocks_per_seq passes 2^31 - 1. */
+
+/* Sequences get other lengths, new_lens [max_seqs] int32 (0 .. max_blocks_per_seq *
+ * block_size, at most 2^31 - 256; seq_lens[b] for no change). A longer one takes free blocks
+ * for its new tokens, a shorter one gives back the blocks behind its end (length 0: all).
+ * Where a sequence is cut inside a block that others held before the call too, it takes a free
+ * one instead, to which the list copies the rows that stay (room: max_seqs).
+ *   num_free   optional [1] int32 (device): free blocks after the call. */
+mla_status mla_pool_resize(const mla_shape *shape, const mla_pool *pool, const int32_t *new_lens, int32_t *copies,
+                           int32_t *num_copies, int32_t *num_free, int32_t *status, void *stream);
+
+/* num_forks sequences begin as others: children[i], of length 0 before, gets the first lens[i]
+ * tokens of parents[i] (lens NULL: all of them). It shares the full blocks of these; for the
+ * rest it takes a block, to which the list copies the rows (room: num_forks, at most 16384).
+ * A parent may appear several times, a child once. parents, children, lens: [num_forks] int32
+ * (device). */
+mla_status mla_pool_fork(const mla_shape *shape, const mla_pool *pool, int32_t num_forks, const int32_t *parents,
+                         const int32_t *children, const int32_t *lens, int32_t *copies, int32_t *num_copies,
+                         int32_t *num_free, int32_t *status, void *stream);
+
+/* Blocks in use move to the front of the pool: with num_live of them, the k-th block in use
+ * with an id of num_live or more goes to the k-th free one below, and table entries follow.
+ * With a list too short for all (max_copies) the first max_copies of these move; further calls
+ * move the others.
+ *   num_live   optional [1] int32 (device): blocks in use. */
+mla_status mla_pool_compact(const mla_shape *shape, const mla_pool *pool, int32_t max_copies, int32_t *copies,
+                            int32_t *num_copies, int32_t *num_live, int32_t *status, void *stream);
+
+/* Copies of cached rows, every kind: rows first .. first + rows - 1 of the source block go to the
+ * same rows of the destination block, for the entries 0 .. num_copies[0] - 1 (at most
+ * max_copies) of `copies` as the pool calls list them, in each of `caches` (host array of
+ * num_caches caches of this shape; 64 a launch). No block is the source of one entry and
+ * the destination of another, and none the destination of two over the same rows. An entry out of
+ * range raises a flag in `status` (optional [1] int32 device word) and is skipped. */
+mla_status mla_cache_copy(const mla_shape *shape, const mla_cache *caches, int32_t num_caches, const int32_t *copies,
+                          const int32_t *num_copies, int32_t max_copies, int32_t *status, void *stream);
+
+/* Which of a batch's drafted tokens stand, and the token that follows them, so that the result
+ * is distributed as the target model's own (speculative sampling). What mla_verify's rows lead
+ * to: with q_len = K + 1 (K = num_drafts), row i's probabilities are target row i.
+ *   target_probs  [B, K + 1, vocab] (dtype MLA_DTYPE_F32 or _BF16), rows target_stride elements
+ *                 apart: row i of sequence b is row b * (K + 1) + i. A row's probabilities are in
+ *                 [0, 1] and add up to at most 2 (they need not add up to 1).
+ *   draft_probs   [B, K, vocab], same type, rows draft_stride elements apart: what draft i was
+ *                 drawn from. NULL: the drafts were not drawn but given, with probability 1.
+ *   draft_tokens  [B, K] int32.
+ *   draft_counts  optional [B] int32: sequence b has the drafts 0 .. draft_counts[b] - 1 (0 .. K)
+ *                 alone; negative: the sequence is left out (accepted 0, tokens -1, no change
+ *                 of its length).
+ *   uniform       [B, K + 1] fp32 random numbers in [0, 1]: K decide on the drafts, the last one
+ *                 draws the token.
+ *   seq_lens, new_lens   optional [B] int32 (both or neither, may be the same): new_lens[b] =
+ *                 seq_lens[b] - K + accepted[b], the length that the drafts that stand leave of
+ *                 one that counts all K of them.
+ *   accepted      [B] int32: how many drafts stand.
+ *   tokens        [B, K + 1] int32: the drafts that stand, the token behind them, then -1.
+ *   status        optional [1] int32 device word; flags are OR-ed into it.
+ * Draft i stands if uniform[b, i] * draft_probs[b, i, x_i] < target_probs[b, i, x_i], decided
+ * exactly, and all drafts before it do. Behind n drafts that stand, the weights are
+ * max(target - draft, 0) of row n (target's row alone where no draft was refused, and where
+ * nothing is left of the difference), and the token is the first whose weights up to it add up to
+ * more than uniform[b, K] times the sum of all (for 1: the last one with any weight). Weights are
+ * held as whole multiples of 2^-62 (cut off) and added exactly.
+ * A sequence with a probability, random number, draft or count out of range among those that
+ * are read (the drafts' own, and the row that draws the token), or whose row has no weight
+ * at all, raises a flag (MLA_ERR_VALUE): accepted 0, tokens -1; one whose length is below K
+ * does too (MLA_ERR_BOUNDS), and keeps its length. At most 256 drafts, vocab at most 2^30.
+ *   Source: "GLM-5.2 speculative drafting ..." (leyten/shard PR #5), TL;DR item 1 (drafts
+ *   verified by the target); the rule is that of speculative sampling. */
+mla_status mla_draft_accept(int32_t B, int32_t num_drafts, int32_t vocab, int32_t dtype, const void *target_probs,
+                            int64_t target_stride, const void *draft_probs, int64_t draft_stride,
+                            const int32_t *draft_tokens, const int32_t *draft_counts, const float *uniform,
+                            const int32_t *seq_lens, int32_t *accepted, int32_t *tokens, int32_t *new_lens,
+                            int32_t *status, void *stream);
 
 /* Fold the output rotation of a rotated-INT2 layer into its up-projection, once
  * per layer: W_folded[h] = R^T . W_UV[h], i.e. W_folded[h][i][j] = sum_k R[k][i] *

@@ -26,6 +26,8 @@ MLA_ERR_BOUNDS = -3
 MLA_ERR_WORKSPACE = -4
 MLA_ERR_CUDA = -5
 MLA_ERR_TIMEOUT = -6
+MLA_ERR_FULL = -7
+MLA_ERR_VALUE = -8
 
 MLA_KV_BF16 = 0
 MLA_KV_FP32 = 1
@@ -50,6 +52,7 @@ EXPORTED = (
     "mla_calib_covariance", "mla_calib_projection_energy", "mla_calib_eigh", "mla_calib_eigh_weighted",
     "mla_calib_project_abs", "mla_calib_thresholds",
     "mla_latent_read", "mla_prefill", "mla_prefill_workspace_bytes", "mla_selftest_gave_up",
+    "mla_pool_resize", "mla_pool_fork", "mla_pool_compact", "mla_cache_copy", "mla_draft_accept",
 )
 
 
@@ -68,6 +71,11 @@ class mla_shape(ctypes.Structure):
 class mla_cache(ctypes.Structure):
     _fields_ = [("latent", ctypes.c_void_p), ("codes", ctypes.c_void_p),
                 ("scale_zero", ctypes.c_void_p), ("rope", ctypes.c_void_p)]
+
+
+class mla_pool(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("ref_count", ctypes.c_void_p),
+                ("max_seqs", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32)]
 
 
 _lib = None
@@ -133,6 +141,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mla_prefill.argtypes = [sp, cp, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp, vp, ctypes.c_float, vp, vp, vp,
                                 sz, vp]
     lib.mla_prefill.restype = i32
+    pp = ctypes.POINTER(mla_pool)
+    lib.mla_pool_resize.argtypes = [sp, pp, vp, vp, vp, vp, vp, vp]
+    lib.mla_pool_fork.argtypes = [sp, pp, i32, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.mla_pool_compact.argtypes = [sp, pp, i32, vp, vp, vp, vp, vp]
+    lib.mla_cache_copy.argtypes = [sp, cp, i32, vp, vp, i32, vp, vp]
+    lib.mla_draft_accept.argtypes = [i32, i32, i32, i32, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    for name in ("mla_pool_resize", "mla_pool_fork", "mla_pool_compact", "mla_cache_copy", "mla_draft_accept"):
+        getattr(lib, name).restype = i32
     lib.mla_profile_enable.argtypes = [i32]
     lib.mla_profile_enable.restype = i32
     lib.mla_profile_read.argtypes = [ctypes.POINTER(ctypes.c_double), i32p, i32p]
@@ -367,6 +383,174 @@ def mla_verify(cache: Cache, block_table, seq_lens, q, W_UV, scale: float, out, 
                           _ptr(q), _ptr(W_UV), _ptr(R), float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
                           int(workspace.numel() * workspace.element_size()), _stream(stream))
     _check(code, "mla_verify")
+
+
+# ---------------------------------------------------------------- the pool's books
+
+def _ints(where, device, *tensors) -> None:
+    """Refuses what the library could not see in a pointer: int32, dense, on the device of the call."""
+    import torch
+    for t in tensors:
+        if t is not None and (t.dtype is not torch.int32 or t.get_device() != device or not t.is_contiguous()):
+            raise MlaError(MLA_ERR_INVALID, where)
+
+
+@dataclasses.dataclass(frozen=True)
+class Pool:
+    """The books of a paged cache (see ``mla_pool``): which blocks each sequence holds. One set
+    serves the caches of all layers. Its tensors stay the same for its lifetime."""
+
+    shape: Shape
+    block_table: object      # [max_seqs, max_blocks_per_seq] int32
+    seq_lens: object         # [max_seqs] int32
+    ref_count: object        # [num_blocks] int32
+
+    def __post_init__(self):
+        table, lens, ref = self.block_table, self.seq_lens, self.ref_count
+        device = table.get_device()
+        _ints("Pool", device, table, lens, ref)
+        if table.dim() != 2 or lens.shape != table.shape[:1] or ref.shape != (self.shape.num_blocks,):
+            raise MlaError(MLA_ERR_INVALID, "Pool")
+        c = mla_pool(_ptr(table), _ptr(lens), _ptr(ref), table.shape[0], table.shape[1])
+        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_ref", ctypes.byref(c))
+        object.__setattr__(self, "_device", device)
+
+    @classmethod
+    def allocate(cls, shape: Shape, max_seqs: int, max_blocks_per_seq: int, device="cuda") -> "Pool":
+        """Books of a pool whose blocks are all free."""
+        import torch
+        return cls(shape, torch.full((max_seqs, max_blocks_per_seq), -1, dtype=torch.int32, device=device),
+                   torch.zeros(max_seqs, dtype=torch.int32, device=device),
+                   torch.zeros(shape.num_blocks, dtype=torch.int32, device=device))
+
+
+@dataclasses.dataclass(frozen=True)
+class Caches:
+    """The caches of several layers, all of one shape, for mla_cache_copy. Keeps their pointers:
+    their tensors stay the same for its lifetime."""
+
+    caches: tuple
+
+    def __init__(self, caches):
+        caches = tuple(caches)
+        if not caches or any(c.shape._fields() != caches[0].shape._fields() for c in caches):
+            raise MlaError(MLA_ERR_INVALID, "Caches")
+        s, device = caches[0].shape, None
+        for c in caches:
+            planes = [t for t in (c.latent, c.codes, c.scale_zero, c.rope) if t is not None]
+            device = planes[0].get_device() if planes and device is None else device
+            if (sum(t.numel() * t.element_size() for t in planes) != c.bytes_per_token() * s.num_blocks * s.block_size
+                    or any(t.get_device() != device or not t.is_contiguous() for t in planes)):
+                raise MlaError(MLA_ERR_INVALID, "Caches")
+        object.__setattr__(self, "caches", caches)
+        object.__setattr__(self, "_c", (mla_cache * len(caches))(*(c.c() for c in caches)))
+        object.__setattr__(self, "_device", device)
+
+
+def _current_device() -> int:
+    import torch
+    return torch.cuda.current_device()
+
+
+def _copy_list(where, device, copies, num_copies, room) -> None:
+    _ints(where, device, copies, num_copies)
+    if copies.dim() != 2 or copies.shape[1] != 4 or copies.shape[0] < room or num_copies.numel() < 1:
+        raise MlaError(MLA_ERR_INVALID, where)
+
+
+def mla_pool_resize(pool: Pool, new_lens, copies, num_copies, num_free=None, status=None, stream=None) -> None:
+    """Sequences get the lengths new_lens [max_seqs] (see include/mla.h); copies
+    [>= max_seqs, 4] and num_copies [1] list what mla_cache_copy then has to move."""
+    lib, device = load_library(), _current_device()
+    _ints("mla_pool_resize", device, new_lens, num_free, status, pool.seq_lens)
+    _copy_list("mla_pool_resize", device, copies, num_copies, pool.seq_lens.shape[0])
+    if new_lens.shape != pool.seq_lens.shape:
+        raise MlaError(MLA_ERR_INVALID, "mla_pool_resize")
+    _check(lib.mla_pool_resize(pool.shape._ref(), pool._ref, _ptr(new_lens), _ptr(copies), _ptr(num_copies),
+                               _ptr(num_free), _ptr(status), _stream(stream)), "mla_pool_resize")
+
+
+def mla_pool_fork(pool: Pool, parents, children, copies, num_copies, lens=None, num_free=None, status=None,
+                  stream=None) -> None:
+    """Sequences children [n], empty before, begin as the first lens [n] tokens (None: all) of
+    parents [n] (see include/mla.h); copies [>= n, 4] and num_copies [1] list what mla_cache_copy
+    then has to move."""
+    lib, device = load_library(), _current_device()
+    n = parents.numel()
+    _ints("mla_pool_fork", device, parents, children, lens, num_free, status, pool.seq_lens)
+    _copy_list("mla_pool_fork", device, copies, num_copies, n)
+    if children.numel() != n or (lens is not None and lens.numel() != n):
+        raise MlaError(MLA_ERR_INVALID, "mla_pool_fork")
+    _check(lib.mla_pool_fork(pool.shape._ref(), pool._ref, n, _ptr(parents), _ptr(children), _ptr(lens), _ptr(copies),
+                             _ptr(num_copies), _ptr(num_free), _ptr(status), _stream(stream)), "mla_pool_fork")
+
+
+def mla_pool_compact(pool: Pool, copies, num_copies, num_live=None, status=None, stream=None) -> None:
+    """Blocks in use move to the front of the pool, at most len(copies) of them (see
+    include/mla.h); copies and num_copies [1] list what mla_cache_copy then has to move."""
+    lib, device = load_library(), _current_device()
+    _ints("mla_pool_compact", device, num_live, status, pool.seq_lens)
+    _copy_list("mla_pool_compact", device, copies, num_copies, 0)
+    _check(lib.mla_pool_compact(pool.shape._ref(), pool._ref, copies.shape[0], _ptr(copies), _ptr(num_copies),
+                                _ptr(num_live), _ptr(status), _stream(stream)), "mla_pool_compact")
+
+
+def mla_cache_copy(caches, copies, num_copies, status=None, stream=None) -> None:
+    """The copies that a pool call listed, in every cache of ``caches`` (a Caches, or one Cache;
+    see include/mla.h)."""
+    lib, device = load_library(), _current_device()
+    if isinstance(caches, Cache):
+        caches = Caches((caches,))
+    _copy_list("mla_cache_copy", device, copies, num_copies, 0)
+    _ints("mla_cache_copy", device, status)
+    if caches._device != device:
+        raise MlaError(MLA_ERR_INVALID, "mla_cache_copy")
+    c = caches._c
+    _check(lib.mla_cache_copy(caches.caches[0].shape._ref(), c, len(c), _ptr(copies), _ptr(num_copies),
+                              copies.shape[0], _ptr(status), _stream(stream)), "mla_cache_copy")
+
+
+# ---------------------------------------------------------------- drafts
+
+def mla_draft_accept(target_probs, draft_tokens, uniform, accepted, tokens, draft_probs=None, draft_counts=None,
+                     seq_lens=None, new_lens=None, status=None, stream=None) -> None:
+    """Which of draft_tokens [B, K] stand by target_probs [B, K + 1, vocab] and draft_probs
+    [B, K, vocab] (None: given with certainty) and uniform [B, K + 1] -> accepted [B], tokens
+    [B, K + 1], new_lens [B] (see include/mla.h). The probabilities' last dimension is dense;
+    rows may lie further apart (a slice of a wider vocabulary)."""
+    import torch
+    lib, device = load_library(), _current_device()
+    B, rows, V = target_probs.shape
+    dtype = target_probs.dtype
+    _ints("mla_draft_accept", device, draft_tokens, draft_counts, seq_lens, accepted, tokens, new_lens, status)
+    ok = (dtype in (torch.float32, torch.bfloat16) and target_probs.get_device() == device
+          and draft_tokens.shape == (B, rows - 1) and tokens.shape == (B, rows) and accepted.shape == (B,)
+          and uniform.shape == (B, rows) and uniform.dtype is torch.float32 and uniform.get_device() == device
+          and uniform.is_contiguous())
+    for t in (draft_counts, seq_lens, new_lens):
+        ok = ok and (t is None or t.shape == (B,))
+    p_stride, ok_p = _row_stride(target_probs)
+    q_stride, ok_q = 0, True
+    if draft_probs is not None:
+        q_stride, ok_q = _row_stride(draft_probs)
+        ok = ok and draft_probs.dtype is dtype and draft_probs.get_device() == device and draft_probs.shape == (B, rows - 1, V)
+    if not (ok and ok_p and ok_q):
+        raise MlaError(MLA_ERR_INVALID, "mla_draft_accept")
+    code = lib.mla_draft_accept(B, rows - 1, V, MLA_DTYPE_F32 if dtype is torch.float32 else MLA_DTYPE_BF16,
+                                _ptr(target_probs), p_stride, _ptr(draft_probs), q_stride, _ptr(draft_tokens),
+                                _ptr(draft_counts), _ptr(uniform), _ptr(seq_lens), _ptr(accepted), _ptr(tokens),
+                                _ptr(new_lens), _ptr(status), _stream(stream))
+    _check(code, "mla_draft_accept")
+
+
+def _row_stride(t):
+    """(elements between the rows of t [B, n, V], whether it has rows that evenly apart)."""
+    B, n, V = t.shape
+    s0, s1, s2 = t.stride()
+    if n <= 1:                           # one row a sequence (or none): its stride is the sequences'
+        s1 = s0 if B > 1 and n else V
+    return s1, (s2 == 1 or V <= 1) and s1 >= V and (B <= 1 or n == 0 or s0 == n * s1)
 
 
 def mla_fold_rotation(shape: Shape, R, W_UV, W_folded, stream=None) -> None:

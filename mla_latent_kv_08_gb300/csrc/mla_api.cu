@@ -623,6 +623,164 @@ mla_status mla_latent_append_index(const mla_shape *shape, const mla_cache *cach
     return MLA_OK;
 }
 
+// ---- the pool's books -------------------------------------------------------
+
+// Sequences a pool may have, and forks of one call: prefix sums over them lie in shared memory.
+constexpr int32_t kPoolMax = 16384;
+
+static mla_status pool_params(const mla_shape *s, const mla_pool *pool, int32_t *copies, int32_t room,
+                              int32_t *num_copies, int32_t *left, int32_t *status, PoolParams &p) {
+    mla_status st = check_shape(s);
+    if (st != MLA_OK) return st;
+    if (!pool || !pool->block_table || !pool->seq_lens || !pool->ref_count || pool->max_seqs < 1 ||
+        pool->max_blocks_per_seq < 1 || room < 0 || (room > 0 && !copies) || !aligned16(copies) || !num_copies)
+        return MLA_ERR_INVALID;
+    if (pool->max_seqs > kPoolMax || (int64_t)pool->max_seqs * pool->max_blocks_per_seq > INT32_MAX ||
+        s->num_blocks > INT32_MAX - 256)
+        return MLA_ERR_UNSUPPORTED;
+    memset(&p, 0, sizeof p);
+    p.table = pool->block_table;
+    p.lens = pool->seq_lens;
+    p.ref = pool->ref_count;
+    p.S = pool->max_seqs;
+    p.W = pool->max_blocks_per_seq;
+    p.N = s->num_blocks;
+    p.bs = s->block_size;
+    const int64_t tokens = (int64_t)p.W * p.bs, longest = (int64_t)INT32_MAX - 255;      // as for the attention calls
+    p.cap = (int32_t)(tokens < longest ? tokens : longest);
+    p.copies = (int4 *)copies;
+    p.num_copies = num_copies;
+    p.left = left;
+    p.status = status;
+    return MLA_OK;
+}
+
+mla_status mla_pool_resize(const mla_shape *shape, const mla_pool *pool, const int32_t *new_lens, int32_t *copies,
+                           int32_t *num_copies, int32_t *num_free, int32_t *status, void *stream) {
+    PoolParams p;
+    mla_status st = pool_params(shape, pool, copies, pool ? pool->max_seqs : 0, num_copies, num_free, status, p);
+    if (st != MLA_OK) return st;
+    if (!new_lens) return MLA_ERR_INVALID;
+    p.new_lens = new_lens;
+    if (launch_pool_resize(p, (cudaStream_t)stream) != cudaSuccess) return MLA_ERR_CUDA;
+    prof_kernels(1);
+    return MLA_OK;
+}
+
+mla_status mla_pool_fork(const mla_shape *shape, const mla_pool *pool, int32_t num_forks, const int32_t *parents,
+                         const int32_t *children, const int32_t *lens, int32_t *copies, int32_t *num_copies,
+                         int32_t *num_free, int32_t *status, void *stream) {
+    PoolParams p;
+    mla_status st = pool_params(shape, pool, copies, num_forks, num_copies, num_free, status, p);
+    if (st != MLA_OK) return st;
+    if (num_forks < 1 || !parents || !children) return MLA_ERR_INVALID;
+    if (num_forks > kPoolMax || (int64_t)num_forks * p.W > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+    p.n = num_forks;
+    p.parents = parents;
+    p.children = children;
+    p.fork_lens = lens;
+    if (launch_pool_fork(p, (cudaStream_t)stream) != cudaSuccess) return MLA_ERR_CUDA;
+    prof_kernels(1);
+    return MLA_OK;
+}
+
+mla_status mla_pool_compact(const mla_shape *shape, const mla_pool *pool, int32_t max_copies, int32_t *copies,
+                            int32_t *num_copies, int32_t *num_live, int32_t *status, void *stream) {
+    PoolParams p;
+    mla_status st = pool_params(shape, pool, copies, max_copies, num_copies, num_live, status, p);
+    if (st != MLA_OK) return st;
+    p.n = max_copies;
+    if (launch_pool_compact(p, (cudaStream_t)stream) != cudaSuccess) return MLA_ERR_CUDA;
+    prof_kernels(1);
+    return MLA_OK;
+}
+
+mla_status mla_cache_copy(const mla_shape *shape, const mla_cache *caches, int32_t num_caches, const int32_t *copies,
+                          const int32_t *num_copies, int32_t max_copies, int32_t *status, void *stream) {
+    mla_status st = check_shape(shape);
+    if (st != MLA_OK) return st;
+    if (!caches || num_caches < 1 || max_copies < 0 || !num_copies || (max_copies > 0 && !copies) || !aligned16(copies))
+        return MLA_ERR_INVALID;
+    if ((int64_t)max_copies * shape->block_size > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+    for (int32_t i = 0; i < num_caches; ++i) {           // all of them before anything is launched
+        ReadParams r;
+        st = read_params(shape, caches + i, r);
+        if (st != MLA_OK) return st;
+    }
+    if (max_copies == 0) return MLA_OK;
+    const ShapeArgs s = shape_args(shape);
+    const bool dense = s.kind == MLA_KV_BF16 || s.kind == MLA_KV_FP32;
+    CopyParams p;
+    memset(&p, 0, sizeof p);
+    if (dense) {
+        p.row_bytes[0] = s.E() * (s.kind == MLA_KV_FP32 ? 4 : 2);
+    } else if (is_mx(s.kind)) {
+        p.row_bytes[0] = s.r;
+        p.row_bytes[1] = s.r / 32;
+        p.row_bytes[2] = 2 * s.dR;
+    } else {
+        p.row_bytes[0] = s.QD() / 4;
+        p.row_bytes[1] = s.QD() / s.gs * 4;
+        p.row_bytes[2] = s.kind == MLA_KV_INT2_ROT ? 2 * s.dR : 0;
+    }
+    p.bs = s.bs;
+    p.num_blocks = s.num_blocks;
+    p.max_copies = max_copies;
+    p.copies = (const int4 *)copies;
+    p.num_copies = num_copies;
+    p.status = status;
+    for (int32_t i0 = 0; i0 < num_caches; i0 += kCopyLayers) {
+        const int32_t n = num_caches - i0 < kCopyLayers ? num_caches - i0 : kCopyLayers;
+        for (int32_t i = 0; i < n; ++i) {
+            const mla_cache &c = caches[i0 + i];
+            p.plane[i][0] = (uint8_t *)(dense ? c.latent : c.codes);
+            p.plane[i][1] = dense ? nullptr : (uint8_t *)c.scale_zero;
+            p.plane[i][2] = dense ? nullptr : (uint8_t *)c.rope;
+        }
+        if (launch_copy(p, n, (cudaStream_t)stream) != cudaSuccess) return MLA_ERR_CUDA;
+        prof_kernels(1);
+    }
+    return MLA_OK;
+}
+
+mla_status mla_draft_accept(int32_t B, int32_t num_drafts, int32_t vocab, int32_t dtype, const void *target_probs,
+                            int64_t target_stride, const void *draft_probs, int64_t draft_stride,
+                            const int32_t *draft_tokens, const int32_t *draft_counts, const float *uniform,
+                            const int32_t *seq_lens, int32_t *accepted, int32_t *tokens, int32_t *new_lens,
+                            int32_t *status, void *stream) {
+    if (B < 1 || num_drafts < 0 || vocab < 1 || (dtype != MLA_DTYPE_F32 && dtype != MLA_DTYPE_BF16))
+        return MLA_ERR_INVALID;
+    if (!target_probs || target_stride < vocab || (draft_probs && draft_stride < vocab) || !uniform || !accepted ||
+        !tokens || (num_drafts > 0 && !draft_tokens) || (!seq_lens) != (!new_lens))
+        return MLA_ERR_INVALID;
+    // outputs apart from the inputs and from one another, but for new_lens, which may be seq_lens
+    const void *outs[3] = {accepted, tokens, new_lens}, *ins[5] = {draft_tokens, draft_counts, uniform, status, seq_lens};
+    for (int i = 0; i < 3; ++i)
+        for (int j = 0; outs[i] && j < (i == 2 ? 4 : 5); ++j)
+            if (outs[i] == ins[j]) return MLA_ERR_INVALID;
+    if (accepted == tokens || accepted == new_lens || tokens == new_lens) return MLA_ERR_INVALID;
+    if (num_drafts > 256 || vocab > (1 << 30) || B > (1 << 26)) return MLA_ERR_UNSUPPORTED;
+    AcceptParams p;
+    p.B = B;
+    p.K = num_drafts;
+    p.V = vocab;
+    p.p = target_probs;
+    p.q = num_drafts > 0 ? draft_probs : nullptr;
+    p.p_stride = target_stride;
+    p.q_stride = draft_stride;
+    p.x = draft_tokens;
+    p.counts = draft_counts;
+    p.u = uniform;
+    p.lens = seq_lens;
+    p.accepted = accepted;
+    p.tokens = tokens;
+    p.new_lens = new_lens;
+    p.status = status;
+    if (launch_accept(p, dtype == MLA_DTYPE_BF16, (cudaStream_t)stream) != cudaSuccess) return MLA_ERR_CUDA;
+    prof_kernels(1);
+    return MLA_OK;
+}
+
 mla_status mla_decode(const mla_shape *shape, const mla_cache *cache, const int32_t *block_table,
                       int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t B, const void *q,
                       const void *W_UV, const float *R, float scale, void *out, float *lse, void *workspace,
@@ -642,6 +800,8 @@ mla_status mla_verify(const mla_shape *shape, const mla_cache *cache, const int3
 static mla_status flags_to_status(int32_t f) {
     if (f & FLAG_TIMEOUT) return MLA_ERR_TIMEOUT;
     if (f & (FLAG_BAD_BLOCK | FLAG_BAD_LENGTH)) return MLA_ERR_BOUNDS;
+    if (f & FLAG_FULL) return MLA_ERR_FULL;
+    if (f & FLAG_BAD_VALUE) return MLA_ERR_VALUE;
     return MLA_OK;
 }
 
@@ -669,6 +829,8 @@ const char *mla_status_string(mla_status s) {
         case MLA_ERR_WORKSPACE: return "workspace too small";
         case MLA_ERR_CUDA: return "CUDA launch or runtime error";
         case MLA_ERR_TIMEOUT: return "bounded device wait gave up (device flag)";
+        case MLA_ERR_FULL: return "too few free cache blocks (device flag)";
+        case MLA_ERR_VALUE: return "probability, random number or drafted token out of range (device flag)";
     }
     return "unknown status";
 }

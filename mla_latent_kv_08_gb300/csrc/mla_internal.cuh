@@ -17,6 +17,8 @@ enum : int32_t {
     FLAG_BAD_BLOCK = 1,      // a block id outside [0, num_blocks) or a logical block past the table
     FLAG_BAD_LENGTH = 2,     // a sequence length outside [q_len, max_blocks * block_size], or above 2^31 - 256
     FLAG_TIMEOUT = 4,        // a bounded wait gave up
+    FLAG_FULL = 8,           // fewer free blocks than a call has to take
+    FLAG_BAD_VALUE = 16,     // a probability, a random number or a drafted token out of range
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -184,6 +186,44 @@ struct PrefillParams {
     float *lse;
 };
 
+// The pool's books (mla_pool_*).
+struct PoolParams {
+    int32_t *table;              // [S, W]
+    int32_t *lens;               // [S]
+    int32_t *ref;                // [N]
+    int32_t S, W, N, bs;
+    int32_t cap;                 // the longest sequence
+    const int32_t *new_lens;     // resize: [S]
+    const int32_t *parents, *children, *fork_lens;      // fork: [n]; fork_lens nullptr: the parents' lengths
+    int32_t n;                   // fork: how many; compact: entries that the list has room for
+    int4 *copies;                // (src, dst, first row, rows)
+    int32_t *num_copies;
+    int32_t *left;               // free blocks after the call (compact: blocks in use), or nullptr
+    int32_t *status;
+};
+
+// mla_cache_copy: up to kCopyLayers caches a launch, up to three arrays each.
+constexpr int kCopyLayers = 64;
+struct CopyParams {
+    uint8_t *plane[kCopyLayers][3];
+    int32_t row_bytes[3];        // 0: no such array
+    int32_t bs, num_blocks, max_copies;
+    const int4 *copies;
+    const int32_t *num_copies;
+    int32_t *status;
+};
+
+// mla_draft_accept
+struct AcceptParams {
+    int32_t B, K, V;
+    const void *p, *q;           // q nullptr: the drafts are certain
+    int64_t p_stride, q_stride;
+    const int32_t *x, *counts;
+    const float *u;
+    const int32_t *lens;
+    int32_t *accepted, *tokens, *new_lens, *status;
+};
+
 // ---- launchers (defined in mla_simt.cu) ------------------------------------
 // Programmatic dependent launch. A kernel launched with launch_pdl may start while
 // the previous kernel of the stream is still running; it calls pdl_trigger() on entry
@@ -223,6 +263,13 @@ cudaError_t launch_append_index(const AppendParams &p, cudaStream_t st);
 cudaError_t launch_fold_rotation(const ShapeArgs &s, const float *R, const void *W_UV, void *W_folded, cudaStream_t st);
 // ---- reading the cache back (defined in mla_read.cu) ------------------------
 cudaError_t launch_read(const ReadParams &p, cudaStream_t st);
+// ---- the pool's books, copies of cached rows (mla_pool.cu, mla_copy.cu) --------
+cudaError_t launch_pool_resize(const PoolParams &p, cudaStream_t st);
+cudaError_t launch_pool_fork(const PoolParams &p, cudaStream_t st);
+cudaError_t launch_pool_compact(const PoolParams &p, cudaStream_t st);
+cudaError_t launch_copy(const CopyParams &p, int32_t layers, cudaStream_t st);
+// ---- which drafted tokens stand (defined in mla_accept.cu) -------------------
+cudaError_t launch_accept(const AcceptParams &p, bool bf16, cudaStream_t st);
 // ---- prefill on the CUDA cores (defined in mla_prefill.cu) ------------------
 cudaError_t launch_prefill_plan(const PrefillParams &p, cudaStream_t st);
 cudaError_t launch_prefill_simt(const PrefillParams &p, cudaStream_t st);
@@ -264,6 +311,36 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
+}
+// Block-wide exclusive scan of one value per thread (blockDim.x a multiple of 32, at
+// most 1024); s_warp holds 33 values.
+template <typename T>
+__device__ __forceinline__ T block_exclusive_scan(T v, T *s_warp, T &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    T incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        T u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+        T x = lane < (int)(blockDim.x >> 5) ? s_warp[lane] : (T)0;
+        T w = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            T u = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += u;
+        }
+        s_warp[lane] = w - x;          // exclusive warp offsets
+        if (lane == 31) s_warp[32] = w;
+    }
+    __syncthreads();
+    const T excl = s_warp[warp] + incl - v;
+    total = s_warp[32];
+    __syncthreads();
+    return excl;
 }
 // Four bf16 values (8 bytes, memory order) widened to fp32.
 __device__ __forceinline__ float4 bf16x4_to_float4(uint2 u) {

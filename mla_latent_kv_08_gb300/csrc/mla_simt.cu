@@ -28,36 +28,6 @@ namespace mla {
 // ============================================================================
 constexpr int kPlanTile = 64;      // plan_tile when the caller leaves it 0
 
-// Block-wide exclusive scan of one int per thread (blockDim.x a multiple of 32, at
-// most 1024).
-__device__ __forceinline__ int block_exclusive_scan(int v, int *s_warp, int &total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int incl = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        int u = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += u;
-    }
-    if (lane == 31) s_warp[warp] = incl;
-    __syncthreads();
-    if (warp == 0) {
-        int x = lane < (int)(blockDim.x >> 5) ? s_warp[lane] : 0;
-        int w = x;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            int u = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += u;
-        }
-        s_warp[lane] = w - x;          // exclusive warp offsets
-        if (lane == 31) s_warp[32] = w;
-    }
-    __syncthreads();
-    const int excl = s_warp[warp] + incl - v;
-    total = s_warp[32];
-    __syncthreads();
-    return excl;
-}
-
 #ifdef MLA_TRACE
 // planner timestamps (globaltimer): entry, after the grid dependency wait, end
 __device__ unsigned long long g_plan_time[3];

@@ -1,0 +1,293 @@
+"""mla_draft_accept against the oracle, which decides in whole numbers of any length: outputs
+are whole numbers and have to be equal."""
+import math
+
+import numpy as np
+import pytest
+
+from oracle import upkeep
+
+pytestmark = pytest.mark.gpu
+
+
+def _case(seed, B, K, V, dtype="fp32", sure=False, ragged=False, near=0.8, device="cuda"):
+    import torch
+    g = torch.Generator().manual_seed(seed)
+    dt = torch.float32 if dtype == "fp32" else torch.bfloat16
+    logits = torch.randn((B, K + 1, V), generator=g) * 3
+    q = torch.softmax(logits[:, :K] + near * torch.randn((B, K, V), generator=g), -1).to(dt)
+    x = torch.multinomial(q.float().view(B * K, V), 1, generator=g).view(B, K).int() if K else torch.empty((B, 0), dtype=torch.int32)
+    c = dict(p=torch.softmax(logits, -1).to(dt), q=None if sure or not K else q, x=x, u=torch.rand((B, K + 1), generator=g),
+             counts=torch.randint(-1, K + 1, (B,), generator=g).int() if ragged else None,
+             lens=torch.randint(K, 9000, (B,), generator=g).int())
+    return {k: v.to(device) if v is not None else None for k, v in c.items()}
+
+
+def _outputs(B, K, device="cuda"):
+    import torch
+    return [torch.full(s, -7, dtype=torch.int32, device=device) for s in ((B,), (B, K + 1), (B,))] + [
+        torch.zeros(1, dtype=torch.int32, device=device)]
+
+
+def _call(c, outs, **kw):
+    import mla_latent_kv_08_gb300 as mla
+    accepted, tokens, new_lens, status = outs
+    mla.mla_draft_accept(c["p"], c["x"], c["u"], accepted, tokens, draft_probs=c["q"], draft_counts=c["counts"],
+                         seq_lens=c["lens"], new_lens=new_lens if c["lens"] is not None else None, status=status, **kw)
+
+
+def _floats(t):
+    return None if t is None else t.double().cpu().numpy().tolist()
+
+
+def _want(c):
+    ints = {k: None if c[k] is None else c[k].cpu().numpy().tolist() for k in ("x", "counts", "lens")}
+    return upkeep.accept(_floats(c["p"]), _floats(c["q"]), ints["x"], _floats(c["u"]), ints["counts"], ints["lens"])
+
+
+def _check(c, outs):
+    want = _want(c)
+    accepted, tokens, new_lens, status = (t.cpu().numpy() for t in outs)
+    np.testing.assert_array_equal(accepted, [w[1] for w in want])
+    np.testing.assert_array_equal(tokens, np.array([w[2] for w in want]).reshape(tokens.shape))
+    if c["lens"] is not None:
+        np.testing.assert_array_equal(new_lens, [w[3] for w in want])
+    assert int(status[0]) == int(np.bitwise_or.reduce([w[0] for w in want]))
+
+
+@pytest.mark.parametrize("sure", [False, True])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("B,K,V", [(1, 0, 1), (1, 1, 1), (3, 2, 2), (5, 4, 31), (2, 3, 32), (2, 7, 33), (4, 1, 511), (1, 5, 4097),
+                                   (7, 3, 1000), (33, 2, 257), (2, 8, 16385), (1, 256, 40), (300, 1, 65)])
+def test_against_the_oracle(gpu_lib, B, K, V, dtype, sure):
+    for ragged in (False, True):
+        c = _case(B * 1000 + K * 10 + V, B, K, V, dtype, sure, ragged)
+        outs = _outputs(B, K)
+        _call(c, outs)
+        _check(c, outs)
+
+
+@pytest.mark.parametrize("B", [1, 2, 5, 9, 20, 40, 80, 200])
+def test_every_split_of_a_row(gpu_lib, B):
+    """The rows of few sequences are split over more CTAs."""
+    for dtype in ("fp32", "bf16"):
+        c = _case(B, B, 1, 3001, dtype, near=4.0)            # most drafts are refused
+        outs = _outputs(B, 1)
+        _call(c, outs)
+        _check(c, outs)
+
+
+def test_one_token_has_everything(gpu_lib):
+    """The token wherever in the row it is, from every random number."""
+    import torch
+    V = 5000
+    at = [0, 1, 31, 32, 255, 256, 511, 512, 1023, 2500, 4095, 4096, 4998, 4999]
+    p = torch.zeros(len(at), 1, V)
+    for b, i in enumerate(at):
+        p[b, 0, i] = 0.7
+    for v in (0.0, 2.0 ** -30, 0.5, 1 - 2.0 ** -24, 1.0):
+        c = dict(p=p.cuda(), q=None, x=torch.empty((len(at), 0), dtype=torch.int32, device="cuda"),
+                 u=torch.full((len(at), 1), v, device="cuda"), counts=None, lens=None)
+        outs = _outputs(len(at), 0)
+        _call(c, outs)
+        np.testing.assert_array_equal(outs[1].cpu().numpy()[:, 0], at)
+        _check(c, outs)
+
+
+def test_borders(gpu_lib):
+    """Sums that the random number meets exactly: the token behind the border. Tokens without
+    weight are never drawn."""
+    import torch
+    p = torch.tensor([0.0, 0.25, 0.0, 0.25, 0.5, 0.0]).expand(6, 1, 6).contiguous()
+    u = torch.tensor([0.0, 0.25 - 2.0 ** -26, 0.25, 0.5 - 2.0 ** -25, 0.5, 1.0])
+    c = dict(p=p.cuda(), q=None, x=torch.empty((6, 0), dtype=torch.int32, device="cuda"), u=u.view(6, 1).cuda(), counts=None, lens=None)
+    outs = _outputs(6, 0)
+    _call(c, outs)
+    assert outs[1].cpu().view(-1).tolist() == [1, 1, 3, 3, 4, 4]
+    _check(c, outs)
+
+
+def test_an_equal_product_is_refused(gpu_lib):
+    """u q = p exactly, and one unit of u to either side."""
+    import torch
+    B, p, q = 3, 0.375, 0.75
+    c = _case(5, B, 1, 8)
+    c["p"], c["q"] = torch.full((B, 2, 8), 0.09, device="cuda"), torch.full((B, 1, 8), 0.03, device="cuda")
+    c["x"].fill_(2)
+    c["p"][:, 0, 2], c["q"][:, 0, 2] = p, q
+    c["u"][:, 0] = torch.tensor([np.nextafter(np.float32(0.5), np.float32(0)), 0.5, np.nextafter(np.float32(0.5), np.float32(1))])
+    outs = _outputs(B, 1)
+    _call(c, outs)
+    assert outs[0].tolist() == [1, 0, 0]
+    _check(c, outs)
+
+
+def test_nothing_left_of_the_difference(gpu_lib):
+    """A refused draft (certain to be: its p is 0) where p is nowhere above q: p itself."""
+    import torch
+    c = _case(6, 4, 2, 300)
+    c["q"][:, 0] = c["p"][:, 0]
+    c["x"][:, 0] = 7
+    c["p"][:, 0, 7] = 0
+    c["p"][1, 0] = 0
+    c["p"][1, 0, 33] = 1e-30                                 # below 2^-62: no weight at all, an error
+    c["q"][1, 0] = 0.001
+    outs = _outputs(4, 2)
+    _call(c, outs)
+    assert outs[0].tolist() == [0, 0, 0, 0] and int(outs[3]) == upkeep.VALUE and outs[1][1].tolist() == [-1] * 3
+    _check(c, outs)
+
+
+def test_small_and_denormal_weights(gpu_lib):
+    import torch
+    c = _case(7, 6, 1, 900)
+    c["p"] = torch.exp2(torch.randint(-70, -10, (6, 2, 900), device="cuda").float()) * (1 + torch.rand(6, 2, 900, device="cuda"))
+    c["p"][0, :, ::3] = 1e-42
+    c["q"] = torch.exp2(torch.randint(-70, -10, (6, 1, 900), device="cuda").float())
+    c["u"][:, 0] = 0.9
+    outs = _outputs(6, 1)
+    _call(c, outs)
+    _check(c, outs)
+
+
+@pytest.mark.parametrize("what", ["nan", "inf", "negative", "above one", "sum", "token", "low token", "count", "u", "u nan", "last u", "q", "empty", "length"])
+def test_values_out_of_range(gpu_lib, what):
+    """The sequence that has them is refused with a flag; the others are as ever."""
+    import torch
+    c = _case(8, 5, 3, 700)
+    c["u"][:, :3] = 1.0                                      # the first draft whose p <= q is refused
+    c["x"][2] = 11
+    c["p"][2, :, 11], c["q"][2, :, 11] = 0.001, 0.002        # of sequence 2, the first
+    bad = {"nan": math.nan, "inf": math.inf, "negative": -1e-9, "above one": 1.5}
+    if what in bad:
+        c["p"][2, 0, 650] = bad[what]
+    elif what == "sum":
+        c["p"][2, 0, 100:103] = 0.9
+    elif what in ("token", "low token"):
+        c["x"][2, 2] = 700 if what == "token" else -1
+    elif what == "count":
+        c["counts"] = torch.tensor([3, 2, 4, 0, -1], dtype=torch.int32, device="cuda")
+    elif what in ("u", "u nan"):
+        c["u"][2, 1] = 1.0001 if what == "u" else math.nan
+    elif what == "last u":
+        c["u"][2, 3] = -0.25
+    elif what == "q":
+        c["q"][2, 0, 0] = math.nan
+    elif what == "empty":
+        c["p"][2, 0] = 0
+    else:
+        c["lens"][2] = 2
+    outs = _outputs(5, 3)
+    _call(c, outs)
+    assert outs[1][2].tolist() == [-1] * 4 and int(outs[0][2]) == 0
+    assert int(outs[3]) == (upkeep.BOUNDS if what == "length" else upkeep.VALUE)
+    _check(c, outs)
+    import mla_latent_kv_08_gb300 as mla
+    assert mla.mla_read_status_word(outs[3])[0] == (mla.MLA_ERR_BOUNDS if what == "length" else mla.MLA_ERR_VALUE)
+
+
+def test_what_is_not_read_does_not_count(gpu_lib):
+    """NaN in rows that draw nothing, in drafts behind a sequence's count, in its random numbers
+    there, and in the vocabulary's padding."""
+    import torch
+    c = _case(9, 4, 4, 640)
+    c["counts"] = torch.tensor([2, 0, -1, 1], dtype=torch.int32, device="cuda")
+    c["u"][:, :4] = 0.0
+    for b, n in enumerate([2, 0, 0, 1]):                     # all stand: row n alone is read as a whole
+        for i in range(5):
+            if i != n:
+                keep = c["p"][b, i, c["x"][b, i]].clone() if i < n else None
+                c["p"][b, i] = math.nan
+                if keep is not None:
+                    c["p"][b, i, c["x"][b, i]] = keep
+        c["x"][b, n:] = 10 ** 6
+        c["u"][b, n:4] = math.nan
+    c["p"][2] = math.nan
+    c["u"][2] = math.nan
+    wide = torch.full((4, 5, 700), math.nan, device="cuda")
+    wide[:, :, :640] = c["p"]
+    c["p"] = wide[:, :, :640]
+    outs = _outputs(4, 4)
+    _call(c, outs)
+    assert outs[0].tolist() == [2, 0, 0, 1] and int(outs[3]) == 0
+    _check(c, outs)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_rows_of_a_wider_vocabulary(gpu_lib, dtype):
+    import torch
+    c = _case(10, 6, 3, 1001, dtype)
+    for k, pad in (("p", 1100), ("q", 1023)):
+        wide = torch.full((*c[k].shape[:2], pad), 0.5, dtype=c[k].dtype, device="cuda")
+        wide[:, :, 5:1006] = c[k]
+        c[k] = wide[:, :, 5:1006]
+    outs = _outputs(6, 3)
+    _call(c, outs)
+    _check(c, outs)
+
+
+def test_lengths_in_place_and_left_out(gpu_lib):
+    import torch
+    c = _case(11, 40, 3, 400, ragged=True)
+    want = _want(c)
+    outs = _outputs(40, 3)
+    outs[2] = c["lens"]                                      # the lengths themselves
+    _call(c, outs)
+    np.testing.assert_array_equal(c["lens"].cpu().numpy(), [w[3] for w in want])
+    np.testing.assert_array_equal(outs[0].cpu().numpy(), [w[1] for w in want])
+    c["lens"] = None
+    _call(c, outs)
+    np.testing.assert_array_equal(outs[0].cpu().numpy(), [w[1] for w in want])
+
+
+def test_captured_twice_and_on_two_streams(gpu_lib):
+    """Two graphs of different sizes replayed in turn over other inputs, then both calls at once."""
+    import torch
+    a, b = _case(12, 3, 4, 3000), _case(13, 50, 2, 700, "bf16", sure=True)
+    oa, ob = _outputs(3, 4), _outputs(50, 2)
+    graphs = []
+    for c, o in ((a, oa), (b, ob)):
+        _call(c, o)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            _call(c, o)
+        graphs.append(g)
+    for seed in (14, 15):
+        for c, n in ((a, _case(seed, 3, 4, 3000)), (b, _case(seed, 50, 2, 700, "bf16", sure=True))):
+            for k in c:
+                if c[k] is not None:
+                    c[k].copy_(n[k])
+        for o in (oa, ob):
+            for t in o[:3]:
+                t.fill_(-9)
+        torch.cuda.synchronize()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        _check(a, oa)
+        _check(b, ob)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(20):
+        _call(a, oa, stream=s1)
+        _call(b, ob, stream=s2)
+    torch.cuda.synchronize()
+    _check(a, oa)
+    _check(b, ob)
+
+
+def test_the_binding_refuses(gpu_lib):
+    import mla_latent_kv_08_gb300 as mla
+    import torch
+    c = _case(16, 3, 2, 50)
+    o = _outputs(3, 2)
+    good = dict(c)
+    for k, v in (("p", c["p"].double()), ("p", c["p"].half()), ("p", c["p"].cpu()), ("p", c["p"][:, :, ::2]), ("p", c["p"][:2]),
+                 ("q", c["q"].bfloat16()), ("q", c["q"][:, :1]), ("x", c["x"].long()), ("x", c["x"][:, :1]),
+                 ("u", c["u"].double()), ("u", c["u"][:, :2]), ("u", c["u"].T.contiguous().T), ("counts", c["lens"][:2]),
+                 ("lens", c["lens"].cpu())):
+        with pytest.raises(mla.MlaError) as e:
+            _call({**good, k: v}, o)
+        assert e.value.code == mla.MLA_ERR_INVALID, k
+    torch.cuda.synchronize()
+    assert all(int(t.max()) == -7 for t in o[:3])
