@@ -500,8 +500,9 @@ mla_status mla_cache_copy(const mla_shape *shape, const mla_cache *caches, int32
  * exactly, and all drafts before it do. Behind n drafts that stand, the weights are
  * max(target - draft, 0) of row n (target's row alone where no draft was refused, and where
  * nothing is left of the difference), and the token is the first whose weights up to it add up to
- * more than uniform[b, K] times the sum of all (for 1: the last one with any weight). Weights are
- * held as whole multiples of 2^-62 (cut off) and added exactly.
+ * more than uniform[b, K] times the sum of all (for 1: the last one with any weight).
+ * Probabilities count as whole multiples of 2^-46 (exact from 2^-23 on, rounded to nearest below;
+ * what is below 2^-47 is never drawn), and are added exactly.
  * A sequence with a probability, random number, draft or count out of range among those that
  * are read (the drafts' own, and the row that draws the token), or whose row has no weight
  * at all, raises a flag (MLA_ERR_VALUE): accepted 0, tokens -1; one whose length is below K

@@ -4,15 +4,23 @@
 // fp64, so this decision is the definition's own. Behind the n drafts that stand, the next
 // token has the weights w_j = max(p_n(j) - q_n(j), 0) (p_n(j) where all drafts stood), and is
 // the first j whose sum w_0 + .. + w_j is above v times the sum of all. Where that is depends
-// on sums over the whole vocabulary: weights are held as whole numbers of 2^-62 (a
-// probability's 24 bits shifted; what is below 2^-62 is cut off) and added in 64 bits, so
-// that a sum is the same in any order and every split of a row gives the same token.
+// on sums over the whole vocabulary: probabilities are held as whole numbers of 2^-46 (exact
+// from 2^-23 on, rounded to nearest below) and added in 64 bits, so that a sum is the same in
+// any order, and every split of a row gives the same token. Over 131072 tokens the roundings
+// move a border by about 2^-39 of the row's weight.
 //
-// A row of target and draft probabilities is read once, by a warp a contiguous part; then
-// the part that holds the token is read again.
+// A row of target and draft probabilities is read once, by a warp a contiguous part, split
+// over a cluster of CTAs; then the part that holds the token is read again. A call is bound by
+// its chain of dependent steps (drafts, their probabilities, the row, the cluster's sums, the
+// token: 4.7 us for 2000 tokens) and by loads in flight: a lane has 32 of each row. 32 sequences
+// of 131072 tokens: 10.9 us, 3.1 TB/s over all of it (8 loads of each row: 15.7; 78 us with a
+// CTA a sequence and conversions to 64 bits in hardware). One sequence of 32000: 5.3 us (19.5);
+// 64 of 50257 in bf16, drafts given: 7.7 us (19.4).
 #include "mla_internal.cuh"
 
 #include <cooperative_groups.h>
+
+#include <utility>
 
 namespace cg = cooperative_groups;
 
@@ -20,50 +28,88 @@ namespace mla {
 namespace {
 
 typedef unsigned long long u64;
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kUnroll = 8;                   // loads of a lane in flight, of each row
+constexpr int kThreads = 256, kWarps = kThreads / 32;   // (512: 5.3 us at 2000 tokens, 1024: 7.3)
+constexpr int kMaxCluster = 16;
+constexpr int kGroup = 1024;                 // tokens that a warp takes at a time
 
 enum Weights { kPlain, kRest, kWithout };    // p; max(p - q, 0); p without one token
 
 __device__ __forceinline__ float widen(float v) { return v; }
 __device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ u64 units(float v) { return __float2ull_rz(v * 0x1p62f); }
 __device__ __forceinline__ bool is_probability(float v) { return v >= 0.f && v <= 1.f; }
 
+// v in [0, 1] as round(v 2^46) = 2^23 hi + lo (and a constant each): v + 1 has the multiples of 2^-23
+// as its last bits, and what that rounding leaves, exact, plus 1.5 2^-23 those of 2^-46. Four
+// additions; shifting the 24 bits of v to their place by the exponent took three times as long.
+struct Fixed {
+    int hi, lo;
+};
+constexpr int kHi = 0x3f800000, kLo = 0x34400000;        // the bits of 1 and of 1.5 2^-23
+__device__ __forceinline__ Fixed fixed(float v) {
+    const float a = __fadd_rn(v, 1.f), rest = __fsub_rn(v, __fsub_rn(a, 1.f));
+    return {__float_as_int(a), __float_as_int(__fadd_rn(rest, __int_as_float(kLo)))};
+}
+__device__ __forceinline__ u64 units(int hi, int lo) { return (u64)(((long long)hi << 23) + lo); }
+
+// A weight, without its constants: max(p - q, 0), p, or nothing.
 template <Weights W, typename T>
-__device__ __forceinline__ u64 weight(T p, T q, bool out) {
-    if (W == kWithout && out) return 0;
-    const u64 a = units(widen(p));
-    if (W != kRest) return a;
-    const u64 b = units(widen(q));
-    return a > b ? a - b : 0;
+__device__ __forceinline__ Fixed weight(T p, T q, bool out) {
+    const Fixed a = fixed(widen(p));
+    if (W == kRest) {
+        const Fixed b = fixed(widen(q));
+        return widen(p) > widen(q) ? Fixed{a.hi - b.hi, a.lo - b.lo} : Fixed{0, 0};
+    }
+    return W == kWithout && out ? Fixed{0, 0} : Fixed{a.hi - kHi, a.lo - kLo};
 }
 
+// What a CTA found in its part of a row.
+struct Part {
+    u64 sum;
+    float p;                                 // sum of the target's probabilities
+    int bad;
+};
 struct Shared {
-    u64 warp[kWarps], scan[33], sum;
-    float warp_p[kWarps], sum_p;             // of the target's probabilities
+    Part all[2][kMaxCluster];                // of every CTA of the cluster, by pass
+    u64 warp[kWarps], scan[33];
+    float warp_p[kWarps];
     int bad, n;
 };
 
-// A warp's sums over [lo, hi) of a row.
+// A warp's sums over [lo, hi) of a row; `bad`: this lane saw what is no probability. In the
+// order of their bits as whole numbers, negative values and NaN come behind 1; only -0 has to
+// be told from them, where there is anything to tell.
 template <Weights W, typename T>
 __device__ __forceinline__ u64 sum_part(const T *p, const T *q, int x, int lo, int hi, float &sum_p, bool &bad) {
     u64 s = 0;
-    for (int i0 = lo + (threadIdx.x & 31); i0 < hi; i0 += 32 * kUnroll) {
-        T a[kUnroll], b[kUnroll];
+    int hi_sum = 0, lo_sum = 0;              // of a few weights
+    uint32_t most = 0;
+    const auto add = [&](T a, T b, int i) {
+        const Fixed w = weight<W>(a, b, i == x);
+        hi_sum += w.hi;
+        lo_sum += w.lo;
+        sum_p += widen(a);
+        most = max(most, max(__float_as_uint(widen(a)), __float_as_uint(widen(b))));
+    };
+    int i0 = lo + (threadIdx.x & 31);
+    for (; i0 + kGroup - 32 < hi; i0 += kGroup) {
+        T a[kGroup / 32], b[kGroup / 32];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            const bool in = i0 + 32 * k < hi;
-            a[k] = in ? p[i0 + 32 * k] : (T)0.f;
-            b[k] = W == kRest && in ? q[i0 + 32 * k] : (T)0.f;
+        for (int k = 0; k < kGroup / 32; ++k) {
+            a[k] = p[i0 + 32 * k];
+            b[k] = W == kRest ? q[i0 + 32 * k] : (T)0.f;
         }
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            s += weight<W>(a[k], b[k], i0 + 32 * k == x);
-            sum_p += widen(a[k]);
-            bad |= !is_probability(widen(a[k])) || !is_probability(widen(b[k]));
-        }
+        for (int k = 0; k < kGroup / 32; ++k) add(a[k], b[k], i0 + 32 * k);
+        s += units(hi_sum, lo_sum);
+        hi_sum = lo_sum = 0;
     }
+#pragma unroll 4
+    for (; i0 < hi; i0 += 32) add(p[i0], W == kRest ? q[i0] : (T)0.f, i0);
+    s += units(hi_sum, lo_sum);
+    bad = false;
+    if (most > 0x3f800000u)
+        for (int i = lo + (threadIdx.x & 31); i < hi; i += 32)
+            bad |= !is_probability(widen(p[i])) || (W == kRest && !is_probability(widen(q[i])));
     return s;
 }
 
@@ -72,18 +118,26 @@ __device__ __forceinline__ u64 sum_part(const T *p, const T *q, int x, int lo, i
 template <Weights W, typename T>
 __device__ __forceinline__ void find_token(const T *p, const T *q, int x, int lo, int hi, u64 base, u64 t, u64 *scan,
                                            int32_t *token) {
-    const int each = (hi - lo + kThreads - 1) / kThreads;
-    const int a = min(hi, lo + (int)threadIdx.x * each), e = min(hi, a + each);
-    u64 s = 0, all;
-    for (int i = a; i < e; ++i) s += weight<W>(p[i], W == kRest ? q[i] : (T)0.f, i == x);
-    u64 at = base + block_exclusive_scan(s, scan, all);
-    if (t < at || t >= at + s) return;
-    for (int i = a; i < e; ++i) {
-        at += weight<W>(p[i], W == kRest ? q[i] : (T)0.f, i == x);
-        if (at > t) {
-            *token = i;
-            return;
+    constexpr int kEach = 4;
+    for (int i0 = lo; i0 < hi; i0 += kEach * kThreads) {
+        const int i = i0 + kEach * (int)threadIdx.x;
+        u64 v[kEach], s = 0, all;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const Fixed f = i + k < hi ? weight<W>(p[i + k], W == kRest ? q[i + k] : (T)0.f, i + k == x) : Fixed{0, 0};
+            v[k] = units(f.hi, f.lo);
+            s += v[k];
         }
+        u64 at = base + block_exclusive_scan(s, scan, all);
+        base += all;
+        if (t >= base) continue;             // for the whole block: not among these
+        if (t < at || t >= at + s) return;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            if (t >= at && t < at + v[k]) *token = i + k;
+            at += v[k];
+        }
+        return;
     }
 }
 
@@ -97,10 +151,16 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams a) 
     const int b = blockIdx.x / C, K = a.K, V = a.V;
     pdl_wait();
     pdl_trigger();
-    const int k = a.counts ? a.counts[b] : K;
-    const int len = a.lens ? a.lens[b] : K;
     const int32_t *x = a.x + (size_t)b * K;
     const float *u = a.u + (size_t)b * (K + 1);
+    // these loads wait for nothing
+    const int xi = tid < K ? x[tid] : 0;
+    const float ui = tid < K ? u[tid] : 0.f, v = u[K];
+    const int k = a.counts ? a.counts[b] : K;
+    const int len = a.lens ? a.lens[b] : K;
+    // new_lens may be seq_lens: no CTA writes before all have read. (And a CTA's shared memory
+    // is there once it has begun.)
+    auto here = cl.barrier_arrive();
     int32_t *tokens = a.tokens + (size_t)b * (K + 1);
     const bool short_len = len < K && k >= 0;
     bool bad = k > K || short_len;
@@ -111,8 +171,6 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams a) 
     __syncthreads();
     if (!bad && k >= 0) {
         if (tid < k) {
-            const int xi = x[tid];
-            const float ui = u[tid];
             if (xi >= 0 && xi < V) {
                 const float p = widen(((const T *)a.p)[((size_t)b * (K + 1) + tid) * a.p_stride + xi]);
                 const float q = a.q ? widen(((const T *)a.q)[((size_t)b * K + tid) * a.q_stride + xi]) : 1.f;
@@ -122,26 +180,27 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams a) 
                 sh.bad = 1;
             }
         }
-        if (tid == 0 && !is_probability(u[K])) sh.bad = 1;
+        if (tid == 0 && !is_probability(v)) sh.bad = 1;
     }
     __syncthreads();
     bad |= sh.bad != 0;
     const int n = sh.n;
-    int token_by = -1;                       // the CTA that finds the token
-    u64 total = 0, base = 0, t = 0;
+    bool mine = false;                       // this CTA's part has the token
+    u64 total = 0, base = 0, own = 0, t = 0;
+    cl.barrier_wait(std::move(here));
     const T *p = (const T *)a.p + ((size_t)b * (K + 1) + max(n, 0)) * a.p_stride;
     const T *q = nullptr;
     int w = kPlain, out = -1;
-    // 32 tokens at a time, evenly over the warps of all CTAs
-    const int64_t groups = (V + 31ll) / 32, warps = (int64_t)C * kWarps;
-    const auto edge = [&](int64_t i) { return (int)min((int64_t)V, groups * i / warps * 32); };
+    // evenly over the warps of all CTAs, a group of tokens at a time where there are so many
+    const int64_t warps = (int64_t)C * kWarps, group = V >= kGroup * warps ? kGroup : 32, groups = (V + group - 1) / group;
+    const auto edge = [&](int64_t i) { return (int)min((int64_t)V, groups * i / warps * group); };
     if (!bad && k >= 0) {
         if (n < k) {
             w = a.q ? kRest : kWithout;
             if (a.q) q = (const T *)a.q + ((size_t)b * K + n) * a.q_stride;
             else out = x[n];
         }
-        for (;;) {
+        for (int pass = 0;; ++pass) {
             const int64_t at = (int64_t)rank * kWarps + warp;
             const int lo = edge(at), hi = edge(at + 1);
             float sum_p = 0.f;
@@ -158,41 +217,38 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams a) 
             }
             if (odd) sh.bad = 1;
             __syncthreads();
-            if (tid == 0) {
-                u64 all = 0;
-                float all_p = 0.f;
+            if (tid < C) {                   // every CTA tells every other
+                Part part = {0, 0.f, sh.bad};
                 for (int i = 0; i < kWarps; ++i) {
-                    all += sh.warp[i];
-                    all_p += sh.warp_p[i];
+                    part.sum += sh.warp[i];
+                    part.p += sh.warp_p[i];
                 }
-                sh.sum = all;
-                sh.sum_p = all_p;
+                cl.map_shared_rank(&sh, tid)->all[pass][rank] = part;
             }
             cl.sync();
             total = 0;
             sum_p = 0.f;
             int odd_row = 0;
             for (int c = 0; c < C; ++c) {
-                const Shared *o = cl.map_shared_rank(&sh, c);
-                if (c == rank) base = total;
-                total += o->sum;
-                sum_p += o->sum_p;
-                odd_row |= o->bad;
+                const Part part = sh.all[pass][c];
+                if (c == rank) {
+                    base = total;
+                    own = part.sum;
+                }
+                total += part.sum;
+                sum_p += part.p;
+                odd_row |= part.bad;
             }
-            cl.sync();                       // (also: nobody's numbers are read any longer)
             // probabilities add up to one; up to two, sums of units stay below 2^63
             bad = odd_row || !(sum_p <= 2.f) || (total == 0 && w == kPlain);
             if (bad || total > 0) break;
             w = kPlain;                      // nothing is left of p - q: p itself
             out = -1;
         }
-        if (!bad) {
-            const float v = u[K];            // t = floor(v total); for 1 the last token that has any weight
+        if (!bad) {                          // t = floor(v total); for 1 the last token that has any weight
             t = v < 1.f ? __umul64hi(__float2ull_rz(v * 0x1p64f), total) : total - 1;
-            token_by = t >= base && t < base + sh.sum ? rank : -1;
+            mine = t >= base && t < base + own;
         }
-    } else {
-        cl.sync();                           // new_lens may be seq_lens: every CTA has read the length
     }
     if (rank == 0) {
         const int stand = bad || k < 0 ? 0 : n;
@@ -204,7 +260,7 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams a) 
             if (bad) raise_flag(a.status, short_len ? FLAG_BAD_LENGTH : FLAG_BAD_VALUE);
         }
     }
-    if (token_by != rank) return;
+    if (!mine) return;
     u64 from = base;
     int i = 0;
     for (; i < kWarps - 1 && t >= from + sh.warp[i]; ++i) from += sh.warp[i];
@@ -214,10 +270,24 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams a) 
     else find_token<kPlain>(p, q, out, lo, hi, from, t, sh.scan, tokens + n);
 }
 
+// CTAs a sequence: up to about 256 in all, and no more than the row has work for. Beyond that the
+// launch of clusters costs more than the split gives (128 sequences of 32000 tokens: 15.1 us
+// with 1, 10.9 with 2, 20.0 with 4; 64 of 50257: 13.9 with 1, 7.7 with 4, 12.3 with 8; 16 of 131072:
+// 9.1 with 8, 10.5 with 16; 4 of them: 8.7 with 8, 6.5 with 16).
+unsigned cluster_size(int32_t B, int32_t V) {
+    unsigned C = 1;
+    while (C < (B <= 8 ? 16u : 8u) && 2 * C * (int64_t)B <= 256 && 1024ll * C < V) C *= 2;
+    return C;
+}
+
 template <typename T>
 cudaError_t launch(const AcceptParams &p, cudaStream_t st) {
+    const unsigned C = cluster_size(p.B, p.V);
+    if (C > 8) {
+        const cudaError_t e = cudaFuncSetAttribute(accept_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
-    const unsigned C = 1;
     cfg.gridDim = dim3((unsigned)p.B * C);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = st;

@@ -118,10 +118,10 @@ def accept(p, q, x, u, counts=None, lens=None):
         if any(not 0 <= v <= 1 for v in row) or (n < k and q is not None and any(not 0 <= v <= 1 for v in q[b][n])) or sum(row) > 2:
             out.append(nothing)
             continue
-        whole = [int(v * 2.0 ** 62) for v in row]
+        whole = [round(v * 2.0 ** 46) for v in row]
         w = whole
         if n < k:
-            less = [2 ** 62 * (j == x[b][n]) for j in range(V)] if q is None else [int(v * 2.0 ** 62) for v in q[b][n]]
+            less = [2 ** 46 * (j == x[b][n]) for j in range(V)] if q is None else [round(v * 2.0 ** 46) for v in q[b][n]]
             w = [max(i - j, 0) for i, j in zip(whole, less)]
             w = w if any(w) else whole
         total = sum(w)

@@ -130,7 +130,7 @@ def test_nothing_left_of_the_difference(gpu_lib):
     c["x"][:, 0] = 7
     c["p"][:, 0, 7] = 0
     c["p"][1, 0] = 0
-    c["p"][1, 0, 33] = 1e-30                                 # below 2^-62: no weight at all, an error
+    c["p"][1, 0, 33] = 1e-30                                 # below 2^-47: no weight at all, an error
     c["q"][1, 0] = 0.001
     outs = _outputs(4, 2)
     _call(c, outs)
