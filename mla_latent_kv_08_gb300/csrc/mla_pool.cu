@@ -14,6 +14,8 @@
 
 #include <cooperative_groups.h>
 
+#include <utility>
+
 namespace cg = cooperative_groups;
 
 namespace mla {
@@ -22,26 +24,70 @@ namespace {
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kPiece = 256;                  // table entries, 8 a lane
 
-struct Shared {
-    int scan[33];
-    long long scan2[33];
-    int warp[kWarps];                        // this CTA's warps: blocks counted
-    int count, flags, freed;
+constexpr int kMaxCluster = 16;
+
+// What a CTA counted, and its flags.
+struct Counted {
+    int free, flags;
 };
 
-// Sums of the CTAs' counts: before this one, all; and every CTA's flags.
+struct Shared {
+    Counted all[kMaxCluster];                // of every CTA of the cluster
+    int2 scan[kWarps];
+    int scan_two[kWarps];
+    int warp[kWarps];                        // this CTA's warps: free blocks
+    int ids[kWarps][128];                    // a step's free blocks
+    int free, flags, freed;
+};
+
+// Sums over the CTAs: free blocks before this one's, all; every CTA's flags.
 struct Totals {
     int before, all, flags;
 };
-__device__ __forceinline__ Totals totals(const cg::cluster_group &cl, Shared &sh) {
+// Every CTA tells every other, and waits for them. `here`: the cluster's arrival at the
+// kernel's start, without which a CTA's shared memory may not be there yet.
+__device__ __forceinline__ Totals exchange(const cg::cluster_group &cl, cg::cluster_group::arrival_token &here, Shared &sh) {
+    cl.barrier_wait(std::move(here));
+    __syncthreads();
+    if (threadIdx.x < cl.num_blocks())
+        cl.map_shared_rank(&sh, threadIdx.x)->all[cl.block_rank()] = Counted{sh.free, sh.flags};
+    cl.sync();
     Totals t = {0, 0, 0};
     for (unsigned c = 0; c < cl.num_blocks(); ++c) {
-        const Shared *o = cl.map_shared_rank(&sh, c);
         if (c == cl.block_rank()) t.before = t.all;
-        t.all += o->count;
-        t.flags |= o->flags;
+        t.all += sh.all[c].free;
+        t.flags |= sh.all[c].flags;
     }
     return t;
+}
+
+// Block-wide exclusive scan of three numbers a thread.
+struct Three {
+    int x, y, z;
+};
+__device__ __forceinline__ Three scan_three(Three v, Shared &sh, Three &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Three in = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, in.x, o), y = __shfl_up_sync(0xffffffffu, in.y, o),
+                  z = __shfl_up_sync(0xffffffffu, in.z, o);
+        if (lane >= o) in.x += x, in.y += y, in.z += z;
+    }
+    __syncthreads();                         // the last scan's sums have been read
+    if (lane == 31) {
+        sh.scan[warp] = make_int2(in.x, in.y);
+        sh.scan_two[warp] = in.z;
+    }
+    __syncthreads();
+    // every warp adds the others' sums up for itself
+    const int2 w = sh.scan[lane];
+    const int wz = sh.scan_two[lane];
+    const bool before = lane < warp;
+    const Three base = {__reduce_add_sync(0xffffffffu, before ? w.x : 0), __reduce_add_sync(0xffffffffu, before ? w.y : 0),
+                        __reduce_add_sync(0xffffffffu, before ? wz : 0)};
+    total = {__reduce_add_sync(0xffffffffu, w.x), __reduce_add_sync(0xffffffffu, w.y), __reduce_add_sync(0xffffffffu, wz)};
+    return {base.x + in.x - v.x, base.y + in.y - v.y, base.z + in.z - v.z};
 }
 
 // The part of the counts that warp w of all counts, in steps of 128.
@@ -67,54 +113,65 @@ __device__ __forceinline__ Free4 free4(const int32_t *ref, int i0, int end) {
     return f;
 }
 
-// Counts the free blocks of every warp's part into sh.warp and sh.count. The caller
-// synchronises the block, then the cluster.
+// Counts the free blocks of every warp's part into sh.warp and sh.free.
 __device__ __forceinline__ void count_free(const PoolParams &p, Shared &sh, int64_t w, int64_t warps) {
-    const int lane = threadIdx.x & 31, lo = part_begin(p.N, w, warps), hi = part_begin(p.N, w + 1, warps);
+    const int lo = part_begin(p.N, w, warps), hi = part_begin(p.N, w + 1, warps);
     int n = 0;
+#pragma unroll 4
     for (int i0 = lo; i0 < hi; i0 += 128) {
         const Free4 f = free4(p.ref, i0, hi);
         n += f.v[0] + f.v[1] + f.v[2] + f.v[3];
     }
     n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0) {
+    if ((threadIdx.x & 31) == 0) {
         sh.warp[threadIdx.x >> 5] = n;
-        if (n) atomicAdd(&sh.count, n);
+        if (n) atomicAdd(&sh.free, n);
     }
 }
 
-// give(rank, block) for each free block of rank below `need`, lowest first.
+// give(rank, block) for each free block of rank below `need`, lowest first. The free ones of
+// a step are gathered first, so that whole warps look their places up.
+__device__ __forceinline__ uint32_t lanes_below() { return (1u << (threadIdx.x & 31)) - 1; }
 template <typename F>
-__device__ __forceinline__ void hand_out(const PoolParams &p, const Shared &sh, int before, int need, int64_t w,
-                                         int64_t warps, F give) {
-    const int lane = threadIdx.x & 31, lo = part_begin(p.N, w, warps), hi = part_begin(p.N, w + 1, warps);
-    int rank = before;
-    for (int i = 0; i < (int)(threadIdx.x >> 5); ++i) rank += sh.warp[i];
-    const uint32_t lower = (1u << lane) - 1;
+__device__ __forceinline__ void hand_out(const PoolParams &p, Shared &sh, int before, int need, int64_t w, int64_t warps, F give) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lo = part_begin(p.N, w, warps), hi = part_begin(p.N, w + 1, warps);
+    int rank = before + __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp[lane] : 0);
+    Free4 f = free4(p.ref, lo, rank < need ? hi : lo);
     for (int i0 = lo; i0 < hi && rank < need; i0 += 128) {
-        const Free4 f = free4(p.ref, i0, hi);
+        const Free4 next = free4(p.ref, i0 + 128, hi);
+        int n = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const uint32_t m = __ballot_sync(0xffffffffu, f.v[k]);
-            const int r = rank + __popc(m & lower);
-            if (f.v[k] && r < need) give(r, i0 + 32 * k + lane);
-            rank += __popc(m);
+            if (f.v[k]) sh.ids[warp][n + __popc(m & lanes_below())] = i0 + 32 * k + lane;
+            n += __popc(m);
         }
+        __syncwarp();
+        for (int q = lane; q < min(n, need - rank); q += 32) give(rank + q, sh.ids[warp][q]);
+        __syncwarp();
+        rank += n;
+        f = next;
     }
 }
 
-// f(list, entry) for the entries of lists whose pieces `pieces` counts: list b has the entries
-// begin(b) .. end(b) - 1. All warps of the cluster take part.
-template <typename R, typename F>
-__device__ __forceinline__ void walk(const int *pieces, int lists, int64_t w, int64_t warps, R range, F f) {
+// f(list, entries' first index, their values, which there are) for the entries of lists whose
+// pieces `pieces` counts: list b has the entries range(b).x .. range(b).y - 1 of the row
+// row(b). A lane gets kLane entries of a piece, 32 apart, all of them loaded before any is
+// used. All warps of the cluster take part.
+constexpr int kLane = kPiece / 32;
+template <typename Range, typename Row, typename F>
+__device__ __forceinline__ void walk(const int *pieces, int lists, int64_t w, int64_t warps, Range range, Row row, F f) {
     const int lane = threadIdx.x & 31, total = pieces[lists];
     for (int64_t c = w; c < total; c += warps) {
         const int b = find_seq(pieces, lists, (int)c);
         const int2 r = range(b);
         const int first = r.x + ((int)c - pieces[b]) * kPiece + lane;
+        const int32_t *from = row(b) + first;
+        int v[kLane];
 #pragma unroll
-        for (int k = 0; k < kPiece / 32; ++k)
-            if (first + 32 * k < r.y) f(b, first + 32 * k);
+        for (int k = 0; k < kLane; ++k) v[k] = first + 32 * k < r.y ? from[32 * k] : 0;
+        f(b, first, v, (r.y - first + 31) / 32);
     }
 }
 
@@ -145,101 +202,101 @@ __device__ __forceinline__ Change change_of(const PoolParams &p, int b) {
     return c;
 }
 
+// Gives back the blocks v of the entries at, at + 32, ..; how many are free now.
+__device__ __forceinline__ int give_back(const PoolParams &p, int32_t *at, const int (&v)[kLane], int n) {
+    int old[kLane], freed = 0;
+#pragma unroll
+    for (int k = 0; k < kLane; ++k)
+        if (k < n && v[k] >= 0) {
+            old[k] = atomicSub(&p.ref[v[k]], 1);
+            at[32 * k] = -1;
+        }
+#pragma unroll
+    for (int k = 0; k < kLane; ++k) freed += k < n && v[k] >= 0 && old[k] == 1;
+    return freed;
+}
+
 __global__ void __launch_bounds__(kThreads) resize_kernel(const PoolParams p) {
     extern __shared__ int dyn[];
     __shared__ Shared sh;
-    int *s_takes = dyn, *s_pieces = dyn + p.S + 1, *s_split = s_pieces + p.S + 1;      // [S + 1] each
+    int *s_takes = dyn, *s_pieces = dyn + p.S + 1;       // [S + 1] each
+    int *s_place = s_pieces + p.S + 1;                   // [S] first entry that takes a block; ~(copy's number) for a cut
     const cg::cluster_group cl = cg::this_cluster();
+    auto here = cl.barrier_arrive();
     const int tid = threadIdx.x;
     const int64_t w = (int64_t)cl.block_rank() * kWarps + (tid >> 5), warps = (int64_t)cl.num_blocks() * kWarps;
+    const int64_t thread = (int64_t)cl.block_rank() * kThreads + tid, threads = (int64_t)cl.num_blocks() * kThreads;
     pdl_wait();
     pdl_trigger();
-    if (tid == 0) sh.count = sh.flags = sh.freed = 0;
-    __syncthreads();
+    if (tid == 0) sh.free = sh.flags = sh.freed = 0;
     // every CTA: what each sequence takes, the pieces of what it gives back, whether its last
     // block is replaced
-    int takes = 0, pieces = 0, splits = 0, flags = 0;
+    Three sum = {0, 0, 0};
+    int flags = 0;
     for (int b0 = 0; b0 < p.S; b0 += kThreads) {
         const int b = b0 + tid;
         Change c = {0, 0, -1, 0};
         if (b < p.S) c = change_of(p, b);
         flags |= c.flags;
-        const int back = c.held > c.wanted ? ceil_div(c.held - c.wanted, kPiece) : 0;
-        long long all2;
-        const long long two = block_exclusive_scan((long long)c.takes() << 32 | back, sh.scan2, all2);
-        int all;
-        const int one = block_exclusive_scan((int)(c.old >= 0), sh.scan, all);
+        Three all;
+        const Three at = scan_three({c.takes(), c.held > c.wanted ? ceil_div(c.held - c.wanted, kPiece) : 0, c.old >= 0}, sh, all);
         if (b < p.S) {
-            s_takes[b] = takes + (int)(two >> 32);
-            s_pieces[b] = pieces + (int)(two & 0xffffffff);
-            s_split[b] = splits + one;
+            s_takes[b] = sum.x + at.x;
+            s_pieces[b] = sum.y + at.y;
+            s_place[b] = c.old >= 0 ? ~(sum.z + at.z) : c.held;
         }
-        takes += (int)(all2 >> 32);
-        pieces += (int)(all2 & 0xffffffff);
-        splits += all;
+        sum = {sum.x + all.x, sum.y + all.y, sum.z + all.z};
     }
+    const int takes = sum.x, splits = sum.z;
     if (tid == 0) {
         s_takes[p.S] = takes;
-        s_pieces[p.S] = pieces;
-        s_split[p.S] = splits;
+        s_pieces[p.S] = sum.y;
     }
-    __syncthreads();
     const auto given = [&](int b) { return make_int2(ceil_div(p.new_lens[b], p.bs), ceil_div(p.lens[b], p.bs)); };
+    const auto row = [&](int b) { return p.table + (size_t)b * p.W; };
     if (!__syncthreads_or(flags))            // lengths are fine: so are the ranges
-        walk(s_pieces, p.S, w, warps, given, [&](int b, int j) {
-            const int t = p.table[(size_t)b * p.W + j];
-            if (t < 0 || t >= p.N) flags |= FLAG_BAD_BLOCK;
+        walk(s_pieces, p.S, w, warps, given, row, [&](int, int, const int (&v)[kLane], int n) {
+#pragma unroll
+            for (int k = 0; k < kLane; ++k)
+                if (k < n && (v[k] < 0 || v[k] >= p.N)) flags |= FLAG_BAD_BLOCK;
         });
     count_free(p, sh, w, warps);
     if (flags) atomicOr(&sh.flags, flags);
-    __syncthreads();
-    cl.sync();
-    Totals t = totals(cl, sh);
+    Totals t = exchange(cl, here, sh);
     if (!t.flags && takes > t.all) t.flags = FLAG_FULL;
     if (t.flags) {                           // nothing is changed
-        if (cl.block_rank() == 0 && tid == 0) {
+        if (thread == 0) {
             raise_flag(p.status, t.flags);
             *p.num_copies = 0;
             if (p.left) *p.left = t.all;
         }
-        cl.sync();
         return;
     }
     hand_out(p, sh, t.before, takes, w, warps, [&](int r, int block) {
-        const int b = find_seq(s_takes, p.S, r);
-        const int len = p.lens[b], to = p.new_lens[b], k = r - s_takes[b];
-        int32_t *row = p.table + (size_t)b * p.W;
-        if (to < len) {                      // the cut's own copy of a shared block
-            const int j = ceil_div(to, p.bs) - 1;
-            p.copies[s_split[b]] = make_int4(row[j], block, 0, to % p.bs);
-            row[j] = block;
-        } else {
-            row[ceil_div(len, p.bs) + k] = block;
+        const int b = find_seq(s_takes, p.S, r), place = s_place[b];
+        int32_t *at = p.table + (size_t)b * p.W + place + (r - s_takes[b]);
+        if (place < 0) {                     // the cut's own copy of a shared block
+            const int to = p.new_lens[b];
+            at = p.table + (size_t)b * p.W + ceil_div(to, p.bs) - 1;
+            p.copies[~place] = make_int4(*at, block, 0, to % p.bs);
         }
+        *at = block;
         p.ref[block] = 1;
     });
     cl.sync();                               // all free blocks have been looked at
     int freed = 0;
-    const auto give_back = [&](int block) { freed += atomicSub(&p.ref[block], 1) == 1; };
-    walk(s_pieces, p.S, w, warps, given, [&](int b, int j) {
-        int32_t *at = p.table + (size_t)b * p.W + j;
-        give_back(*at);
-        *at = -1;
+    walk(s_pieces, p.S, w, warps, given, row, [&](int b, int j, const int (&v)[kLane], int n) {
+        freed += give_back(p, p.table + (size_t)b * p.W + j, v, n);
     });
-    for (int64_t i = (int64_t)cl.block_rank() * kThreads + tid; i < splits; i += (int64_t)cl.num_blocks() * kThreads)
-        give_back(p.copies[i].x);
+    for (int64_t i = thread; i < splits; i += threads) freed += atomicSub(&p.ref[p.copies[i].x], 1) == 1;
     freed = __reduce_add_sync(0xffffffffu, freed);
-    if ((tid & 31) == 0 && freed) atomicAdd(&sh.freed, freed);
+    if ((tid & 31) == 0 && freed) atomicAdd(&cl.map_shared_rank(&sh, 0)->freed, freed);
     cl.sync();                               // lengths have been read
-    for (int64_t b = (int64_t)cl.block_rank() * kThreads + tid; b < p.S; b += (int64_t)cl.num_blocks() * kThreads)
-        p.lens[b] = p.new_lens[b];
-    if (cl.block_rank() == 0 && tid == 0) {
+    for (int64_t b = thread; b < p.S; b += threads) p.lens[b] = p.new_lens[b];
+    if (thread == 0) {
         *p.num_copies = splits;
-        int left = t.all - takes;
-        for (unsigned c = 0; c < cl.num_blocks(); ++c) left += cl.map_shared_rank(&sh, c)->freed;
-        if (p.left) *p.left = left;
+        if (p.left) *p.left = t.all - takes + sh.freed;
     }
-    cl.sync();
 }
 
 // ---- fork -------------------------------------------------------------------
@@ -250,14 +307,17 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const PoolParams p) {
     int *s_takes = dyn, *s_pieces = dyn + p.n + 1, *s_len = s_pieces + p.n + 1;         // [n + 1] each
     uint32_t *s_child = (uint32_t *)(s_len + p.n + 1);                                   // a bit a sequence
     const cg::cluster_group cl = cg::this_cluster();
+    auto here = cl.barrier_arrive();
     const int tid = threadIdx.x;
     const int64_t w = (int64_t)cl.block_rank() * kWarps + (tid >> 5), warps = (int64_t)cl.num_blocks() * kWarps;
+    const int64_t thread = (int64_t)cl.block_rank() * kThreads + tid, threads = (int64_t)cl.num_blocks() * kThreads;
     pdl_wait();
     pdl_trigger();
-    if (tid == 0) sh.count = sh.flags = sh.freed = 0;
+    if (tid == 0) sh.free = sh.flags = 0;
     for (int i = tid; i < (p.S + 31) / 32; i += kThreads) s_child[i] = 0;
     __syncthreads();
-    int takes = 0, pieces = 0, flags = 0;
+    Three sum = {0, 0, 0};
+    int flags = 0;
     for (int i0 = 0; i0 < p.n; i0 += kThreads) {
         const int i = i0 + tid;
         int len = 0;
@@ -270,88 +330,108 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const PoolParams p) {
                 len = p.fork_lens ? p.fork_lens[i] : most;
                 const uint32_t bit = 1u << (c & 31);
                 // an empty sequence, and each but once
-                if (most < 0 || most > p.cap || len < 0 || len > most || p.lens[c] != 0 || (atomicOr(&s_child[c / 32], bit) & bit)) {
+                if (most < 0 || most > p.cap || len < 0 || len > most || p.lens[c] != 0 ||
+                    (atomicOr(&s_child[c / 32], bit) & bit)) {
                     flags |= FLAG_BAD_LENGTH;
                     len = 0;
                 }
             }
         }
-        long long all;
-        const long long two = block_exclusive_scan(
-            (long long)(len % p.bs != 0) << 32 | ceil_div(len / p.bs, kPiece), sh.scan2, all);
+        Three all;
+        const Three at = scan_three({len % p.bs != 0, ceil_div(len / p.bs, kPiece), 0}, sh, all);
         if (i < p.n) {
-            s_takes[i] = takes + (int)(two >> 32);
-            s_pieces[i] = pieces + (int)(two & 0xffffffff);
+            s_takes[i] = sum.x + at.x;
+            s_pieces[i] = sum.y + at.y;
             s_len[i] = len;
         }
-        takes += (int)(all >> 32);
-        pieces += (int)(all & 0xffffffff);
+        sum = {sum.x + all.x, sum.y + all.y, 0};
     }
+    const int takes = sum.x;
     if (tid == 0) {
         s_takes[p.n] = takes;
-        s_pieces[p.n] = pieces;
+        s_pieces[p.n] = sum.y;
     }
-    __syncthreads();
     const auto common = [&](int i) { return make_int2(0, s_len[i] / p.bs); };
+    const auto parent = [&](int i) { return p.table + (size_t)p.parents[i] * p.W; };
     if (!__syncthreads_or(flags)) {
-        walk(s_pieces, p.n, w, warps, common, [&](int i, int j) {
-            const int t = p.table[(size_t)p.parents[i] * p.W + j];
-            if (t < 0 || t >= p.N) flags |= FLAG_BAD_BLOCK;
+        walk(s_pieces, p.n, w, warps, common, parent, [&](int, int, const int (&v)[kLane], int n) {
+#pragma unroll
+            for (int k = 0; k < kLane; ++k)
+                if (k < n && (v[k] < 0 || v[k] >= p.N)) flags |= FLAG_BAD_BLOCK;
         });
-        for (int i = tid; i < p.n; i += kThreads)
+        for (int64_t i = thread; i < p.n; i += threads)
             if (s_len[i] % p.bs) {
-                const int t = p.table[(size_t)p.parents[i] * p.W + s_len[i] / p.bs];
+                const int t = parent((int)i)[s_len[i] / p.bs];
                 if (t < 0 || t >= p.N) flags |= FLAG_BAD_BLOCK;
             }
     }
     count_free(p, sh, w, warps);
     if (flags) atomicOr(&sh.flags, flags);
-    __syncthreads();
-    cl.sync();
-    Totals t = totals(cl, sh);
+    Totals t = exchange(cl, here, sh);
     if (!t.flags && takes > t.all) t.flags = FLAG_FULL;
     if (t.flags) {                           // nothing is changed
-        if (cl.block_rank() == 0 && tid == 0) {
+        if (thread == 0) {
             raise_flag(p.status, t.flags);
             *p.num_copies = 0;
             if (p.left) *p.left = t.all;
         }
-        cl.sync();
         return;
     }
     hand_out(p, sh, t.before, takes, w, warps, [&](int r, int block) {
         const int i = find_seq(s_takes, p.n, r), j = s_len[i] / p.bs;
-        p.copies[r] = make_int4(p.table[(size_t)p.parents[i] * p.W + j], block, 0, s_len[i] % p.bs);
+        p.copies[r] = make_int4(parent(i)[j], block, 0, s_len[i] % p.bs);
         p.table[(size_t)p.children[i] * p.W + j] = block;
         p.ref[block] = 1;
     });
-    walk(s_pieces, p.n, w, warps, common, [&](int i, int j) {
-        const int block = p.table[(size_t)p.parents[i] * p.W + j];
-        p.table[(size_t)p.children[i] * p.W + j] = block;
-        atomicAdd(&p.ref[block], 1);         // of a block in use: no free one is mistaken for it
+    // counts of blocks in use: no free one is mistaken for such a one, or the other way round
+    walk(s_pieces, p.n, w, warps, common, parent, [&](int i, int j, const int (&v)[kLane], int n) {
+        int32_t *to = p.table + (size_t)p.children[i] * p.W + j;
+#pragma unroll
+        for (int k = 0; k < kLane; ++k)
+            if (k < n) {
+                to[32 * k] = v[k];
+                atomicAdd(&p.ref[v[k]], 1);
+            }
     });
-    for (int64_t i = (int64_t)cl.block_rank() * kThreads + tid; i < p.n; i += (int64_t)cl.num_blocks() * kThreads)
-        p.lens[p.children[i]] = s_len[i];
-    if (cl.block_rank() == 0 && tid == 0) {
+    for (int64_t i = thread; i < p.n; i += threads) p.lens[p.children[i]] = s_len[i];
+    if (thread == 0) {
         *p.num_copies = takes;
         if (p.left) *p.left = t.all - takes;
     }
-    cl.sync();                               // nobody's numbers are read any longer
 }
 
 // ---- compact ----------------------------------------------------------------
+
+// Entries v of a table at at, at + 32, ..: those of moved blocks (none below `first`) follow.
+// Whether any is out of range.
+__device__ __forceinline__ bool follow(const PoolParams &p, int first, int32_t *at, const int (&v)[kLane], int n) {
+    int to[kLane];
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < kLane; ++k) {
+        to[k] = -1;
+        if (k >= n) continue;
+        if (v[k] < 0 || v[k] >= p.N) bad = true;         // left as it is
+        else if (v[k] >= first) to[k] = ~p.ref[v[k]];
+    }
+#pragma unroll
+    for (int k = 0; k < kLane; ++k)
+        if (to[k] >= 0) at[32 * k] = to[k];
+    return bad;
+}
 
 __global__ void __launch_bounds__(kThreads) compact_kernel(const PoolParams p) {
     extern __shared__ int dyn[];
     __shared__ Shared sh;
     int *s_pieces = dyn;                     // [S + 1]
     const cg::cluster_group cl = cg::this_cluster();
+    auto here = cl.barrier_arrive();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t w = (int64_t)cl.block_rank() * kWarps + warp, warps = (int64_t)cl.num_blocks() * kWarps;
+    const int64_t thread = (int64_t)cl.block_rank() * kThreads + tid, threads = (int64_t)cl.num_blocks() * kThreads;
     pdl_wait();
     pdl_trigger();
-    if (tid == 0) sh.count = sh.flags = 0;
-    __syncthreads();
+    if (tid == 0) sh.free = sh.flags = 0;
     int pieces = 0, flags = 0;
     for (int b0 = 0; b0 < p.S; b0 += kThreads) {
         const int b = b0 + tid;
@@ -360,25 +440,22 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const PoolParams p) {
             flags |= FLAG_BAD_LENGTH;
             len = 0;
         }
-        int all;
-        const int one = block_exclusive_scan(ceil_div(ceil_div(len, p.bs), kPiece), sh.scan, all);
-        if (b < p.S) s_pieces[b] = pieces + one;
-        pieces += all;
+        Three all;
+        const Three at = scan_three({ceil_div(ceil_div(len, p.bs), kPiece), 0, 0}, sh, all);
+        if (b < p.S) s_pieces[b] = pieces + at.x;
+        pieces += all.x;
     }
     if (tid == 0) s_pieces[p.S] = pieces;
     if (flags) atomicOr(&sh.flags, flags);
     count_free(p, sh, w, warps);
-    __syncthreads();
-    cl.sync();
-    const Totals t = totals(cl, sh);
+    const Totals t = exchange(cl, here, sh);
     const int live = p.N - t.all;
     if (t.flags) {
-        if (cl.block_rank() == 0 && tid == 0) {
+        if (thread == 0) {
             raise_flag(p.status, t.flags);
             *p.num_copies = 0;
             if (p.left) *p.left = live;
         }
-        cl.sync();
         return;
     }
     // free blocks below `live`: those of the warps before the one with id `live`, and some of
@@ -386,83 +463,106 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const PoolParams p) {
     int64_t wl = 0;
     for (int64_t a = 0, e = warps; a < e;) {             // the last warp that begins at or below `live`
         const int64_t m = (a + e) / 2;
-        if (part_begin(p.N, m, warps) <= live) { wl = m; a = m + 1; } else e = m;
+        if (part_begin(p.N, m, warps) <= live) {
+            wl = m;
+            a = m + 1;
+        } else {
+            e = m;
+        }
     }
-    int holes = 0;
-    for (int64_t i = lane; i < wl; i += 32) holes += cl.map_shared_rank(&sh, (unsigned)(i / kWarps))->warp[i % kWarps];
-    for (int i = part_begin(p.N, wl, warps) + lane; i < live; i += 32) holes += p.ref[i] == 0;
+    const int cta = (int)(wl / kWarps);
+    int holes = lane < (int)(wl % kWarps) ? cl.map_shared_rank(&sh, cta)->warp[lane] : 0;
+    if (lane < cta) holes += sh.all[lane].free;
+#pragma unroll 4
+    for (int i0 = part_begin(p.N, wl, warps); i0 < live; i0 += 128) {
+        const Free4 f = free4(p.ref, i0, live);
+        holes += f.v[0] + f.v[1] + f.v[2] + f.v[3];
+    }
     holes = __reduce_add_sync(0xffffffffu, holes);
     const int moves = min(holes, p.n);
     // the k-th used block from `live` on goes to the k-th free one below
     {
         const int lo = part_begin(p.N, w, warps), hi = part_begin(p.N, w + 1, warps);
-        int rank = t.before;                 // free blocks before
-        for (int i = 0; i < warp; ++i) rank += sh.warp[i];
-        const uint32_t lower = (1u << lane) - 1;
+        int rank = t.before + __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp[lane] : 0);      // free blocks before
+        Free4 f = free4(p.ref, lo, hi);
         for (int i0 = lo; i0 < hi; i0 += 128) {
-            const Free4 f = free4(p.ref, i0, hi);
+            const Free4 next = free4(p.ref, i0 + 128, hi);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const uint32_t mask = __ballot_sync(0xffffffffu, f.v[k]);
-                const int r = rank + __popc(mask & lower), i = i0 + 32 * k + lane;
+                const int r = rank + __popc(mask & lanes_below()), i = i0 + 32 * k + lane;
                 rank += __popc(mask);
                 if (i >= hi) continue;
                 if (i < live) {
                     if (f.v[k] && r < moves) p.copies[r].y = i;
                 } else if (!f.v[k]) {
                     const int m = i - live - (r - holes);            // used blocks from `live` on before this one
-                    if (m < moves) {
-                        p.copies[m].x = i;
-                        p.copies[m].z = 0;
-                        p.copies[m].w = p.bs;
-                    }
+                    if (m < moves) p.copies[m].x = i;
                 }
             }
+            f = next;
         }
     }
     cl.sync();
     // a moved block's count goes with it; where it was, where it went is noted for the tables
-    const int64_t thread = (int64_t)cl.block_rank() * kThreads + tid, threads = (int64_t)cl.num_blocks() * kThreads;
-    for (int64_t i = thread; i < moves; i += threads) {
-        const int4 c = p.copies[i];
-        p.ref[c.y] = p.ref[c.x];
-        p.ref[c.x] = ~c.y;
+    for (int64_t i0 = thread; i0 < moves; i0 += 4 * threads) {
+        int2 c[4];
+        int count[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i0 + k * threads < moves) c[k] = *(const int2 *)(p.copies + i0 + k * threads);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i0 + k * threads < moves) count[k] = p.ref[c[k].x];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i0 + k * threads < moves) {
+                *((int2 *)(p.copies + i0 + k * threads) + 1) = make_int2(0, p.bs);
+                p.ref[c[k].y] = count[k];
+                p.ref[c[k].x] = ~c[k].y;
+            }
     }
-    cl.sync();
-    const auto held = [&](int b) { return make_int2(0, ceil_div(p.lens[b], p.bs)); };
-    walk(s_pieces, p.S, w, warps, held, [&](int b, int j) {
-        int32_t *at = p.table + (size_t)b * p.W + j;
-        const int block = *at;
-        if (block < 0 || block >= p.N) {
-            raise_flag(p.status, FLAG_BAD_BLOCK);        // left as it is
-        } else if (block >= live) {
-            const int to = ~p.ref[block];
-            if (to >= 0) *at = to;
-        }
-    });
-    cl.sync();
-    for (int64_t i = thread; i < moves; i += threads) p.ref[p.copies[i].x] = 0;
-    if (cl.block_rank() == 0 && tid == 0) {
+    if (thread == 0) {
         *p.num_copies = moves;
         if (p.left) *p.left = live;
     }
+    cl.sync();
+    const auto held = [&](int b) { return make_int2(0, ceil_div(p.lens[b], p.bs)); };
+    const auto row = [&](int b) { return p.table + (size_t)b * p.W; };
+    walk(s_pieces, p.S, w, warps, held, row, [&](int b, int j, const int (&v)[kLane], int n) {
+        if (follow(p, live, p.table + (size_t)b * p.W + j, v, n)) flags = FLAG_BAD_BLOCK;
+    });
+    if (flags) raise_flag(p.status, flags);
+    cl.sync();
+    for (int64_t i = thread; i < moves; i += threads) p.ref[p.copies[i].x] = 0;
 }
 
-constexpr unsigned kCluster = 1;
+// CTAs of the cluster, for `rows` rows of the table. Turnovers of 500 sequences, 33k entries and
+// blocks: 35.9 us with 1, 23.2 with 2, 12.6 with 8 and 16; of 512, 600k entries and 290k blocks: 159,
+// -, 32, 21. A step of 16 sequences, 1700 entries and blocks: 6.6 with 1 to 4, 6.9 with 16;
+// compaction, whose phases are more: 9.2 with 1, 9.5 with 2, 10.4 with 8, 11.5 with 16.
+unsigned cluster_size(const PoolParams &p, int32_t rows) {
+    const int64_t n = (int64_t)rows * p.W + p.N;
+    return n <= 16384 ? 2 : n <= 131072 ? 8 : 16;
+}
 
-cudaError_t launch(void (*kern)(PoolParams), const PoolParams &p, size_t smem, cudaStream_t st) {
-    if (smem > 40960) {                      // with the static part, more than a launch may have without asking
+cudaError_t launch(void (*kern)(PoolParams), const PoolParams &p, unsigned cluster, size_t smem, cudaStream_t st) {
+    if (smem > 24576) {                      // with the static part, more than a launch may have without asking
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
+    if (cluster > 8) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kCluster);
+    cfg.gridDim = dim3(cluster);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kCluster;
+    attr[0].val.clusterDim.x = cluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
@@ -474,13 +574,14 @@ cudaError_t launch(void (*kern)(PoolParams), const PoolParams &p, size_t smem, c
 }  // namespace
 
 cudaError_t launch_pool_resize(const PoolParams &p, cudaStream_t st) {
-    return launch(resize_kernel, p, 3 * sizeof(int) * ((size_t)p.S + 1), st);
+    return launch(resize_kernel, p, cluster_size(p, p.S), 3 * sizeof(int) * ((size_t)p.S + 1), st);
 }
 cudaError_t launch_pool_fork(const PoolParams &p, cudaStream_t st) {
-    return launch(fork_kernel, p, 3 * sizeof(int) * ((size_t)p.n + 1) + sizeof(uint32_t) * (((size_t)p.S + 31) / 32), st);
+    const size_t smem = 3 * sizeof(int) * ((size_t)p.n + 1) + sizeof(uint32_t) * (((size_t)p.S + 31) / 32);
+    return launch(fork_kernel, p, cluster_size(p, p.n), smem, st);
 }
 cudaError_t launch_pool_compact(const PoolParams &p, cudaStream_t st) {
-    return launch(compact_kernel, p, sizeof(int) * ((size_t)p.S + 1), st);
+    return launch(compact_kernel, p, cluster_size(p, p.S), sizeof(int) * ((size_t)p.S + 1), st);
 }
 
 }  // namespace mla
