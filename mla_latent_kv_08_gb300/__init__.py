@@ -387,12 +387,34 @@ def mla_verify(cache: Cache, block_table, seq_lens, q, W_UV, scale: float, out, 
 
 # ---------------------------------------------------------------- the pool's books
 
-def _ints(where, device, *tensors) -> None:
-    """Refuses what the library could not see in a pointer: int32, dense, on the device of the call."""
+def _here(stream):
+    """(the current device, the stream's handle) of a call."""
     import torch
+    device = torch.cuda.current_device()
+    return device, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
+def _ints(where, device, *tensors) -> list:
+    """The tensors' pointers (None for None). Refuses what the library could not see in a pointer:
+    they are int32, dense, and on the device of the call."""
+    import torch
+    int32, out = torch.int32, []
     for t in tensors:
-        if t is not None and (t.dtype is not torch.int32 or t.get_device() != device or not t.is_contiguous()):
+        if t is None:
+            out.append(None)
+            continue
+        if t.dtype is not int32 or t.get_device() != device or not t.is_contiguous():
             raise MlaError(MLA_ERR_INVALID, where)
+        out.append(t.data_ptr())
+    return out
+
+
+def _check_list(where, copies, num_copies, room) -> int:
+    """The entries that a list of copies has room for, at least ``room`` of them."""
+    n = copies.shape[0]
+    if copies.shape != (n, 4) or n < room or num_copies.numel() < 1:
+        raise MlaError(MLA_ERR_INVALID, where)
+    return n
 
 
 @dataclasses.dataclass(frozen=True)
@@ -408,13 +430,13 @@ class Pool:
     def __post_init__(self):
         table, lens, ref = self.block_table, self.seq_lens, self.ref_count
         device = table.get_device()
-        _ints("Pool", device, table, lens, ref)
+        pointers = _ints("Pool", device, table, lens, ref)
         if table.dim() != 2 or lens.shape != table.shape[:1] or ref.shape != (self.shape.num_blocks,):
             raise MlaError(MLA_ERR_INVALID, "Pool")
-        c = mla_pool(_ptr(table), _ptr(lens), _ptr(ref), table.shape[0], table.shape[1])
+        c = mla_pool(*pointers, table.shape[0], table.shape[1])
         object.__setattr__(self, "_c", c)
-        object.__setattr__(self, "_ref", ctypes.byref(c))
-        object.__setattr__(self, "_device", device)
+        object.__setattr__(self, "_args", (self.shape._ref(), ctypes.byref(c)))
+        object.__setattr__(self, "_at", (device, table.shape[0]))
 
     @classmethod
     def allocate(cls, shape: Shape, max_seqs: int, max_blocks_per_seq: int, device="cuda") -> "Pool":
@@ -444,31 +466,20 @@ class Caches:
                     or any(t.get_device() != device or not t.is_contiguous() for t in planes)):
                 raise MlaError(MLA_ERR_INVALID, "Caches")
         object.__setattr__(self, "caches", caches)
-        object.__setattr__(self, "_c", (mla_cache * len(caches))(*(c.c() for c in caches)))
+        c = (mla_cache * len(caches))(*(c.c() for c in caches))
+        object.__setattr__(self, "_args", (s._ref(), c, len(caches)))
         object.__setattr__(self, "_device", device)
-
-
-def _current_device() -> int:
-    import torch
-    return torch.cuda.current_device()
-
-
-def _copy_list(where, device, copies, num_copies, room) -> None:
-    _ints(where, device, copies, num_copies)
-    if copies.dim() != 2 or copies.shape[1] != 4 or copies.shape[0] < room or num_copies.numel() < 1:
-        raise MlaError(MLA_ERR_INVALID, where)
 
 
 def mla_pool_resize(pool: Pool, new_lens, copies, num_copies, num_free=None, status=None, stream=None) -> None:
     """Sequences get the lengths new_lens [max_seqs] (see include/mla.h); copies
     [>= max_seqs, 4] and num_copies [1] list what mla_cache_copy then has to move."""
-    lib, device = load_library(), _current_device()
-    _ints("mla_pool_resize", device, new_lens, num_free, status, pool.seq_lens)
-    _copy_list("mla_pool_resize", device, copies, num_copies, pool.seq_lens.shape[0])
-    if new_lens.shape != pool.seq_lens.shape:
+    device, stream = _here(stream)
+    new, lst, num, free, word = _ints("mla_pool_resize", device, new_lens, copies, num_copies, num_free, status)
+    _check_list("mla_pool_resize", copies, num_copies, pool._at[1])
+    if pool._at != (device, new_lens.numel()):
         raise MlaError(MLA_ERR_INVALID, "mla_pool_resize")
-    _check(lib.mla_pool_resize(pool.shape._ref(), pool._ref, _ptr(new_lens), _ptr(copies), _ptr(num_copies),
-                               _ptr(num_free), _ptr(status), _stream(stream)), "mla_pool_resize")
+    _check(load_library().mla_pool_resize(*pool._args, new, lst, num, free, word, stream), "mla_pool_resize")
 
 
 def mla_pool_fork(pool: Pool, parents, children, copies, num_copies, lens=None, num_free=None, status=None,
@@ -476,39 +487,38 @@ def mla_pool_fork(pool: Pool, parents, children, copies, num_copies, lens=None, 
     """Sequences children [n], empty before, begin as the first lens [n] tokens (None: all) of
     parents [n] (see include/mla.h); copies [>= n, 4] and num_copies [1] list what mla_cache_copy
     then has to move."""
-    lib, device = load_library(), _current_device()
+    device, stream = _here(stream)
     n = parents.numel()
-    _ints("mla_pool_fork", device, parents, children, lens, num_free, status, pool.seq_lens)
-    _copy_list("mla_pool_fork", device, copies, num_copies, n)
-    if children.numel() != n or (lens is not None and lens.numel() != n):
+    a, c, some, lst, num, free, word = _ints("mla_pool_fork", device, parents, children, lens, copies, num_copies, num_free,
+                                             status)
+    _check_list("mla_pool_fork", copies, num_copies, n)
+    if pool._at[0] != device or children.numel() != n or (lens is not None and lens.numel() != n):
         raise MlaError(MLA_ERR_INVALID, "mla_pool_fork")
-    _check(lib.mla_pool_fork(pool.shape._ref(), pool._ref, n, _ptr(parents), _ptr(children), _ptr(lens), _ptr(copies),
-                             _ptr(num_copies), _ptr(num_free), _ptr(status), _stream(stream)), "mla_pool_fork")
+    _check(load_library().mla_pool_fork(*pool._args, n, a, c, some, lst, num, free, word, stream), "mla_pool_fork")
 
 
 def mla_pool_compact(pool: Pool, copies, num_copies, num_live=None, status=None, stream=None) -> None:
     """Blocks in use move to the front of the pool, at most len(copies) of them (see
     include/mla.h); copies and num_copies [1] list what mla_cache_copy then has to move."""
-    lib, device = load_library(), _current_device()
-    _ints("mla_pool_compact", device, num_live, status, pool.seq_lens)
-    _copy_list("mla_pool_compact", device, copies, num_copies, 0)
-    _check(lib.mla_pool_compact(pool.shape._ref(), pool._ref, copies.shape[0], _ptr(copies), _ptr(num_copies),
-                                _ptr(num_live), _ptr(status), _stream(stream)), "mla_pool_compact")
+    device, stream = _here(stream)
+    lst, num, live, word = _ints("mla_pool_compact", device, copies, num_copies, num_live, status)
+    room = _check_list("mla_pool_compact", copies, num_copies, 0)
+    if pool._at[0] != device:
+        raise MlaError(MLA_ERR_INVALID, "mla_pool_compact")
+    _check(load_library().mla_pool_compact(*pool._args, room, lst, num, live, word, stream), "mla_pool_compact")
 
 
 def mla_cache_copy(caches, copies, num_copies, status=None, stream=None) -> None:
     """The copies that a pool call listed, in every cache of ``caches`` (a Caches, or one Cache;
     see include/mla.h)."""
-    lib, device = load_library(), _current_device()
+    device, stream = _here(stream)
     if isinstance(caches, Cache):
         caches = Caches((caches,))
-    _copy_list("mla_cache_copy", device, copies, num_copies, 0)
-    _ints("mla_cache_copy", device, status)
+    lst, num, word = _ints("mla_cache_copy", device, copies, num_copies, status)
+    room = _check_list("mla_cache_copy", copies, num_copies, 0)
     if caches._device != device:
         raise MlaError(MLA_ERR_INVALID, "mla_cache_copy")
-    c = caches._c
-    _check(lib.mla_cache_copy(caches.caches[0].shape._ref(), c, len(c), _ptr(copies), _ptr(num_copies),
-                              copies.shape[0], _ptr(status), _stream(stream)), "mla_cache_copy")
+    _check(load_library().mla_cache_copy(*caches._args, lst, num, room, word, stream), "mla_cache_copy")
 
 
 # ---------------------------------------------------------------- drafts
@@ -520,28 +530,27 @@ def mla_draft_accept(target_probs, draft_tokens, uniform, accepted, tokens, draf
     [B, K + 1], new_lens [B] (see include/mla.h). The probabilities' last dimension is dense;
     rows may lie further apart (a slice of a wider vocabulary)."""
     import torch
-    lib, device = load_library(), _current_device()
+    device, stream = _here(stream)
     B, rows, V = target_probs.shape
-    dtype = target_probs.dtype
-    _ints("mla_draft_accept", device, draft_tokens, draft_counts, seq_lens, accepted, tokens, new_lens, status)
-    ok = (dtype in (torch.float32, torch.bfloat16) and target_probs.get_device() == device
-          and draft_tokens.shape == (B, rows - 1) and tokens.shape == (B, rows) and accepted.shape == (B,)
+    dtype, K = target_probs.dtype, rows - 1
+    x, counts, lens, n, out, new, word = _ints("mla_draft_accept", device, draft_tokens, draft_counts, seq_lens, accepted,
+                                               tokens, new_lens, status)
+    p_stride, ok = _row_stride(target_probs)
+    ok = (ok and dtype in (torch.float32, torch.bfloat16) and target_probs.get_device() == device
+          and draft_tokens.shape == (B, K) and tokens.shape == (B, rows) and accepted.shape == (B,)
           and uniform.shape == (B, rows) and uniform.dtype is torch.float32 and uniform.get_device() == device
           and uniform.is_contiguous())
     for t in (draft_counts, seq_lens, new_lens):
         ok = ok and (t is None or t.shape == (B,))
-    p_stride, ok_p = _row_stride(target_probs)
-    q_stride, ok_q = 0, True
+    q, q_stride = None, 0
     if draft_probs is not None:
-        q_stride, ok_q = _row_stride(draft_probs)
-        ok = ok and draft_probs.dtype is dtype and draft_probs.get_device() == device and draft_probs.shape == (B, rows - 1, V)
-    if not (ok and ok_p and ok_q):
+        q, (q_stride, dense) = draft_probs.data_ptr(), _row_stride(draft_probs)
+        ok = ok and dense and draft_probs.dtype is dtype and draft_probs.get_device() == device and draft_probs.shape == (B, K, V)
+    if not ok:
         raise MlaError(MLA_ERR_INVALID, "mla_draft_accept")
-    code = lib.mla_draft_accept(B, rows - 1, V, MLA_DTYPE_F32 if dtype is torch.float32 else MLA_DTYPE_BF16,
-                                _ptr(target_probs), p_stride, _ptr(draft_probs), q_stride, _ptr(draft_tokens),
-                                _ptr(draft_counts), _ptr(uniform), _ptr(seq_lens), _ptr(accepted), _ptr(tokens),
-                                _ptr(new_lens), _ptr(status), _stream(stream))
-    _check(code, "mla_draft_accept")
+    _check(load_library().mla_draft_accept(B, K, V, MLA_DTYPE_F32 if dtype is torch.float32 else MLA_DTYPE_BF16,
+                                           target_probs.data_ptr(), p_stride, q, q_stride, x, counts, uniform.data_ptr(), lens,
+                                           n, out, new, word, stream), "mla_draft_accept")
 
 
 def _row_stride(t):

@@ -633,7 +633,8 @@ static mla_status pool_params(const mla_shape *s, const mla_pool *pool, int32_t 
     mla_status st = check_shape(s);
     if (st != MLA_OK) return st;
     if (!pool || !pool->block_table || !pool->seq_lens || !pool->ref_count || pool->max_seqs < 1 ||
-        pool->max_blocks_per_seq < 1 || room < 0 || (room > 0 && !copies) || !aligned16(copies) || !num_copies)
+        pool->max_blocks_per_seq < 1 || room < 0 || (room > 0 && !copies) || !aligned16(copies) || !num_copies ||
+        num_copies == left || num_copies == status || (left && left == status))
         return MLA_ERR_INVALID;
     if (pool->max_seqs > kPoolMax || (int64_t)pool->max_seqs * pool->max_blocks_per_seq > INT32_MAX ||
         s->num_blocks > INT32_MAX - 256)
@@ -701,7 +702,7 @@ mla_status mla_cache_copy(const mla_shape *shape, const mla_cache *caches, int32
     if (st != MLA_OK) return st;
     if (!caches || num_caches < 1 || max_copies < 0 || !num_copies || (max_copies > 0 && !copies) || !aligned16(copies))
         return MLA_ERR_INVALID;
-    if ((int64_t)max_copies * shape->block_size > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+    if ((int64_t)max_copies * shape->block_size > INT32_MAX - 65536) return MLA_ERR_UNSUPPORTED;     // tasks, and a grid more
     for (int32_t i = 0; i < num_caches; ++i) {           // all of them before anything is launched
         ReadParams r;
         st = read_params(shape, caches + i, r);

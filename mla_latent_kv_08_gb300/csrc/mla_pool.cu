@@ -5,11 +5,20 @@
 // places that need one: prefix sums over the places and over the counts give every place its
 // block, so that nothing depends on the order in which threads run. One cluster of CTAs, in
 // phases with a cluster barrier between them: (1) what each sequence needs, what is free, and
-// whether anything is wrong; (2) nothing at all if so; else blocks are handed out; (3) others
+// whether anything is wrong; (2) nothing at all if so, else blocks are handed out; (3) others
 // are given back. Blocks that a call gives back are not handed out by it.
 //
 // A warp counts a contiguous part of the counts, 128 at a time. Lists of table entries are
-// walked in pieces of kPiece entries, a warp a piece.
+// walked in pieces of kPiece entries, a warp a piece, whose loads are all in flight before the
+// first is used.
+//
+// Small calls are bound by their chain of dependent steps, of about half a microsecond each (a
+// load from L2 takes 0.4, a barrier 0.5 to 1): a step of 32 sequences takes 6.4 us, a fork of one 5.8,
+// compaction of 500 blocks 7.4. Large ones by the scattered accesses that 16 SMs can issue: 512
+// sequences that give back 100k entries of 290k blocks 20.5 us (with a step's free blocks looked
+// up one by one 32, with entries loaded one by one 36), 200 forks of 230k entries 17.6 us, 300k
+// entries that follow 70k moved blocks 27 us. Walking them in a second kernel on all SMs instead took
+// 19.3, 13.7 and 24.3 us, but two or three launches.
 #include "mla_internal.cuh"
 
 #include <cooperative_groups.h>
@@ -21,10 +30,9 @@ namespace cg = cooperative_groups;
 namespace mla {
 namespace {
 
-constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kPiece = 256;                  // table entries, 8 a lane
-
+constexpr int kMaxThreads = 1024, kMaxWarps = kMaxThreads / 32;
 constexpr int kMaxCluster = 16;
+constexpr int kPiece = 256;                  // table entries
 
 // What a CTA counted, and its flags.
 struct Counted {
@@ -33,11 +41,11 @@ struct Counted {
 
 struct Shared {
     Counted all[kMaxCluster];                // of every CTA of the cluster
-    int2 scan[kWarps];
-    int scan_two[kWarps];
-    int warp[kWarps];                        // this CTA's warps: free blocks
-    int ids[kWarps][128];                    // a step's free blocks
-    int free, flags, freed;
+    int2 scan[kMaxWarps];
+    int scan_two[kMaxWarps];
+    int warp[kMaxWarps];                     // this CTA's warps: free blocks
+    int ids[kMaxWarps][128];                 // a step's free blocks
+    int free, flags;
 };
 
 // Sums over the CTAs: free blocks before this one's, all; every CTA's flags.
@@ -66,7 +74,7 @@ struct Three {
     int x, y, z;
 };
 __device__ __forceinline__ Three scan_three(Three v, Shared &sh, Three &total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     Three in = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -81,8 +89,8 @@ __device__ __forceinline__ Three scan_three(Three v, Shared &sh, Three &total) {
     }
     __syncthreads();
     // every warp adds the others' sums up for itself
-    const int2 w = sh.scan[lane];
-    const int wz = sh.scan_two[lane];
+    const int2 w = lane < warps ? sh.scan[lane] : make_int2(0, 0);
+    const int wz = lane < warps ? sh.scan_two[lane] : 0;
     const bool before = lane < warp;
     const Three base = {__reduce_add_sync(0xffffffffu, before ? w.x : 0), __reduce_add_sync(0xffffffffu, before ? w.y : 0),
                         __reduce_add_sync(0xffffffffu, before ? wz : 0)};
@@ -90,11 +98,15 @@ __device__ __forceinline__ Three scan_three(Three v, Shared &sh, Three &total) {
     return {base.x + in.x - v.x, base.y + in.y - v.y, base.z + in.z - v.z};
 }
 
-// The part of the counts that warp w of all counts, in steps of 128.
-__device__ __forceinline__ int part_begin(int N, int64_t w, int64_t warps) {
-    const int64_t steps = (N + 127ll) / 128;
-    return (int)min((int64_t)N, steps * w / warps * 128);
-}
+// The part of the counts that a warp counts, in steps of 128: `each` blocks a warp.
+struct Parts {
+    int64_t each;
+    int N;
+    __device__ __forceinline__ Parts(int N, int warps) : each((N + 127ll) / 128), N(N) {
+        each = ((unsigned)each + (unsigned)warps - 1) / (unsigned)warps * 128ll;
+    }
+    __device__ __forceinline__ int begin(int w) const { return (int)min((int64_t)N, w * each); }
+};
 
 // Whether blocks i0 + lane + 32 k below `end`, k = 0 .. 3, are free.
 struct Free4 {
@@ -114,8 +126,8 @@ __device__ __forceinline__ Free4 free4(const int32_t *ref, int i0, int end) {
 }
 
 // Counts the free blocks of every warp's part into sh.warp and sh.free.
-__device__ __forceinline__ void count_free(const PoolParams &p, Shared &sh, int64_t w, int64_t warps) {
-    const int lo = part_begin(p.N, w, warps), hi = part_begin(p.N, w + 1, warps);
+__device__ __forceinline__ void count_free(const PoolParams &p, Shared &sh, const Parts &parts, int w) {
+    const int lo = parts.begin(w), hi = parts.begin(w + 1);
     int n = 0;
 #pragma unroll 4
     for (int i0 = lo; i0 < hi; i0 += 128) {
@@ -133,9 +145,9 @@ __device__ __forceinline__ void count_free(const PoolParams &p, Shared &sh, int6
 // a step are gathered first, so that whole warps look their places up.
 __device__ __forceinline__ uint32_t lanes_below() { return (1u << (threadIdx.x & 31)) - 1; }
 template <typename F>
-__device__ __forceinline__ void hand_out(const PoolParams &p, Shared &sh, int before, int need, int64_t w, int64_t warps, F give) {
+__device__ __forceinline__ void hand_out(const PoolParams &p, Shared &sh, const Parts &parts, int w, int before, int need, F give) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int lo = part_begin(p.N, w, warps), hi = part_begin(p.N, w + 1, warps);
+    const int lo = parts.begin(w), hi = parts.begin(w + 1);
     int rank = before + __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp[lane] : 0);
     Free4 f = free4(p.ref, lo, rank < need ? hi : lo);
     for (int i0 = lo; i0 < hi && rank < need; i0 += 128) {
@@ -155,18 +167,17 @@ __device__ __forceinline__ void hand_out(const PoolParams &p, Shared &sh, int be
     }
 }
 
-// f(list, entries' first index, their values, which there are) for the entries of lists whose
-// pieces `pieces` counts: list b has the entries range(b).x .. range(b).y - 1 of the row
-// row(b). A lane gets kLane entries of a piece, 32 apart, all of them loaded before any is
-// used. All warps of the cluster take part.
+// f(list, first entry, values, how many) for the entries of lists whose pieces `pieces` counts:
+// list b has the entries range(b).x .. range(b).y - 1 of the row row(b). A lane gets kLane
+// entries of a piece, 32 apart. All warps of the cluster take part.
 constexpr int kLane = kPiece / 32;
 template <typename Range, typename Row, typename F>
-__device__ __forceinline__ void walk(const int *pieces, int lists, int64_t w, int64_t warps, Range range, Row row, F f) {
+__device__ __forceinline__ void walk(const int *pieces, int lists, int w, int warps, Range range, Row row, F f) {
     const int lane = threadIdx.x & 31, total = pieces[lists];
-    for (int64_t c = w; c < total; c += warps) {
-        const int b = find_seq(pieces, lists, (int)c);
+    for (int c = w; c < total; c += warps) {
+        const int b = find_seq(pieces, lists, c);
         const int2 r = range(b);
-        const int first = r.x + ((int)c - pieces[b]) * kPiece + lane;
+        const int first = r.x + (c - pieces[b]) * kPiece + lane;
         const int32_t *from = row(b) + first;
         int v[kLane];
 #pragma unroll
@@ -202,38 +213,25 @@ __device__ __forceinline__ Change change_of(const PoolParams &p, int b) {
     return c;
 }
 
-// Gives back the blocks v of the entries at, at + 32, ..; how many are free now.
-__device__ __forceinline__ int give_back(const PoolParams &p, int32_t *at, const int (&v)[kLane], int n) {
-    int old[kLane], freed = 0;
-#pragma unroll
-    for (int k = 0; k < kLane; ++k)
-        if (k < n && v[k] >= 0) {
-            old[k] = atomicSub(&p.ref[v[k]], 1);
-            at[32 * k] = -1;
-        }
-#pragma unroll
-    for (int k = 0; k < kLane; ++k) freed += k < n && v[k] >= 0 && old[k] == 1;
-    return freed;
-}
-
-__global__ void __launch_bounds__(kThreads) resize_kernel(const PoolParams p) {
+__global__ void __launch_bounds__(kMaxThreads, 1) resize_kernel(const PoolParams p) {
     extern __shared__ int dyn[];
     __shared__ Shared sh;
     int *s_takes = dyn, *s_pieces = dyn + p.S + 1;       // [S + 1] each
-    int *s_place = s_pieces + p.S + 1;                   // [S] first entry that takes a block; ~(copy's number) for a cut
+    int *s_place = s_pieces + p.S + 1;                   // [S] first entry that changes; ~(copy's number) for a cut's copy
     const cg::cluster_group cl = cg::this_cluster();
     auto here = cl.barrier_arrive();
-    const int tid = threadIdx.x;
-    const int64_t w = (int64_t)cl.block_rank() * kWarps + (tid >> 5), warps = (int64_t)cl.num_blocks() * kWarps;
-    const int64_t thread = (int64_t)cl.block_rank() * kThreads + tid, threads = (int64_t)cl.num_blocks() * kThreads;
+    const Parts parts(p.N, gridDim.x * blockDim.x / 32);
+    const int tid = threadIdx.x, block = blockDim.x;
+    const int thread = blockIdx.x * block + tid, threads = gridDim.x * block;       // of the cluster
+    const int w = thread >> 5, warps = threads >> 5;
     pdl_wait();
     pdl_trigger();
-    if (tid == 0) sh.free = sh.flags = sh.freed = 0;
+    if (tid == 0) sh.free = sh.flags = 0;
     // every CTA: what each sequence takes, the pieces of what it gives back, whether its last
     // block is replaced
     Three sum = {0, 0, 0};
     int flags = 0;
-    for (int b0 = 0; b0 < p.S; b0 += kThreads) {
+    for (int b0 = 0; b0 < p.S; b0 += block) {
         const int b = b0 + tid;
         Change c = {0, 0, -1, 0};
         if (b < p.S) c = change_of(p, b);
@@ -243,7 +241,7 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const PoolParams p) {
         if (b < p.S) {
             s_takes[b] = sum.x + at.x;
             s_pieces[b] = sum.y + at.y;
-            s_place[b] = c.old >= 0 ? ~(sum.z + at.z) : c.held;
+            s_place[b] = c.old >= 0 ? ~(sum.z + at.z) : min(c.held, c.wanted);
         }
         sum = {sum.x + all.x, sum.y + all.y, sum.z + all.z};
     }
@@ -260,7 +258,7 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const PoolParams p) {
             for (int k = 0; k < kLane; ++k)
                 if (k < n && (v[k] < 0 || v[k] >= p.N)) flags |= FLAG_BAD_BLOCK;
         });
-    count_free(p, sh, w, warps);
+    count_free(p, sh, parts, w);
     if (flags) atomicOr(&sh.flags, flags);
     Totals t = exchange(cl, here, sh);
     if (!t.flags && takes > t.all) t.flags = FLAG_FULL;
@@ -272,7 +270,7 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const PoolParams p) {
         }
         return;
     }
-    hand_out(p, sh, t.before, takes, w, warps, [&](int r, int block) {
+    hand_out(p, sh, parts, w, t.before, takes, [&](int r, int block) {
         const int b = find_seq(s_takes, p.S, r), place = s_place[b];
         int32_t *at = p.table + (size_t)b * p.W + place + (r - s_takes[b]);
         if (place < 0) {                     // the cut's own copy of a shared block
@@ -283,42 +281,58 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const PoolParams p) {
         *at = block;
         p.ref[block] = 1;
     });
-    cl.sync();                               // all free blocks have been looked at
-    int freed = 0;
-    walk(s_pieces, p.S, w, warps, given, row, [&](int b, int j, const int (&v)[kLane], int n) {
-        freed += give_back(p, p.table + (size_t)b * p.W + j, v, n);
-    });
-    for (int64_t i = thread; i < splits; i += threads) freed += atomicSub(&p.ref[p.copies[i].x], 1) == 1;
-    freed = __reduce_add_sync(0xffffffffu, freed);
-    if ((tid & 31) == 0 && freed) atomicAdd(&cl.map_shared_rank(&sh, 0)->freed, freed);
-    cl.sync();                               // lengths have been read
-    for (int64_t b = thread; b < p.S; b += threads) p.lens[b] = p.new_lens[b];
+    for (int b = thread; b < p.S; b += threads) p.lens[b] = p.new_lens[b];
     if (thread == 0) {
         *p.num_copies = splits;
-        if (p.left) *p.left = t.all - takes + sh.freed;
+        if (p.left) *p.left = t.all - takes;
     }
+    if (sum.y == 0 && splits == 0) return;   // nothing is given back
+    cl.sync();                               // all free blocks have been looked at
+    int freed = 0;
+    // lengths are new ones now: a row's entries end with its first -1
+    const auto rest = [&](int b) {
+        return make_int2(s_place[b] >= 0 ? s_place[b] : ceil_div(p.new_lens[b], p.bs), p.W);
+    };
+    walk(s_pieces, p.S, w, warps, rest, row, [&](int b, int j, const int (&v)[kLane], int n) {
+        int32_t *at = p.table + (size_t)b * p.W + j;
+        int old[kLane];
+#pragma unroll
+        for (int k = 0; k < kLane; ++k) {
+            old[k] = 0;
+            if (k < n && v[k] >= 0 && v[k] < p.N) {
+                old[k] = atomicSub(&p.ref[v[k]], 1);
+                at[32 * k] = -1;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kLane; ++k) freed += old[k] == 1;
+    });
+    for (int i = thread; i < splits; i += threads) freed += atomicSub(&p.ref[p.copies[i].x], 1) == 1;
+    freed = __reduce_add_sync(0xffffffffu, freed);
+    if (p.left && (tid & 31) == 0 && freed) atomicAdd(p.left, freed);
 }
 
 // ---- fork -------------------------------------------------------------------
 
-__global__ void __launch_bounds__(kThreads) fork_kernel(const PoolParams p) {
+__global__ void __launch_bounds__(kMaxThreads, 1) fork_kernel(const PoolParams p) {
     extern __shared__ int dyn[];
     __shared__ Shared sh;
     int *s_takes = dyn, *s_pieces = dyn + p.n + 1, *s_len = s_pieces + p.n + 1;         // [n + 1] each
     uint32_t *s_child = (uint32_t *)(s_len + p.n + 1);                                   // a bit a sequence
     const cg::cluster_group cl = cg::this_cluster();
     auto here = cl.barrier_arrive();
-    const int tid = threadIdx.x;
-    const int64_t w = (int64_t)cl.block_rank() * kWarps + (tid >> 5), warps = (int64_t)cl.num_blocks() * kWarps;
-    const int64_t thread = (int64_t)cl.block_rank() * kThreads + tid, threads = (int64_t)cl.num_blocks() * kThreads;
+    const Parts parts(p.N, gridDim.x * blockDim.x / 32);
+    const int tid = threadIdx.x, block = blockDim.x;
+    const int thread = blockIdx.x * block + tid, threads = gridDim.x * block;       // of the cluster
+    const int w = thread >> 5, warps = threads >> 5;
     pdl_wait();
     pdl_trigger();
     if (tid == 0) sh.free = sh.flags = 0;
-    for (int i = tid; i < (p.S + 31) / 32; i += kThreads) s_child[i] = 0;
+    for (int i = tid; i < (p.S + 31) / 32; i += block) s_child[i] = 0;
     __syncthreads();
     Three sum = {0, 0, 0};
     int flags = 0;
-    for (int i0 = 0; i0 < p.n; i0 += kThreads) {
+    for (int i0 = 0; i0 < p.n; i0 += block) {
         const int i = i0 + tid;
         int len = 0;
         if (i < p.n) {
@@ -359,13 +373,13 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const PoolParams p) {
             for (int k = 0; k < kLane; ++k)
                 if (k < n && (v[k] < 0 || v[k] >= p.N)) flags |= FLAG_BAD_BLOCK;
         });
-        for (int64_t i = thread; i < p.n; i += threads)
+        for (int i = thread; i < p.n; i += threads)
             if (s_len[i] % p.bs) {
-                const int t = parent((int)i)[s_len[i] / p.bs];
+                const int t = parent(i)[s_len[i] / p.bs];
                 if (t < 0 || t >= p.N) flags |= FLAG_BAD_BLOCK;
             }
     }
-    count_free(p, sh, w, warps);
+    count_free(p, sh, parts, w);
     if (flags) atomicOr(&sh.flags, flags);
     Totals t = exchange(cl, here, sh);
     if (!t.flags && takes > t.all) t.flags = FLAG_FULL;
@@ -377,7 +391,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const PoolParams p) {
         }
         return;
     }
-    hand_out(p, sh, t.before, takes, w, warps, [&](int r, int block) {
+    hand_out(p, sh, parts, w, t.before, takes, [&](int r, int block) {
         const int i = find_seq(s_takes, p.n, r), j = s_len[i] / p.bs;
         p.copies[r] = make_int4(parent(i)[j], block, 0, s_len[i] % p.bs);
         p.table[(size_t)p.children[i] * p.W + j] = block;
@@ -393,7 +407,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const PoolParams p) {
                 atomicAdd(&p.ref[v[k]], 1);
             }
     });
-    for (int64_t i = thread; i < p.n; i += threads) p.lens[p.children[i]] = s_len[i];
+    for (int i = thread; i < p.n; i += threads) p.lens[p.children[i]] = s_len[i];
     if (thread == 0) {
         *p.num_copies = takes;
         if (p.left) *p.left = t.all - takes;
@@ -420,20 +434,21 @@ __device__ __forceinline__ bool follow(const PoolParams &p, int first, int32_t *
     return bad;
 }
 
-__global__ void __launch_bounds__(kThreads) compact_kernel(const PoolParams p) {
+__global__ void __launch_bounds__(kMaxThreads, 1) compact_kernel(const PoolParams p) {
     extern __shared__ int dyn[];
     __shared__ Shared sh;
     int *s_pieces = dyn;                     // [S + 1]
     const cg::cluster_group cl = cg::this_cluster();
     auto here = cl.barrier_arrive();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t w = (int64_t)cl.block_rank() * kWarps + warp, warps = (int64_t)cl.num_blocks() * kWarps;
-    const int64_t thread = (int64_t)cl.block_rank() * kThreads + tid, threads = (int64_t)cl.num_blocks() * kThreads;
+    const Parts parts(p.N, gridDim.x * blockDim.x / 32);
+    const int tid = threadIdx.x, block = blockDim.x, lane = tid & 31, warp = tid >> 5;
+    const int thread = blockIdx.x * block + tid, threads = gridDim.x * block;       // of the cluster
+    const int w = thread >> 5, warps = threads >> 5;
     pdl_wait();
     pdl_trigger();
     if (tid == 0) sh.free = sh.flags = 0;
     int pieces = 0, flags = 0;
-    for (int b0 = 0; b0 < p.S; b0 += kThreads) {
+    for (int b0 = 0; b0 < p.S; b0 += block) {
         const int b = b0 + tid;
         int len = b < p.S ? p.lens[b] : 0;
         if (len < 0 || len > p.cap) {
@@ -447,7 +462,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const PoolParams p) {
     }
     if (tid == 0) s_pieces[p.S] = pieces;
     if (flags) atomicOr(&sh.flags, flags);
-    count_free(p, sh, w, warps);
+    count_free(p, sh, parts, w);
     const Totals t = exchange(cl, here, sh);
     const int live = p.N - t.all;
     if (t.flags) {
@@ -460,21 +475,12 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const PoolParams p) {
     }
     // free blocks below `live`: those of the warps before the one with id `live`, and some of
     // that one's own. There are as many used blocks from `live` on.
-    int64_t wl = 0;
-    for (int64_t a = 0, e = warps; a < e;) {             // the last warp that begins at or below `live`
-        const int64_t m = (a + e) / 2;
-        if (part_begin(p.N, m, warps) <= live) {
-            wl = m;
-            a = m + 1;
-        } else {
-            e = m;
-        }
-    }
-    const int cta = (int)(wl / kWarps);
-    int holes = lane < (int)(wl % kWarps) ? cl.map_shared_rank(&sh, cta)->warp[lane] : 0;
+    const int wl = min((int)((unsigned)live / (unsigned)parts.each), warps - 1);
+    const int cta = wl / (block / 32);
+    int holes = lane < wl % (block / 32) ? cl.map_shared_rank(&sh, cta)->warp[lane] : 0;
     if (lane < cta) holes += sh.all[lane].free;
 #pragma unroll 4
-    for (int i0 = part_begin(p.N, wl, warps); i0 < live; i0 += 128) {
+    for (int i0 = parts.begin(wl); i0 < live; i0 += 128) {
         const Free4 f = free4(p.ref, i0, live);
         holes += f.v[0] + f.v[1] + f.v[2] + f.v[3];
     }
@@ -482,7 +488,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const PoolParams p) {
     const int moves = min(holes, p.n);
     // the k-th used block from `live` on goes to the k-th free one below
     {
-        const int lo = part_begin(p.N, w, warps), hi = part_begin(p.N, w + 1, warps);
+        const int lo = parts.begin(w), hi = parts.begin(w + 1);
         int rank = t.before + __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp[lane] : 0);      // free blocks before
         Free4 f = free4(p.ref, lo, hi);
         for (int i0 = lo; i0 < hi; i0 += 128) {
@@ -534,35 +540,39 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const PoolParams p) {
     });
     if (flags) raise_flag(p.status, flags);
     cl.sync();
-    for (int64_t i = thread; i < moves; i += threads) p.ref[p.copies[i].x] = 0;
+    for (int i = thread; i < moves; i += threads) p.ref[p.copies[i].x] = 0;
 }
 
-// CTAs of the cluster, for `rows` rows of the table. Turnovers of 500 sequences, 33k entries and
-// blocks: 35.9 us with 1, 23.2 with 2, 12.6 with 8 and 16; of 512, 600k entries and 290k blocks: 159,
-// -, 32, 21. A step of 16 sequences, 1700 entries and blocks: 6.6 with 1 to 4, 6.9 with 16;
-// compaction, whose phases are more: 9.2 with 1, 9.5 with 2, 10.4 with 8, 11.5 with 16.
-unsigned cluster_size(const PoolParams &p, int32_t rows) {
+// The cluster, for `rows` rows of the table. Turnovers of 500 sequences, 33k entries and 19k blocks:
+// 35.9 us with one CTA of 1024 threads, 23.2 with 2, 12.6 with 8 and 16; of 512 sequences, 600k
+// entries and 290k blocks: 159, -, 32, 21. A step of 32 sequences, 4200 entries and 2400 blocks: 6.4 us
+// with 2 of 512 threads, 7.2 with 2 of 1024, 8.2 with 8 of 1024; compaction of 64, 16k entries and 12k
+// blocks 10.4 with 8 of 512, 11.7 with 8 of 1024, of 500, 33k and 24k: 15.1 and 12.4.
+struct Cluster {
+    unsigned ctas, threads;
+};
+Cluster cluster_of(const PoolParams &p, int32_t rows) {
     const int64_t n = (int64_t)rows * p.W + p.N;
-    return n <= 16384 ? 2 : n <= 131072 ? 8 : 16;
+    return {n <= 16384 ? 2u : n <= 131072 ? 8u : 16u, n <= 32768 ? 512u : 1024u};
 }
 
-cudaError_t launch(void (*kern)(PoolParams), const PoolParams &p, unsigned cluster, size_t smem, cudaStream_t st) {
+cudaError_t launch(void (*kern)(PoolParams), const PoolParams &p, Cluster c, size_t smem, cudaStream_t st) {
     if (smem > 24576) {                      // with the static part, more than a launch may have without asking
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    if (cluster > 8) {
+    if (c.ctas > 8) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(cluster);
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3(c.ctas);
+    cfg.blockDim = dim3(c.threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.x = c.ctas;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
@@ -574,14 +584,14 @@ cudaError_t launch(void (*kern)(PoolParams), const PoolParams &p, unsigned clust
 }  // namespace
 
 cudaError_t launch_pool_resize(const PoolParams &p, cudaStream_t st) {
-    return launch(resize_kernel, p, cluster_size(p, p.S), 3 * sizeof(int) * ((size_t)p.S + 1), st);
+    return launch(resize_kernel, p, cluster_of(p, p.S), 3 * sizeof(int) * ((size_t)p.S + 1), st);
 }
 cudaError_t launch_pool_fork(const PoolParams &p, cudaStream_t st) {
     const size_t smem = 3 * sizeof(int) * ((size_t)p.n + 1) + sizeof(uint32_t) * (((size_t)p.S + 31) / 32);
-    return launch(fork_kernel, p, cluster_size(p, p.n), smem, st);
+    return launch(fork_kernel, p, cluster_of(p, p.n), smem, st);
 }
 cudaError_t launch_pool_compact(const PoolParams &p, cudaStream_t st) {
-    return launch(compact_kernel, p, cluster_size(p, p.S), sizeof(int) * ((size_t)p.S + 1), st);
+    return launch(compact_kernel, p, cluster_of(p, p.S), sizeof(int) * ((size_t)p.S + 1), st);
 }
 
 }  // namespace mla

@@ -276,6 +276,23 @@ def test_captured_twice_and_on_two_streams(gpu_lib):
     _check(b, ob)
 
 
+def test_a_long_row_captured(gpu_lib):
+    """16 CTAs a sequence, asked for while a graph is captured."""
+    import torch
+    c, o = _case(21, 1, 2, 40000), _outputs(1, 2)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        _call(c, o)
+    for seed in (22, 23):
+        n = _case(seed, 1, 2, 40000)
+        for k in c:
+            if c[k] is not None:
+                c[k].copy_(n[k])
+        g.replay()
+        torch.cuda.synchronize()
+        _check(c, o)
+
+
 def test_the_binding_refuses(gpu_lib):
     import mla_latent_kv_08_gb300 as mla
     import torch

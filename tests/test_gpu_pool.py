@@ -224,6 +224,29 @@ def test_many_sequences_and_blocks(gpu_lib):
     assert p.compact() == 0
 
 
+def test_a_large_pool_captured(gpu_lib):
+    """A cluster of 16 CTAs and much shared memory, asked for while a graph is captured."""
+    import torch
+    S = 2000
+    p = Pair(S, 70, 60000, 4)
+    new = p.ints([(b * 31) % 90 for b in range(S)])
+    half = p.ints([(b * 31) % 90 // 2 for b in range(S)])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        p.mla.mla_pool_resize(p.pool, new, p.copies, p.n, status=p.status)
+        p.mla.mla_pool_resize(p.pool, half, p.copies, p.n, num_free=p.left, status=p.status)
+        p.mla.mla_pool_compact(p.pool, p.copies, p.n, status=p.status)
+    k = upkeep.Books(S, 70, 60000, 4)
+    for _ in range(2):
+        g.replay()
+        k.resize([(b * 31) % 90 for b in range(S)])
+        left = k.resize([(b * 31) % 90 // 2 for b in range(S)])[2]
+        k.compact(60000)
+        assert int(p.status) == 0 and int(p.left) == left
+        np.testing.assert_array_equal(p.pool.block_table.cpu().numpy(), k.table())
+        np.testing.assert_array_equal(p.pool.ref_count.cpu().numpy(), k.ref)
+
+
 def test_books_at_any_address(gpu_lib):
     """Arrays that begin four bytes behind a boundary."""
     import mla_latent_kv_08_gb300 as mla
