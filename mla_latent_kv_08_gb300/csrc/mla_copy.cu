@@ -6,8 +6,9 @@
 // once out. A CTA takes kPart bytes of an entry at a time, all of which it loads before it
 // stores any: kUnroll 16-byte loads a thread. 200 whole blocks of the 8-bit cache in 24 layers (403 MB
 // in and out): 63.5 us, 6.3 TB/s of the copy rate's 6.7 (array by array, with 8 CTAs an SM: 78 us;
-// 8 KB a task: 93 us, 32 KB: 71 us). 24 tails of 1 to 64 rows in 32 layers (61 MB): 13.4 us; 8 in one
-// layer: 2.0 us.
+// 8 KB a task: 93 us, 32 KB: 71 us). 24 tails of 1 to 64 rows in 32 layers (61 MB): 12.1 us (13.3 where
+// a bf16 row's one array goes the way of three); 8 in one layer: 1.7 us. An empty list costs 1 to 3 us,
+// by the CTAs that its room asks for: 16 an SM at most (24 would copy 1 to 2 % faster).
 #include "mla_internal.cuh"
 
 namespace mla {
@@ -17,8 +18,8 @@ constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
 constexpr int kPart = kThreads * kUnroll * 16;       // bytes of a CTA's task, at most
 
-// U: the type of a load, which divides every row's bytes.
-template <typename U>
+// U: the type of a load, which divides every row's bytes. ARRAYS: of a cache, 1 or 3.
+template <typename U, int ARRAYS>
 __global__ void __launch_bounds__(kThreads) copy_kernel(const __grid_constant__ CopyParams p, int part_rows, int parts) {
     pdl_wait();
     pdl_trigger();
@@ -40,26 +41,30 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(const __grid_constant__ 
         }
         const int rows = min(part_rows, c.w - at);
         if (rows <= 0 || c.x == c.y) continue;
-        // the rows are contiguous in each array; the arrays' pieces one behind the other
+        // the rows are contiguous in each array; the arrays' pieces are numbered one behind the other
         const size_t from = (size_t)c.x * p.bs + c.z + at, to = (size_t)c.y * p.bs + c.z + at;
-        const int m0 = rows * u0, m1 = m0 + rows * u1, m2 = m1 + rows * u2;
-        for (int i0 = tid; i0 < m2; i0 += kUnroll * kThreads) {
+        const int m0 = rows * u0, m1 = m0 + rows * u1, m = ARRAYS == 1 ? m0 : m1 + rows * u2;
+        const U *const s0 = p0 + from * u0, *const s1 = p1 + from * u1, *const s2 = p2 + from * u2;
+        U *const d0 = p0 + to * u0, *const d1 = p1 + to * u1, *const d2 = p2 + to * u2;
+        for (int i0 = tid; i0 < m; i0 += kUnroll * kThreads) {
             U v[kUnroll];
 #pragma unroll
             for (int j = 0; j < kUnroll; ++j) {
                 const int i = i0 + j * kThreads;
-                if (i < m2) v[j] = i < m0 ? p0[from * u0 + i] : i < m1 ? p1[from * u1 + (i - m0)] : p2[from * u2 + (i - m1)];
+                if (i < m) v[j] = ARRAYS == 1 || i < m0 ? s0[i] : i < m1 ? s1[i - m0] : s2[i - m1];
             }
 #pragma unroll
             for (int j = 0; j < kUnroll; ++j) {
                 const int i = i0 + j * kThreads;
-                if (i >= m2) break;
-                if (i < m0) p0[to * u0 + i] = v[j];
-                else if (i < m1) p1[to * u1 + (i - m0)] = v[j];
-                else p2[to * u2 + (i - m1)] = v[j];
+                if (i < m) *(ARRAYS == 1 || i < m0 ? d0 + i : i < m1 ? d1 + (i - m0) : d2 + (i - m1)) = v[j];
             }
         }
     }
+}
+
+template <typename U>
+cudaError_t launch(const CopyParams &p, dim3 grid, int part_rows, int parts, cudaStream_t st) {
+    return launch_pdl(p.row_bytes[1] ? copy_kernel<U, 3> : copy_kernel<U, 1>, grid, dim3(kThreads), 0, st, p, part_rows, parts);
 }
 
 }  // namespace
@@ -79,11 +84,11 @@ cudaError_t launch_copy(const CopyParams &p, int32_t layers, cudaStream_t st) {
     const int64_t tasks = (int64_t)p.max_copies * parts, most = (16ll * sms + layers - 1) / layers;
     const dim3 grid((unsigned)(tasks < most ? tasks : most), (unsigned)layers);
     switch (bits & -bits) {                  // rows begin at multiples of it in every array
-        case 16: return launch_pdl(copy_kernel<uint4>, grid, dim3(kThreads), 0, st, p, part_rows, parts);
-        case 8: return launch_pdl(copy_kernel<uint2>, grid, dim3(kThreads), 0, st, p, part_rows, parts);
-        case 4: return launch_pdl(copy_kernel<uint32_t>, grid, dim3(kThreads), 0, st, p, part_rows, parts);
-        case 2: return launch_pdl(copy_kernel<uint16_t>, grid, dim3(kThreads), 0, st, p, part_rows, parts);
-        default: return launch_pdl(copy_kernel<uint8_t>, grid, dim3(kThreads), 0, st, p, part_rows, parts);
+        case 16: return launch<uint4>(p, grid, part_rows, parts, st);
+        case 8: return launch<uint2>(p, grid, part_rows, parts, st);
+        case 4: return launch<uint32_t>(p, grid, part_rows, parts, st);
+        case 2: return launch<uint16_t>(p, grid, part_rows, parts, st);
+        default: return launch<uint8_t>(p, grid, part_rows, parts, st);
     }
 }
 
