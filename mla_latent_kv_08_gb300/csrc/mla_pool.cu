@@ -13,8 +13,8 @@
 // first is used.
 //
 // Small calls are bound by their chain of dependent steps, of about half a microsecond each (a
-// load from L2 takes 0.4, a barrier 0.5 to 1): a step of 32 sequences takes 6.4 us, a fork of one 5.8,
-// compaction of 500 blocks 7.4. Large ones by the scattered accesses that 16 SMs can issue: 512
+// load from L2 takes 0.4, a cluster's barrier 0.5 to 1): a step of 32 sequences takes 6.3 us, a fork of
+// one 4.8, compaction of 500 blocks 4.4. Large ones by the scattered accesses that 16 SMs can issue: 512
 // sequences that give back 100k entries of 290k blocks 20.5 us (with a step's free blocks looked
 // up one by one 32, with entries loaded one by one 36), 200 forks of 230k entries 17.6 us, 300k
 // entries that follow 70k moved blocks 27 us. Walking them in a second kernel on all SMs instead took
@@ -543,17 +543,20 @@ __global__ void __launch_bounds__(kMaxThreads, 1) compact_kernel(const PoolParam
     for (int i = thread; i < moves; i += threads) p.ref[p.copies[i].x] = 0;
 }
 
-// The cluster, for `rows` rows of the table. Turnovers of 500 sequences, 33k entries and 19k blocks:
-// 35.9 us with one CTA of 1024 threads, 23.2 with 2, 12.6 with 8 and 16; of 512 sequences, 600k
-// entries and 290k blocks: 159, -, 32, 21. A step of 32 sequences, 4200 entries and 2400 blocks: 6.4 us
-// with 2 of 512 threads, 7.2 with 2 of 1024, 8.2 with 8 of 1024; compaction of 64, 16k entries and 12k
-// blocks 10.4 with 8 of 512, 11.7 with 8 of 1024, of 500, 33k and 24k: 15.1 and 12.4.
+// The cluster, for `rows` rows of the table. A CTA alone is launched without one, and its barriers
+// cost little: a step of 16 sequences, 1000 entries and 700 blocks takes 4.6 us with 512 threads,
+// 5.3 with 1024, 5.8 with two CTAs of 512; compaction of them 4.6, 5.5, 7.6. Turnover of 64 sequences,
+// 4300 entries and 2600 blocks: 10.8, 9.0, 9.2; compaction 9.0, 7.9, 9.8. With 16k entries and 12k blocks
+// compaction takes 10.4 us with 8 CTAs of 512, 11.7 with 8 of 1024, 18.6 with one; with 33k and 24k
+// 15.1, 12.4 and 41. Turnover of 512 sequences, 600k entries and 290k blocks: 32 us with 8 of 1024, 21
+// with 16, 159 with one.
 struct Cluster {
     unsigned ctas, threads;
 };
 Cluster cluster_of(const PoolParams &p, int32_t rows) {
     const int64_t n = (int64_t)rows * p.W + p.N;
-    return {n <= 16384 ? 2u : n <= 131072 ? 8u : 16u, n <= 32768 ? 512u : 1024u};
+    if (n <= 12288) return {1, n <= 4096 ? 512u : 1024u};
+    return {n <= 131072 ? 8u : 16u, n <= 32768 ? 512u : 1024u};
 }
 
 cudaError_t launch(void (*kern)(PoolParams), const PoolParams &p, Cluster c, size_t smem, cudaStream_t st) {
@@ -571,13 +574,13 @@ cudaError_t launch(void (*kern)(PoolParams), const PoolParams &p, Cluster c, siz
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = c.ctas;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = c.ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = c.ctas > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
