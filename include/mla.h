@@ -442,7 +442,8 @@ typedef struct {
  * MLA_ERR_UNSUPPORTED where max_seqs * max_blocks_per_seq passes 2^31 - 1. */
 
 /* Sequences get other lengths, new_lens [max_seqs] int32 (0 .. max_blocks_per_seq *
- * block_size, at most 2^31 - 256; seq_lens[b] for no change). A longer one takes free blocks
+ * block_size, at most 2^31 - 256; seq_lens[b] for no change), an array other than the pool's
+ * seq_lens. A longer one takes free blocks
  * for its new tokens, a shorter one gives back the blocks behind its end (length 0: all).
  * Where a sequence is cut inside a block that others held before the call too, it takes a free
  * one instead, to which the list copies the rows that stay (room: max_seqs).
@@ -492,7 +493,8 @@ mla_status mla_cache_copy(const mla_shape *shape, const mla_cache *caches, int32
  *                 draws the token.
  *   seq_lens, new_lens   optional [B] int32 (both or neither, may be the same): new_lens[b] =
  *                 seq_lens[b] - K + accepted[b], the length that the drafts that stand leave of
- *                 one that counts all K of them.
+ *                 one that counts all K of them. With a pool's seq_lens, new_lens is an array
+ *                 of its own, for mla_pool_resize.
  *   accepted      [B] int32: how many drafts stand.
  *   tokens        [B, K + 1] int32: the drafts that stand, the token behind them, then -1.
  *   status        optional [1] int32 device word; flags are OR-ed into it.

@@ -411,10 +411,9 @@ def _ints(where, device, *tensors) -> list:
 
 def _check_list(where, copies, num_copies, room) -> int:
     """The entries that a list of copies has room for, at least ``room`` of them."""
-    n = copies.shape[0]
-    if copies.shape != (n, 4) or n < room or num_copies.numel() < 1:
+    if copies.dim() != 2 or copies.shape[1] != 4 or copies.shape[0] < room or num_copies.numel() < 1:
         raise MlaError(MLA_ERR_INVALID, where)
-    return n
+    return copies.shape[0]
 
 
 @dataclasses.dataclass(frozen=True)

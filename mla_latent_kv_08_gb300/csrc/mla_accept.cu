@@ -62,11 +62,12 @@ __device__ __forceinline__ Fixed weight(T p, T q, bool out) {
     return W == kWithout && out ? Fixed{0, 0} : Fixed{a.hi - kHi, a.lo - kLo};
 }
 
-// What a CTA found in its part of a row.
+// What a CTA found in its part of a row, and what every CTA finds for itself: whether anything
+// is wrong, how many drafts stand and which weights come behind them (below 0: left out).
 struct Part {
     u64 sum;
     float p;                                 // sum of the target's probabilities
-    int bad;
+    int bad, found;
 };
 struct Shared {
     Part all[2][kMaxCluster];                // of every CTA of the cluster, by pass
@@ -75,7 +76,7 @@ struct Shared {
     int bad, n;
 };
 
-// A warp's sums over [lo, hi) of a row; `bad`: this lane saw what is no probability. In the
+// A warp's sums over [lo, hi) of a row; `bad` is set where this lane saw what is no probability. In the
 // order of their bits as whole numbers, negative values and NaN come behind 1; only -0 has to
 // be told from them, where there is anything to tell.
 template <Weights W, typename T>
@@ -106,7 +107,6 @@ __device__ __forceinline__ u64 sum_part(const T *p, const T *q, int x, int lo, i
 #pragma unroll 4
     for (; i0 < hi; i0 += 32) add(p[i0], W == kRest ? q[i0] : (T)0.f, i0);
     s += units(hi_sum, lo_sum);
-    bad = false;
     if (most > 0x3f800000u)
         for (int i = lo + (threadIdx.x & 31); i < hi; i += 32)
             bad |= !is_probability(widen(p[i])) || (W == kRest && !is_probability(widen(q[i])));
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams a) 
     const bool short_len = len < K && k >= 0;
     bool bad = k > K || short_len;
     if (tid == 0) {
-        sh.n = bad ? 0 : k;
+        sh.n = bad ? 0 : max(k, 0);
         sh.bad = 0;
     }
     __syncthreads();
@@ -185,78 +185,81 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams a) 
     __syncthreads();
     bad |= sh.bad != 0;
     const int n = sh.n;
-    bool mine = false;                       // this CTA's part has the token
+    bool mine = false, left_out = false;     // this CTA's part has the token; the sequence has none
     u64 total = 0, base = 0, own = 0, t = 0;
-    cl.barrier_wait(std::move(here));
-    const T *p = (const T *)a.p + ((size_t)b * (K + 1) + max(n, 0)) * a.p_stride;
+    const T *p = (const T *)a.p + ((size_t)b * (K + 1) + n) * a.p_stride;
     const T *q = nullptr;
     int w = kPlain, out = -1;
+    const bool reads = !bad && k >= 0;
+    if (reads && n < k) {
+        w = a.q ? kRest : kWithout;
+        if (a.q) q = (const T *)a.q + ((size_t)b * K + n) * a.q_stride;
+        else out = x[n];
+    }
     // evenly over the warps of all CTAs, a group of tokens at a time where there are so many
     const int64_t warps = (int64_t)C * kWarps, group = V >= kGroup * warps ? kGroup : 32, groups = (V + group - 1) / group;
     const auto edge = [&](int64_t i) { return (int)min((int64_t)V, groups * i / warps * group); };
-    if (!bad && k >= 0) {
-        if (n < k) {
-            w = a.q ? kRest : kWithout;
-            if (a.q) q = (const T *)a.q + ((size_t)b * K + n) * a.q_stride;
-            else out = x[n];
-        }
-        for (int pass = 0;; ++pass) {
-            const int64_t at = (int64_t)rank * kWarps + warp;
-            const int lo = edge(at), hi = edge(at + 1);
-            float sum_p = 0.f;
-            bool odd = false;
-            u64 s = w == kRest ? sum_part<kRest>(p, q, out, lo, hi, sum_p, odd)
-                    : w == kWithout ? sum_part<kWithout>(p, q, out, lo, hi, sum_p, odd)
-                                    : sum_part<kPlain>(p, q, out, lo, hi, sum_p, odd);
+    cl.barrier_wait(std::move(here));
+    for (int pass = 0;; ++pass) {
+        const int64_t at = (int64_t)rank * kWarps + warp;
+        const int lo = edge(at), hi = reads ? edge(at + 1) : lo, found = k < 0 ? -1 : 4 * n + w;
+        float sum_p = 0.f;
+        bool odd = bad;
+        u64 s = w == kRest ? sum_part<kRest>(p, q, out, lo, hi, sum_p, odd)
+                : w == kWithout ? sum_part<kWithout>(p, q, out, lo, hi, sum_p, odd)
+                                : sum_part<kPlain>(p, q, out, lo, hi, sum_p, odd);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            sum_p = warp_sum(sum_p);
-            if (lane == 0) {
-                sh.warp[warp] = s;
-                sh.warp_p[warp] = sum_p;
-            }
-            if (odd) sh.bad = 1;
-            __syncthreads();
-            if (tid < C) {                   // every CTA tells every other
-                Part part = {0, 0.f, sh.bad};
-                for (int i = 0; i < kWarps; ++i) {
-                    part.sum += sh.warp[i];
-                    part.p += sh.warp_p[i];
-                }
-                cl.map_shared_rank(&sh, tid)->all[pass][rank] = part;
-            }
-            cl.sync();
-            total = 0;
-            sum_p = 0.f;
-            int odd_row = 0;
-            for (int c = 0; c < C; ++c) {
-                const Part part = sh.all[pass][c];
-                if (c == rank) {
-                    base = total;
-                    own = part.sum;
-                }
-                total += part.sum;
-                sum_p += part.p;
-                odd_row |= part.bad;
-            }
-            // probabilities add up to one; up to two, sums of units stay below 2^63
-            bad = odd_row || !(sum_p <= 2.f) || (total == 0 && w == kPlain);
-            if (bad || total > 0) break;
-            w = kPlain;                      // nothing is left of p - q: p itself
-            out = -1;
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        sum_p = warp_sum(sum_p);
+        if (lane == 0) {
+            sh.warp[warp] = s;
+            sh.warp_p[warp] = sum_p;
         }
-        if (!bad) {                          // t = floor(v total); for 1 the last token that has any weight
-            t = v < 1.f ? __umul64hi(__float2ull_rz(v * 0x1p64f), total) : total - 1;
-            mine = t >= base && t < base + own;
+        if (odd) sh.bad = 1;
+        __syncthreads();
+        if (tid < C) {                       // every CTA tells every other
+            Part part = {0, 0.f, sh.bad, found};
+            for (int i = 0; i < kWarps; ++i) {
+                part.sum += sh.warp[i];
+                part.p += sh.warp_p[i];
+            }
+            cl.map_shared_rank(&sh, tid)->all[pass][rank] = part;
         }
+        cl.sync();
+        // from here on all CTAs go the same way, whatever else: should they have found different
+        // things (inputs that another stream changes meanwhile), the sequence is refused
+        total = 0;
+        sum_p = 0.f;
+        int odd_row = 0;
+        for (int c = 0; c < C; ++c) {
+            const Part part = sh.all[pass][c];
+            if (c == rank) {
+                base = total;
+                own = part.sum;
+            }
+            total += part.sum;
+            sum_p += part.p;
+            odd_row |= part.bad | (part.found != sh.all[pass][0].found);
+        }
+        // probabilities add up to one; up to two, whole numbers stay far below 2^64
+        left_out = !odd_row && found < 0;
+        bad = odd_row || !(sum_p <= 2.f) || (total == 0 && w == kPlain && !left_out);
+        if (bad || left_out || total > 0) break;
+        w = kPlain;                          // nothing is left of p - q: p itself
+        out = -1;
+    }
+    if (!bad && !left_out) {                 // t = floor(v total); for 1 the last token that has any weight
+        t = v < 1.f ? __umul64hi(__float2ull_rz(v * 0x1p64f), total) : total - 1;
+        mine = t >= base && t < base + own;
     }
     if (rank == 0) {
-        const int stand = bad || k < 0 ? 0 : n;
+        const bool none = bad || left_out;
+        const int stand = none ? 0 : n;
         for (int i = tid; i <= K; i += kThreads)
-            if (bad || k < 0 || i != n) tokens[i] = i < stand ? x[i] : -1;
+            if (none || i != n) tokens[i] = i < stand ? x[i] : -1;
         if (tid == 0) {
             a.accepted[b] = stand;
-            if (a.new_lens) a.new_lens[b] = k < 0 || short_len ? len : len - K + stand;
+            if (a.new_lens) a.new_lens[b] = left_out || short_len ? len : len - K + stand;
             if (bad) raise_flag(a.status, short_len ? FLAG_BAD_LENGTH : FLAG_BAD_VALUE);
         }
     }

@@ -661,7 +661,7 @@ mla_status mla_pool_resize(const mla_shape *shape, const mla_pool *pool, const i
     PoolParams p;
     mla_status st = pool_params(shape, pool, copies, pool ? pool->max_seqs : 0, num_copies, num_free, status, p);
     if (st != MLA_OK) return st;
-    if (!new_lens) return MLA_ERR_INVALID;
+    if (!new_lens || new_lens == pool->seq_lens) return MLA_ERR_INVALID;
     p.new_lens = new_lens;
     if (launch_pool_resize(p, (cudaStream_t)stream) != cudaSuccess) return MLA_ERR_CUDA;
     prof_kernels(1);

@@ -34,9 +34,10 @@ constexpr int kMaxThreads = 1024, kMaxWarps = kMaxThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kPiece = 256;                  // table entries
 
-// What a CTA counted, and its flags.
+// What a CTA counted: free blocks of its part; and what every CTA finds for itself: the blocks
+// that the call takes, whether it gives any back, what is wrong.
 struct Counted {
-    int free, flags;
+    int free, takes, back, flags;
 };
 
 struct Shared {
@@ -48,24 +49,30 @@ struct Shared {
     int free, flags;
 };
 
-// Sums over the CTAs: free blocks before this one's, all; every CTA's flags.
+// Free blocks before this CTA's part, all of them; every CTA's flags.
 struct Totals {
     int before, all, flags;
 };
 // Every CTA tells every other, and waits for them. `here`: the cluster's arrival at the
-// kernel's start, without which a CTA's shared memory may not be there yet.
-__device__ __forceinline__ Totals exchange(const cg::cluster_group &cl, cg::cluster_group::arrival_token &here, Shared &sh) {
+// kernel's start, without which a CTA's shared memory may not be there yet. From here on
+// all CTAs go the same way, whatever else: should they have found different things (books that
+// another stream changes meanwhile), the call is refused.
+__device__ __forceinline__ Totals exchange(const cg::cluster_group &cl, cg::cluster_group::arrival_token &here, Shared &sh,
+                                           int takes, int back) {
     cl.barrier_wait(std::move(here));
     __syncthreads();
     if (threadIdx.x < cl.num_blocks())
-        cl.map_shared_rank(&sh, threadIdx.x)->all[cl.block_rank()] = Counted{sh.free, sh.flags};
+        cl.map_shared_rank(&sh, threadIdx.x)->all[cl.block_rank()] = Counted{sh.free, takes, back, sh.flags};
     cl.sync();
     Totals t = {0, 0, 0};
     for (unsigned c = 0; c < cl.num_blocks(); ++c) {
+        const Counted &o = sh.all[c];
         if (c == cl.block_rank()) t.before = t.all;
-        t.all += sh.all[c].free;
-        t.flags |= sh.all[c].flags;
+        t.all += o.free;
+        t.flags |= o.flags;
+        if (o.takes != sh.all[0].takes || o.back != sh.all[0].back) t.flags |= FLAG_BAD_LENGTH;
     }
+    if (!t.flags && sh.all[0].takes > t.all) t.flags = FLAG_FULL;
     return t;
 }
 
@@ -260,8 +267,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) resize_kernel(const PoolParams
         });
     count_free(p, sh, parts, w);
     if (flags) atomicOr(&sh.flags, flags);
-    Totals t = exchange(cl, here, sh);
-    if (!t.flags && takes > t.all) t.flags = FLAG_FULL;
+    const bool back = sum.y > 0 || splits > 0;
+    const Totals t = exchange(cl, here, sh, takes, back);
     if (t.flags) {                           // nothing is changed
         if (thread == 0) {
             raise_flag(p.status, t.flags);
@@ -286,7 +293,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) resize_kernel(const PoolParams
         *p.num_copies = splits;
         if (p.left) *p.left = t.all - takes;
     }
-    if (sum.y == 0 && splits == 0) return;   // nothing is given back
+    if (!back) return;
     cl.sync();                               // all free blocks have been looked at
     int freed = 0;
     // lengths are new ones now: a row's entries end with its first -1
@@ -307,7 +314,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1) resize_kernel(const PoolParams
 #pragma unroll
         for (int k = 0; k < kLane; ++k) freed += old[k] == 1;
     });
-    for (int i = thread; i < splits; i += threads) freed += atomicSub(&p.ref[p.copies[i].x], 1) == 1;
+    for (int i = thread; i < splits; i += threads) {
+        const int old = p.copies[i].x;
+        if (old >= 0 && old < p.N) freed += atomicSub(&p.ref[old], 1) == 1;
+    }
     freed = __reduce_add_sync(0xffffffffu, freed);
     if (p.left && (tid & 31) == 0 && freed) atomicAdd(p.left, freed);
 }
@@ -366,7 +376,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1) fork_kernel(const PoolParams p
         s_pieces[p.n] = sum.y;
     }
     const auto common = [&](int i) { return make_int2(0, s_len[i] / p.bs); };
-    const auto parent = [&](int i) { return p.table + (size_t)p.parents[i] * p.W; };
+    // (sequences have been found in range)
+    const auto sequence = [&](int i) { return min((unsigned)i, (unsigned)p.S - 1u); };
+    const auto parent = [&](int i) { return p.table + (size_t)sequence(p.parents[i]) * p.W; };
+    const auto child = [&](int i) { return p.table + (size_t)sequence(p.children[i]) * p.W; };
     if (!__syncthreads_or(flags)) {
         walk(s_pieces, p.n, w, warps, common, parent, [&](int, int, const int (&v)[kLane], int n) {
 #pragma unroll
@@ -381,8 +394,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) fork_kernel(const PoolParams p
     }
     count_free(p, sh, parts, w);
     if (flags) atomicOr(&sh.flags, flags);
-    Totals t = exchange(cl, here, sh);
-    if (!t.flags && takes > t.all) t.flags = FLAG_FULL;
+    const Totals t = exchange(cl, here, sh, takes, 0);
     if (t.flags) {                           // nothing is changed
         if (thread == 0) {
             raise_flag(p.status, t.flags);
@@ -394,20 +406,20 @@ __global__ void __launch_bounds__(kMaxThreads, 1) fork_kernel(const PoolParams p
     hand_out(p, sh, parts, w, t.before, takes, [&](int r, int block) {
         const int i = find_seq(s_takes, p.n, r), j = s_len[i] / p.bs;
         p.copies[r] = make_int4(parent(i)[j], block, 0, s_len[i] % p.bs);
-        p.table[(size_t)p.children[i] * p.W + j] = block;
+        child(i)[j] = block;
         p.ref[block] = 1;
     });
     // counts of blocks in use: no free one is mistaken for such a one, or the other way round
     walk(s_pieces, p.n, w, warps, common, parent, [&](int i, int j, const int (&v)[kLane], int n) {
-        int32_t *to = p.table + (size_t)p.children[i] * p.W + j;
+        int32_t *to = child(i) + j;
 #pragma unroll
         for (int k = 0; k < kLane; ++k)
-            if (k < n) {
+            if (k < n && v[k] >= 0 && v[k] < p.N) {
                 to[32 * k] = v[k];
                 atomicAdd(&p.ref[v[k]], 1);
             }
     });
-    for (int i = thread; i < p.n; i += threads) p.lens[p.children[i]] = s_len[i];
+    for (int i = thread; i < p.n; i += threads) p.lens[sequence(p.children[i])] = s_len[i];
     if (thread == 0) {
         *p.num_copies = takes;
         if (p.left) *p.left = t.all - takes;
@@ -463,7 +475,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) compact_kernel(const PoolParam
     if (tid == 0) s_pieces[p.S] = pieces;
     if (flags) atomicOr(&sh.flags, flags);
     count_free(p, sh, parts, w);
-    const Totals t = exchange(cl, here, sh);
+    const Totals t = exchange(cl, here, sh, 0, 0);
     const int live = p.N - t.all;
     if (t.flags) {
         if (thread == 0) {

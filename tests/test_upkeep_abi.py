@@ -76,15 +76,15 @@ def test_status_strings(lib):
 def test_resize_arguments(lib):
     import mla_latent_kv_08_gb300 as mla
 
-    def call(shape=_shape(), pool=None, new=FAKE, copies=FAKE, n=FAKE):
+    def call(shape=_shape(), pool=None, new=FAKE2, copies=FAKE, n=FAKE):
         pool = pool or _pool(mla)
         return lib.mla_pool_resize(ctypes.byref(shape.c()), ctypes.byref(pool), new, copies, n, None, None, None)
     for kw in [dict(pool=_pool(mla, **b)) for b in BAD_POOLS] + [
-            dict(new=None), dict(copies=None), dict(copies=ODD), dict(n=None), dict(shape=_shape(kv_lora_rank=7))]:
+            dict(new=None), dict(new=FAKE), dict(copies=None), dict(copies=ODD), dict(n=None), dict(shape=_shape(kv_lora_rank=7))]:
         assert call(**kw) == mla.MLA_ERR_INVALID, kw
     pool, s = _pool(mla), _shape().c()
     for outs in ((FAKE, None), (None, FAKE), (FAKE2, FAKE2)):            # of num_copies (FAKE), num_free and status two the same
-        assert lib.mla_pool_resize(ctypes.byref(s), ctypes.byref(pool), FAKE, FAKE, FAKE, *outs, None) == mla.MLA_ERR_INVALID
+        assert lib.mla_pool_resize(ctypes.byref(s), ctypes.byref(pool), FAKE2, FAKE, FAKE, *outs, None) == mla.MLA_ERR_INVALID
     assert call(pool=_pool(mla, max_seqs=16385)) == mla.MLA_ERR_UNSUPPORTED
     assert call(pool=_pool(mla, max_seqs=16384, max_blocks_per_seq=1 << 17)) == mla.MLA_ERR_UNSUPPORTED
     assert lib.mla_pool_resize(ctypes.byref(_shape().c()), None, FAKE, FAKE, FAKE, None, None, None) == mla.MLA_ERR_INVALID
