@@ -11,11 +11,11 @@
 //
 // A row of target and draft probabilities is read once, by a warp a contiguous part, split
 // over a cluster of CTAs; then the part that holds the token is read again. A call is bound by
-// its chain of dependent steps (drafts, their probabilities, the row, the cluster's sums, the
-// token: 4.7 us for 2000 tokens) and by loads in flight: a lane has 32 of each row. 32 sequences
-// of 131072 tokens: 10.9 us, 3.1 TB/s over all of it (8 loads of each row: 15.7; 78 us with a
-// CTA a sequence and conversions to 64 bits in hardware). One sequence of 32000: 5.3 us (19.5);
-// 64 of 50257 in bf16, drafts given: 7.7 us (19.4).
+// its chain of dependent steps (the drafts, their probabilities, the row, the cluster's sums, the
+// token: 4.1 us for 500 tokens) and, for a batch, by memory in the middle of it: a lane has 32 loads of
+// each row in flight. 32 sequences of 131072 tokens: 10.8 us, of which the rows take 4.6 at 6.0 TB/s
+// (8 loads of each row: 15.7; 78 us with a CTA a sequence and conversions to 64 bits in hardware). One
+// sequence of 32000: 4.7 us (19.5); 64 of 50257 in bf16, drafts given: 7.2 us (19.4).
 #include "mla_internal.cuh"
 
 #include <cooperative_groups.h>
@@ -118,7 +118,7 @@ __device__ __forceinline__ u64 sum_part(const T *p, const T *q, int x, int lo, i
 template <Weights W, typename T>
 __device__ __forceinline__ void find_token(const T *p, const T *q, int x, int lo, int hi, u64 base, u64 t, u64 *scan,
                                            int32_t *token) {
-    constexpr int kEach = 4;
+    constexpr int kEach = 8;
     for (int i0 = lo; i0 < hi; i0 += kEach * kThreads) {
         const int i = i0 + kEach * (int)threadIdx.x;
         u64 v[kEach], s = 0, all;
@@ -197,11 +197,12 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams a) 
         else out = x[n];
     }
     // evenly over the warps of all CTAs, a group of tokens at a time where there are so many
-    const int64_t warps = (int64_t)C * kWarps, group = V >= kGroup * warps ? kGroup : 32, groups = (V + group - 1) / group;
-    const auto edge = [&](int64_t i) { return (int)min((int64_t)V, groups * i / warps * group); };
+    const unsigned warps = C * kWarps, group = V >= kGroup * (int64_t)warps ? kGroup : 32;
+    const unsigned each = ((V + group - 1) / group + warps - 1) / warps * group;         // tokens of a warp
+    const auto edge = [&](int i) { return (int)min((int64_t)V, (int64_t)i * each); };
     cl.barrier_wait(std::move(here));
     for (int pass = 0;; ++pass) {
-        const int64_t at = (int64_t)rank * kWarps + warp;
+        const int at = rank * kWarps + warp;
         const int lo = edge(at), hi = reads ? edge(at + 1) : lo, found = k < 0 ? -1 : 4 * n + w;
         float sum_p = 0.f;
         bool odd = bad;
@@ -228,19 +229,19 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams a) 
         cl.sync();
         // from here on all CTAs go the same way, whatever else: should they have found different
         // things (inputs that another stream changes meanwhile), the sequence is refused
-        total = 0;
-        sum_p = 0.f;
-        int odd_row = 0;
-        for (int c = 0; c < C; ++c) {
-            const Part part = sh.all[pass][c];
-            if (c == rank) {
-                base = total;
-                own = part.sum;
-            }
-            total += part.sum;
-            sum_p += part.p;
-            odd_row |= part.bad | (part.found != sh.all[pass][0].found);
+        // lane c looks at CTA c's part
+        const Part part = lane < C ? sh.all[pass][lane] : Part{0, 0.f, 0, 0};
+        const bool odd_row = __any_sync(0xffffffffu, lane < C && (part.bad || part.found != sh.all[pass][0].found));
+        sum_p = warp_sum(part.p);
+        u64 upto = part.sum;
+#pragma unroll
+        for (int o = 1; o < kMaxCluster; o <<= 1) {
+            const u64 v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
         }
+        total = __shfl_sync(0xffffffffu, upto, kMaxCluster - 1);
+        own = __shfl_sync(0xffffffffu, part.sum, rank);
+        base = __shfl_sync(0xffffffffu, upto, rank) - own;
         // probabilities add up to one; up to two, whole numbers stay far below 2^64
         left_out = !odd_row && found < 0;
         bad = odd_row || !(sum_p <= 2.f) || (total == 0 && w == kPlain && !left_out);
@@ -264,22 +265,30 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams a) 
         }
     }
     if (!mine) return;
-    u64 from = base;
-    int i = 0;
-    for (; i < kWarps - 1 && t >= from + sh.warp[i]; ++i) from += sh.warp[i];
-    const int lo = edge((int64_t)rank * kWarps + i), hi = edge((int64_t)rank * kWarps + i + 1);
+    // the warp whose part has it: the last of those that begin at or before t
+    u64 from = lane < kWarps ? sh.warp[lane] : 0;
+    const u64 its = from;
+#pragma unroll
+    for (int o = 1; o < kWarps; o <<= 1) {
+        const u64 v = __shfl_up_sync(0xffffffffu, from, o);
+        if (lane >= o) from += v;
+    }
+    from += base - its;
+    const int i = 31 - __clz(__ballot_sync(0xffffffffu, lane < kWarps && from <= t));
+    from = __shfl_sync(0xffffffffu, from, i);
+    const int lo = edge(rank * kWarps + i), hi = edge(rank * kWarps + i + 1);
     if (w == kRest) find_token<kRest>(p, q, out, lo, hi, from, t, sh.scan, tokens + n);
     else if (w == kWithout) find_token<kWithout>(p, q, out, lo, hi, from, t, sh.scan, tokens + n);
     else find_token<kPlain>(p, q, out, lo, hi, from, t, sh.scan, tokens + n);
 }
 
-// CTAs a sequence: up to about 256 in all, and no more than the row has work for. Beyond that the
-// launch of clusters costs more than the split gives (128 sequences of 32000 tokens: 15.1 us
+// CTAs a sequence: as many as there is room for at two an SM, and no more than the row has work for.
+// A second round of clusters costs more than the split gives (128 sequences of 32000 tokens: 15.1 us
 // with 1, 10.9 with 2, 20.0 with 4; 64 of 50257: 13.9 with 1, 7.7 with 4, 12.3 with 8; 16 of 131072:
-// 9.1 with 8, 10.5 with 16; 4 of them: 8.7 with 8, 6.5 with 16).
+// 9.1 with 8, 10.5 with 16; 4 of them: 8.7 with 8, 6.5 with 16; 150 of 32000: 14.2 with 1, 11.1 with 2).
 unsigned cluster_size(int32_t B, int32_t V) {
     unsigned C = 1;
-    while (C < (B <= 8 ? 16u : 8u) && 2 * C * (int64_t)B <= 256 && 1024ll * C < V) C *= 2;
+    while (C < (B <= 8 ? 16u : 8u) && 2 * C * (int64_t)B <= 304 && 1024ll * C < V) C *= 2;
     return C;
 }
 
