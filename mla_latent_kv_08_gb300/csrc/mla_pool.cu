@@ -46,7 +46,7 @@ struct Shared {
     int scan_two[kMaxWarps];
     int warp[kMaxWarps];                     // this CTA's warps: free blocks
     int ids[kMaxWarps][128];                 // a step's free blocks
-    int free, flags;
+    int flags;
 };
 
 // Free blocks before this CTA's part, all of them; every CTA's flags.
@@ -61,8 +61,11 @@ __device__ __forceinline__ Totals exchange(const cg::cluster_group &cl, cg::clus
                                            int takes, int back) {
     cl.barrier_wait(std::move(here));
     __syncthreads();
-    if (threadIdx.x < cl.num_blocks())
-        cl.map_shared_rank(&sh, threadIdx.x)->all[cl.block_rank()] = Counted{sh.free, takes, back, sh.flags};
+    if (threadIdx.x < 32) {
+        const int free = __reduce_add_sync(0xffffffffu, threadIdx.x < blockDim.x / 32 ? sh.warp[threadIdx.x] : 0);
+        if (threadIdx.x < cl.num_blocks())
+            cl.map_shared_rank(&sh, threadIdx.x)->all[cl.block_rank()] = Counted{free, takes, back, sh.flags};
+    }
     cl.sync();
     Totals t = {0, 0, 0};
     for (unsigned c = 0; c < cl.num_blocks(); ++c) {
@@ -132,7 +135,7 @@ __device__ __forceinline__ Free4 free4(const int32_t *ref, int i0, int end) {
     return f;
 }
 
-// Counts the free blocks of every warp's part into sh.warp and sh.free.
+// Counts the free blocks of every warp's part into sh.warp.
 __device__ __forceinline__ void count_free(const PoolParams &p, Shared &sh, const Parts &parts, int w) {
     const int lo = parts.begin(w), hi = parts.begin(w + 1);
     int n = 0;
@@ -142,10 +145,7 @@ __device__ __forceinline__ void count_free(const PoolParams &p, Shared &sh, cons
         n += f.v[0] + f.v[1] + f.v[2] + f.v[3];
     }
     n = __reduce_add_sync(0xffffffffu, n);
-    if ((threadIdx.x & 31) == 0) {
-        sh.warp[threadIdx.x >> 5] = n;
-        if (n) atomicAdd(&sh.free, n);
-    }
+    if ((threadIdx.x & 31) == 0) sh.warp[threadIdx.x >> 5] = n;
 }
 
 // give(rank, block) for each free block of rank below `need`, lowest first. The free ones of
@@ -203,8 +203,7 @@ struct Change {
     int held, wanted, old, flags;
     __device__ __forceinline__ int takes() const { return (wanted > held ? wanted - held : 0) + (old >= 0); }
 };
-__device__ __forceinline__ Change change_of(const PoolParams &p, int b) {
-    const int len = p.lens[b], to = p.new_lens[b];
+__device__ __forceinline__ Change change_of(const PoolParams &p, int b, int len, int to) {
     Change c = {0, 0, -1, 0};
     if (len < 0 || len > p.cap || to < 0 || to > p.cap) {
         c.flags = FLAG_BAD_LENGTH;
@@ -233,15 +232,20 @@ __global__ void __launch_bounds__(kMaxThreads, 1) resize_kernel(const PoolParams
     const int w = thread >> 5, warps = threads >> 5;
     pdl_wait();
     pdl_trigger();
-    if (tid == 0) sh.free = sh.flags = 0;
+    if (tid == 0) sh.flags = 0;
     // every CTA: what each sequence takes, the pieces of what it gives back, whether its last
     // block is replaced
     Three sum = {0, 0, 0};
-    int flags = 0;
+    int flags = 0, len = tid < p.S ? p.lens[tid] : 0, to = tid < p.S ? p.new_lens[tid] : 0;
+    count_free(p, sh, parts, w);             // while these are on their way
     for (int b0 = 0; b0 < p.S; b0 += block) {
         const int b = b0 + tid;
         Change c = {0, 0, -1, 0};
-        if (b < p.S) c = change_of(p, b);
+        if (b < p.S) c = change_of(p, b, len, to);
+        if (b + block < p.S) {
+            len = p.lens[b + block];
+            to = p.new_lens[b + block];
+        }
         flags |= c.flags;
         Three all;
         const Three at = scan_three({c.takes(), c.held > c.wanted ? ceil_div(c.held - c.wanted, kPiece) : 0, c.old >= 0}, sh, all);
@@ -265,7 +269,6 @@ __global__ void __launch_bounds__(kMaxThreads, 1) resize_kernel(const PoolParams
             for (int k = 0; k < kLane; ++k)
                 if (k < n && (v[k] < 0 || v[k] >= p.N)) flags |= FLAG_BAD_BLOCK;
         });
-    count_free(p, sh, parts, w);
     if (flags) atomicOr(&sh.flags, flags);
     const bool back = sum.y > 0 || splits > 0;
     const Totals t = exchange(cl, here, sh, takes, back);
@@ -337,16 +340,16 @@ __global__ void __launch_bounds__(kMaxThreads, 1) fork_kernel(const PoolParams p
     const int w = thread >> 5, warps = threads >> 5;
     pdl_wait();
     pdl_trigger();
-    if (tid == 0) sh.free = sh.flags = 0;
+    if (tid == 0) sh.flags = 0;
     for (int i = tid; i < (p.S + 31) / 32; i += block) s_child[i] = 0;
     __syncthreads();
     Three sum = {0, 0, 0};
-    int flags = 0;
+    int flags = 0, a = tid < p.n ? p.parents[tid] : 0, c = tid < p.n ? p.children[tid] : 0;
+    count_free(p, sh, parts, w);             // while these are on their way
     for (int i0 = 0; i0 < p.n; i0 += block) {
         const int i = i0 + tid;
         int len = 0;
         if (i < p.n) {
-            const int a = p.parents[i], c = p.children[i];
             if (a < 0 || a >= p.S || c < 0 || c >= p.S) {
                 flags |= FLAG_BAD_LENGTH;
             } else {
@@ -360,6 +363,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1) fork_kernel(const PoolParams p
                     len = 0;
                 }
             }
+        }
+        if (i + block < p.n) {
+            a = p.parents[i + block];
+            c = p.children[i + block];
         }
         Three all;
         const Three at = scan_three({len % p.bs != 0, ceil_div(len / p.bs, kPiece), 0}, sh, all);
@@ -392,7 +399,6 @@ __global__ void __launch_bounds__(kMaxThreads, 1) fork_kernel(const PoolParams p
                 if (t < 0 || t >= p.N) flags |= FLAG_BAD_BLOCK;
             }
     }
-    count_free(p, sh, parts, w);
     if (flags) atomicOr(&sh.flags, flags);
     const Totals t = exchange(cl, here, sh, takes, 0);
     if (t.flags) {                           // nothing is changed
@@ -458,7 +464,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) compact_kernel(const PoolParam
     const int w = thread >> 5, warps = threads >> 5;
     pdl_wait();
     pdl_trigger();
-    if (tid == 0) sh.free = sh.flags = 0;
+    if (tid == 0) sh.flags = 0;
     int pieces = 0, flags = 0;
     for (int b0 = 0; b0 < p.S; b0 += block) {
         const int b = b0 + tid;
