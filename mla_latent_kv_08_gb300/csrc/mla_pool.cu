@@ -8,7 +8,8 @@
 // whether anything is wrong; (2) nothing at all if so, else blocks are handed out; (3) others
 // are given back. Blocks that a call gives back are not handed out by it.
 //
-// A warp counts a contiguous part of the counts, 128 at a time. Lists of table entries are
+// A warp counts a contiguous part of the counts, 128 at a time; consecutive parts belong to
+// different CTAs, so that all of them hand out the lowest free blocks. Lists of table entries are
 // walked in pieces of kPiece entries, a warp a piece, whose loads are all in flight before the
 // first is used.
 //
@@ -34,22 +35,23 @@ constexpr int kMaxThreads = 1024, kMaxWarps = kMaxThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kPiece = 256;                  // table entries
 
-// What a CTA counted: free blocks of its part; and what every CTA finds for itself: the blocks
-// that the call takes, whether it gives any back, what is wrong.
-struct Counted {
-    int free, takes, back, flags;
+// What every CTA finds for itself: the blocks that the call takes, whether it gives any back,
+// what is wrong.
+struct Found {
+    int takes, back, flags;
 };
 
 struct Shared {
-    Counted all[kMaxCluster];                // of every CTA of the cluster
+    Found all[kMaxCluster];                  // of every CTA of the cluster
+    int free[kMaxCluster * kMaxWarps];       // free blocks of every warp's part
     int2 scan[kMaxWarps];
     int scan_two[kMaxWarps];
-    int warp[kMaxWarps];                     // this CTA's warps: free blocks
+    int warp[kMaxWarps];                     // this CTA's warps: free blocks of their parts
     int ids[kMaxWarps][128];                 // a step's free blocks
     int flags;
 };
 
-// Free blocks before this CTA's part, all of them; every CTA's flags.
+// Free blocks before this warp's part, all of them; every CTA's flags.
 struct Totals {
     int before, all, flags;
 };
@@ -58,20 +60,23 @@ struct Totals {
 // all CTAs go the same way, whatever else: should they have found different things (books that
 // another stream changes meanwhile), the call is refused.
 __device__ __forceinline__ Totals exchange(const cg::cluster_group &cl, cg::cluster_group::arrival_token &here, Shared &sh,
-                                           int takes, int back) {
+                                           int w, int warps, int takes, int back) {
+    const int tid = threadIdx.x, C = cl.num_blocks(), rank = cl.block_rank();
     cl.barrier_wait(std::move(here));
     __syncthreads();
-    if (threadIdx.x < 32) {
-        const int free = __reduce_add_sync(0xffffffffu, threadIdx.x < blockDim.x / 32 ? sh.warp[threadIdx.x] : 0);
-        if (threadIdx.x < cl.num_blocks())
-            cl.map_shared_rank(&sh, threadIdx.x)->all[cl.block_rank()] = Counted{free, takes, back, sh.flags};
-    }
+    if (tid < warps) cl.map_shared_rank(&sh, tid % C)->free[tid / C * C + rank] = sh.warp[tid / C];
+    if (tid < C) cl.map_shared_rank(&sh, tid)->all[rank] = Found{takes, back, sh.flags};
     cl.sync();
     Totals t = {0, 0, 0};
-    for (unsigned c = 0; c < cl.num_blocks(); ++c) {
-        const Counted &o = sh.all[c];
-        if (c == cl.block_rank()) t.before = t.all;
-        t.all += o.free;
+    for (int i = tid & 31; i < warps; i += 32) {
+        const int n = sh.free[i];
+        t.all += n;
+        t.before += i < w ? n : 0;
+    }
+    t.all = __reduce_add_sync(0xffffffffu, t.all);
+    t.before = __reduce_add_sync(0xffffffffu, t.before);
+    for (int c = 0; c < C; ++c) {
+        const Found &o = sh.all[c];
         t.flags |= o.flags;
         if (o.takes != sh.all[0].takes || o.back != sh.all[0].back) t.flags |= FLAG_BAD_LENGTH;
     }
@@ -155,7 +160,7 @@ template <typename F>
 __device__ __forceinline__ void hand_out(const PoolParams &p, Shared &sh, const Parts &parts, int w, int before, int need, F give) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int lo = parts.begin(w), hi = parts.begin(w + 1);
-    int rank = before + __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp[lane] : 0);
+    int rank = before;
     Free4 f = free4(p.ref, lo, rank < need ? hi : lo);
     for (int i0 = lo; i0 < hi && rank < need; i0 += 128) {
         const Free4 next = free4(p.ref, i0 + 128, hi);
@@ -229,7 +234,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) resize_kernel(const PoolParams
     const Parts parts(p.N, gridDim.x * blockDim.x / 32);
     const int tid = threadIdx.x, block = blockDim.x;
     const int thread = blockIdx.x * block + tid, threads = gridDim.x * block;       // of the cluster
-    const int w = thread >> 5, warps = threads >> 5;
+    const int w = (tid >> 5) * gridDim.x + blockIdx.x, warps = threads >> 5;
     pdl_wait();
     pdl_trigger();
     if (tid == 0) sh.flags = 0;
@@ -271,7 +276,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) resize_kernel(const PoolParams
         });
     if (flags) atomicOr(&sh.flags, flags);
     const bool back = sum.y > 0 || splits > 0;
-    const Totals t = exchange(cl, here, sh, takes, back);
+    const Totals t = exchange(cl, here, sh, w, warps, takes, back);
     if (t.flags) {                           // nothing is changed
         if (thread == 0) {
             raise_flag(p.status, t.flags);
@@ -337,7 +342,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) fork_kernel(const PoolParams p
     const Parts parts(p.N, gridDim.x * blockDim.x / 32);
     const int tid = threadIdx.x, block = blockDim.x;
     const int thread = blockIdx.x * block + tid, threads = gridDim.x * block;       // of the cluster
-    const int w = thread >> 5, warps = threads >> 5;
+    const int w = (tid >> 5) * gridDim.x + blockIdx.x, warps = threads >> 5;
     pdl_wait();
     pdl_trigger();
     if (tid == 0) sh.flags = 0;
@@ -400,7 +405,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) fork_kernel(const PoolParams p
             }
     }
     if (flags) atomicOr(&sh.flags, flags);
-    const Totals t = exchange(cl, here, sh, takes, 0);
+    const Totals t = exchange(cl, here, sh, w, warps, takes, 0);
     if (t.flags) {                           // nothing is changed
         if (thread == 0) {
             raise_flag(p.status, t.flags);
@@ -459,9 +464,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) compact_kernel(const PoolParam
     const cg::cluster_group cl = cg::this_cluster();
     auto here = cl.barrier_arrive();
     const Parts parts(p.N, gridDim.x * blockDim.x / 32);
-    const int tid = threadIdx.x, block = blockDim.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, block = blockDim.x, lane = tid & 31;
     const int thread = blockIdx.x * block + tid, threads = gridDim.x * block;       // of the cluster
-    const int w = thread >> 5, warps = threads >> 5;
+    const int w = (tid >> 5) * gridDim.x + blockIdx.x, warps = threads >> 5;
     pdl_wait();
     pdl_trigger();
     if (tid == 0) sh.flags = 0;
@@ -481,7 +486,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) compact_kernel(const PoolParam
     if (tid == 0) s_pieces[p.S] = pieces;
     if (flags) atomicOr(&sh.flags, flags);
     count_free(p, sh, parts, w);
-    const Totals t = exchange(cl, here, sh, 0, 0);
+    const Totals t = exchange(cl, here, sh, w, warps, 0, 0);
     const int live = p.N - t.all;
     if (t.flags) {
         if (thread == 0) {
@@ -494,9 +499,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) compact_kernel(const PoolParam
     // free blocks below `live`: those of the warps before the one with id `live`, and some of
     // that one's own. There are as many used blocks from `live` on.
     const int wl = min((int)((unsigned)live / (unsigned)parts.each), warps - 1);
-    const int cta = wl / (block / 32);
-    int holes = lane < wl % (block / 32) ? cl.map_shared_rank(&sh, cta)->warp[lane] : 0;
-    if (lane < cta) holes += sh.all[lane].free;
+    int holes = 0;
+    for (int i = lane; i < wl; i += 32) holes += sh.free[i];
 #pragma unroll 4
     for (int i0 = parts.begin(wl); i0 < live; i0 += 128) {
         const Free4 f = free4(p.ref, i0, live);
@@ -507,7 +511,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) compact_kernel(const PoolParam
     // the k-th used block from `live` on goes to the k-th free one below
     {
         const int lo = parts.begin(w), hi = parts.begin(w + 1);
-        int rank = t.before + __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp[lane] : 0);      // free blocks before
+        int rank = t.before;                 // free blocks before
         Free4 f = free4(p.ref, lo, hi);
         for (int i0 = lo; i0 < hi; i0 += 128) {
             const Free4 next = free4(p.ref, i0 + 128, hi);
