@@ -14,12 +14,12 @@
 // first is used.
 //
 // Small calls are bound by their chain of dependent steps, of about half a microsecond each (a
-// load from L2 takes 0.4, a cluster's barrier 0.5 to 1): a step of 32 sequences takes 6.3 us, a fork of
-// one 4.8, compaction of 500 blocks 4.4. Large ones by the scattered accesses that 16 SMs can issue: 512
-// sequences that give back 100k entries of 290k blocks 20.5 us (with a step's free blocks looked
-// up one by one 32, with entries loaded one by one 36), 200 forks of 230k entries 17.6 us, 300k
-// entries that follow 70k moved blocks 27 us. Walking them in a second kernel on all SMs instead took
-// 19.3, 13.7 and 24.3 us, but two or three launches.
+// load from L2 takes 0.4, a cluster's barrier 0.5 to 1): a step of 32 sequences takes 5.7 us, a fork of
+// one 4.7, compaction of 500 blocks 4.5. Large ones by the scattered accesses that 16 SMs can issue: 512
+// sequences that give back 100k entries of 290k blocks 19.6 us (with a step's free blocks looked
+// up one by one 32, with entries loaded one by one 36), 200 forks of 230k entries 16.6 us, 300k
+// entries that follow 70k moved blocks 27.6 us. Walking them in a second kernel on all SMs took 19.3,
+// 13.7 and 24.3 us when this took 21.1, 17.6 and 28.9, but two or three launches.
 #include "mla_internal.cuh"
 
 #include <cooperative_groups.h>

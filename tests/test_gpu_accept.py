@@ -276,6 +276,21 @@ def test_captured_twice_and_on_two_streams(gpu_lib):
     _check(b, ob)
 
 
+def test_rows_past_32_bits(gpu_lib):
+    """256 drafts over five million tokens: the last row begins 5 GB behind the first."""
+    import torch
+    K, V = 256, 5000003
+    p = torch.zeros((1, K + 1, V), device="cuda")
+    x = (torch.arange(K, device="cuda") * 19531 + 7).int().view(1, K)
+    p[0, torch.arange(K), x[0].long()] = 1.0
+    p[0, K, V - 3], p[0, K, 5] = 0.5, 0.5
+    for v, token in ((0.25, 5), (0.75, V - 3)):
+        c = dict(p=p, q=None, x=x, u=torch.full((1, K + 1), v, device="cuda"), counts=None, lens=None)
+        outs = _outputs(1, K)
+        _call(c, outs)
+        assert int(outs[0]) == K and int(outs[1][0, K]) == token and torch.equal(outs[1][:, :K], x) and int(outs[3]) == 0
+
+
 def test_a_long_row_captured(gpu_lib):
     """16 CTAs a sequence, asked for while a graph is captured."""
     import torch

@@ -224,6 +224,39 @@ def test_many_sequences_and_blocks(gpu_lib):
     assert p.compact() == 0
 
 
+def test_a_table_past_32_bits(gpu_lib):
+    """As many entries as a table may have (8.6 GB), the last rows in use, and half a billion blocks."""
+    import mla_latent_kv_08_gb300 as mla
+    import torch
+    S, W, N = 16384, 131071, 1 << 29
+    shape = mla.Shape(num_heads=8, kv_lora_rank=32, rope_dim=8, v_head_dim=8, block_size=2, num_blocks=N)
+    pool = mla.Pool.allocate(shape, S, W)
+    copies, n, left, status = (torch.zeros(v, dtype=torch.int32, device="cuda") for v in ((S, 4), (1,), (1,), (1,)))
+    pool.ref_count[:N - 200000] = 1                          # all but the last are somebody else's
+    new = torch.zeros(S, dtype=torch.int32, device="cuda")
+    new[S - 1], new[0] = 2 * W - 1, 3
+    mla.mla_pool_resize(pool, new, copies, n, num_free=left, status=status)
+    free = torch.arange(N - 200000, N, dtype=torch.int32, device="cuda")
+    assert int(status) == 0 and int(n) == 0 and int(left) == 200000 - 2 - W
+    assert torch.equal(pool.block_table[0, :2], free[:2]) and int(pool.block_table[0, 2]) == -1
+    assert torch.equal(pool.block_table[S - 1], free[2:2 + W])
+    one = torch.ones(1, dtype=torch.int32, device="cuda")
+    mla.mla_pool_fork(pool, (S - 1) * one, (S - 2) * one, copies, n, num_free=left, status=status)
+    assert int(status) == 0 and copies[0].tolist() == [int(free[1 + W]), int(free[2 + W]), 0, 1]
+    assert torch.equal(pool.block_table[S - 2, :W - 1], free[2:1 + W]) and int(pool.block_table[S - 2, W - 1]) == int(free[2 + W])
+    assert int(pool.ref_count[int(free[W])]) == 2 and int(pool.seq_lens[S - 2]) == 2 * W - 1
+    pool.ref_count[:1000] = 0                                # room at the front, for some of them
+    mla.mla_pool_compact(pool, copies, n, num_live=left, status=status)
+    assert int(status) == 0 and int(n) == 1000 and int(left) == N - 200000 + W + 3 - 1000
+    assert copies[:3, :2].tolist() == [[int(left) + i, i] for i in range(3)]
+    moved = torch.arange(1000, dtype=torch.int32, device="cuda")
+    assert torch.equal(pool.block_table[S - 1, W - 999:], moved[:999]) and int(pool.block_table[S - 2, W - 1]) == 999
+    new.zero_()
+    mla.mla_pool_resize(pool, new, copies, n, num_free=left, status=status)
+    assert int(status) == 0 and int(left) == 200000 + 1000 and not pool.ref_count[:1000].any()
+    assert int(pool.block_table[S - 2:].max()) == -1 and not pool.ref_count[N - 200000:].any()
+
+
 def test_a_large_pool_captured(gpu_lib):
     """A cluster of 16 CTAs and much shared memory, asked for while a graph is captured."""
     import torch
