@@ -416,7 +416,7 @@ def _check_list(where, copies, num_copies, room) -> int:
     return copies.shape[0]
 
 
-@dataclasses.dataclass(frozen=True)
+@dataclasses.dataclass(frozen=True, eq=False)
 class Pool:
     """The books of a paged cache (see ``mla_pool``): which blocks each sequence holds. One set
     serves the caches of all layers. Its tensors stay the same for its lifetime."""
@@ -446,7 +446,7 @@ class Pool:
                    torch.zeros(shape.num_blocks, dtype=torch.int32, device=device))
 
 
-@dataclasses.dataclass(frozen=True)
+@dataclasses.dataclass(frozen=True, eq=False)
 class Caches:
     """The caches of several layers, all of one shape, for mla_cache_copy. Keeps their pointers:
     their tensors stay the same for its lifetime."""

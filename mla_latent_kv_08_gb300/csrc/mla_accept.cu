@@ -284,11 +284,15 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams a) 
 
 // CTAs a sequence: as many as there is room for at two an SM, and no more than the row has work for.
 // A second round of clusters costs more than the split gives (128 sequences of 32000 tokens: 15.1 us
-// with 1, 10.9 with 2, 20.0 with 4; 64 of 50257: 13.9 with 1, 7.7 with 4, 12.3 with 8; 16 of 131072:
-// 9.1 with 8, 10.5 with 16; 4 of them: 8.7 with 8, 6.5 with 16; 150 of 32000: 14.2 with 1, 11.1 with 2).
+// with 1, 10.9 with 2, 20.0 with 4; 64 of 50257: 13.9 with 1, 7.7 with 4, 12.3 with 8; 150 of 32000: 14.2
+// with 1, 11.1 with 2), but for long rows, whose CTAs it spreads over the SMs (100 of 200000: 44.9 with
+// 2, 36.9 with 4; 40 of 131072: 14.7 with 4, 13.5 with 8; 60 of 100000: 16.0 with 4, 17.1 with 7). 16 for few
+// sequences (12 of 131072: 8.5 with 8, 7.0 with 16; 20: 9.1, 10.5). Odd numbers are slower than the next
+// lower power of two.
 unsigned cluster_size(int32_t B, int32_t V) {
+    const unsigned most = B <= 12 ? 16 : 8;
     unsigned C = 1;
-    while (C < (B <= 8 ? 16u : 8u) && 2 * C * (int64_t)B <= 304 && 1024ll * C < V) C *= 2;
+    while (C < most && 1024ll * C < V && 2 * C * (int64_t)B <= ((unsigned)V / C < 32768 ? 304 : 416)) C *= 2;
     return C;
 }
 

@@ -161,6 +161,7 @@ def test_handles_check_their_tensors():
             mla.Pool(s, *bad)
     with pytest.raises(AttributeError):
         pool.seq_lens = l                         # the handle keeps the pointers
+    assert pool == pool and pool != mla.Pool(s, t, l, r) and len({pool, pool}) == 1
     one, other = mla.Cache.allocate(s, device="cpu"), mla.Cache.allocate(_shape(num_blocks=9), device="cpu")
     mla.Caches([one, one])
     for bad in ([], [one, other], [mla.Cache(s)], [mla.Cache(s, latent=other.latent)],
