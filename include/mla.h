@@ -439,20 +439,22 @@ typedef struct {
  *     they were. Run mla_cache_copy on every layer's cache before the next call that appends
  *     to or reads the caches, or changes the books;
  *   - is one launch, without a workspace.
- * MLA_ERR_UNSUPPORTED where max_seqs * max_blocks_per_seq passes 2^31 - 1. */
+ * Calls on one pool are ordered by the caller (one stream, or events between streams).
+ * MLA_ERR_UNSUPPORTED where max_seqs * max_blocks_per_seq, or num_forks * max_blocks_per_seq,
+ * passes 2^31 - 1. */
 
 /* Sequences get other lengths, new_lens [max_seqs] int32 (0 .. max_blocks_per_seq *
  * block_size, at most 2^31 - 256; seq_lens[b] for no change), an array other than the pool's
- * seq_lens. A longer one takes free blocks
- * for its new tokens, a shorter one gives back the blocks behind its end (length 0: all).
- * Where a sequence is cut inside a block that others held before the call too, it takes a free
- * one instead, to which the list copies the rows that stay (room: max_seqs).
+ * seq_lens. A longer one takes free blocks for its new tokens, a shorter one gives back the
+ * blocks behind its end (length 0: all). Where a sequence is cut inside a block that others
+ * held before the call too, it takes a free one instead, to which the list copies the rows
+ * that stay (room: max_seqs).
  *   num_free   optional [1] int32 (device): free blocks after the call. */
 mla_status mla_pool_resize(const mla_shape *shape, const mla_pool *pool, const int32_t *new_lens, int32_t *copies,
                            int32_t *num_copies, int32_t *num_free, int32_t *status, void *stream);
 
 /* num_forks sequences begin as others: children[i], of length 0 before, gets the first lens[i]
- * tokens of parents[i] (lens NULL: all of them). It shares the full blocks of these; for the
+ * tokens of parents[i] (0 .. its length; lens NULL: all of them). It shares the full blocks of these; for the
  * rest it takes a block, to which the list copies the rows (room: num_forks, at most 16384).
  * A parent may appear several times, a child once. parents, children, lens: [num_forks] int32
  * (device). */
@@ -463,7 +465,8 @@ mla_status mla_pool_fork(const mla_shape *shape, const mla_pool *pool, int32_t n
 /* Blocks in use move to the front of the pool: with num_live of them, the k-th block in use
  * with an id of num_live or more goes to the k-th free one below, and table entries follow.
  * With a list too short for all (max_copies) the first max_copies of these move; further calls
- * move the others.
+ * move the others. A table entry out of range is left as it is and raises MLA_ERR_BOUNDS; the
+ * others follow all the same.
  *   num_live   optional [1] int32 (device): blocks in use. */
 mla_status mla_pool_compact(const mla_shape *shape, const mla_pool *pool, int32_t max_copies, int32_t *copies,
                             int32_t *num_copies, int32_t *num_live, int32_t *status, void *stream);
