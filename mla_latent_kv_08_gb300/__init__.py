@@ -536,11 +536,10 @@ def mla_draft_accept(target_probs, draft_tokens, uniform, accepted, tokens, draf
                                                tokens, new_lens, status)
     p_stride, ok = _row_stride(target_probs)
     ok = (ok and dtype in (torch.float32, torch.bfloat16) and target_probs.get_device() == device
-          and draft_tokens.shape == (B, K) and tokens.shape == (B, rows) and accepted.shape == (B,)
-          and uniform.shape == (B, rows) and uniform.dtype is torch.float32 and uniform.get_device() == device
-          and uniform.is_contiguous())
-    for t in (draft_counts, seq_lens, new_lens):
-        ok = ok and (t is None or t.shape == (B,))
+          and draft_tokens.shape == (B, K) and uniform.shape == tokens.shape == (B, rows) and accepted.shape == (B,)
+          and uniform.dtype is torch.float32 and uniform.get_device() == device and uniform.is_contiguous()
+          and (counts is None or draft_counts.shape == (B,)) and (lens is None or seq_lens.shape == (B,))
+          and (new is None or new_lens.shape == (B,)))
     q, q_stride = None, 0
     if draft_probs is not None:
         q, (q_stride, dense) = draft_probs.data_ptr(), _row_stride(draft_probs)
@@ -555,6 +554,8 @@ def mla_draft_accept(target_probs, draft_tokens, uniform, accepted, tokens, draf
 def _row_stride(t):
     """(elements between the rows of t [B, n, V], whether it has rows that evenly apart)."""
     B, n, V = t.shape
+    if t.is_contiguous():
+        return V, True
     s0, s1, s2 = t.stride()
     if n <= 1:                           # one row a sequence (or none): its stride is the sequences'
         s1 = s0 if B > 1 and n else V
