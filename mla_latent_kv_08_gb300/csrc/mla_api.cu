@@ -625,9 +625,6 @@ mla_status mla_latent_append_index(const mla_shape *shape, const mla_cache *cach
 
 // ---- the pool's books -------------------------------------------------------
 
-// Sequences a pool may have, and forks of one call: prefix sums over them lie in shared memory.
-constexpr int32_t kPoolMax = 16384;
-
 static mla_status pool_params(const mla_shape *s, const mla_pool *pool, int32_t *copies, int32_t room,
                               int32_t *num_copies, int32_t *left, int32_t *status, PoolParams &p) {
     mla_status st = check_shape(s);

@@ -186,7 +186,9 @@ struct PrefillParams {
     float *lse;
 };
 
-// The pool's books (mla_pool_*).
+// The pool's books (mla_pool_*). Sequences a pool may have, and forks of one call: prefix sums over
+// them lie in shared memory.
+constexpr int32_t kPoolMax = 16384;
 struct PoolParams {
     int32_t *table;              // [S, W]
     int32_t *lens;               // [S]

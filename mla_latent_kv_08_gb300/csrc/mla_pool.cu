@@ -581,9 +581,17 @@ Cluster cluster_of(const PoolParams &p, int32_t rows) {
     return {n <= 131072 ? 8u : 16u, n <= 32768 ? 512u : 1024u};
 }
 
-cudaError_t launch(void (*kern)(PoolParams), const PoolParams &p, Cluster c, size_t smem, cudaStream_t st) {
+// Bytes of shared memory for n sequences (forks: n forks among S sequences).
+constexpr size_t resize_smem(size_t S) { return 3 * sizeof(int) * (S + 1); }
+constexpr size_t fork_smem(size_t n, size_t S) { return 3 * sizeof(int) * (n + 1) + sizeof(uint32_t) * ((S + 31) / 32); }
+constexpr size_t compact_smem(size_t S) { return sizeof(int) * (S + 1); }
+
+// most: the kernel's smem at its largest. The limit is the kernel's, for every thread of the process: all
+// of them set it to this, since a smaller one, set between another thread's and its launch, would have that
+// launch refused.
+cudaError_t launch(void (*kern)(PoolParams), const PoolParams &p, Cluster c, size_t smem, size_t most, cudaStream_t st) {
     if (smem > 24576) {                      // with the static part, more than a launch may have without asking
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
         if (e != cudaSuccess) return e;
     }
     if (c.ctas > 8) {
@@ -609,14 +617,13 @@ cudaError_t launch(void (*kern)(PoolParams), const PoolParams &p, Cluster c, siz
 }  // namespace
 
 cudaError_t launch_pool_resize(const PoolParams &p, cudaStream_t st) {
-    return launch(resize_kernel, p, cluster_of(p, p.S), 3 * sizeof(int) * ((size_t)p.S + 1), st);
+    return launch(resize_kernel, p, cluster_of(p, p.S), resize_smem(p.S), resize_smem(kPoolMax), st);
 }
 cudaError_t launch_pool_fork(const PoolParams &p, cudaStream_t st) {
-    const size_t smem = 3 * sizeof(int) * ((size_t)p.n + 1) + sizeof(uint32_t) * (((size_t)p.S + 31) / 32);
-    return launch(fork_kernel, p, cluster_of(p, p.n), smem, st);
+    return launch(fork_kernel, p, cluster_of(p, p.n), fork_smem(p.n, p.S), fork_smem(kPoolMax, kPoolMax), st);
 }
 cudaError_t launch_pool_compact(const PoolParams &p, cudaStream_t st) {
-    return launch(compact_kernel, p, cluster_of(p, p.S), sizeof(int) * ((size_t)p.S + 1), st);
+    return launch(compact_kernel, p, cluster_of(p, p.S), compact_smem(p.S), compact_smem(kPoolMax), st);
 }
 
 }  // namespace mla

@@ -349,6 +349,44 @@ def test_the_binding_refuses(gpu_lib):
     assert int(p.pool.ref_count.sum()) == 0
 
 
+def test_two_host_threads(gpu_lib):
+    """Pools of many and of few sequences, each with a thread and a stream of its own: what one call
+    needs of shared memory is not what another's launch finds."""
+    import ctypes
+    import threading
+    import mla_latent_kv_08_gb300 as mla
+    import torch
+    pairs = [(Pair(16384, 2, 5000, 4), 3000), (Pair(3000, 2, 5000, 4), 3000)]
+    failed, jobs = [], []
+    for p, calls in pairs:
+        S = p.pool.seq_lens.numel()
+        S_new = [p.ints([b % 5 if b < 2500 else 0 for b in range(S)]), p.ints([b % 3 if b < 2500 else 0 for b in range(S)])]
+        n = 3000 if S > 3000 else 2100
+        forks = p.ints([0] * n)                              # refused, all of them: a child several times
+        jobs.append((p, calls, S_new, forks, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def work(p, calls, new, forks, stream):
+        shape, pool, s = p.pool._args[0], p.pool._args[1], ctypes.c_void_p(stream.cuda_stream)
+        ptr = [ctypes.c_void_p(t.data_ptr()) for t in (*new, forks, p.copies, p.n, p.status)]
+        for i in range(calls):
+            codes = [gpu_lib.mla_pool_resize(shape, pool, ptr[i % 2], ptr[3], ptr[4], None, ptr[5], s),
+                     gpu_lib.mla_pool_fork(shape, pool, forks.numel(), ptr[2], ptr[2], None, ptr[3], ptr[4], None, None, s),
+                     gpu_lib.mla_pool_compact(shape, pool, 0, ptr[3], ptr[4], None, ptr[5], s)]
+            failed.extend(c for c in codes if c != mla.MLA_OK)
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, (len(failed), set(failed))
+    for p, calls, new, _, _ in jobs:
+        assert int(p.status) == 0
+        np.testing.assert_array_equal(p.pool.seq_lens.cpu().numpy(), new[1].cpu().numpy())
+        assert int((p.pool.ref_count > 0).sum()) == int((new[1] > 0).sum()) == int((p.pool.block_table >= 0).sum())
+
+
 # ------------------------------------------------------------------ copies
 
 KINDS = ["BF16", "FP32", "MXFP8", "INT2_ROT", "INT2_ROT_QR", "INT2_JOINT"]
