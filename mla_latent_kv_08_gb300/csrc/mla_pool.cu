@@ -33,7 +33,7 @@ namespace {
 
 constexpr int kMaxThreads = 1024, kMaxWarps = kMaxThreads / 32;
 constexpr int kMaxCluster = 16;
-constexpr int kPiece = 256;                  // table entries
+constexpr int kPiece = 256;                  // table entries (a number of them, less one, fits a byte)
 
 // What every CTA finds for itself: the blocks that the call takes, whether it gives any back,
 // what is wrong.
@@ -229,6 +229,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) resize_kernel(const PoolParams
     __shared__ Shared sh;
     int *s_takes = dyn, *s_pieces = dyn + p.S + 1;       // [S + 1] each
     int *s_place = s_pieces + p.S + 1;                   // [S] first entry that changes; ~(copy's number) for a cut's copy
+    uint8_t *s_last = (uint8_t *)(s_place + p.S + 1);    // [S] entries of the last piece given back, less one
     const cg::cluster_group cl = cg::this_cluster();
     auto here = cl.barrier_arrive();
     const Parts parts(p.N, gridDim.x * blockDim.x / 32);
@@ -258,6 +259,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) resize_kernel(const PoolParams
             s_takes[b] = sum.x + at.x;
             s_pieces[b] = sum.y + at.y;
             s_place[b] = c.old >= 0 ? ~(sum.z + at.z) : min(c.held, c.wanted);
+            s_last[b] = (uint8_t)(c.held - c.wanted - 1);
         }
         sum = {sum.x + all.x, sum.y + all.y, sum.z + all.z};
     }
@@ -304,9 +306,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1) resize_kernel(const PoolParams
     if (!back) return;
     cl.sync();                               // all free blocks have been looked at
     int freed = 0;
-    // lengths are new ones now: a row's entries end with its first -1
+    // the entries of `given` once more: lengths are new ones now
     const auto rest = [&](int b) {
-        return make_int2(s_place[b] >= 0 ? s_place[b] : ceil_div(p.new_lens[b], p.bs), p.W);
+        const int first = s_place[b] >= 0 ? s_place[b] : ceil_div(p.new_lens[b], p.bs);
+        return make_int2(first, first + (s_pieces[b + 1] - s_pieces[b] - 1) * kPiece + s_last[b] + 1);
     };
     walk(s_pieces, p.S, w, warps, rest, row, [&](int b, int j, const int (&v)[kLane], int n) {
         int32_t *at = p.table + (size_t)b * p.W + j;
@@ -582,9 +585,12 @@ Cluster cluster_of(const PoolParams &p, int32_t rows) {
 }
 
 // Bytes of shared memory for n sequences (forks: n forks among S sequences).
-constexpr size_t resize_smem(size_t S) { return 3 * sizeof(int) * (S + 1); }
+constexpr size_t resize_smem(size_t S) { return 3 * sizeof(int) * (S + 1) + S; }
 constexpr size_t fork_smem(size_t n, size_t S) { return 3 * sizeof(int) * (n + 1) + sizeof(uint32_t) * ((S + 31) / 32); }
 constexpr size_t compact_smem(size_t S) { return sizeof(int) * (S + 1); }
+
+static_assert(resize_smem(kPoolMax) + sizeof(Shared) <= 227 * 1024 && fork_smem(kPoolMax, kPoolMax) + sizeof(Shared) <= 227 * 1024,
+              "a CTA's shared memory");
 
 // most: the kernel's smem at its largest. The limit is the kernel's, for every thread of the process: all
 // of them set it to this, since a smaller one, set between another thread's and its launch, would have that

@@ -349,6 +349,49 @@ def test_the_binding_refuses(gpu_lib):
     assert int(p.pool.ref_count.sum()) == 0
 
 
+@pytest.mark.parametrize("S,W,N,bs", [(6, 600, 2500, 4), (40, 900, 30000, 2), (200, 1100, 90000, 3)])
+def test_what_lies_behind_a_sequence_is_not_given_back(gpu_lib, S, W, N, bs):
+    """Tables padded with valid block ids, as the attention calls take them: a sequence gives back
+    what it held, and nothing of what its row has behind that."""
+    for seed in range(4):
+        rng = random.Random(seed)
+        table, lens, ref = _books(rng, S, W, N, bs)
+        for b in range(S):                                   # ends at and around whole pieces of the walk
+            if lens[b] and rng.random() < 0.3:
+                n = rng.choice([1, 255, 256, 257, 512, 513])
+                while -(-lens[b] // bs) > n:
+                    j = -(-lens[b] // bs) - 1
+                    ref[table[b][j]] -= 1
+                    table[b][j] = -1
+                    lens[b] = j * bs
+        p = Pair(S, W, N, bs)
+        p.set(table, lens, ref)
+        held = [-(-n // bs) for n in lens]
+        pad = _padding(p, rng)
+        mask = p.torch.arange(W, device="cuda") >= p.ints(held)[:, None]
+        p.pool.block_table.copy_(p.torch.where(mask, pad, p.pool.block_table))
+        new = [rng.choice([0, rng.randint(0, n), max(0, n - rng.randint(0, 2 * bs)), n // bs // 2 * bs, n, min(W * bs, n + rng.randint(0, bs))]) for n in lens]
+        p.mla.mla_pool_resize(p.pool, p.ints(new), p.copies, p.n, num_free=p.left, status=p.status)
+        flags, copies, left = p.k.resize(new)
+        assert flags == 0 and int(p.status) == 0 and int(p.n) == len(copies) and int(p.left) == left
+        np.testing.assert_array_equal(p.copies.cpu().numpy()[:len(copies)], np.array(copies, np.int32).reshape(-1, 4))
+        np.testing.assert_array_equal(p.pool.ref_count.cpu().numpy(), p.k.ref)
+        np.testing.assert_array_equal(p.pool.seq_lens.cpu().numpy(), p.k.lens)
+        want, pads = np.array(p.k.table()), pad.cpu().numpy()
+        for b, (h, n) in enumerate(zip(held, new)):
+            end = max(h, -(-n // bs))
+            want[b, end:] = pads[b, end:]
+        np.testing.assert_array_equal(p.pool.block_table.cpu().numpy(), want)
+
+
+def _padding(p, rng):
+    """Entries behind the sequences' ends: 0, and any block there is."""
+    S, W = p.pool.block_table.shape
+    g = p.torch.Generator(device="cuda").manual_seed(rng.randrange(1 << 30))
+    some = p.torch.randint(0, p.shape.num_blocks, (S, W), generator=g, device="cuda", dtype=p.torch.int32)
+    return some * (p.torch.rand((S, W), generator=g, device="cuda") < 0.3).int()
+
+
 def test_two_host_threads(gpu_lib):
     """Pools of many and of few sequences, each with a thread and a stream of its own: what one call
     needs of shared memory is not what another's launch finds."""
