@@ -465,8 +465,7 @@ mla_status mla_pool_fork(const mla_shape *shape, const mla_pool *pool, int32_t n
 /* Blocks in use move to the front of the pool: with num_live of them, the k-th block in use
  * with an id of num_live or more goes to the k-th free one below, and table entries follow.
  * With a list too short for all (max_copies) the first max_copies of these move; further calls
- * move the others. A table entry out of range is left as it is and raises MLA_ERR_BOUNDS; the
- * others follow all the same.
+ * move the others.
  *   num_live   optional [1] int32 (device): blocks in use. */
 mla_status mla_pool_compact(const mla_shape *shape, const mla_pool *pool, int32_t max_copies, int32_t *copies,
                             int32_t *num_copies, int32_t *num_live, int32_t *status, void *stream);

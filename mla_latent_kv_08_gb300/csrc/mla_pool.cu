@@ -443,21 +443,13 @@ __global__ void __launch_bounds__(kMaxThreads, 1) fork_kernel(const PoolParams p
 // ---- compact ----------------------------------------------------------------
 
 // Entries v of a table at at, at + 32, ..: those of moved blocks (none below `first`) follow.
-// Whether any is out of range.
-__device__ __forceinline__ bool follow(const PoolParams &p, int first, int32_t *at, const int (&v)[kLane], int n) {
+__device__ __forceinline__ void follow(const PoolParams &p, int first, int32_t *at, const int (&v)[kLane], int n) {
     int to[kLane];
-    bool bad = false;
 #pragma unroll
-    for (int k = 0; k < kLane; ++k) {
-        to[k] = -1;
-        if (k >= n) continue;
-        if (v[k] < 0 || v[k] >= p.N) bad = true;         // left as it is
-        else if (v[k] >= first) to[k] = ~p.ref[v[k]];
-    }
+    for (int k = 0; k < kLane; ++k) to[k] = k < n && v[k] >= first && v[k] < p.N ? ~p.ref[v[k]] : -1;
 #pragma unroll
     for (int k = 0; k < kLane; ++k)
         if (to[k] >= 0) at[32 * k] = to[k];
-    return bad;
 }
 
 __global__ void __launch_bounds__(kMaxThreads, 1) compact_kernel(const PoolParams p) {
@@ -487,6 +479,14 @@ __global__ void __launch_bounds__(kMaxThreads, 1) compact_kernel(const PoolParam
         pieces += all.x;
     }
     if (tid == 0) s_pieces[p.S] = pieces;
+    const auto held = [&](int b) { return make_int2(0, ceil_div(p.lens[b], p.bs)); };
+    const auto row = [&](int b) { return p.table + (size_t)b * p.W; };
+    if (!__syncthreads_or(flags))            // lengths are fine: so are the ranges
+        walk(s_pieces, p.S, w, warps, held, row, [&](int, int, const int (&v)[kLane], int n) {
+#pragma unroll
+            for (int k = 0; k < kLane; ++k)
+                if (k < n && (v[k] < 0 || v[k] >= p.N)) flags |= FLAG_BAD_BLOCK;
+        });
     if (flags) atomicOr(&sh.flags, flags);
     count_free(p, sh, parts, w);
     const Totals t = exchange(cl, here, sh, w, warps, 0, 0);
@@ -558,12 +558,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) compact_kernel(const PoolParam
         if (p.left) *p.left = live;
     }
     cl.sync();
-    const auto held = [&](int b) { return make_int2(0, ceil_div(p.lens[b], p.bs)); };
-    const auto row = [&](int b) { return p.table + (size_t)b * p.W; };
     walk(s_pieces, p.S, w, warps, held, row, [&](int b, int j, const int (&v)[kLane], int n) {
-        if (follow(p, live, p.table + (size_t)b * p.W + j, v, n)) flags = FLAG_BAD_BLOCK;
+        follow(p, live, p.table + (size_t)b * p.W + j, v, n);
     });
-    if (flags) raise_flag(p.status, flags);
     cl.sync();
     for (int i = thread; i < moves; i += threads) p.ref[p.copies[i].x] = 0;
 }

@@ -392,6 +392,39 @@ def _padding(p, rng):
     return some * (p.torch.rand((S, W), generator=g, device="cuda") < 0.3).int()
 
 
+@pytest.mark.parametrize("S,W,N,bs", [(3, 4, 30, 8), (60, 300, 9000, 4), (300, 500, 60000, 2)])
+def test_compaction_changes_everything_or_nothing(gpu_lib, S, W, N, bs):
+    """A table entry out of range, wherever it is: no block moves, and no copy is listed."""
+    import torch
+    rng = random.Random(S)
+    books = _books(rng, S, W, N, bs, empty=0.0)
+    p = Pair(S, W, N, bs)
+    p.set(*books)
+    full = [b for b in range(S) if books[1][b]]
+    for bad in (-1, N, 2 ** 31 - 1, -2 ** 31):
+        b = rng.choice(full)
+        held = -(-books[1][b] // bs)
+        for j in (0, held - 1, rng.randrange(held)):
+            p.pool.block_table[b, j] = bad
+            before = [t.clone() for t in (p.pool.block_table, p.pool.seq_lens, p.pool.ref_count)]
+            p.mla.mla_pool_compact(p.pool, p.copies, p.n, num_live=p.left, status=p.status)
+            assert int(p.status) == 1 and int(p.n) == 0 and int(p.left) == sum(c > 0 for c in books[2])
+            assert p.mla.mla_read_status_word(p.status)[0] == p.mla.MLA_ERR_BOUNDS
+            assert bool((p.copies == -5).all())
+            for t, was in zip((p.pool.block_table, p.pool.seq_lens, p.pool.ref_count), before):
+                assert torch.equal(t, was)
+            p.status.zero_()
+            p.pool.block_table[b, j] = books[0][b][j]
+    end = -(-books[1][full[0]] // bs)
+    if end < W:                                              # behind a sequence's end nothing is looked at
+        p.pool.block_table[full[0], end] = N
+        p.mla.mla_pool_compact(p.pool, p.copies, p.n, status=p.status)
+        assert int(p.status) == 0 and int(p.pool.block_table[full[0], end]) == N
+    p.copies.fill_(-5)
+    p.set(*books)
+    assert p.compact() == 0
+
+
 def test_two_host_threads(gpu_lib):
     """Pools of many and of few sequences, each with a thread and a stream of its own: what one call
     needs of shared memory is not what another's launch finds."""
