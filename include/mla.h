@@ -441,7 +441,7 @@ typedef struct {
  *   - is one launch, without a workspace.
  * Calls on one pool are ordered by the caller (one stream, or events between streams).
  * MLA_ERR_UNSUPPORTED where max_seqs * max_blocks_per_seq, or num_forks * max_blocks_per_seq,
- * passes 2^31 - 1. */
+ * passes 2^31 - 1, or num_blocks 2^31 - 257. */
 
 /* Sequences get other lengths, new_lens [max_seqs] int32 (0 .. max_blocks_per_seq *
  * block_size, at most 2^31 - 256; seq_lens[b] for no change), an array other than the pool's
@@ -465,7 +465,7 @@ mla_status mla_pool_fork(const mla_shape *shape, const mla_pool *pool, int32_t n
 /* Blocks in use move to the front of the pool: with num_live of them, the k-th block in use
  * with an id of num_live or more goes to the k-th free one below, and table entries follow.
  * With a list too short for all (max_copies) the first max_copies of these move; further calls
- * move the others.
+ * move the others. max_copies is as mla_cache_copy takes it (MLA_ERR_UNSUPPORTED).
  *   num_live   optional [1] int32 (device): blocks in use. */
 mla_status mla_pool_compact(const mla_shape *shape, const mla_pool *pool, int32_t max_copies, int32_t *copies,
                             int32_t *num_copies, int32_t *num_live, int32_t *status, void *stream);
@@ -473,9 +473,11 @@ mla_status mla_pool_compact(const mla_shape *shape, const mla_pool *pool, int32_
 /* Copies of cached rows, every kind: rows first .. first + rows - 1 of the source block go to the
  * same rows of the destination block, for the entries 0 .. num_copies[0] - 1 (at most
  * max_copies) of `copies` as the pool calls list them, in each of `caches` (host array of
- * num_caches caches of this shape; 64 a launch). No block is the source of one entry and
- * the destination of another, and none the destination of two over the same rows. An entry out of
- * range raises a flag in `status` (optional [1] int32 device word) and is skipped. */
+ * num_caches caches of this shape; 64 a launch). max_copies is at most
+ * 16384, or max_copies * block_size at most 2^31 - 65537 (MLA_ERR_UNSUPPORTED). No block is the
+ * source of one entry and the destination of another, and none the destination of two over the
+ * same rows. An entry out of range raises a flag in `status` (optional [1] int32 device word) and
+ * is skipped. */
 mla_status mla_cache_copy(const mla_shape *shape, const mla_cache *caches, int32_t num_caches, const int32_t *copies,
                           const int32_t *num_copies, int32_t max_copies, int32_t *status, void *stream);
 

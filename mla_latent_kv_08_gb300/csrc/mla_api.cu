@@ -625,6 +625,12 @@ mla_status mla_latent_append_index(const mla_shape *shape, const mla_cache *cach
 
 // ---- the pool's books -------------------------------------------------------
 
+// Lists of copies: those of as many entries as a resize or a fork writes for blocks of any size, longer
+// ones up to so many rows. mla_pool_compact refuses what mla_cache_copy would, before the books change.
+static bool too_long(const mla_shape *s, int32_t room) {
+    return room > kPoolMax && (int64_t)room * s->block_size > INT32_MAX - 65536;
+}
+
 static mla_status pool_params(const mla_shape *s, const mla_pool *pool, int32_t *copies, int32_t room,
                               int32_t *num_copies, int32_t *left, int32_t *status, PoolParams &p) {
     mla_status st = check_shape(s);
@@ -634,7 +640,7 @@ static mla_status pool_params(const mla_shape *s, const mla_pool *pool, int32_t 
         num_copies == left || num_copies == status || (left && left == status))
         return MLA_ERR_INVALID;
     if (pool->max_seqs > kPoolMax || (int64_t)pool->max_seqs * pool->max_blocks_per_seq > INT32_MAX ||
-        s->num_blocks > INT32_MAX - 256)
+        s->num_blocks > INT32_MAX - 256 || too_long(s, room))
         return MLA_ERR_UNSUPPORTED;
     memset(&p, 0, sizeof p);
     p.table = pool->block_table;
@@ -699,7 +705,7 @@ mla_status mla_cache_copy(const mla_shape *shape, const mla_cache *caches, int32
     if (st != MLA_OK) return st;
     if (!caches || num_caches < 1 || max_copies < 0 || !num_copies || (max_copies > 0 && !copies) || !aligned16(copies))
         return MLA_ERR_INVALID;
-    if ((int64_t)max_copies * shape->block_size > INT32_MAX - 65536) return MLA_ERR_UNSUPPORTED;     // tasks, and a grid more
+    if (too_long(shape, max_copies)) return MLA_ERR_UNSUPPORTED;
     for (int32_t i = 0; i < num_caches; ++i) {           // all of them before anything is launched
         ReadParams r;
         st = read_params(shape, caches + i, r);

@@ -20,19 +20,27 @@ constexpr int kPart = kThreads * kUnroll * 16;       // bytes of a CTA's task, a
 
 // U: the type of a load, which divides every row's bytes. ARRAYS: of a cache, 1 or 3.
 template <typename U, int ARRAYS>
-__global__ void __launch_bounds__(kThreads) copy_kernel(const __grid_constant__ CopyParams p, int part_rows, int parts) {
+__global__ void __launch_bounds__(kThreads) copy_kernel(const __grid_constant__ CopyParams p, int part_rows, unsigned parts) {
     pdl_wait();
     pdl_trigger();
     const int layer = blockIdx.y, tid = threadIdx.x;
-    const int n = max(0, min(*p.num_copies, p.max_copies)) * parts;
+    const unsigned n = max(0, min(*p.num_copies, p.max_copies));
     const int u0 = p.row_bytes[0] / sizeof(U), u1 = p.row_bytes[1] / sizeof(U), u2 = p.row_bytes[2] / sizeof(U);
     U *const p0 = (U *)p.plane[layer][0], *const p1 = (U *)p.plane[layer][1], *const p2 = (U *)p.plane[layer][2];
-    int task = blockIdx.x;
-    int4 next = task < n ? p.copies[task / parts] : make_int4(0, 0, 0, 0);
-    for (; task < n; task += gridDim.x) {
+    // a task is a part of an entry; all of them may be more than 2^32
+    const unsigned step = gridDim.x / parts, step_part = gridDim.x % parts;
+    unsigned entry = blockIdx.x / parts, part = blockIdx.x % parts;
+    int4 next = entry < n ? p.copies[entry] : make_int4(0, 0, 0, 0);
+    while (entry < n) {
         const int4 c = next;
-        const int at = (task % parts) * part_rows;
-        if (task + gridDim.x < n) next = p.copies[(task + gridDim.x) / parts];
+        const int at = part * part_rows;
+        entry += step;
+        part += step_part;
+        if (part >= parts) {
+            part -= parts;
+            ++entry;
+        }
+        if (entry < n) next = p.copies[entry];
         const bool ok = c.x >= 0 && c.x < p.num_blocks && c.y >= 0 && c.y < p.num_blocks && c.z >= 0 && c.w >= 0 &&
                         c.z <= p.bs && c.w <= p.bs - c.z;
         if (!ok) {
@@ -63,7 +71,7 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(const __grid_constant__ 
 }
 
 template <typename U>
-cudaError_t launch(const CopyParams &p, dim3 grid, int part_rows, int parts, cudaStream_t st) {
+cudaError_t launch(const CopyParams &p, dim3 grid, int part_rows, unsigned parts, cudaStream_t st) {
     return launch_pdl(p.row_bytes[1] ? copy_kernel<U, 3> : copy_kernel<U, 1>, grid, dim3(kThreads), 0, st, p, part_rows, parts);
 }
 
@@ -76,7 +84,7 @@ cudaError_t launch_copy(const CopyParams &p, int32_t layers, cudaStream_t st) {
         bits |= p.row_bytes[k];
     }
     const int part_rows = row >= kPart ? 1 : kPart / row < p.bs ? kPart / row : p.bs;
-    const int parts = (p.bs + part_rows - 1) / part_rows;
+    const unsigned parts = ((unsigned)p.bs + part_rows - 1) / part_rows;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

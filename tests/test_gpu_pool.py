@@ -587,3 +587,26 @@ def test_copies_past_32_bits(gpu_lib):
     assert torch.equal(c.latent[5], c.latent[N - 1])
     assert torch.equal(c.latent[N - 200, 3:63], c.latent[1, 3:63]) and not c.latent[N - 200, :3].any() and not c.latent[N - 200, 63:].any()
     assert not c.latent[N - 201].any() and not c.latent[4].any() and not c.latent[6].any()
+
+
+def test_lists_of_long_blocks(gpu_lib):
+    """As many entries as a resize or a fork may list, in blocks of 2^28 rows: 2^32 tasks, of which the
+    first, the last, and some in between do anything."""
+    import mla_latent_kv_08_gb300 as mla
+    import torch
+    bs, n = 1 << 28, 16384
+    shape = mla.Shape(num_heads=8, kv_lora_rank=8, rope_dim=0, v_head_dim=16, block_size=bs, num_blocks=4)
+    c = mla.Cache.allocate(shape)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    c.latent[0].random_(-100, 100, generator=g)
+    lst = torch.zeros((n, 4), dtype=torch.int32, device="cuda")
+    entries = {0: [0, 1, 0, 5000], 8191: [0, 2, bs - 3000, 3000], 8192: [0, 2, 1025, 1023], n - 1: [0, 3, bs - 1500, 1500]}
+    for i, e in entries.items():
+        lst[i] = torch.tensor(e, dtype=torch.int32)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mla.mla_cache_copy(c, lst, torch.tensor([n], dtype=torch.int32, device="cuda"), status=status)
+    assert int(status) == 0
+    for _, d, f, k in entries.values():
+        assert torch.equal(c.latent[d, f:f + k], c.latent[0, f:f + k])
+    assert not c.latent[1, 5000:].any() and not c.latent[3, :bs - 1500].any()
+    assert not c.latent[2, :1025].any() and not c.latent[2, 2048:bs - 3000].any()

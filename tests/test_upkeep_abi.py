@@ -147,6 +147,16 @@ def test_accept_arguments(lib):
         assert call(**kw) == mla.MLA_ERR_UNSUPPORTED, kw
 
 
+def test_lists_that_no_copy_call_takes(lib):
+    """A list that mla_cache_copy refuses is refused before the books change."""
+    import mla_latent_kv_08_gb300 as mla
+    dense = mla.mla_cache(4096, None, None, None)
+    for shape, room in ((_shape(), 1 << 26), (_shape(), 1 << 25), (_shape(block_size=1 << 20), 16385), (_shape(block_size=131069), 16385)):
+        s = ctypes.byref(shape.c())
+        assert lib.mla_cache_copy(s, ctypes.byref(dense), 1, FAKE, FAKE, room, None, None) == mla.MLA_ERR_UNSUPPORTED
+        assert lib.mla_pool_compact(s, ctypes.byref(_pool(mla)), room, FAKE, FAKE, None, None, None) == mla.MLA_ERR_UNSUPPORTED
+
+
 # ------------------------------------------------------------------ refusals of the binding
 
 def test_handles_check_their_tensors():
