@@ -62,6 +62,12 @@ __device__ __forceinline__ Fixed weight(T p, T q, bool out) {
     return W == kWithout && out ? Fixed{0, 0} : Fixed{a.hi - kHi, a.lo - kLo};
 }
 
+// floor(v total), v in [0, 1): v's bits down to 2^-64, below 2^-17 those down to 2^-81, which are all
+// of v from 2^-57 on; total is below 2^49, so that for less it is 0.
+__device__ __forceinline__ u64 share(float v, u64 total) {
+    return v < 0x1p-17f ? __umul64hi(__float2ull_rz(v * 0x1p81f), total) >> 17 : __umul64hi(__float2ull_rz(v * 0x1p64f), total);
+}
+
 // What a CTA found in its part of a row, and what every CTA finds for itself: whether anything
 // is wrong, how many drafts stand and which weights come behind them (below 0: left out).
 struct Part {
@@ -250,7 +256,7 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams a) 
         out = -1;
     }
     if (!bad && !left_out) {                 // t = floor(v total); for 1 the last token that has any weight
-        t = v < 1.f ? __umul64hi(__float2ull_rz(v * 0x1p64f), total) : total - 1;
+        t = v < 1.f ? share(v, total) : total - 1;
         mine = t >= base && t < base + own;
     }
     if (rank == 0) {

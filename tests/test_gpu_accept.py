@@ -107,6 +107,29 @@ def test_borders(gpu_lib):
     _check(c, outs)
 
 
+def test_the_smallest_random_numbers(gpu_lib):
+    """A border of 16 units that a random number of 2^-42 and a bit passes by less than a unit's
+    millionth; then random ones down to where every border is 0."""
+    import torch
+    p = torch.tensor([2.0 ** -42, 1 - 2.0 ** -24, (2 ** 22 - 17) * 2.0 ** -46]).expand(3, 1, 3).contiguous()
+    u = torch.tensor([2.0 ** -42, 2.0 ** -42 * (1 + 2.0 ** -23), 2.0 ** -42 * (1 + 2.0 ** -22)])
+    c = dict(p=p.cuda(), q=None, x=torch.empty((3, 0), dtype=torch.int32, device="cuda"), u=u.view(3, 1).cuda(), counts=None, lens=None)
+    outs = _outputs(3, 0)
+    _call(c, outs)
+    assert outs[1].cpu().view(-1).tolist() == [0, 1, 1]
+    _check(c, outs)
+    B, V = 400, 130
+    g = torch.Generator().manual_seed(31)
+    p = torch.randint(0, 3, (B, 1, V), generator=g).float() * 2.0 ** -46
+    p[:, 0, V - 1], p[:, 0, V - 2] = 1 - 2.0 ** -24, 2.0 ** -25
+    u = torch.exp2(-torch.randint(38, 62, (B, 1), generator=g).float()) * (1 + torch.rand((B, 1), generator=g))
+    u[0], u[1], u[2] = 2.0 ** -149, 2.0 ** -126, 0.0
+    c = dict(p=p.cuda(), q=None, x=torch.empty((B, 0), dtype=torch.int32, device="cuda"), u=u.cuda(), counts=None, lens=None)
+    outs = _outputs(B, 0)
+    _call(c, outs)
+    _check(c, outs)
+
+
 def test_an_equal_product_is_refused(gpu_lib):
     """u q = p exactly, and one unit of u to either side."""
     import torch
