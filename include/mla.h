@@ -486,7 +486,8 @@ mla_status mla_cache_copy(const mla_shape *shape, const mla_cache *caches, int32
  * to: with q_len = K + 1 (K = num_drafts), row i's probabilities are target row i.
  *   target_probs  [B, K + 1, vocab] (dtype MLA_DTYPE_F32 or _BF16), rows target_stride elements
  *                 apart: row i of sequence b is row b * (K + 1) + i. A row's probabilities are in
- *                 [0, 1] and add up to at most 2 (they need not add up to 1).
+ *                 [0, 1] and add up to at most 2 (they need not add up to 1; a row that adds
+ *                 up to more may be refused, and is from 4 on).
  *   draft_probs   [B, K, vocab], same type, rows draft_stride elements apart: what draft i was
  *                 drawn from. NULL: the drafts were not drawn but given, with probability 1.
  *   draft_tokens  [B, K] int32.

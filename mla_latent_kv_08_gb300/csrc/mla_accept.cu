@@ -248,9 +248,11 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams a) 
         total = __shfl_sync(0xffffffffu, upto, kMaxCluster - 1);
         own = __shfl_sync(0xffffffffu, part.sum, rank);
         base = __shfl_sync(0xffffffffu, upto, rank) - own;
-        // probabilities add up to one; up to two, whole numbers stay far below 2^64
+        // probabilities add up to one, at most to two. Their sum here is an fp32 one, whose order follows
+        // from the split: a lane's additions, 2^22 at most, each round up by at most 2^-24 of a sum, a
+        // quarter of it in all. So what adds up to two is never refused, and whole numbers stay below 2^49
         left_out = !odd_row && found < 0;
-        bad = odd_row || !(sum_p <= 2.f) || (total == 0 && w == kPlain && !left_out);
+        bad = odd_row || !(sum_p <= 2.5f) || (total == 0 && w == kPlain && !left_out);
         if (bad || left_out || total > 0) break;
         w = kPlain;                          // nothing is left of p - q: p itself
         out = -1;

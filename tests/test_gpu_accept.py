@@ -1,6 +1,7 @@
 """mla_draft_accept against the oracle, which decides in whole numbers of any length: outputs
 are whole numbers and have to be equal."""
 import math
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -53,6 +54,55 @@ def _check(c, outs):
     if c["lens"] is not None:
         np.testing.assert_array_equal(new_lens, [w[3] for w in want])
     assert int(status[0]) == int(np.bitwise_or.reduce([w[0] for w in want]))
+
+
+def _want_long(c):
+    """What the oracle says, row by row in numpy's 64-bit whole numbers: for long rows whose values
+    are all in range."""
+    B, K1, V = c["p"].shape
+    K, out = K1 - 1, []
+    x, u = c["x"].cpu().tolist(), c["u"].double().cpu().tolist()
+    counts = [K] * B if c["counts"] is None else c["counts"].cpu().tolist()
+    lens = [0] * B if c["lens"] is None else c["lens"].cpu().tolist()
+
+    def whole(t):
+        return np.rint(t.double().cpu().numpy() * 2.0 ** 46).astype(np.int64)
+    for b in range(B):
+        if counts[b] < 0:
+            out.append((0, 0, [-1] * K1, lens[b]))
+            continue
+        n = 0
+        while n < counts[b] and Fraction(u[b][n]) * (1 if c["q"] is None else Fraction(float(c["q"][b, n, x[b][n]]))) < Fraction(float(c["p"][b, n, x[b][n]])):
+            n += 1
+        row = whole(c["p"][b, n])
+        w = row
+        if n < counts[b]:
+            less = np.zeros(V, np.int64)
+            if c["q"] is None:
+                less[x[b][n]] = 2 ** 46
+            w = np.maximum(row - (less if c["q"] is None else whole(c["q"][b, n])), 0)
+            w = w if w.any() else row
+        upto = np.cumsum(w)
+        border = Fraction(u[b][K]) * int(upto[-1])
+        token = int(np.flatnonzero(w)[-1]) if u[b][K] == 1 else int(np.searchsorted(upto, border.numerator // border.denominator, side="right"))
+        out.append((0, n, x[b][:n] + [token] + [-1] * (K - n), lens[b] - K + n))
+    return out
+
+
+def _check_long(c, outs):
+    want = _want_long(c)
+    accepted, tokens, new_lens, status = (t.cpu().numpy() for t in outs)
+    np.testing.assert_array_equal(accepted, [w[1] for w in want])
+    np.testing.assert_array_equal(tokens, [w[2] for w in want])
+    if c["lens"] is not None:
+        np.testing.assert_array_equal(new_lens, [w[3] for w in want])
+    assert int(status[0]) == 0
+
+
+def test_the_long_oracle_is_the_oracle(gpu_lib):
+    for sure in (False, True):
+        c = _case(40, 6, 3, 700, sure=sure, ragged=True, near=2.0)
+        assert [w for w in _want_long(c)] == [w for w in _want(c)]
 
 
 @pytest.mark.parametrize("sure", [False, True])
@@ -128,6 +178,26 @@ def test_the_smallest_random_numbers(gpu_lib):
     outs = _outputs(B, 0)
     _call(c, outs)
     _check(c, outs)
+
+
+def test_rows_that_add_up_to_two(gpu_lib):
+    """As much as a row may: none is refused, however it is split and added."""
+    import torch
+    for B, V in ((200, 12000), (60, 12000), (3, 70001)):
+        g = torch.Generator().manual_seed(B)
+        w = torch.rand((B, V), generator=g, dtype=torch.float64) + 1
+        p = (w / w.sum(-1, keepdim=True) * 2).float()
+        units = (p.double() * 2.0 ** 60).long().sum(-1)      # whole ones: p is above 2^-36
+        p[:, 0] = (p[:, 0].double() - (units - 2 ** 61).clamp(min=0).double() * 2.0 ** -60 - 2.0 ** -40).float()
+        units = (p.double() * 2.0 ** 60).long().sum(-1)
+        assert int(units.max()) <= 2 ** 61 and int(units.min()) > 2 ** 61 - 2 ** 38
+        c = dict(p=p.view(B, 1, V).cuda(), q=None, x=torch.empty((B, 0), dtype=torch.int32, device="cuda"),
+                 u=torch.rand((B, 1), generator=g).cuda(), counts=None, lens=None)
+        outs = _outputs(B, 0)
+        _call(c, outs)
+        assert int(outs[3]) == 0 and int(outs[1].min()) >= 0
+        want = _want_long(c)
+        np.testing.assert_array_equal(outs[1].cpu().numpy()[:, 0], [w[2][0] for w in want])
 
 
 def test_an_equal_product_is_refused(gpu_lib):
