@@ -401,6 +401,24 @@ def test_a_long_row_captured(gpu_lib):
         _check(c, o)
 
 
+def test_sizes_past_32_bits_are_refused(gpu_lib):
+    """A vocabulary of 2^32 + 3: not one of 3."""
+    import mla_latent_kv_08_gb300 as mla
+    import torch
+    for B, K, V in ((1, 0, 2 ** 32 + 3), (2 ** 32 + 1, 0, 1)):
+        p = torch.empty((B, K + 1, V), dtype=torch.bfloat16, device="cuda")
+        i = torch.zeros((B, K + 1), dtype=torch.int32, device="cuda")
+        o = torch.full((B, K + 1), -7, dtype=torch.int32, device="cuda")
+        n = torch.full((B,), -7, dtype=torch.int32, device="cuda")
+        u = torch.zeros((B, K + 1), device="cuda")
+        with pytest.raises(mla.MlaError) as e:
+            mla.mla_draft_accept(p, i[:, :K], u, n, o)
+        assert e.value.code == mla.MLA_ERR_UNSUPPORTED
+        torch.cuda.synchronize()
+        assert int(n[0]) == -7 and int(o[0, 0]) == -7
+        del p, i, o, n, u
+
+
 def test_the_binding_refuses(gpu_lib):
     import mla_latent_kv_08_gb300 as mla
     import torch

@@ -180,6 +180,24 @@ def test_handles_check_their_tensors():
             mla.Caches(bad)
 
 
+def test_sizes_past_32_bits_are_refused():
+    """Sizes that a 32-bit argument would cut to small ones."""
+    import mla_latent_kv_08_gb300 as mla
+    import torch
+
+    def ints(*shape):
+        return torch.empty(shape, dtype=torch.int32, device="meta")
+    s = _shape()
+    for S, W in ((1, 2 ** 32 + 4), (2 ** 32 + 1, 1), (1, 2 ** 31)):
+        with pytest.raises(mla.MlaError) as e:
+            mla.Pool(s, ints(S, W), ints(S), ints(10))
+        assert e.value.code == mla.MLA_ERR_UNSUPPORTED
+    for n in (2 ** 31, 2 ** 32 + 1):
+        with pytest.raises(mla.MlaError) as e:
+            mla._check_list("a list", ints(n, 4), ints(1), 0)
+        assert e.value.code == mla.MLA_ERR_UNSUPPORTED
+
+
 def test_row_strides():
     import mla_latent_kv_08_gb300 as mla
     import torch
