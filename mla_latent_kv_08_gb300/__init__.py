@@ -261,16 +261,20 @@ class Cache:
         dt = torch.float32 if shape.kind == MLA_KV_FP32 else torch.bfloat16
         return cls(shape, latent=alloc((nb, bs, r + dR + shape.index_dim), dtype=dt, device=device))
 
-    def bytes_per_token(self) -> int:
+    def row_bytes(self) -> tuple:
+        """A token's bytes in latent, codes, scale_zero and rope."""
         s = self.shape
         if s.kind == MLA_KV_INT2_ROT:
-            return s.kv_lora_rank // 4 + (s.kv_lora_rank // s.group_size) * 4 + 2 * s.rope_dim
+            return 0, s.kv_lora_rank // 4, (s.kv_lora_rank // s.group_size) * 4, 2 * s.rope_dim
         if s.kind in (MLA_KV_INT2_ROT_QR, MLA_KV_INT2_JOINT):
             qd = s.kv_lora_rank + s.rope_dim
-            return qd // 4 + (qd // s.group_size) * 4
+            return 0, qd // 4, (qd // s.group_size) * 4, 0
         if s.kind == MLA_KV_MXFP8:
-            return s.kv_lora_rank + s.kv_lora_rank // 32 + 2 * s.rope_dim
-        return (4 if s.kind == MLA_KV_FP32 else 2) * (s.kv_lora_rank + s.rope_dim + s.index_dim)
+            return 0, s.kv_lora_rank, s.kv_lora_rank // 32, 2 * s.rope_dim
+        return (4 if s.kind == MLA_KV_FP32 else 2) * (s.kv_lora_rank + s.rope_dim + s.index_dim), 0, 0, 0
+
+    def bytes_per_token(self) -> int:
+        return sum(self.row_bytes())
 
 
 # ---------------------------------------------------------------- entry points
@@ -467,11 +471,12 @@ class Caches:
             raise MlaError(MLA_ERR_INVALID, "Caches")
         s, device = caches[0].shape, None
         for c in caches:
-            planes = [t for t in (c.latent, c.codes, c.scale_zero, c.rope) if t is not None]
-            device = planes[0].get_device() if planes and device is None else device
-            if (sum(t.numel() * t.element_size() for t in planes) != c.bytes_per_token() * s.num_blocks * s.block_size
-                    or any(t.get_device() != device or not t.is_contiguous() for t in planes)):
-                raise MlaError(MLA_ERR_INVALID, "Caches")
+            for t, row in zip((c.latent, c.codes, c.scale_zero, c.rope), c.row_bytes()):
+                if t is not None and device is None:
+                    device = t.get_device()
+                size = 0 if t is None else t.numel() * t.element_size()
+                if size != row * s.num_blocks * s.block_size or (t is not None and (t.get_device() != device or not t.is_contiguous())):
+                    raise MlaError(MLA_ERR_INVALID, "Caches")
         object.__setattr__(self, "caches", caches)
         c = (mla_cache * len(caches))(*(c.c() for c in caches))
         object.__setattr__(self, "_args", (s._ref(), c, len(caches)))

@@ -198,6 +198,23 @@ def test_sizes_past_32_bits_are_refused():
         assert e.value.code == mla.MLA_ERR_UNSUPPORTED
 
 
+def test_every_array_of_a_cache_has_its_size():
+    import mla_latent_kv_08_gb300 as mla
+    import torch
+    for kind in (mla.MLA_KV_MXFP8, mla.MLA_KV_INT2_ROT, mla.MLA_KV_INT2_ROT_QR, mla.MLA_KV_INT2_JOINT):
+        s = _shape(kind=kind)
+        c = mla.Cache.allocate(s, device="cpu")
+        mla.Caches([c])
+        swapped = mla.Cache(s, codes=c.scale_zero, scale_zero=c.codes, rope=c.rope)          # as many bytes in all
+        rest = c.codes.numel() + c.scale_zero.numel() * c.scale_zero.element_size() - 1
+        moved = mla.Cache(s, codes=torch.zeros(rest, dtype=torch.uint8), scale_zero=torch.zeros(1, dtype=torch.uint8), rope=c.rope)
+        for bad in (swapped, moved, mla.Cache(s, codes=c.codes, rope=c.rope), mla.Cache(s, latent=c.codes, scale_zero=c.scale_zero, rope=c.rope)):
+            with pytest.raises(mla.MlaError):
+                mla.Caches([c, bad])
+    for kind in (mla.MLA_KV_BF16, mla.MLA_KV_FP32):
+        mla.Caches([mla.Cache.allocate(_shape(kind=kind, index_dim=64), device="cpu")])
+
+
 def test_row_strides():
     import mla_latent_kv_08_gb300 as mla
     import torch
