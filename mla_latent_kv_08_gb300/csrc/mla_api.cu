@@ -703,7 +703,8 @@ mla_status mla_cache_copy(const mla_shape *shape, const mla_cache *caches, int32
                           const int32_t *num_copies, int32_t max_copies, int32_t *status, void *stream) {
     mla_status st = check_shape(shape);
     if (st != MLA_OK) return st;
-    if (!caches || num_caches < 1 || max_copies < 0 || !num_copies || (max_copies > 0 && !copies) || !aligned16(copies))
+    if (!caches || num_caches < 1 || max_copies < 0 || !num_copies || num_copies == status ||
+        (max_copies > 0 && !copies) || !aligned16(copies))
         return MLA_ERR_INVALID;
     if (too_long(shape, max_copies)) return MLA_ERR_UNSUPPORTED;
     for (int32_t i = 0; i < num_caches; ++i) {           // all of them before anything is launched

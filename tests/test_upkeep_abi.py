@@ -157,6 +157,12 @@ def test_lists_that_no_copy_call_takes(lib):
         assert lib.mla_pool_compact(s, ctypes.byref(_pool(mla)), room, FAKE, FAKE, None, None, None) == mla.MLA_ERR_UNSUPPORTED
 
 
+def test_a_copy_counts_apart_from_its_flags(lib):
+    import mla_latent_kv_08_gb300 as mla
+    dense = mla.mla_cache(4096, None, None, None)
+    assert lib.mla_cache_copy(ctypes.byref(_shape().c()), ctypes.byref(dense), 1, FAKE, FAKE2, 3, FAKE2, None) == mla.MLA_ERR_INVALID
+
+
 # ------------------------------------------------------------------ refusals of the binding
 
 def test_handles_check_their_tensors():
