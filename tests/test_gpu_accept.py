@@ -401,6 +401,71 @@ def test_a_long_row_captured(gpu_lib):
         _check(c, o)
 
 
+# Sequences and a vocabulary whose warps each have more than 1024 tokens, with 1, 2, 4, 8 and 16 CTAs a
+# row; and one whose warps have 800.
+LONG = [(160, 8195), (80, 16389), (40, 32771), (13, 65539), (1, 131075), (3, 131075), (2, 102401)]
+
+
+@pytest.mark.parametrize("sure", [False, True])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("B,V", LONG)
+def test_long_parts_of_every_split(gpu_lib, B, V, dtype, sure):
+    """Every kind of weights in the loop over many tokens at a time: p alone (no drafts, or all stand), the
+    difference, p without the draft."""
+    for K, near in ((0, 1.0), (1, 4.0)):
+        c = _case(B + V, B, K, V, dtype, sure, near=near)
+        outs = _outputs(B, K)
+        _call(c, outs)
+        _check_long(c, outs)
+        for v in (0.0, 1 - 2.0 ** -24, 1.0):                 # the first token that has weight, and the last
+            c["u"][:, K] = v
+            if K:
+                c["u"][:, 0] = 1.0
+            _call(c, outs)
+            _check_long(c, outs)
+
+
+@pytest.mark.parametrize("B,V", LONG)
+def test_long_rows_with_nothing_left(gpu_lib, B, V):
+    """p <= q throughout, p = 0 at the draft: the second pass over the row, in p's own weights."""
+    for dtype in ("fp32", "bf16"):
+        c = _case(V, B, 1, V, dtype)
+        c["q"][:, 0] = c["p"][:, 0]
+        c["x"][:, 0] = V - 2
+        c["p"][:, 0, V - 2] = 0
+        outs = _outputs(B, 1)
+        _call(c, outs)
+        assert not outs[0].any()
+        _check_long(c, outs)
+
+
+@pytest.mark.parametrize("B,V", LONG)
+def test_values_out_of_range_deep_in_a_long_row(gpu_lib, B, V):
+    """One value of one row, wherever it is: that sequence is refused, the others are as ever."""
+    import torch
+    c = _case(V + 1, B, 1, V, near=2.0)
+    c["u"][:, 0], c["x"][:, 0] = 1.0, 5                      # the draft is refused: both rows are read
+    c["p"][:, 0, 5], c["q"][:, 0, 5] = 1e-6, 2e-6
+    good, negative_zero = _outputs(B, 1), _outputs(B, 1)
+    _call(c, good)
+    _check_long(c, good)
+    b = B // 2
+    for which in ("p", "q"):
+        for i in (6, 31, 1023, 1024, V // 2 + 1, V - 1030, V - 1):
+            for value in (math.nan, -2.0 ** -140, 1 + 2.0 ** -23):
+                keep = c[which][b, 0, i].clone()
+                c[which][b, 0, i] = value
+                outs = _outputs(B, 1)
+                _call(c, outs)
+                assert int(outs[3]) == upkeep.VALUE and int(outs[0][b]) == 0 and outs[1][b].tolist() == [-1, -1], (which, i, value)
+                rest = torch.arange(B, device="cuda") != b
+                assert torch.equal(outs[1][rest], good[1][rest])
+                c[which][b, 0, i] = keep
+    c["p"][b, 0, V - 7] = c["q"][b, 0, V - 7] = -0.0         # is a probability
+    _call(c, negative_zero)
+    _check_long(c, negative_zero)
+
+
 def test_sizes_past_32_bits_are_refused(gpu_lib):
     """A vocabulary of 2^32 + 3: not one of 3."""
     import mla_latent_kv_08_gb300 as mla
