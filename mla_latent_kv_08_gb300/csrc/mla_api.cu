@@ -83,7 +83,7 @@ static mla_status check_shape(const mla_shape *s) {
             return MLA_ERR_INVALID;
     }
     // generic kernel limits (shared-memory tiles sized from r and d_R)
-    if (s->kv_lora_rank > 1024 || s->rope_dim > 128) return MLA_ERR_UNSUPPORTED;
+    if (s->kv_lora_rank > kMaxRank || s->rope_dim > kMaxRope) return MLA_ERR_UNSUPPORTED;
     return MLA_OK;
 }
 
@@ -489,7 +489,7 @@ static mla_status check_prefill(const mla_shape *s, int32_t B, int32_t num_q, in
     mla_status st = check_shape(s);
     if (st != MLA_OK) return st;
     if (B < 1 || num_q < 0 || max_tokens < 0 || dn < 8 || dn % 8) return MLA_ERR_INVALID;
-    if (is_int2(s->kind) || dn > 512 || s->v_head_dim > 1024) return MLA_ERR_UNSUPPORTED;
+    if (is_int2(s->kind) || dn > kMaxNope || s->v_head_dim > 1024) return MLA_ERR_UNSUPPORTED;
     // dense rows and tiles are counted in 32 bits
     if ((int64_t)max_tokens + 128ll * B > INT32_MAX - 256 || (int64_t)num_q + 256ll * B > INT32_MAX - 256)
         return MLA_ERR_UNSUPPORTED;

@@ -226,6 +226,13 @@ struct AcceptParams {
     int32_t *accepted, *tokens, *new_lens, *status;
 };
 
+// ---- shapes -----------------------------------------------------------------
+// The largest latent, rope key and d_n of a shape. A kernel's shared memory follows from them: its limit
+// is set to what the largest shape needs, by every call to the same value. It is the kernel's, for all
+// threads of the process, and one call's own need, set between another's set and its launch, would have
+// that launch refused.
+constexpr int kMaxRank = 1024, kMaxRope = 128, kMaxRow = kMaxRank + kMaxRope, kMaxNope = 512;
+
 // ---- launchers (defined in mla_simt.cu) ------------------------------------
 // Programmatic dependent launch. A kernel launched with launch_pdl may start while
 // the previous kernel of the stream is still running; it calls pdl_trigger() on entry

@@ -253,16 +253,20 @@ __global__ void __launch_bounds__(256) prefill_simt_kernel(PrefillParams p) {
     if (p.lse && tid < rows_here) p.lse[(qrow0 + tid) * H + h] = (sM[tid] + log2f(sL[tid])) * kLn2;
 }
 
+static constexpr size_t prefill_smem(size_t dqk) {
+    return sizeof(float) * (kPQ * dqk + kPT * (dqk + 1) + kPQ * kPT + 3 * kPQ);
+}
+
 template <typename T>
 static cudaError_t prefill_simt_t(const PrefillParams &p, cudaStream_t st) {
     const unsigned mt = (unsigned)(p.cap_rows / 64);
     expand_simt_kernel<T, true><<<dim3(mt, (p.dn + 63) / 64, p.nh), 256, 0, st>>>(p);
     expand_simt_kernel<T, false><<<dim3(mt, (p.s.dv + 63) / 64, p.nh), 256, 0, st>>>(p);
-    const int dqk = p.dn + p.s.dR;
-    const size_t smem = sizeof(float) * ((size_t)kPQ * dqk + (size_t)kPT * (dqk + 1) + kPQ * kPT + 3 * kPQ);
+    const size_t smem = prefill_smem(p.dn + p.s.dR);
     const dim3 grid((unsigned)(p.num_q / kPQ + p.B), p.nh);
     auto go = [&](void (*kern)(PrefillParams)) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)prefill_smem(kMaxNope + kMaxRope));
         if (e != cudaSuccess) return e;
         kern<<<grid, 256, smem, st>>>(p);
         return cudaGetLastError();

@@ -252,23 +252,26 @@ __global__ void __launch_bounds__(256) qprep_kernel(DecodeParams p, const float 
     }
 }
 
+static constexpr size_t qprep_smem(size_t RD) { return 32 * RD * sizeof(float); }
+
 template <int OUT>
 static cudaError_t launch_qprep_t(const DecodeParams &p, const float *R, void *q_prep, cudaStream_t st) {
     const int rows = p.B * p.q_len * p.s.H;
     const int RD = p.s.RD();
-    const size_t smem = (size_t)32 * RD * sizeof(float);
+    const size_t smem = qprep_smem(RD);
+    constexpr int kMost = (int)qprep_smem(kMaxRow);
     dim3 grid((rows + 31) / 32);
     if (RD <= 256) {
-        cudaFuncSetAttribute(qprep_kernel<1, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(qprep_kernel<1, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         qprep_kernel<1, OUT><<<grid, 256, smem, st>>>(p, R, q_prep, rows);
     } else if (RD <= 512) {
-        cudaFuncSetAttribute(qprep_kernel<2, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(qprep_kernel<2, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         qprep_kernel<2, OUT><<<grid, 256, smem, st>>>(p, R, q_prep, rows);
     } else if (RD <= 768) {
-        cudaFuncSetAttribute(qprep_kernel<3, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(qprep_kernel<3, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         qprep_kernel<3, OUT><<<grid, 256, smem, st>>>(p, R, q_prep, rows);
     } else {
-        cudaFuncSetAttribute(qprep_kernel<4, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(qprep_kernel<4, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         qprep_kernel<4, OUT><<<grid, 256, smem, st>>>(p, R, q_prep, rows);
     }
     return cudaGetLastError();
@@ -568,23 +571,27 @@ __global__ void __launch_bounds__(256) decode_simt_kernel(DecodeParams p) {
     }
 }
 
+static constexpr size_t decode_smem(size_t D) {
+    return sizeof(float) * (kRB * D + kTT * (D + 1) + kRB * kTT + 3 * kRB) + sizeof(int) * kTT;
+}
+
 template <int KIND>
 static cudaError_t launch_decode_kind(const DecodeParams &p, int32_t max_work, cudaStream_t st) {
     const int D = p.s.D();
-    const size_t smem = sizeof(float) * ((size_t)kRB * D + (size_t)kTT * (D + 1) + kRB * kTT + 3 * kRB) +
-                        sizeof(int) * kTT;
+    const size_t smem = decode_smem(D);
+    constexpr int kMost = (int)decode_smem(kMaxRow);
     dim3 grid(max_work, (p.q_len * p.s.H + kRB - 1) / kRB);
     if (p.s.OD() <= 256) {
-        cudaFuncSetAttribute(decode_simt_kernel<KIND, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(decode_simt_kernel<KIND, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         decode_simt_kernel<KIND, 1><<<grid, 256, smem, st>>>(p);
     } else if (p.s.OD() <= 512) {
-        cudaFuncSetAttribute(decode_simt_kernel<KIND, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(decode_simt_kernel<KIND, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         decode_simt_kernel<KIND, 2><<<grid, 256, smem, st>>>(p);
     } else if (p.s.OD() <= 768) {
-        cudaFuncSetAttribute(decode_simt_kernel<KIND, 3>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(decode_simt_kernel<KIND, 3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         decode_simt_kernel<KIND, 3><<<grid, 256, smem, st>>>(p);
     } else {
-        cudaFuncSetAttribute(decode_simt_kernel<KIND, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(decode_simt_kernel<KIND, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         decode_simt_kernel<KIND, 4><<<grid, 256, smem, st>>>(p);
     }
     return cudaGetLastError();
@@ -706,14 +713,17 @@ __global__ void __launch_bounds__(256) combine_kernel(CombineParams p) {
     }
 }
 
+static constexpr size_t combine_smem(size_t OD, size_t r) { return sizeof(float) * (kCR * (OD + r) + kCR); }
+
 cudaError_t launch_combine(const CombineParams &p, cudaStream_t st) {
-    const size_t smem = sizeof(float) * ((size_t)kCR * (p.s.OD() + p.s.r) + kCR);
+    const size_t smem = combine_smem(p.s.OD(), p.s.r);
+    constexpr int kMost = (int)combine_smem(kMaxRow, kMaxRank);
     dim3 grid(p.s.H, (p.B * p.q_len + kCR - 1) / kCR);
     if (p.s.kind == MLA_KV_FP32) {
-        cudaFuncSetAttribute(combine_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(combine_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         combine_kernel<true><<<grid, 256, smem, st>>>(p);
     } else {
-        cudaFuncSetAttribute(combine_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(combine_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         combine_kernel<false><<<grid, 256, smem, st>>>(p);
     }
     return cudaGetLastError();
@@ -1030,6 +1040,11 @@ cudaError_t launch_plan_prep(const DecodeParams &p, int32_t max_work, const Appe
     return launch_pdl(kern, grid, dim3(nt), (size_t)nt * 28, st, p, max_work, pp);
 }
 
+// RD rotated dims in columns of `cols`, and dR of the rope key as codes.
+static constexpr size_t append_int2_smem(size_t RD, size_t cols, size_t dR) {
+    return sizeof(float) * (kAT * ((RD + 3) & ~(size_t)3) + 2 * kAKC * cols + kAT * (cols + 1) + kAT * dR);
+}
+
 cudaError_t launch_append(const AppendParams &p, cudaStream_t st) {
     if (p.num_new == 0) return cudaSuccess;
     if (p.s.kind == MLA_KV_BF16) {
@@ -1049,21 +1064,20 @@ cudaError_t launch_append(const AppendParams &p, cudaStream_t st) {
                 cols = c;
                 break;
             }
-        const int RDp = (RD + 3) & ~3;
-        const size_t smem = sizeof(float) * ((size_t)kAT * RDp + (size_t)2 * kAKC * cols + (size_t)kAT * (cols + 1) +
-                                             (p.s.kind == MLA_KV_INT2_ROT_QR ? (size_t)kAT * p.s.dR : 0));
+        const size_t smem = append_int2_smem(RD, cols, p.s.kind == MLA_KV_INT2_ROT_QR ? p.s.dR : 0);
+        constexpr int kMost = (int)append_int2_smem(kMaxRow, 128, kMaxRope);
         dim3 grid((p.num_new + kAT - 1) / kAT, (p.s.RD() + cols - 1) / cols);
         if (cols == 128) {
-            cudaFuncSetAttribute(append_int2_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            cudaFuncSetAttribute(append_int2_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
             append_int2_kernel<128><<<grid, kAThreads, smem, st>>>(p, cols);
         } else if (cols == 96) {
-            cudaFuncSetAttribute(append_int2_kernel<96>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            cudaFuncSetAttribute(append_int2_kernel<96>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
             append_int2_kernel<96><<<grid, kAThreads, smem, st>>>(p, cols);
         } else if (cols == 64) {
-            cudaFuncSetAttribute(append_int2_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            cudaFuncSetAttribute(append_int2_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
             append_int2_kernel<64><<<grid, kAThreads, smem, st>>>(p, cols);
         } else {
-            cudaFuncSetAttribute(append_int2_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            cudaFuncSetAttribute(append_int2_kernel<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
             append_int2_kernel<0><<<grid, kAThreads, smem, st>>>(p, cols);
         }
     }
