@@ -415,16 +415,12 @@ def _ints(where, device, *tensors) -> list:
 
 def _check_list(where, copies, num_copies, room) -> int:
     """The entries that a list of copies has room for, at least ``room`` of them."""
-    if copies.dim() != 2 or copies.shape[1] != 4 or copies.shape[0] < room or num_copies.numel() < 1:
+    n, width = copies.shape if copies.dim() == 2 else (0, 0)
+    if width != 4 or n < room or num_copies.numel() < 1:
         raise MlaError(MLA_ERR_INVALID, where)
-    _check_sizes(where, copies.shape[0])
-    return copies.shape[0]
-
-
-def _check_sizes(where, *sizes) -> None:
-    """Refuses sizes that the library's 32-bit arguments would cut to others."""
-    if max(sizes) > 0x7fffffff:
+    if n >> 31:                          # (here and below: sizes that 32-bit arguments would cut to others)
         raise MlaError(MLA_ERR_UNSUPPORTED, where)
+    return n
 
 
 @dataclasses.dataclass(frozen=True, eq=False)
@@ -443,7 +439,8 @@ class Pool:
         pointers = _ints("Pool", device, table, lens, ref)
         if table.dim() != 2 or lens.shape != table.shape[:1] or ref.shape != (self.shape.num_blocks,):
             raise MlaError(MLA_ERR_INVALID, "Pool")
-        _check_sizes("Pool", *table.shape, *ref.shape)
+        if max(*table.shape, *ref.shape) >> 31:
+            raise MlaError(MLA_ERR_UNSUPPORTED, "Pool")
         c = mla_pool(*pointers, table.shape[0], table.shape[1])
         object.__setattr__(self, "_c", c)
         object.__setattr__(self, "_args", (self.shape._ref(), ctypes.byref(c)))
@@ -559,7 +556,8 @@ def mla_draft_accept(target_probs, draft_tokens, uniform, accepted, tokens, draf
         ok = ok and dense and draft_probs.dtype is dtype and draft_probs.get_device() == device and draft_probs.shape == (B, K, V)
     if not ok:
         raise MlaError(MLA_ERR_INVALID, "mla_draft_accept")
-    _check_sizes("mla_draft_accept", B, rows, V)
+    if (B | rows | V) >> 31:
+        raise MlaError(MLA_ERR_UNSUPPORTED, "mla_draft_accept")
     _check(load_library().mla_draft_accept(B, K, V, MLA_DTYPE_F32 if dtype is torch.float32 else MLA_DTYPE_BF16,
                                            target_probs.data_ptr(), p_stride, q, q_stride, x, counts, uniform.data_ptr(), lens,
                                            n, out, new, word, stream), "mla_draft_accept")
