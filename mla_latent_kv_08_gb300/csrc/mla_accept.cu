@@ -290,25 +290,31 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams a) 
     else find_token<kPlain>(p, q, out, lo, hi, from, t, sh.scan, tokens + n);
 }
 
-// CTAs a sequence: as many as there is room for at two an SM, and no more than the row has work for.
-// A second round of clusters costs more than the split gives (128 sequences of 32000 tokens: 15.1 us
-// with 1, 10.9 with 2, 20.0 with 4; 64 of 50257: 13.9 with 1, 7.7 with 4, 12.3 with 8; 150 of 32000: 14.2
-// with 1, 11.1 with 2), but for long rows, whose CTAs it spreads over the SMs (100 of 200000: 44.9 with
-// 2, 36.9 with 4; 40 of 131072: 14.7 with 4, 13.5 with 8; 60 of 100000: 16.0 with 4, 17.1 with 7). 16 for few
-// sequences (12 of 131072: 8.5 with 8, 7.0 with 16; 20: 9.1, 10.5). Odd numbers are slower than the next
-// lower power of two.
-unsigned cluster_size(int32_t B, int32_t V) {
-    const unsigned most = B <= 12 ? 16 : 8;
+// CTAs a sequence: a power of two up to 8 (odd numbers are slower than the next lower one), with 1024
+// tokens each at least, and two CTAs an SM at most: a second round of clusters costs more than the split
+// gives (an fp32 row and a draft's: 32 sequences of 50257 tokens 7.3 us with 8 and 8.5 with 4, 40 11.2 and
+// 9.4; 72 of 32000 7.6 with 4 and 8.4 with 2, 80 10.1 and 9.3; 190 14.6 with 2, 14.4 with 1). Parts of 32768 tokens and more are halved up to 2.75 CTAs an SM, since the halves spread
+// over the SMs (52 of 200000: 23.9 with 8, 26.0 with 4; 104: 38.6 with 4, 45.4 with 2). Few sequences
+// get 16 (12 of 131072: 6.8 with 16, 8.2 with 8; 20: 10.3, 9.2), as long as that is 4 CTAs for 3 SMs.
+// No limit is the best one for every length: 220 of 200000 take 83.3 with the 1 of this rule, 63.1
+// with 4; 160 of 32000 13.8 with its 1, 11.8 with 2; 40 of 129280 14.4 with its 4, 13.4 with 8; 20 of
+// 200000 13.9 with its 8, 13.4 with 16.
+unsigned cluster_size(int32_t B, int32_t V, int32_t sms) {
+    const unsigned most = 16ll * B <= 4 * sms / 3 ? 16 : 8;
     unsigned C = 1;
-    while (C < most && 1024ll * C < V && 2 * C * (int64_t)B <= ((unsigned)V / C < 32768 ? 304 : 416)) C *= 2;
+    while (C < most && 1024ll * C < V && 2 * C * (int64_t)B <= ((unsigned)V / C < 32768 ? 2 * sms : 11 * sms / 4)) C *= 2;
     return C;
 }
 
 template <typename T>
 cudaError_t launch(const AcceptParams &p, cudaStream_t st) {
-    const unsigned C = cluster_size(p.B, p.V);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const unsigned C = cluster_size(p.B, p.V, sms);
     if (C > 8) {
-        const cudaError_t e = cudaFuncSetAttribute(accept_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        e = cudaFuncSetAttribute(accept_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
