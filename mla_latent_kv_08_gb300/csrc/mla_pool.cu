@@ -465,10 +465,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1) compact_kernel(const PoolParam
     pdl_wait();
     pdl_trigger();
     if (tid == 0) sh.flags = 0;
-    int pieces = 0, flags = 0;
+    int pieces = 0, flags = 0, next = tid < p.S ? p.lens[tid] : 0;
+    count_free(p, sh, parts, w);             // while these are on their way
     for (int b0 = 0; b0 < p.S; b0 += block) {
         const int b = b0 + tid;
-        int len = b < p.S ? p.lens[b] : 0;
+        int len = next;
+        next = b + block < p.S ? p.lens[b + block] : 0;
         if (len < 0 || len > p.cap) {
             flags |= FLAG_BAD_LENGTH;
             len = 0;
@@ -488,7 +490,6 @@ __global__ void __launch_bounds__(kMaxThreads, 1) compact_kernel(const PoolParam
                 if (k < n && (v[k] < 0 || v[k] >= p.N)) flags |= FLAG_BAD_BLOCK;
         });
     if (flags) atomicOr(&sh.flags, flags);
-    count_free(p, sh, parts, w);
     const Totals t = exchange(cl, here, sh, w, warps, 0, 0);
     const int live = p.N - t.all;
     if (t.flags) {
