@@ -5,9 +5,12 @@
 // that an entry is up to three contiguous pieces a layer. Memory bound: the bytes once in,
 // once out. A CTA takes kPart bytes of an entry at a time, all of which it loads before it
 // stores any: kUnroll 16-byte loads a thread. 200 whole blocks of the 8-bit cache in 24 layers (403 MB
-// in and out): 63.5 us, 6.3 TB/s of the copy rate's 6.7 (array by array, with 8 CTAs an SM: 78 us;
-// 8 KB a task: 93 us, 32 KB: 71 us). 24 tails of 1 to 64 rows in 32 layers (61 MB): 12.1 us (13.3 where
-// a bf16 row's one array goes the way of three); 8 in one layer: 1.7 us. An empty list costs 1 to 3 us,
+// in and out): 63.1 us, 6.4 TB/s of the copy rate's 6.7 (array by array, with 8 CTAs an SM: 78 us;
+// 8 KB a task: 93 us, 32 KB: 71 us); of bf16 rows (708 MB) 107.7 us, 6.6 TB/s; of fp32 ones (1416 MB)
+// 212 us, 6.7 TB/s; of rotated 2-bit ones (197 MB) 34.5 us, 5.7 TB/s; with the rope key as codes too
+// (133 MB) 26.4 us, 5.0 TB/s: its rows of 144 and 72 bytes go in 8-byte loads, since all loads are as wide
+// as the narrowest array has them. 24 tails of 1 to 64 rows in 32 layers (61 MB): 11.9 us (13.3 where a
+// bf16 row's one array goes the way of three); 8 in one layer: 1.7 us. An empty list costs 1 to 3 us,
 // by the CTAs that its room asks for: 16 an SM at most (24 would copy 1 to 2 % faster).
 #include "mla_internal.cuh"
 

@@ -15,11 +15,12 @@
 //
 // Small calls are bound by their chain of dependent steps, of about half a microsecond each (a
 // load from L2 takes 0.4, a cluster's barrier 0.5 to 1): a step of 32 sequences takes 5.7 us, a fork of
-// one 4.7, compaction of 500 blocks 4.5. Large ones by the scattered accesses that 16 SMs can issue: 512
-// sequences that give back 100k entries of 290k blocks 19.6 us (with a step's free blocks looked
+// one 4.7, compaction of 500 blocks 4.9. Large ones by the scattered accesses that 16 SMs can issue: 512
+// sequences that give back 100k entries of 290k blocks 19.7 us (with a step's free blocks looked
 // up one by one 32, with entries loaded one by one 36), 200 forks of 230k entries 16.6 us, 300k
-// entries that follow 70k moved blocks 27.6 us. Walking them in a second kernel on all SMs took 19.3,
-// 13.7 and 24.3 us when this took 21.1, 17.6 and 28.9, but two or three launches.
+// entries that follow 70k moved blocks 27.7 us. Walking them in a second kernel on all SMs took 19.3,
+// 13.7 and 24.3 us when this took 21.1, 17.6 and 28.9, in two or three launches: less in a captured
+// graph, as much for a call of its own.
 #include "mla_internal.cuh"
 
 #include <cooperative_groups.h>
@@ -567,12 +568,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1) compact_kernel(const PoolParam
 }
 
 // The cluster, for `rows` rows of the table. A CTA alone is launched without one, and its barriers
-// cost little: a step of 16 sequences, 1000 entries and 700 blocks takes 4.6 us with 512 threads,
-// 5.3 with 1024, 5.8 with two CTAs of 512; compaction of them 4.6, 5.5, 7.6. Turnover of 64 sequences,
-// 4300 entries and 2600 blocks: 10.8, 9.0, 9.2; compaction 9.0, 7.9, 9.8. With 16k entries and 12k blocks
-// compaction takes 10.4 us with 8 CTAs of 512, 11.7 with 8 of 1024, 18.6 with one; with 33k and 24k
-// 15.1, 12.4 and 41. Turnover of 512 sequences, 600k entries and 290k blocks: 32 us with 8 of 1024, 21
-// with 16, 159 with one.
+// cost little: a step of 16 sequences, 1000 entries and 700 blocks takes 4.2 us with 512 threads,
+// 4.8 with 1024, 5.6 with two CTAs of 512; compaction of them 5.0, 5.7, 8.0. Turnover of 64 sequences,
+// 4300 entries and 2600 blocks: 9.9, 8.2, 8.7; compaction 10.4, 9.0, 10.4 (8 CTAs 8.9). With 16k entries and
+// 12k blocks compaction takes 9.3 us with 8 CTAs of 512, 10.4 with 8 of 1024, 13.1 with one; with 33k and
+// 24k 17.4, 14.0 and 50 (16 CTAs 12.5). Turnover of 512 sequences, 580k entries and 320k blocks: 33.5 us
+// with 8 of 1024, 21.2 with 16, 196 with one.
 struct Cluster {
     unsigned ctas, threads;
 };
