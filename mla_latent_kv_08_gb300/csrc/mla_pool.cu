@@ -19,8 +19,8 @@
 // sequences that give back 100k entries of 290k blocks 19.7 us (with a step's free blocks looked
 // up one by one 32, with entries loaded one by one 36), 200 forks of 230k entries 16.6 us, 300k
 // entries that follow 70k moved blocks 27.7 us. Walking them in a second kernel on all SMs took 19.3,
-// 13.7 and 24.3 us when this took 21.1, 17.6 and 28.9, in two or three launches: less in a captured
-// graph, as much for a call of its own.
+// 13.7 and 24.3 us when this took 21.1, 17.6 and 28.9, in two or three launches, which a call outside a
+// captured graph pays for on the host.
 #include "mla_internal.cuh"
 
 #include <cooperative_groups.h>
